@@ -359,3 +359,17 @@ def linear(x, w_packed, scales, tensor_scale: float, out=None, out_dtype=None, s
                               out.data_ptr(), m, n, k, y_dtype, tile, stream.cuda_stream)
     _check(st, "nvfp4_linear" if tile is None else "nvfp4_linear_tiled")
     return out
+
+
+# The serving step around the products (paged NVFP4 cache, sampling) lives in
+# serving.py, which needs torch; its names are this package's, loaded on first use.
+_SERVING = ("KvCache", "kv_append", "kv_read", "kv_attention", "kv_attention_workspace", "kv_weights", "kv_evict", "sample")
+
+
+def __getattr__(name):
+    if name in _SERVING:
+        from . import serving
+        for n in _SERVING:
+            globals()[n] = getattr(serving, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -20,9 +20,10 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libnvfp4_w4a16.so")
 ARCH = "gfx950"
 
-HOST_SOURCES = ["host/pack.cpp", "host/tiles.cpp"]
+HOST_SOURCES = ["host/pack.cpp", "host/tiles.cpp", "host/kv_shapes.cpp"]
 HIP_SOURCES = ["kernels/nvfp4_linear.hip", "kernels/nvfp4_gemm.hip", "kernels/nvfp4_fused.hip",
-               "kernels/w8a16.hip", "kernels/read_probe.hip", "kernels/library_gemm.hip"]
+               "kernels/w8a16.hip", "kernels/read_probe.hip", "kernels/library_gemm.hip",
+               "kernels/kv_cache.hip", "kernels/kv_attention.hip", "kernels/kv_evict.hip", "kernels/sample.hip"]
 
 # -ffp-contract=off keeps the packer's float64 steps unfused (bit-exact rule).
 HOST_FLAGS = ["-std=c++17", "-O3", "-fPIC", "-ffp-contract=off", "-Wall", "-Wextra",

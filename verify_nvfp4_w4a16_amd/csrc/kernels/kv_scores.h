@@ -1,0 +1,130 @@
+// Which slots a query row of the paged cache sees, and its scores: shared by
+// the attention kernels and by the one that sums the weights of slots.
+#pragma once
+
+#include "kv_common.h"
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct KvScores {
+    const uint16_t* q;
+    int64_t q_pitch, q_head_pitch;
+    int heads, group;      // query heads, and those of one kv head
+    int window;            // 0: no limit
+    int causal;
+    float scale;           // of q . (e4m3 * e2m1): the caller's times K's tensor scale
+    float cap, cap_inv2;   // softcap and 2 / softcap (0: none)
+
+    // z * log2(e) of a product's sum x, whose row was scaled by its own power
+    // of two (f is scale over that power, times log2(e) where there is no cap).
+    __device__ __forceinline__ float shape(float x, float f) const {
+        const float z = x * f;
+        if (cap == 0.0f) return z;
+        // cap * tanh(z / cap) with tanh y = 1 - 2 / (1 + exp(2 y)): exact limits at both ends
+        const float e = __builtin_amdgcn_exp2f(z * (cap_inv2 * kLog2e));
+        return (cap - 2.0f * cap / (1.0f + e)) * kLog2e;
+    }
+};
+
+inline KvScores kv_scores(const nvfp4_kv_cache_t* c, const nvfp4_kv_queries_t* q) {
+    KvScores s;
+    s.q = static_cast<const uint16_t*>(q->q);
+    s.q_pitch = q->q_pitch;
+    s.q_head_pitch = q->q_head_pitch;
+    s.heads = static_cast<int>(q->heads);
+    s.group = static_cast<int>(q->heads / c->kv_heads);
+    s.window = static_cast<int>(q->window < (int64_t(1) << 29) ? q->window : 0);   // no sequence is longer
+    s.causal = q->causal;
+    s.scale = q->scale * c->k_scale;
+    s.cap = q->softcap;
+    s.cap_inv2 = q->softcap > 0.0f ? 2.0f / q->softcap : 0.0f;
+    return s;
+}
+
+// Slots [lo, hi) that some row of a set sees and [lo_all, hi_all) that all see.
+struct Span {
+    int lo, hi, lo_all, hi_all;
+};
+
+// One query row: its packed token, its query head within the group, and its slots [lo, hi).
+struct QueryRow {
+    int token, g, lo, hi;
+};
+
+// The rows of one sequence and kv head: row r is new token r / group, query
+// head r % group of the group.
+struct QueryRows {
+    int first_token, new_tokens, len, count, group;
+
+    __device__ __forceinline__ QueryRows(const KvView& v, const KvScores& sc, int s) {
+        first_token = v.start(s);
+        new_tokens = max(v.start(s + 1) - first_token, 0);
+        len = v.len(s);
+        group = sc.group;
+        count = new_tokens * group;
+    }
+    __device__ __forceinline__ int see_lo(const KvScores& sc, int i) const {
+        return sc.window > 0 ? max(len - new_tokens + i - sc.window + 1, 0) : 0;
+    }
+    __device__ __forceinline__ int see_hi(const KvScores& sc, int i) const {
+        return sc.causal ? max(min(len, len - new_tokens + i + 1), 0) : len;
+    }
+    // For rows first .. last (both below count).
+    __device__ __forceinline__ Span span(const KvScores& sc, int first, int last) const {
+        const int i0 = first / group, i1 = last / group;
+        return Span{see_lo(sc, i0), see_hi(sc, i1), see_lo(sc, i1), see_hi(sc, i0)};
+    }
+    // A row at or beyond count stands in for the last one (its result is dropped).
+    __device__ __forceinline__ QueryRow row(const KvScores& sc, int r) const {
+        r = min(r, count - 1);
+        const int i = r / group;
+        return QueryRow{first_token + i, r - i * group, see_lo(sc, i), see_hi(sc, i)};
+    }
+    // Index of a row in [total][heads].
+    __device__ __forceinline__ int64_t place(const KvScores& sc, int r, int hk) const {
+        const int i = r / group;
+        return int64_t(first_token + i) * sc.heads + hk * group + (r - i * group);
+    }
+};
+
+// A query row's 32 (D = 128) of D / 4 dims b * D/4 .. as f16 operands.  bf16
+// reaches further than f16, so the row is scaled by the power of two that puts
+// its largest magnitude into [2^14, 2^15): every element within 2^-28 of it
+// keeps all its bits.  The four lanes that share the row agree on the power.
+// Returns the factor that turns a sum of products into the score (times
+// log2(e) where the scores are not capped).
+template <int D>
+__device__ __forceinline__ float load_query(const KvView& v, const KvScores& sc, const QueryRow& r, int hk, int b,
+                                            f16x8 (&q)[D / 32]) {
+    const uint16_t* p = sc.q + int64_t(r.token) * sc.q_pitch + int64_t(hk * sc.group + r.g) * sc.q_head_pitch + b * (D / 4);
+    u32x4 raw[D / 32];
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        raw[i] = load16(p + 8 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            top = fmaxf(top, fabsf(bits_f32(raw[i][j] << 16)));
+            top = fmaxf(top, fabsf(bits_f32(raw[i][j] & 0xffff0000u)));
+        }
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // the power from the exponent field, held to what 2^14 / 2^e needs to stay finite
+    const int e = min(max(int(f32_bits(top) >> 23) - 127, -100), 126);
+    const float up = ldexpf(1.0f, 14 - e);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            q[i][2 * j] = static_cast<_Float16>(bits_f32(raw[i][j] << 16) * up);
+            q[i][2 * j + 1] = static_cast<_Float16>(bits_f32(raw[i][j] & 0xffff0000u) * up);
+        }
+    const float f = sc.scale * ldexpf(1.0f, e - 14);
+    return sc.cap == 0.0f ? f * kLog2e : f;
+}
+
+}  // namespace

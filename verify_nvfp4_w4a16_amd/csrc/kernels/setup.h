@@ -18,6 +18,9 @@ int gemm_setup();
 // Kernel attributes of the FP8 (W8A16) kernels.
 int w8a16_setup();
 
+// Kernel attributes of the attention over the paged cache (LDS beyond 64 KB).
+int kv_setup();
+
 // The current device's CU count (after device_setup; 256 if unknown).
 int device_cus();
 
