@@ -21,6 +21,9 @@ int w8a16_setup();
 // Kernel attributes of the attention over the paged cache (LDS beyond 64 KB).
 int kv_setup();
 
+// Kernel attributes of nvfp4_sample's kernels (LDS beyond 64 KB).
+int sample_setup();
+
 // The current device's CU count (after device_setup; 256 if unknown).
 int device_cus();
 
