@@ -25,6 +25,10 @@ namespace {
 
 constexpr int kWaves = 4;
 
+// Scores may outgrow the running maximum by this much (in powers of two)
+// before the sums are rescaled: the weights then stay below 2^8, within f16.
+constexpr float kSlack = 8.0f;
+
 struct AttendArgs {
     KvView v;
     KvScores sc;
@@ -121,7 +125,7 @@ kv_attend_rows_kernel(AttendArgs a) {
 
     const QueryRow me = rows.row(a.sc, row0 + n);
     f16x8 q[D / 32];
-    const float to_log2 = load_query<D>(a.v, a.sc, me, hk, b, q);
+    const float to_log2 = load_query<D / 32, 8, 16>(a.sc, query_at(a.sc, me, hk) + b * (D / 4), q);
 
     f32x4 o[D / 16];
 #pragma unroll
@@ -159,7 +163,7 @@ kv_attend_rows_kernel(AttendArgs a) {
             for (int i = 1; i < 16; ++i) top = fmaxf(top, p[i]);
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            if (__any(top > m)) {
+            if (__any(top > m + kSlack)) {
                 const float grown = fmaxf(m, top);
                 const float keep = grown == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
                 m = grown;
@@ -257,6 +261,220 @@ kv_attend_rows_kernel(AttendArgs a) {
     if (a.lse && d0 == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
 }
 
+// ---- many query rows
+
+// A workgroup takes 128 rows, 32 a wavefront, and decodes each page once for
+// all of them into LDS as f16: K [64 slots][D], V [D][64 slots], in 16-byte
+// chunks whose place within a row is permuted so that the lanes of a matrix
+// operand's read fall on different banks.
+template <int D>
+struct PageTiles {
+    static constexpr int kBytes = 2 * kPage * D * 2;
+
+    static __device__ __forceinline__ int k_at(int slot, int chunk) {
+        return (slot * (D / 8) + (chunk ^ (D == 64 ? (slot >> 1) & 7 : slot & 15))) * 16;
+    }
+    static __device__ __forceinline__ int v_at(int dim, int block) {
+        return kPage * D * 2 + (dim * 8 + (block ^ ((dim >> 1) & 7))) * 16;
+    }
+};
+
+// A thread's share of a page: D / 4 dims of one slot's K, D / 32 dims of one
+// 8-slot block's V.
+template <int D>
+struct PageShare {
+    uint32_t k[D / 32], v[D / 32];
+    uint32_t ks, vs[2];
+
+    __device__ __forceinline__ void load(const uint8_t* rec, int tid) {
+        using R = KvRecord<D>;
+        const int slot = tid >> 2, part = tid & 3;
+        PageRegs<D>::template load<D / 32>(k, rec + R::k_code(slot) + part * (D / 8));
+        const uint8_t* p = rec + R::k_scale(slot, part * (D / 64));
+        if constexpr (D == 64)
+            ks = *p;
+        else if constexpr (D == 128)
+            ks = *reinterpret_cast<const uint16_t*>(p);
+        else
+            ks = *reinterpret_cast<const uint32_t*>(p);
+        const int block = tid >> 5, dim = (tid & 31) * (D / 32);
+        PageRegs<D>::template load<D / 32>(v, rec + R::v_code(block, dim));
+        PageRegs<D>::template load<2>(vs, rec + R::v_scale(block, dim / 16));
+    }
+
+    template <int J>
+    __device__ __forceinline__ void put_k(char* lds, int slot, int part) const {
+        if constexpr (J < D / 64) {
+            const f16x2 s = scale_both<J>(ks);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<f16x8*>(lds + PageTiles<D>::k_at(slot, part * (D / 32) + 2 * J + e)) =
+                    decode_row(k[2 * J + e], s);
+            put_k<J + 1>(lds, slot, part);
+        }
+    }
+
+    // left: slots of the page before the sequence's end; what lies after may
+    // hold anything, and becomes 0 in V (scores of such slots are masked).
+    __device__ __forceinline__ void put(char* lds, int tid, int left) {
+        put_k<0>(lds, tid >> 2, tid & 3);
+        const int block = tid >> 5, dim = (tid & 31) * (D / 32);
+        if (left < kPage) {
+            const int live = left - 8 * block;
+            const uint64_t mask = live <= 0 ? 0 : live >= 8 ? ~0ull : (1ull << (8 * live)) - 1;
+            vs[0] &= uint32_t(mask);
+            vs[1] &= uint32_t(mask >> 32);
+        }
+        const f16x2 sc[4] = {scale_pair<0>(vs[0]), scale_pair<1>(vs[0]), scale_pair<0>(vs[1]), scale_pair<1>(vs[1])};
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            *reinterpret_cast<f16x8*>(lds + PageTiles<D>::v_at(dim + i, block)) = decode_slots(v[i], sc);
+    }
+};
+
+constexpr int kTileRows = 32 * kWaves;
+
+template <int D>
+__global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
+kv_attend_tile_kernel(AttendArgs a) {
+    extern __shared__ char tiles[];   // two pages
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int n = lane & 31, b = lane >> 5;
+    const int s = blockIdx.y, split = blockIdx.x % a.splits;
+    const int hk = blockIdx.x / a.splits % a.v.kv_heads;
+    const QueryRows rows(a.v, a.sc, s);
+    // the last rows see most: they begin first
+    const int tile = int(gridDim.x / a.splits / a.v.kv_heads) - 1 - int(blockIdx.x / a.splits / a.v.kv_heads);
+    const int row0 = tile * kTileRows;
+    if (row0 >= rows.count) return;
+
+    const Span all = rows.span(a.sc, row0, min(row0 + kTileRows, rows.count) - 1);
+    const int page_lo = all.lo / kPage, page_hi = (all.hi + kPage - 1) / kPage;
+    const int per = (max(page_hi - page_lo, 0) + a.splits - 1) / a.splits;
+    const int begin = page_lo + split * per, end = min(begin + per, page_hi);
+
+    const int my0 = row0 + wave * 32;
+    const QueryRow me = rows.row(a.sc, my0 + n);
+    const Span span = rows.span(a.sc, min(my0, rows.count - 1), min(my0 + 32, rows.count) - 1);
+    f16x8 q[D / 16];   // step i: dims 16 i + 8 b ..
+    const float to_log2 = load_query<D / 16, 16, 32>(a.sc, query_at(a.sc, me, hk) + 8 * b, q);
+
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f;
+    // Row r of a 32-slot operand is slot r with bits 2 and 3 exchanged: a
+    // lane's scores 8 t .. 8 t + 7 are then those of 8 consecutive slots.
+    const int slot_n = (n & ~12) | ((n & 4) << 1) | ((n & 8) >> 1);
+
+    PageShare<D> share;
+    const uint8_t* rec = begin < end ? a.v.record<D>(s, begin, hk) : nullptr;
+    if (rec) share.load(rec, tid);
+    for (int page = begin; page < end; ++page) {
+        char* lds = tiles + ((page - begin) & 1) * PageTiles<D>::kBytes;
+        const int base = page * kPage;
+        if (rec) share.put(lds, tid, rows.len - base);
+        const uint8_t* now = rec;
+        rec = page + 1 < end ? a.v.record<D>(s, page + 1, hk) : nullptr;
+        __syncthreads();
+        if (rec) share.load(rec, tid);
+        if (!now || base >= span.hi || base + kPage <= span.lo) continue;
+
+        f32x16 z[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            z[h] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const f16x8 k = *reinterpret_cast<const f16x8*>(lds + PageTiles<D>::k_at(32 * h + slot_n, 2 * i + b));
+                z[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[i], z[h], 0, 0, 0);
+            }
+        }
+        float p[32];   // [h][t][8 consecutive slots]: slot 32 h + 16 t + 8 b + j
+#pragma unroll
+        for (int i = 0; i < 32; ++i) p[i] = a.sc.shape(z[i >> 4][i & 15], to_log2);
+        if (base < span.lo_all || base + kPage > span.hi_all) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int slot = base + 16 * (i >> 3) + 8 * b + (i & 7);
+                p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
+            }
+        }
+        float top = p[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) top = fmaxf(top, p[i]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (__any(top > m + kSlack)) {
+            const float grown = fmaxf(m, top);
+            const float keep = grown == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
+            m = grown;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) o[i] *= keep;
+        }
+        const float base_m = m == -INFINITY ? 0.0f : m;
+        f16x8 pt[4];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float e = __builtin_amdgcn_exp2f(p[i] - base_m);
+            l += e;
+            pt[i >> 3][i & 7] = static_cast<_Float16>(e);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const f16x8 v = *reinterpret_cast<const f16x8*>(lds + PageTiles<D>::v_at(32 * i + n, 2 * t + b));
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pt[t], o[i], 0, 0, 0);
+            }
+    }
+    l += __shfl_xor(l, 32);
+    if (l != l && m == -INFINITY) m = 0.0f;   // all scores NaN: the row stays NaN
+
+    const bool live = my0 + n < rows.count;
+    const int64_t at = rows.place(a.sc, min(my0 + n, rows.count - 1), hk);
+    if (a.splits > 1) {
+        if (!live) return;
+        const int64_t slice = int64_t(a.v.total) * a.sc.heads;
+        float* po = a.part_o + (split * slice + at) * D;
+        if (m > -INFINITY)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int c = 0; c < 16; c += 4)
+                    *reinterpret_cast<f32x4*>(po + 32 * i + 2 * c + 4 * b) = f32x4{o[i][c], o[i][c + 1], o[i][c + 2], o[i][c + 3]};
+        if (b == 0) {
+            a.part_ml[(split * slice + at) * 2] = m;
+            a.part_ml[(split * slice + at) * 2 + 1] = l;
+        }
+        return;
+    }
+    // bf16 rows through LDS, then 16-byte stores along them
+    const float f = l > 0.0f || l != l ? a.v_scale / l : 0.0f;
+    if (a.lse && live && b == 0) a.lse[at] = (m + log2f(l)) * kLn2;
+    __syncthreads();
+    constexpr int kRow = D * 2 + 16;   // bytes of a staged row
+    char* stage = tiles + wave * 32 * kRow;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+            uint16_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = f32_to_bf16_rne(o[i][c + j] * f);
+            u32x2 x;
+            __builtin_memcpy(&x, w, 8);
+            *reinterpret_cast<u32x2*>(stage + n * kRow + (32 * i + 2 * c + 4 * b) * 2) = x;
+        }
+    __syncthreads();
+    for (int i = lane; i < 32 * (D / 8); i += 64) {
+        const int r = i / (D / 8), part = i % (D / 8);
+        if (my0 + r >= rows.count) break;
+        *reinterpret_cast<u32x4*>(a.out + rows.place(a.sc, my0 + r, hk) * D + 8 * part) =
+            *reinterpret_cast<const u32x4*>(stage + r * kRow + 16 * part);
+    }
+}
+
 // Joins the splits of one row in split order: one wavefront a row.
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -288,22 +506,40 @@ kv_join_kernel(AttendArgs a) {
     if (a.lse && lane == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
 }
 
-// Workgroups that each get `splits` parts of their sequences' pages.
-int split_count(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
+// How a call is laid out: 16-row or 128-row workgroups, and over how many
+// workgroups each sequence's pages are split.
+struct Plan {
+    bool tile;
+    int64_t row_tiles;
+    int splits;
+};
+
+Plan plan_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
     const int64_t rows = q->max_q * (q->heads / c->kv_heads);
-    const int64_t base = s->seqs * c->kv_heads * ((rows + 15) / 16);
+    Plan p;
+    p.tile = rows > 32;
+    const int64_t per_tile = p.tile ? kTileRows : 16;
+    p.row_tiles = (rows + per_tile - 1) / per_tile;
+    p.splits = 1;
+    const int64_t base = s->seqs * c->kv_heads * p.row_tiles;
     int64_t slots = q->max_kv;
     if (q->window > 0) slots = std::min(slots, q->window + q->max_q);
     const int64_t pages = (slots + kPage - 1) / kPage;
-    if (base == 0 || pages == 0) return 1;
-    int64_t splits = std::max<int64_t>((1024 + base - 1) / base, (slots + 4095) / 4096);
-    splits = std::min(splits, (pages + kWaves - 1) / kWaves);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(splits, 256)));
+    if (base == 0 || pages == 0) return p;
+    int64_t splits;
+    if (p.tile) {
+        splits = std::min((512 + base - 1) / base, (pages + 3) / 4);
+    } else {
+        splits = std::max<int64_t>((1024 + base - 1) / base, (slots + 4095) / 4096);
+        splits = std::min(splits, (pages + kWaves - 1) / kWaves);
+    }
+    p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(splits, 256)));
+    return p;
 }
 
 int64_t workspace_bytes_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
-    const int splits = split_count(c, s, q);
-    return splits == 1 ? 0 : int64_t(splits) * s->total * q->heads * (c->head_dim + 2) * int64_t(sizeof(float));
+    const int64_t splits = plan_of(c, s, q).splits;
+    return splits == 1 ? 0 : splits * s->total * q->heads * (c->head_dim + 2) * int64_t(sizeof(float));
 }
 
 template <int D>
@@ -312,17 +548,28 @@ constexpr size_t rows_lds() {
 }
 
 template <int D>
-bool allow_lds() {
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kv_attend_rows_kernel<D>),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLdsBytes) == hipSuccess;
+constexpr size_t tile_lds() {
+    return 2 * PageTiles<D>::kBytes;   // at least the staged rows of the output
 }
 
 template <int D>
-int launch_attend(const AttendArgs& a, int64_t rows, hipStream_t st) {
-    const int64_t blocks = (rows + 15) / 16 * a.v.kv_heads * a.splits;
+bool allow_lds() {
+    static_assert(tile_lds<D>() >= kTileRows * (D * 2 + 16) && tile_lds<D>() <= kMaxLdsBytes);
+    for (const void* fn : {reinterpret_cast<const void*>(kv_attend_rows_kernel<D>),
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D>)})
+        if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLdsBytes) != hipSuccess) return false;
+    return true;
+}
+
+template <int D>
+int launch_attend(const AttendArgs& a, const Plan& plan, hipStream_t st) {
+    const int64_t blocks = plan.row_tiles * a.v.kv_heads * plan.splits;
     if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL(kv_attend_rows_kernel<D>, dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(64 * kWaves),
-                       rows_lds<D>(), st, a);
+    const dim3 grid(static_cast<unsigned>(blocks), a.v.seqs);
+    if (plan.tile)
+        hipLaunchKernelGGL(kv_attend_tile_kernel<D>, grid, dim3(64 * kWaves), tile_lds<D>(), st, a);
+    else
+        hipLaunchKernelGGL(kv_attend_rows_kernel<D>, grid, dim3(64 * kWaves), rows_lds<D>(), st, a);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     if (a.splits > 1) {
         const int64_t slice = int64_t(a.v.total) * a.sc.heads;
@@ -371,15 +618,15 @@ extern "C" int nvfp4_kv_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_
     a.sc = kv_scores(cache, queries);
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    a.splits = split_count(cache, seqs, queries);
+    const Plan plan = plan_of(cache, seqs, queries);
+    a.splits = plan.splits;
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = a.splits > 1 ? a.part_o + int64_t(a.splits) * seqs->total * queries->heads * cache->head_dim : nullptr;
     a.v_scale = cache->v_scale;
-    const int64_t rows = queries->max_q * a.sc.group;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (cache->head_dim) {
-        case 64: return launch_attend<64>(a, rows, s);
-        case 128: return launch_attend<128>(a, rows, s);
-        default: return launch_attend<256>(a, rows, s);
+        case 64: return launch_attend<64>(a, plan, s);
+        case 128: return launch_attend<128>(a, plan, s);
+        default: return launch_attend<256>(a, plan, s);
     }
 }

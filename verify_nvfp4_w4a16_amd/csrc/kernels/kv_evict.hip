@@ -81,7 +81,7 @@ kv_weights_kernel(WeightArgs a) {
         for (int r0 = i_lo * rows.group; r0 < r_hi; r0 += 16) {
             f16x8 q[D / 32];
             const QueryRow me = rows.row(a.sc, r0 + n);
-            const float f_n = load_query<D>(a.v, a.sc, me, hk, b, q);
+            const float f_n = load_query<D / 32, 8, 16>(a.sc, query_at(a.sc, me, hk) + b * (D / 4), q);
             const float lse_n = a.lse[rows.place(a.sc, min(r0 + n, rows.count - 1), hk)];
             const bool live_n = r0 + n < r_hi && lse_n != -INFINITY;
             const int lo_n = live_n ? me.lo : 0, hi_n = live_n ? me.hi : 0;

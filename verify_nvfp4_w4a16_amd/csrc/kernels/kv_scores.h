@@ -90,34 +90,32 @@ struct QueryRows {
     }
 };
 
-// A query row's 32 (D = 128) of D / 4 dims b * D/4 .. as f16 operands.  bf16
-// reaches further than f16, so the row is scaled by the power of two that puts
-// its largest magnitude into [2^14, 2^15): every element within 2^-28 of it
-// keeps all its bits.  The four lanes that share the row agree on the power.
-// Returns the factor that turns a sum of products into the score (times
-// log2(e) where the scores are not capped).
-template <int D>
-__device__ __forceinline__ float load_query(const KvView& v, const KvScores& sc, const QueryRow& r, int hk, int b,
-                                            f16x8 (&q)[D / 32]) {
-    const uint16_t* p = sc.q + int64_t(r.token) * sc.q_pitch + int64_t(hk * sc.group + r.g) * sc.q_head_pitch + b * (D / 4);
-    u32x4 raw[D / 32];
+// A query row as f16 operands: N pieces of 8 dims, piece i at p + i * STEP.
+// bf16 reaches further than f16, so the row is scaled by the power of two that
+// puts its largest magnitude into [2^14, 2^15): every element within 2^-28 of
+// it keeps all its bits.  The lanes that share the row (those whose numbers
+// differ in bits FIRST .. 32) agree on the power.  Returns the factor that turns
+// a sum of products into the score (times log2(e) where scores are not capped).
+template <int N, int STEP, int FIRST>
+__device__ __forceinline__ float load_query(const KvScores& sc, const uint16_t* p, f16x8 (&q)[N]) {
+    u32x4 raw[N];
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        raw[i] = load16(p + 8 * i);
+    for (int i = 0; i < N; ++i) {
+        raw[i] = load16(p + STEP * i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             top = fmaxf(top, fabsf(bits_f32(raw[i][j] << 16)));
             top = fmaxf(top, fabsf(bits_f32(raw[i][j] & 0xffff0000u)));
         }
     }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
+#pragma unroll
+    for (int d = FIRST; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     // the power from the exponent field, held to what 2^14 / 2^e needs to stay finite
     const int e = min(max(int(f32_bits(top) >> 23) - 127, -100), 126);
     const float up = ldexpf(1.0f, 14 - e);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             q[i][2 * j] = static_cast<_Float16>(bits_f32(raw[i][j] << 16) * up);
@@ -125,6 +123,10 @@ __device__ __forceinline__ float load_query(const KvView& v, const KvScores& sc,
         }
     const float f = sc.scale * ldexpf(1.0f, e - 14);
     return sc.cap == 0.0f ? f * kLog2e : f;
+}
+
+__device__ __forceinline__ const uint16_t* query_at(const KvScores& sc, const QueryRow& r, int hk) {
+    return sc.q + int64_t(r.token) * sc.q_pitch + int64_t(hk * sc.group + r.g) * sc.q_head_pitch;
 }
 
 }  // namespace
