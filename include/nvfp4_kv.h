@@ -116,7 +116,9 @@ typedef struct {
     int64_t q_head_pitch;   /* elements from head to head, a multiple of 8 */
     int64_t heads;          /* a multiple of kv_heads; heads / kv_heads <= 256 */
     int64_t max_q;          /* no sequence has more new tokens, 0..2^24 */
-    int64_t max_kv;         /* no sequence is longer, 0..64 * table_pitch */
+    int64_t max_kv;         /* no sequence is longer, 0..64 * table_pitch (the
+                               launch is sized by both: one that is more is
+                               taken for one of that size) */
     int64_t window;         /* slots a query sees at most, 0: no limit */
     float scale;            /* finite */
     float softcap;          /* scores become softcap * tanh(score / softcap); 0: not */

@@ -24,6 +24,9 @@
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kRowTile = 16;          // few rows: of one workgroup
+constexpr int kTileRows = 32 * kWaves;  // many rows
+constexpr int kItems = 2048;
 
 // Scores may outgrow the running maximum by this much (in powers of two)
 // before the sums are rescaled: the weights then stay below 2^8, within f16.
@@ -36,9 +39,124 @@ struct AttendArgs {
     float* lse;
     float* part_o;    // [splits][total * heads][D]: sums of exp2(z - m) v, without the V scale
     float* part_ml;   // [splits][total * heads][2]: m and the sum of exp2(z - m)
-    int splits;
+    bool tile;        // 128-row workgroups
+    int splits;       // workgroups over the pages of a row tile, `chunk` pages each
+    int chunk;
+    int row_tiles;    // of the longest sequence
+    int32_t* plan;    // few rows: the planned items (kv_plan_kernel), or NULL where splits and chunk say all
     float v_scale;
 };
+
+__device__ __forceinline__ int pages_lo(const Span& s) { return s.lo / kPage; }
+__device__ __forceinline__ int pages_hi(const Span& s) { return (s.hi + kPage - 1) / kPage; }
+
+// Tile: the workgroups that take the pages of a row tile (at least one).
+__device__ __forceinline__ int used_splits(const AttendArgs& a, const Span& s) {
+    return min(max((pages_hi(s) - pages_lo(s) + a.chunk - 1) / a.chunk, 1), a.splits);
+}
+
+// Few rows.  A segment is one row tile and kv head of a sequence: the pages
+// its rows see, at least one.  Segments are cut into chunks of the same number
+// of pages, and each chunk is a workgroup's item.  Where the host's bound on
+// the lengths does not leave many workgroups without work, the grid itself
+// numbers the items: parts x sequences x segments.  Else a first kernel counts
+// them from the lengths: the whole chunks of all segments, then what is left
+// at the segments' ends, so that long and short sequences together keep the
+// card evenly busy to the end.  (A workgroup without work still holds its
+// registers and LDS while it reads a length: 32 one-token steps over 3 ..
+// 131071 slots took 183 us with 14000 such, 113 us planned.)
+__device__ __forceinline__ int segment_pages(const AttendArgs& a, const QueryRows& rows) {
+    const Span span = rows.span(a.sc, 0, rows.count - 1);
+    return max(pages_hi(span) - pages_lo(span), 1);
+}
+
+__device__ __forceinline__ int segment_count(const AttendArgs& a, const QueryRows& rows) {
+    return (rows.count + kRowTile - 1) / kRowTile * a.v.kv_heads;
+}
+
+constexpr int kPlanThreads = 1024;
+
+// plan: [0] the chunk, [1] the number of whole chunks, [2 + s] the whole chunks
+// before sequence s, [2 + seqs + s] the rests before it.
+__global__ void __launch_bounds__(kPlanThreads)
+kv_plan_kernel(AttendArgs a) {
+    __shared__ int64_t tmp[kPlanThreads / 64][2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // sums of x and y over the threads before this one; the totals are added to all_x and all_y
+    auto scan = [&](int64_t x, int64_t y, int64_t* before_x, int64_t* before_y, int64_t* all_x, int64_t* all_y) {
+        int64_t sx = x, sy = y;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t ux = __shfl_up(sx, d), uy = __shfl_up(sy, d);
+            if (lane >= d) sx += ux, sy += uy;
+        }
+        __syncthreads();
+        if (lane == 63) tmp[wave][0] = sx, tmp[wave][1] = sy;
+        __syncthreads();
+        int64_t bx = *all_x, by = *all_y, ax = bx, ay = by;
+        for (int w = 0; w < kPlanThreads / 64; ++w) {
+            if (w < wave) bx += tmp[w][0], by += tmp[w][1];
+            ax += tmp[w][0], ay += tmp[w][1];
+        }
+        *before_x = bx + sx - x, *before_y = by + sy - y, *all_x = ax, *all_y = ay;
+    };
+    int64_t all = 0, none = 0, b0, b1;
+    for (int s = tid; s - tid < a.v.seqs; s += kPlanThreads) {
+        int64_t size = 0;
+        if (s < a.v.seqs) {
+            const QueryRows rows(a.v, a.sc, s);
+            if (rows.count > 0) size = int64_t(segment_count(a, rows)) * segment_pages(a, rows);
+        }
+        scan(size, 0, &b0, &b1, &all, &none);
+    }
+    // about kItems chunks, none shorter than the host's
+    const int chunk = static_cast<int>(max((all + kItems - 1) / kItems, int64_t(a.chunk)));
+    int64_t whole = 0, rest = 0;
+    for (int s = tid; s - tid < a.v.seqs; s += kPlanThreads) {
+        int64_t w = 0, r = 0;
+        if (s < a.v.seqs) {
+            const QueryRows rows(a.v, a.sc, s);
+            if (rows.count > 0) {
+                const int pages = segment_pages(a, rows), count = segment_count(a, rows);
+                w = int64_t(count) * (pages / chunk), r = pages % chunk ? count : 0;
+            }
+        }
+        scan(w, r, &b0, &b1, &whole, &rest);
+        if (s < a.v.seqs) a.plan[2 + s] = static_cast<int>(b0), a.plan[2 + a.v.seqs + s] = static_cast<int>(b1);
+    }
+    if (tid == 0) a.plan[0] = chunk, a.plan[1] = static_cast<int>(whole);
+}
+
+struct Item {
+    int s, segment, part, chunk;   // s < 0: none
+};
+
+// The last of the ascending p[0 .. n) that is at most w, by 64 at a time.
+__device__ __forceinline__ int last_at_most(const int32_t* p, int n, int w) {
+    const int lane = threadIdx.x & 63;
+    int at = 0;
+    for (int step = n > 4096 ? 4096 : n > 64 ? 64 : 1;; step /= 64) {
+        const int i = at + lane * step;
+        at += (__popcll(__ballot(i < n && p[i] <= w)) - 1) * step;
+        if (step == 1) return at;
+    }
+}
+
+__device__ __forceinline__ Item find_item(const AttendArgs& a, int w) {
+    const int segments = a.row_tiles * a.v.kv_heads;
+    if (!a.plan) return Item{w / segments % a.v.seqs, w % segments, w / segments / a.v.seqs, a.chunk};
+    const int chunk = a.plan[0], whole = a.plan[1];
+    const bool rest = w >= whole;
+    if (rest) w -= whole;
+    const int32_t* before = a.plan + 2 + (rest ? a.v.seqs : 0);
+    const int s = last_at_most(before, a.v.seqs, w), in = w - before[s];
+    // the last of equal entries is the one that has items, unless w lies after all
+    const QueryRows rows(a.v, a.sc, s);
+    if (rows.count == 0) return Item{-1, 0, 0, 0};
+    const int pages = segment_pages(a, rows), each = rest ? (pages % chunk != 0) : pages / chunk;
+    if (each == 0 || in >= each * segment_count(a, rows)) return Item{-1, 0, 0, 0};
+    return Item{s, in / each, rest ? pages / chunk : in % each, chunk};
+}
 
 // What one wavefront holds of a page: codes and scales as the operands need them.
 template <int D>
@@ -104,25 +222,41 @@ __device__ __forceinline__ f16x8 to_f16x8(const float* p) {
     return r;
 }
 
-// Few query rows: a wavefront takes 16 of them and whole pages, decoded from
-// registers.  See the launch for the split and what it measured.
+// 16 query rows and one item's pages: the wavefronts take every fourth page,
+// decoded from registers, and join in LDS in wavefront order.
 template <int D>
-__global__ void __launch_bounds__(64 * kWaves)
+__global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
 kv_attend_rows_kernel(AttendArgs a) {
     extern __shared__ float lds[];   // [kWaves][16][D] sums, then [kWaves][16][2] statistics
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // the wavefront's number as a scalar: its pages and their addresses are then scalars too
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, b = lane >> 4;
-    const int s = blockIdx.y, split = blockIdx.x % a.splits;
-    const int hk = blockIdx.x / a.splits % a.v.kv_heads, tile = blockIdx.x / a.splits / a.v.kv_heads;
+    const Item item = find_item(a, blockIdx.x);
+    if (item.s < 0) return;
+    const int s = item.s, hk = item.segment % a.v.kv_heads, row0 = item.segment / a.v.kv_heads * kRowTile;
     const QueryRows rows(a.v, a.sc, s);
-    const int row0 = tile * 16;
     if (row0 >= rows.count) return;
+    const int pages = segment_pages(a, rows);
+    if (item.part > 0 && item.part * item.chunk >= pages) return;
+    const Span whole = rows.span(a.sc, 0, rows.count - 1), span = rows.span(a.sc, row0, min(row0 + kRowTile, rows.count) - 1);
+    const int begin = pages_lo(whole) + item.part * item.chunk, end = min(begin + item.chunk, pages_hi(whole));
 
-    const Span span = rows.span(a.sc, row0, min(row0 + 16, rows.count) - 1);
-    const int page_lo = span.lo / kPage, page_hi = (span.hi + kPage - 1) / kPage;
-    const int per = (max(page_hi - page_lo, 0) + a.splits - 1) / a.splits;
-    const int begin = page_lo + split * per, end = min(begin + per, page_hi);
-
+    // Page numbers are read 64 at a time, one a lane, so that a page's loads
+    // never wait for the table; the next page is on its way while one is
+    // worked on, in two sets of registers that take turns.
+    int page = begin + wave, ids = -1, at_id = 0, id = -1;
+    auto read_ids = [&](int p) {
+        const int mine = p + kWaves * lane;
+        ids = mine < end ? a.v.page_id(s, mine) : -1;
+        at_id = 0;
+    };
+    PageRegs<D> even, odd;
+    const bool any = page < end && a.v.pages > 0;
+    if (any) {
+        read_ids(page);
+        id = __builtin_amdgcn_readlane(ids, at_id++);
+        even.load_page(a.v.record_or_first<D>(id, hk), n, b);
+    }
     const QueryRow me = rows.row(a.sc, row0 + n);
     f16x8 q[D / 32];
     const float to_log2 = load_query<D / 32, 8, 16>(a.sc, query_at(a.sc, me, hk) + b * (D / 4), q);
@@ -132,72 +266,81 @@ kv_attend_rows_kernel(AttendArgs a) {
     for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
 
-    PageRegs<D> cur;
-    int page = begin + wave;
-    const uint8_t* rec = page < end ? a.v.record<D>(s, page, hk) : nullptr;
-    if (rec) cur.load_page(rec, n, b);
-    while (page < end) {
-        const int next = page + kWaves;
-        const uint8_t* next_rec = next < end ? a.v.record<D>(s, next, hk) : nullptr;
-        PageRegs<D> ahead;
-        if (next_rec) ahead.load_page(next_rec, n, b);
-        if (rec) {
-            const int base = page * kPage;
-            f32x4 z[4];
-            z[0] = score_groups<D, 0, 0>(cur, q, f32x4{0, 0, 0, 0});
-            z[1] = score_groups<D, 1, 0>(cur, q, f32x4{0, 0, 0, 0});
-            z[2] = score_groups<D, 2, 0>(cur, q, f32x4{0, 0, 0, 0});
-            z[3] = score_groups<D, 3, 0>(cur, q, f32x4{0, 0, 0, 0});
-            float p[16];   // [h][8 consecutive slots]
+    auto add_page = [&](PageRegs<D>& cur, int page) {
+        const int base = page * kPage;
+        f32x4 z[4];
+        z[0] = score_groups<D, 0, 0>(cur, q, f32x4{0, 0, 0, 0});
+        z[1] = score_groups<D, 1, 0>(cur, q, f32x4{0, 0, 0, 0});
+        z[2] = score_groups<D, 2, 0>(cur, q, f32x4{0, 0, 0, 0});
+        z[3] = score_groups<D, 3, 0>(cur, q, f32x4{0, 0, 0, 0});
+        float p[16];   // [h][8 consecutive slots]
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] = a.sc.shape(z[i >> 2][i & 3], to_log2);
-            if (base < span.lo_all || base + kPage > span.hi_all) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int slot = base + 32 * (i >> 3) + 8 * b + (i & 7);
-                    p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
-                }
-            }
-            float top = p[0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) top = fmaxf(top, p[i]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (__any(top > m + kSlack)) {
-                const float grown = fmaxf(m, top);
-                const float keep = grown == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
-                m = grown;
-                l *= keep;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) o[i] *= keep;
-            }
-            const float base_m = m == -INFINITY ? 0.0f : m;
+        for (int i = 0; i < 16; ++i) p[i] = z[i >> 2][i & 3];
+        a.sc.shape(p, to_log2);
+        if (base < span.lo_all || base + kPage > span.hi_all) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(p[i] - base_m);
-                l += p[i];
-            }
-            // slots from the length on hold anything: their scales become 0
-            const int left = rows.len - base;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (left < kPage) {
-                    const int live = left - 32 * h - 8 * b;
-                    const uint64_t mask = live <= 0 ? 0 : live >= 8 ? ~0ull : (1ull << (8 * live)) - 1;
-                    cur.vs[h][0] &= uint32_t(mask);
-                    cur.vs[h][1] &= uint32_t(mask >> 32);
-                }
-                const f16x8 pt = to_f16x8(p + 8 * h);
-                const f16x2 sc[4] = {scale_pair<0>(cur.vs[h][0]), scale_pair<1>(cur.vs[h][0]),
-                                     scale_pair<0>(cur.vs[h][1]), scale_pair<1>(cur.vs[h][1])};
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_slots(cur.v[h][i], sc), pt, o[i], 0, 0, 0);
+                const int slot = base + 32 * (i >> 3) + 8 * b + (i & 7);
+                p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
             }
         }
-        cur = ahead;
-        rec = next_rec;
-        page = next;
+        float top = p[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, p[i]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (__any(top > m + kSlack)) {
+            const float grown = fmaxf(m, top);
+            const float keep = grown == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
+            m = grown;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[i] *= keep;
+        }
+        const float base_m = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(p[i] - base_m);
+            l += p[i];
+        }
+        // slots from the length on hold anything: their scales become 0
+        const int left = rows.len - base;
+        if (left < kPage) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int live = left - 32 * h - 8 * b;
+                const uint64_t mask = live <= 0 ? 0 : live >= 8 ? ~0ull : (1ull << (8 * live)) - 1;
+                cur.vs[h][0] &= uint32_t(mask);
+                cur.vs[h][1] &= uint32_t(mask >> 32);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f16x8 pt = to_f16x8(p + 8 * h);
+            const f16x2 sc[4] = {scale_pair<0>(cur.vs[h][0]), scale_pair<1>(cur.vs[h][0]),
+                                 scale_pair<0>(cur.vs[h][1]), scale_pair<1>(cur.vs[h][1])};
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_slots(cur.v[h][i], sc), pt, o[i], 0, 0, 0);
+        }
+    };
+
+    if (any) {
+        __builtin_amdgcn_s_waitcnt(0x0f70);   // all loads: the loop's waits then count its own alone
+        auto turn = [&](PageRegs<D>& cur, PageRegs<D>& ahead) {
+            if (at_id == 64) read_ids(page + kWaves);
+            const int next = __builtin_amdgcn_readlane(ids, at_id++);
+            ahead.load_page(a.v.record_or_first<D>(next, hk), n, b);
+            if (a.v.has(id)) add_page(cur, page);
+            id = next;
+            page += kWaves;
+        };
+        for (;;) {
+            turn(even, odd);
+            if (page >= end) break;
+            turn(odd, even);
+            if (page >= end) break;
+        }
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -234,16 +377,16 @@ kv_attend_rows_kernel(AttendArgs a) {
         }
     }
     const int64_t at = rows.place(a.sc, row0 + r, hk);
-    if (a.splits > 1) {
-        const int64_t slice = int64_t(a.v.total) * a.sc.heads;
-        float* po = a.part_o + (split * slice + at) * D + d0;
+    if (pages > item.chunk) {
+        const int64_t to = int64_t(blockIdx.x) * kRowTile + r;
+        float* po = a.part_o + to * D + d0;
         if (top > -INFINITY)
 #pragma unroll
             for (int i = 0; i < kPer; i += 4)
                 *reinterpret_cast<f32x4*>(po + i) = f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
         if (d0 == 0) {
-            a.part_ml[(split * slice + at) * 2] = top;
-            a.part_ml[(split * slice + at) * 2 + 1] = sum;
+            a.part_ml[to * 2] = top;
+            a.part_ml[to * 2 + 1] = sum;
         }
         return;
     }
@@ -332,26 +475,28 @@ struct PageShare {
     }
 };
 
-constexpr int kTileRows = 32 * kWaves;
+constexpr int kMaxSplits = 1024;
 
 template <int D>
 __global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
 kv_attend_tile_kernel(AttendArgs a) {
     extern __shared__ char tiles[];   // two pages
+    constexpr int kStep = D == 256 ? 1 : 2;   // 32-slot tiles between rescalings: registers decide
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = lane & 31, b = lane >> 5;
-    const int s = blockIdx.y, split = blockIdx.x % a.splits;
-    const int hk = blockIdx.x / a.splits % a.v.kv_heads;
+    const int s = blockIdx.y, split = blockIdx.z;
+    const int hk = blockIdx.x % a.v.kv_heads;
     const QueryRows rows(a.v, a.sc, s);
     // the last rows see most: they begin first
-    const int tile = int(gridDim.x / a.splits / a.v.kv_heads) - 1 - int(blockIdx.x / a.splits / a.v.kv_heads);
+    const int tile = int(gridDim.x / a.v.kv_heads) - 1 - int(blockIdx.x / a.v.kv_heads);
     const int row0 = tile * kTileRows;
     if (row0 >= rows.count) return;
 
     const Span all = rows.span(a.sc, row0, min(row0 + kTileRows, rows.count) - 1);
-    const int page_lo = all.lo / kPage, page_hi = (all.hi + kPage - 1) / kPage;
-    const int per = (max(page_hi - page_lo, 0) + a.splits - 1) / a.splits;
-    const int begin = page_lo + split * per, end = min(begin + per, page_hi);
+    const int used = used_splits(a, all);
+    if (split >= used) return;
+    const int begin = pages_lo(all) + split * a.chunk;
+    const int end = split + 1 < used ? begin + a.chunk : pages_hi(all);
 
     const int my0 = row0 + wave * 32;
     const QueryRow me = rows.row(a.sc, my0 + n);
@@ -368,72 +513,79 @@ kv_attend_tile_kernel(AttendArgs a) {
     const int slot_n = (n & ~12) | ((n & 4) << 1) | ((n & 8) >> 1);
 
     PageShare<D> share;
-    const uint8_t* rec = begin < end ? a.v.record<D>(s, begin, hk) : nullptr;
-    if (rec) share.load(rec, tid);
-    for (int page = begin; page < end; ++page) {
+    const int last = a.v.pages > 0 ? end : begin;
+    int id = begin < last ? a.v.page_id(s, begin) : -1;
+    int next_id = begin + 1 < last ? a.v.page_id(s, begin + 1) : -1;
+    if (begin < last) share.load(a.v.record_or_first<D>(id, hk), tid);
+    for (int page = begin; page < last; ++page) {
         char* lds = tiles + ((page - begin) & 1) * PageTiles<D>::kBytes;
         const int base = page * kPage;
-        if (rec) share.put(lds, tid, rows.len - base);
-        const uint8_t* now = rec;
-        rec = page + 1 < end ? a.v.record<D>(s, page + 1, hk) : nullptr;
+        share.put(lds, tid, rows.len - base);
+        const bool here = a.v.has(id);
+        id = next_id;
         __syncthreads();
-        if (rec) share.load(rec, tid);
-        if (!now || base >= span.hi || base + kPage <= span.lo) continue;
+        share.load(a.v.record_or_first<D>(id, hk), tid);
+        next_id = page + 2 < last ? a.v.page_id(s, page + 2) : -1;
+        if (!here || base >= span.hi || base + kPage <= span.lo) continue;
 
-        f32x16 z[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            z[h] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        for (int half = 0; half < 2; half += kStep) {   // kStep 32-slot tiles at a time
+            f32x16 z[kStep];
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const f16x8 k = *reinterpret_cast<const f16x8*>(lds + PageTiles<D>::k_at(32 * h + slot_n, 2 * i + b));
-                z[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[i], z[h], 0, 0, 0);
+            for (int h = 0; h < kStep; ++h) {
+                z[h] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const f16x8 k = *reinterpret_cast<const f16x8*>(lds + PageTiles<D>::k_at(32 * (half + h) + slot_n, 2 * i + b));
+                    z[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[i], z[h], 0, 0, 0);
+                }
             }
-        }
-        float p[32];   // [h][t][8 consecutive slots]: slot 32 h + 16 t + 8 b + j
+            float p[16 * kStep];   // [t][8 consecutive slots]: slot 32 half + 16 t + 8 b + j
 #pragma unroll
-        for (int i = 0; i < 32; ++i) p[i] = a.sc.shape(z[i >> 4][i & 15], to_log2);
-        if (base < span.lo_all || base + kPage > span.hi_all) {
+            for (int i = 0; i < 16 * kStep; ++i) p[i] = z[i >> 4][i & 15];
+            a.sc.shape(p, to_log2);
+            if (base < span.lo_all || base + kPage > span.hi_all) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int slot = base + 16 * (i >> 3) + 8 * b + (i & 7);
-                p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
+                for (int i = 0; i < 16 * kStep; ++i) {
+                    const int slot = base + 32 * half + 16 * (i >> 3) + 8 * b + (i & 7);
+                    p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
+                }
             }
-        }
-        float top = p[0];
+            float top = p[0];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) top = fmaxf(top, p[i]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (__any(top > m + kSlack)) {
-            const float grown = fmaxf(m, top);
-            const float keep = grown == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
-            m = grown;
-            l *= keep;
+            for (int i = 1; i < 16 * kStep; ++i) top = fmaxf(top, p[i]);
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (__any(top > m + kSlack)) {
+                const float grown = fmaxf(m, top);
+                const float keep = grown == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
+                m = grown;
+                l *= keep;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] *= keep;
-        }
-        const float base_m = m == -INFINITY ? 0.0f : m;
-        f16x8 pt[4];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float e = __builtin_amdgcn_exp2f(p[i] - base_m);
-            l += e;
-            pt[i >> 3][i & 7] = static_cast<_Float16>(e);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const f16x8 v = *reinterpret_cast<const f16x8*>(lds + PageTiles<D>::v_at(32 * i + n, 2 * t + b));
-                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pt[t], o[i], 0, 0, 0);
+                for (int i = 0; i < D / 32; ++i) o[i] *= keep;
             }
+            const float base_m = m == -INFINITY ? 0.0f : m;
+            f16x8 pt[2 * kStep];
+#pragma unroll
+            for (int i = 0; i < 16 * kStep; ++i) {
+                const float e = __builtin_amdgcn_exp2f(p[i] - base_m);
+                l += e;
+                pt[i >> 3][i & 7] = static_cast<_Float16>(e);
+            }
+#pragma unroll
+            for (int t = 0; t < 2 * kStep; ++t)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const f16x8 v = *reinterpret_cast<const f16x8*>(lds + PageTiles<D>::v_at(32 * i + n, 2 * (2 * half + t) + b));
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pt[t], o[i], 0, 0, 0);
+                }
+        }
     }
     l += __shfl_xor(l, 32);
     if (l != l && m == -INFINITY) m = 0.0f;   // all scores NaN: the row stays NaN
 
     const bool live = my0 + n < rows.count;
     const int64_t at = rows.place(a.sc, min(my0 + n, rows.count - 1), hk);
-    if (a.splits > 1) {
+    if (used > 1) {
         if (!live) return;
         const int64_t slice = int64_t(a.v.total) * a.sc.heads;
         float* po = a.part_o + (split * slice + at) * D;
@@ -475,35 +627,81 @@ kv_attend_tile_kernel(AttendArgs a) {
     }
 }
 
-// Joins the splits of one row in split order: one wavefront a row.
+// Joins the parts of one row, one workgroup a row: the wavefronts take every
+// fourth part and meet in LDS, both in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(64 * kWaves)
 kv_join_kernel(AttendArgs a) {
+    __shared__ float sums[kWaves][D];
+    __shared__ float weight[kWaves];
     const int64_t slice = int64_t(a.v.total) * a.sc.heads;
-    const int64_t at = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (at >= slice) return;
-    const int token = static_cast<int>(at / a.sc.heads);
-    if (token < a.v.start(0) || token >= a.v.start(a.v.seqs)) return;   // no sequence's row
+    const int64_t at = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int token = static_cast<int>(at / a.sc.heads), head = static_cast<int>(at % a.sc.heads);
+    const int s = last_sequence(a.v, [&](int i) { return a.v.start(i) <= token; });
+    if (s < 0) return;
+    const QueryRows rows(a.v, a.sc, s);
+    const int r = (token - rows.first_token) * rows.group + head % rows.group;
+    if (r >= rows.count) return;   // no sequence's row
+    // where part p of the row lies: the parts of a tile a slice apart, an item's by its number
+    int used;
+    int64_t first, step, last;
+    if (a.tile) {
+        const int row0 = r / kTileRows * kTileRows;
+        used = used_splits(a, rows.span(a.sc, row0, min(row0 + kTileRows, rows.count) - 1));
+        first = at, step = slice, last = at + (used - 1) * slice;
+    } else {
+        const int pages = segment_pages(a, rows), chunk = a.plan ? a.plan[0] : a.chunk;
+        const int segment = r / kRowTile * a.v.kv_heads + head / rows.group;
+        used = (pages + chunk - 1) / chunk;
+        if (a.plan) {
+            first = a.plan[2 + s] + segment * (pages / chunk), step = 1;
+            last = pages % chunk ? a.plan[1] + a.plan[2 + a.v.seqs + s] + segment : first + used - 1;
+        } else {
+            step = int64_t(a.row_tiles) * a.v.kv_heads * a.v.seqs;
+            first = int64_t(s) * a.row_tiles * a.v.kv_heads + segment;
+            last = first + (used - 1) * step;
+        }
+        first = first * kRowTile + r % kRowTile, last = last * kRowTile + r % kRowTile, step *= kRowTile;
+    }
+    if (used == 1) return;         // written already
+    auto place = [&](int p) { return p == used - 1 ? last : first + p * step; };
+
     float top = -INFINITY;
-    for (int p = 0; p < a.splits; ++p) top = fmaxf(top, a.part_ml[(p * slice + at) * 2]);
+    for (int p = lane; p < used; p += 64) top = fmaxf(top, a.part_ml[place(p) * 2]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     constexpr int kPer = D / 64;
     float acc[kPer] = {}, sum = 0.0f;
-    if (top > -INFINITY) {
-        for (int p = 0; p < a.splits; ++p) {
-            const float m = a.part_ml[(p * slice + at) * 2];
-            if (m == -INFINITY) continue;
-            const float f = __builtin_amdgcn_exp2f(m - top);
-            sum += f * a.part_ml[(p * slice + at) * 2 + 1];
-            const float* po = a.part_o + (p * slice + at) * D + lane * kPer;
+#pragma unroll 4
+    for (int p = wave; p < used; p += kWaves) {
+        const float m = a.part_ml[place(p) * 2];
+        const float part = a.part_ml[place(p) * 2 + 1];
+        const float* po = a.part_o + place(p) * D + lane * kPer;
+        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+        sum += m == -INFINITY ? 0.0f : f * part;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] += f * po[i];
+        for (int i = 0; i < kPer; ++i) {
+            const float x = po[i];   // not written where the part saw nothing
+            acc[i] += m == -INFINITY ? 0.0f : f * x;
         }
     }
-    const float f = sum > 0.0f || sum != sum ? a.v_scale / sum : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) a.out[at * D + lane * kPer + i] = f32_to_bf16_rne(acc[i] * f);
-    if (a.lse && lane == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
+    for (int i = 0; i < kPer; ++i) sums[wave][lane * kPer + i] = acc[i];
+    if (lane == 0) weight[wave] = sum;
+    __syncthreads();
+    if (tid >= D / 2) return;
+    sum = weight[0] + weight[1] + weight[2] + weight[3];
+    const float f = sum > 0.0f || sum != sum ? a.v_scale / sum : 0.0f;
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int d = 2 * tid + j;
+        const float x = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
+        w |= uint32_t(f32_to_bf16_rne(x * f)) << (16 * j);
+    }
+    *reinterpret_cast<uint32_t*>(a.out + at * D + 2 * tid) = w;
+    if (a.lse && tid == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
 }
 
 // How a call is laid out: 16-row or 128-row workgroups, and over how many
@@ -511,35 +709,46 @@ kv_join_kernel(AttendArgs a) {
 struct Plan {
     bool tile;
     int64_t row_tiles;
-    int splits;
+    int splits, chunk;   // tile
+    bool planned;        // else
+    int items;
+    int64_t part_rows;   // rows of partial results
 };
 
 Plan plan_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
     const int64_t rows = q->max_q * (q->heads / c->kv_heads);
-    Plan p;
+    Plan p{};
     p.tile = rows > 32;
-    const int64_t per_tile = p.tile ? kTileRows : 16;
+    const int64_t per_tile = p.tile ? kTileRows : kRowTile;
     p.row_tiles = (rows + per_tile - 1) / per_tile;
-    p.splits = 1;
-    const int64_t base = s->seqs * c->kv_heads * p.row_tiles;
+    const int64_t base = std::max<int64_t>(s->seqs * c->kv_heads * p.row_tiles, 1);
     int64_t slots = q->max_kv;
     if (q->window > 0) slots = std::min(slots, q->window + q->max_q);
-    const int64_t pages = (slots + kPage - 1) / kPage;
-    if (base == 0 || pages == 0) return p;
-    int64_t splits;
+    const int64_t pages = std::max<int64_t>((slots + kPage - 1) / kPage + (q->window > 0), 1);
+    // Pages of a workgroup: as many as leave 512, which fills the card twice;
+    // few rows take 32 at most, so that the last to end is not late by much.
+    const int64_t most = p.tile ? pages : std::min<int64_t>(pages, 32);
+    const int64_t chunk = std::min(std::max<int64_t>(pages * base / 512, kWaves), std::max<int64_t>(most, 1));
+    p.splits = static_cast<int>((pages + chunk - 1) / chunk);
     if (p.tile) {
-        splits = std::min((512 + base - 1) / base, (pages + 3) / 4);
+        p.splits = std::min(p.splits, kMaxSplits);
+        p.chunk = static_cast<int>((pages + p.splits - 1) / p.splits);
+        p.part_rows = p.splits > 1 ? p.splits * s->total * q->heads : 0;
     } else {
-        splits = std::max<int64_t>((1024 + base - 1) / base, (slots + 4095) / 4096);
-        splits = std::min(splits, (pages + kWaves - 1) / kWaves);
+        p.chunk = static_cast<int>(chunk);
+        p.planned = p.splits > 2 && base * p.splits > 2048;
+        // planned: at most kItems whole chunks, and a rest a segment
+        p.items = static_cast<int>(p.planned ? std::min(base * p.splits, base + kItems) : base * p.splits);
+        p.part_rows = p.splits > 1 ? int64_t(p.items) * kRowTile : 0;
     }
-    p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(splits, 256)));
     return p;
 }
 
+int64_t plan_bytes(const nvfp4_kv_seqs_t* s) { return (2 + 2 * s->seqs + 3) / 4 * 16; }
+
 int64_t workspace_bytes_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
-    const int64_t splits = plan_of(c, s, q).splits;
-    return splits == 1 ? 0 : splits * s->total * q->heads * (c->head_dim + 2) * int64_t(sizeof(float));
+    const Plan p = plan_of(c, s, q);
+    return p.part_rows * (c->head_dim + 2) * int64_t(sizeof(float)) + (p.planned ? plan_bytes(s) : 0);
 }
 
 template <int D>
@@ -563,17 +772,23 @@ bool allow_lds() {
 
 template <int D>
 int launch_attend(const AttendArgs& a, const Plan& plan, hipStream_t st) {
-    const int64_t blocks = plan.row_tiles * a.v.kv_heads * plan.splits;
-    if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    const dim3 grid(static_cast<unsigned>(blocks), a.v.seqs);
-    if (plan.tile)
-        hipLaunchKernelGGL(kv_attend_tile_kernel<D>, grid, dim3(64 * kWaves), tile_lds<D>(), st, a);
-    else
-        hipLaunchKernelGGL(kv_attend_rows_kernel<D>, grid, dim3(64 * kWaves), rows_lds<D>(), st, a);
+    if (plan.tile) {
+        // parts of a tile's pages along the slowest axis: those that short sequences do not need come last
+        const int64_t blocks = plan.row_tiles * a.v.kv_heads;
+        if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
+        hipLaunchKernelGGL(kv_attend_tile_kernel<D>, dim3(static_cast<unsigned>(blocks), a.v.seqs, plan.splits),
+                           dim3(64 * kWaves), tile_lds<D>(), st, a);
+    } else {
+        if (plan.planned) {
+            hipLaunchKernelGGL(kv_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
+            if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+        }
+        hipLaunchKernelGGL(kv_attend_rows_kernel<D>, dim3(plan.items), dim3(64 * kWaves), rows_lds<D>(), st, a);
+    }
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-    if (a.splits > 1) {
+    if (plan.part_rows > 0) {
         const int64_t slice = int64_t(a.v.total) * a.sc.heads;
-        hipLaunchKernelGGL(kv_join_kernel<D>, dim3(static_cast<unsigned>((slice + 3) / 4)), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(kv_join_kernel<D>, dim3(static_cast<unsigned>(slice)), dim3(64 * kWaves), 0, st, a);
         if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     }
     return NVFP4_OK;
@@ -619,9 +834,13 @@ extern "C" int nvfp4_kv_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
     const Plan plan = plan_of(cache, seqs, queries);
+    a.tile = plan.tile;
     a.splits = plan.splits;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = a.splits > 1 ? a.part_o + int64_t(a.splits) * seqs->total * queries->heads * cache->head_dim : nullptr;
+    a.chunk = plan.chunk;
+    a.row_tiles = static_cast<int>(plan.row_tiles);
+    a.plan = plan.planned ? static_cast<int32_t*>(workspace) : nullptr;
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + (plan.planned ? plan_bytes(seqs) : 0));
+    a.part_ml = plan.part_rows > 0 ? a.part_o + plan.part_rows * cache->head_dim : nullptr;
     a.v_scale = cache->v_scale;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (cache->head_dim) {

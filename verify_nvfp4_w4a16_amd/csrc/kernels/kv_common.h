@@ -61,13 +61,24 @@ struct KvView {
         const int t = q_starts[s];
         return t < 0 ? 0 : (t > total ? total : t);
     }
-    // Record of (logical page p of sequence s, head h); nullptr for a page
-    // outside the cache.  p is below table_pitch.
+    // Number of logical page p (below table_pitch) of sequence s.
+    __device__ __forceinline__ int page_id(int s, int p) const { return table[int64_t(s) * table_pitch + p]; }
+    __device__ __forceinline__ bool has(int page) const { return page >= 0 && page < pages; }
+    // Record of (page, head h); nullptr for a page outside the cache.
+    template <int D>
+    __device__ __forceinline__ uint8_t* record_of(int page, int h) const {
+        return has(page) ? data + (int64_t(page) * kv_heads + h) * KvRecord<D>::kBytes : nullptr;
+    }
+    // The same for loads ahead of use, which are made whether the page is
+    // there or not (a load under a condition would make every wait for loads
+    // assume that it was not made): the cache's first page stands in.
+    template <int D>
+    __device__ __forceinline__ const uint8_t* record_or_first(int page, int h) const {
+        return data + (int64_t(has(page) ? page : 0) * kv_heads + h) * KvRecord<D>::kBytes;
+    }
     template <int D>
     __device__ __forceinline__ uint8_t* record(int s, int p, int h) const {
-        const int64_t page = table[int64_t(s) * table_pitch + p];
-        if (page < 0 || page >= pages) return nullptr;
-        return data + (page * kv_heads + h) * KvRecord<D>::kBytes;
+        return record_of<D>(page_id(s, p), h);
     }
 };
 
@@ -124,20 +135,26 @@ __device__ __forceinline__ f16x8 decode_slots(uint32_t w, const f16x2 (&s)[4]) {
     return join(codes_f16<0>(w) * s[0], codes_f16<1>(w) * s[1], codes_f16<2>(w) * s[2], codes_f16<3>(w) * s[3]);
 }
 
-// The sequence that unit `u` belongs to, where sequence s's units begin at
-// start(s) / 8 + 2 s: enough for every 8-slot block its rows touch, wherever
-// they begin.  All 64 lanes take part; every wavefront gets the same answer.
-__device__ __forceinline__ int unit_sequence(const KvView& v, int u) {
+// The number of sequences, less one, for which below(s) holds, where it holds
+// for none after one for which it does not.  All 64 lanes take part.
+template <class Fn>
+__device__ __forceinline__ int last_sequence(const KvView& v, Fn below) {
     const int lane = threadIdx.x & 63;
     int found = 0;
     for (int base = 0; base < v.seqs; base += 64) {
         const int s = base + lane;
-        const bool below = s < v.seqs && v.start(s) / 8 + 2 * s <= u;
-        const int n = __popcll(__ballot(below));
+        const int n = __popcll(__ballot(s < v.seqs && below(s)));
         found += n;
-        if (n < 64) break;   // starts never decrease, so none follows
+        if (n < 64) break;
     }
-    return found - 1;        // unit 0 is at or after sequence 0's begin
+    return found - 1;
+}
+
+// The sequence that unit `u` belongs to, where sequence s's units begin at
+// start(s) / 8 + 2 s: enough for every 8-slot block its rows touch, wherever
+// they begin.
+__device__ __forceinline__ int unit_sequence(const KvView& v, int u) {
+    return last_sequence(v, [&](int s) { return v.start(s) / 8 + 2 * s <= u; });
 }
 
 inline int64_t unit_count(const nvfp4_kv_seqs_t* s) { return s->total / 8 + 2 * s->seqs; }

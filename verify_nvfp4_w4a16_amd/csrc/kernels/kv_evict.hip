@@ -97,10 +97,12 @@ kv_weights_kernel(WeightArgs a) {
                 const float f = __shfl(f_n, 4 * b + c);
                 const float lse = __shfl(lse_n, 4 * b + c) * kLog2e;
                 const int lo = __shfl(lo_n, 4 * b + c), hi = __shfl(hi_n, 4 * b + c);
+                float x[4] = {z[0][c], z[1][c], z[2][c], z[3][c]};
+                a.sc.shape(x, f);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const int slot = base + 32 * (t >> 1) + (n >> 2) * 8 + (t & 1) * 4 + (n & 3);
-                    const float p = __builtin_amdgcn_exp2f(a.sc.shape(z[t][c], f) - lse);
+                    const float p = __builtin_amdgcn_exp2f(x[t] - lse);
                     sum[t] += slot >= lo && slot < hi ? p : 0.0f;
                 }
             }

@@ -14,18 +14,27 @@ struct KvScores {
     int64_t q_pitch, q_head_pitch;
     int heads, group;      // query heads, and those of one kv head
     int window;            // 0: no limit
+    int max_q, max_kv;     // what the launch was sized for: sequences are held to it
     int causal;
     float scale;           // of q . (e4m3 * e2m1): the caller's times K's tensor scale
     float cap, cap_inv2;   // softcap and 2 / softcap (0: none)
 
-    // z * log2(e) of a product's sum x, whose row was scaled by its own power
+    // z * log2(e) of products' sums x, whose row was scaled by its own power
     // of two (f is scale over that power, times log2(e) where there is no cap).
-    __device__ __forceinline__ float shape(float x, float f) const {
-        const float z = x * f;
-        if (cap == 0.0f) return z;
+    template <int N>
+    __device__ __forceinline__ void shape(float (&x)[N], float f) const {
+        if (cap == 0.0f) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] *= f;
+            return;
+        }
         // cap * tanh(z / cap) with tanh y = 1 - 2 / (1 + exp(2 y)): exact limits at both ends
-        const float e = __builtin_amdgcn_exp2f(z * (cap_inv2 * kLog2e));
-        return (cap - 2.0f * cap / (1.0f + e)) * kLog2e;
+        const float g = f * (cap_inv2 * kLog2e), c = cap * kLog2e;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float e = __builtin_amdgcn_exp2f(x[i] * g);
+            x[i] = c - 2.0f * c * __builtin_amdgcn_rcpf(1.0f + e);
+        }
     }
 };
 
@@ -37,6 +46,8 @@ inline KvScores kv_scores(const nvfp4_kv_cache_t* c, const nvfp4_kv_queries_t* q
     s.heads = static_cast<int>(q->heads);
     s.group = static_cast<int>(q->heads / c->kv_heads);
     s.window = static_cast<int>(q->window < (int64_t(1) << 29) ? q->window : 0);   // no sequence is longer
+    s.max_q = static_cast<int>(q->max_q);
+    s.max_kv = static_cast<int>(q->max_kv);
     s.causal = q->causal;
     s.scale = q->scale * c->k_scale;
     s.cap = q->softcap;
@@ -59,10 +70,12 @@ struct QueryRow {
 struct QueryRows {
     int first_token, new_tokens, len, count, group;
 
+    __device__ __forceinline__ QueryRows(int first, int count_new, int length, int of_kv_head)
+        : first_token(first), new_tokens(count_new), len(length), count(count_new * of_kv_head), group(of_kv_head) {}
     __device__ __forceinline__ QueryRows(const KvView& v, const KvScores& sc, int s) {
         first_token = v.start(s);
-        new_tokens = max(v.start(s + 1) - first_token, 0);
-        len = v.len(s);
+        new_tokens = min(max(v.start(s + 1) - first_token, 0), sc.max_q);
+        len = min(v.len(s), sc.max_kv);
         group = sc.group;
         count = new_tokens * group;
     }
