@@ -182,7 +182,7 @@ struct PageRegs {
         }
     }
 
-    __device__ __forceinline__ void load_page(const uint8_t* rec, int n, int b) {
+    __device__ __forceinline__ void load_k(const uint8_t* rec, int n, int b) {
         using R = KvRecord<D>;
 #pragma unroll
         for (int ht = 0; ht < 4; ++ht) {
@@ -190,6 +190,9 @@ struct PageRegs {
             load<D / 32>(k[ht], rec + R::k_code(slot) + b * (D / 8));
         }
         load<D / 64>(ks, rec + R::kKScales + (n * 4 + b) * (D / 16));
+    }
+    __device__ __forceinline__ void load_v(const uint8_t* rec, int n, int b) {
+        using R = KvRecord<D>;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             load<D / 16>(v[h], rec + R::v_code(4 * h + b, n * (D / 16)));
@@ -225,7 +228,7 @@ __device__ __forceinline__ f16x8 to_f16x8(const float* p) {
 // 16 query rows and one item's pages: the wavefronts take every fourth page,
 // decoded from registers, and join in LDS in wavefront order.
 template <int D>
-__global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(64 * kWaves, 2)
 kv_attend_rows_kernel(AttendArgs a) {
     extern __shared__ float lds[];   // [kWaves][16][D] sums, then [kWaves][16][2] statistics
     // the wavefront's number as a scalar: its pages and their addresses are then scalars too
@@ -242,20 +245,24 @@ kv_attend_rows_kernel(AttendArgs a) {
     const int begin = pages_lo(whole) + item.part * item.chunk, end = min(begin + item.chunk, pages_hi(whole));
 
     // Page numbers are read 64 at a time, one a lane, so that a page's loads
-    // never wait for the table; the next page is on its way while one is
-    // worked on, in two sets of registers that take turns.
+    // never wait for the table.  The next page's K is on its way once the
+    // scores are formed, its V once the sums are: one set of registers, and
+    // four wavefronts a SIMD to cover the wait, measured better than two sets
+    // and two wavefronts (see the launch).
     int page = begin + wave, ids = -1, at_id = 0, id = -1;
     auto read_ids = [&](int p) {
         const int mine = p + kWaves * lane;
         ids = mine < end ? a.v.page_id(s, mine) : -1;
         at_id = 0;
     };
-    PageRegs<D> even, odd;
+    PageRegs<D> cur;
     const bool any = page < end && a.v.pages > 0;
     if (any) {
         read_ids(page);
         id = __builtin_amdgcn_readlane(ids, at_id++);
-        even.load_page(a.v.record_or_first<D>(id, hk), n, b);
+        const uint8_t* rec = a.v.record_or_first<D>(id, hk);
+        cur.load_k(rec, n, b);
+        cur.load_v(rec, n, b);
     }
     const QueryRow me = rows.row(a.sc, row0 + n);
     f16x8 q[D / 32];
@@ -266,22 +273,28 @@ kv_attend_rows_kernel(AttendArgs a) {
     for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
 
-    auto add_page = [&](PageRegs<D>& cur, int page) {
+    if (any) __builtin_amdgcn_s_waitcnt(0x0f70);   // all loads: the loop's waits then count its own alone
+    while (page < end && a.v.pages > 0) {
         const int base = page * kPage;
+        const bool here = a.v.has(id);
         f32x4 z[4];
         z[0] = score_groups<D, 0, 0>(cur, q, f32x4{0, 0, 0, 0});
         z[1] = score_groups<D, 1, 0>(cur, q, f32x4{0, 0, 0, 0});
         z[2] = score_groups<D, 2, 0>(cur, q, f32x4{0, 0, 0, 0});
         z[3] = score_groups<D, 3, 0>(cur, q, f32x4{0, 0, 0, 0});
+        if (at_id == 64) read_ids(page + kWaves);
+        id = __builtin_amdgcn_readlane(ids, at_id++);
+        const uint8_t* next = a.v.record_or_first<D>(id, hk);
+        cur.load_k(next, n, b);
         float p[16];   // [h][8 consecutive slots]
 #pragma unroll
         for (int i = 0; i < 16; ++i) p[i] = z[i >> 2][i & 3];
         a.sc.shape(p, to_log2);
-        if (base < span.lo_all || base + kPage > span.hi_all) {
+        if (!here || base < span.lo_all || base + kPage > span.hi_all) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int slot = base + 32 * (i >> 3) + 8 * b + (i & 7);
-                p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
+                p[i] = here && slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
             }
         }
         float top = p[0];
@@ -303,8 +316,8 @@ kv_attend_rows_kernel(AttendArgs a) {
             p[i] = __builtin_amdgcn_exp2f(p[i] - base_m);
             l += p[i];
         }
-        // slots from the length on hold anything: their scales become 0
-        const int left = rows.len - base;
+        // slots from the length on hold anything, and so does the page that stands in for none: their scales become 0
+        const int left = here ? rows.len - base : 0;
         if (left < kPage) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -323,24 +336,8 @@ kv_attend_rows_kernel(AttendArgs a) {
             for (int i = 0; i < D / 16; ++i)
                 o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_slots(cur.v[h][i], sc), pt, o[i], 0, 0, 0);
         }
-    };
-
-    if (any) {
-        __builtin_amdgcn_s_waitcnt(0x0f70);   // all loads: the loop's waits then count its own alone
-        auto turn = [&](PageRegs<D>& cur, PageRegs<D>& ahead) {
-            if (at_id == 64) read_ids(page + kWaves);
-            const int next = __builtin_amdgcn_readlane(ids, at_id++);
-            ahead.load_page(a.v.record_or_first<D>(next, hk), n, b);
-            if (a.v.has(id)) add_page(cur, page);
-            id = next;
-            page += kWaves;
-        };
-        for (;;) {
-            turn(even, odd);
-            if (page >= end) break;
-            turn(odd, even);
-            if (page >= end) break;
-        }
+        cur.load_v(next, n, b);
+        page += kWaves;
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -725,10 +722,12 @@ Plan plan_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv
     int64_t slots = q->max_kv;
     if (q->window > 0) slots = std::min(slots, q->window + q->max_q);
     const int64_t pages = std::max<int64_t>((slots + kPage - 1) / kPage + (q->window > 0), 1);
-    // Pages of a workgroup: as many as leave 512, which fills the card twice;
-    // few rows take 32 at most, so that the last to end is not late by much.
-    const int64_t most = p.tile ? pages : std::min<int64_t>(pages, 32);
-    const int64_t chunk = std::min(std::max<int64_t>(pages * base / 512, kWaves), std::max<int64_t>(most, 1));
+    // Pages of a workgroup: as many as leave 512, which fills the card twice.
+    // Few rows take 32 at most, so that the last to end is not late by much,
+    // and 8 at least, or all of 16: the second launch that parts need costs as
+    // much as a wavefront's two or three pages more.
+    const int64_t low = p.tile ? kWaves : pages <= 16 ? pages : 8, high = p.tile ? pages : std::max<int64_t>(low, 32);
+    const int64_t chunk = std::min(std::max((pages * base + 511) / 512, low), std::max<int64_t>(high, 1));
     p.splits = static_cast<int>((pages + chunk - 1) / chunk);
     if (p.tile) {
         p.splits = std::min(p.splits, kMaxSplits);

@@ -131,7 +131,8 @@ def _out(name, t, shape, dtype, device):
 
 
 def _stream(stream, device) -> int:
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    # the raw handle at once: torch.cuda.current_stream() would build a Stream object (2 us) first
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def kv_append(cache: KvCache, k, v, table, kv_lens, q_starts, stream=None) -> None:
