@@ -36,6 +36,9 @@ constexpr int kDigit = 10;                   // bits of a selection step within 
 constexpr int kMassBits = 45;                // a chunk's bin: at most 2^14 tokens of 2^30, the number above the mass
 constexpr unsigned long long kOneToken = 1ull << kMassBits;
 constexpr int kListMax = 8192;
+constexpr int kShort = 256;                  // list length up to which every token is ranked against all
+constexpr uint32_t kNoKey = 0xffffffffu;
+constexpr int kMaxThreads = 256;             // launch 1: pieces of 4096
 
 struct SampleArgs {
     const void* logits;
@@ -49,7 +52,8 @@ struct SampleArgs {
     int32_t* token;
     float* logprob;
     int chunks;
-    float* chunk_max;            // [rows][chunks]
+    int pieces;
+    float* piece_max;            // [rows][pieces]
     unsigned long long* bins;    // [rows][chunks][kBins]
 };
 
@@ -72,47 +76,71 @@ __device__ __forceinline__ float weight(float x, float top, float inverse) {
 
 __device__ __forceinline__ uint32_t weight_key(float w) { return f32_bits(w) - kOneBits; }   // w >= 1
 __device__ __forceinline__ float key_weight(uint32_t k) { return bits_f32(k + kOneBits); }
+__device__ __forceinline__ uint64_t key_mass(uint32_t k) { return uint32_t(key_weight(k)); }   // at most 2^30, or the bound of its bin
 
 __device__ __forceinline__ int key_bin(uint32_t k) { return int(k >> kBinShift); }
 
-// ---- launch 1: the largest logit of each chunk
-
-template <bool F32>
-__device__ __forceinline__ void load_chunk(const void* row, int begin, int vocab, float (&x)[kPer]) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int i = begin + j * kThreads + int(threadIdx.x);
-        x[j] = i < vocab ? logit<F32>(row, i) : -INFINITY;
-    }
-}
+// ---- launch 1: the largest logit of each piece
 
 __device__ __forceinline__ const void* row_of(const SampleArgs& a, int r, int size) {
     return static_cast<const char*>(a.logits) + int64_t(r) * a.pitch * size;
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kThreads)
-sample_max_kernel(SampleArgs a) {
-    __shared__ float tmp[kRowWaves];
-    const int r = blockIdx.y, c = blockIdx.x;
+// The thread's kPer logits of the `threads * kPer` from `begin` on, -inf beyond
+// the vocabulary: 16 bytes at a time where the rows are aligned for it.
+// Element e of the result is token token_at(e).
+template <bool F32, bool WIDE, int THREADS>
+struct Piece {
+    static constexpr int kVec = WIDE ? (F32 ? 4 : 8) : 1;
     float x[kPer];
-    load_chunk<F32>(row_of(a, r, F32 ? 4 : 2), c * kChunk, a.vocab, x);
-    float top = x[0];
+
+    __device__ __forceinline__ int token_at(int begin, int e) const {
+        return begin + (e / kVec * THREADS + int(threadIdx.x)) * kVec + e % kVec;
+    }
+    __device__ __forceinline__ void load(const void* row, int begin, int vocab) {
 #pragma unroll
-    for (int j = 1; j < kPer; ++j) top = fmaxf(top, x[j]);
+        for (int v = 0; v < kPer / kVec; ++v) {
+            const int i = token_at(begin, v * kVec);
+            if constexpr (WIDE) {
+                if (i + kVec <= vocab) {
+                    const u32x4 raw = load16(static_cast<const char*>(row) + int64_t(i) * (F32 ? 4 : 2));
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j)
+                        x[v * kVec + j] = F32 ? bits_f32(raw[j % 4]) : bits_f32(j % 2 ? raw[j / 2 % 4] & 0xffff0000u : raw[j / 2 % 4] << 16);
+                    continue;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) x[v * kVec + j] = i + j < vocab ? logit<F32>(row, i + j) : -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[e] = x[e] != x[e] ? -INFINITY : x[e];
+    }
+};
+
+template <bool F32, bool WIDE>
+__global__ void __launch_bounds__(kMaxThreads)
+sample_max_kernel(SampleArgs a) {
+    __shared__ float tmp[kMaxThreads / 64];
+    const int r = blockIdx.y, c = blockIdx.x;
+    Piece<F32, WIDE, kMaxThreads> p;
+    p.load(row_of(a, r, F32 ? 4 : 2), c * kMaxThreads * kPer, a.vocab);
+    float top = p.x[0];
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) top = fmaxf(top, p.x[j]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = top;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kRowWaves; ++w) top = fmaxf(top, tmp[w]);
-        a.chunk_max[int64_t(r) * a.chunks + c] = top;
+        for (int w = 1; w < kMaxThreads / 64; ++w) top = fmaxf(top, tmp[w]);
+        a.piece_max[int64_t(r) * a.pieces + c] = top;
     }
 }
 
 __device__ __forceinline__ float row_max(const SampleArgs& a, int r) {
     float top = -INFINITY;
-    for (int c = threadIdx.x & 63; c < a.chunks; c += 64) top = fmaxf(top, a.chunk_max[int64_t(r) * a.chunks + c]);
+    for (int c = threadIdx.x & 63; c < a.pieces; c += 64) top = fmaxf(top, a.piece_max[int64_t(r) * a.pieces + c]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     return top;
@@ -125,20 +153,20 @@ __device__ __forceinline__ float row_inverse(const SampleArgs& a, int r) {
 
 // ---- launch 2: each chunk's tokens and mass by bins of the weight
 
-template <bool F32>
+template <bool F32, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
 sample_bins_kernel(SampleArgs a) {
     __shared__ unsigned long long bins[kBins];
     const int r = blockIdx.y, c = blockIdx.x, tid = threadIdx.x;
-    float x[kPer];
-    load_chunk<F32>(row_of(a, r, F32 ? 4 : 2), c * kChunk, a.vocab, x);
+    Piece<F32, WIDE, kThreads> p;
+    p.load(row_of(a, r, F32 ? 4 : 2), c * kChunk, a.vocab);
     const float top = row_max(a, r), inverse = row_inverse(a, r);
     if (tid < kBins) bins[tid] = 0;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const float w = weight(x[j], top, inverse);
-        if (w >= 1.0f) atomicAdd(&bins[key_bin(weight_key(w))], kOneToken | (unsigned long long)w);
+        const float w = weight(p.x[j], top, inverse);
+        if (w >= 1.0f) atomicAdd(&bins[key_bin(weight_key(w))], kOneToken | (unsigned long long)uint32_t(w));
     }
     __syncthreads();
     if (tid < kBins) a.bins[(int64_t(r) * a.chunks + c) * kBins + tid] = bins[tid];
@@ -176,20 +204,40 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* tmp, uint64
 }
 
 struct RowShared {
-    uint32_t count[kThreads];
+    uint32_t count[kThreads];        // a selection step's bins
     uint64_t mass[kThreads];
+    uint32_t above_n[kThreads];      // the row's bins: tokens and mass in higher ones
+    uint64_t above_m[kThreads];
     uint64_t tmp[kRowWaves];
     uint64_t found[4];
     uint64_t chunk_mass[kMaxChunks];
-    uint32_t list_key[kListMax];
+    uint32_t list_key[kListMax];     // kNoKey: not one of the bins' after all
     uint32_t list_index[kListMax];
     int listed;
+    int chunk_has[kMaxChunks];       // tokens of those bins
 };
+
+// The lowest of the row's bins at which fewer than `most` tokens, or a mass
+// below `limit`, lie above.  Both fall towards higher bins, so a halving search
+// that every thread makes by itself finds it.  The caller knows that the rule
+// ends among the row's tokens, and then the bin has one.
+template <bool BY_MASS>
+__device__ __forceinline__ int row_bin(const RowShared& sh, uint64_t most, double limit) {
+    int lo = 0, hi = kBins - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (BY_MASS ? double(sh.above_m[mid]) < limit : sh.above_n[mid] < most)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
 
 // Of `size` (at most kThreads) bins in sh.count and sh.mass the lowest with
 // any token at which those above it are fewer than `most` (by count) or weigh
 // less than `limit` (by mass), `above` of either being above all the bins.
-// found = bin, above it, its tokens, its mass; bin -1 if none.
+// found = bin, above it, its tokens; bin ~0 if none.
 template <bool BY_MASS>
 __device__ void find_bin(RowShared& sh, int size, uint64_t above, uint64_t most, double limit) {
     const int tid = threadIdx.x, bin = size - 1 - tid;   // thread 0 has the highest
@@ -207,7 +255,7 @@ __device__ void find_bin(RowShared& sh, int size, uint64_t above, uint64_t most,
     uint64_t last = ~0ull;
 #pragma unroll
     for (int w = 0; w < kRowWaves; ++w) last = sh.tmp[w] != ~0ull ? sh.tmp[w] : last;
-    if (uint64_t(tid) == last) sh.found[0] = uint64_t(bin), sh.found[1] = mine, sh.found[2] = n, sh.found[3] = m;
+    if (uint64_t(tid) == last) sh.found[0] = uint64_t(bin), sh.found[1] = mine, sh.found[2] = n;
     __syncthreads();
 }
 
@@ -232,8 +280,8 @@ struct Tokens {
     }
 };
 
-// The exact key at which find_bin's rule stops within bin `bin`, above of
-// either above the bin: found as there, for the tokens of that key.
+// The exact key at which find_bin's rule stops within bin `bin`, `above` of
+// either above the bin; found[1] and [2] as there, for the tokens of that key.
 template <bool BY_MASS, bool F32>
 __device__ uint32_t find_key(RowShared& sh, const Tokens<F32>& tokens, int bin, uint64_t above, uint64_t most, double limit) {
     uint32_t key = uint32_t(bin) << kBinShift, mask = ~0u << kBinShift;
@@ -246,7 +294,7 @@ __device__ uint32_t find_key(RowShared& sh, const Tokens<F32>& tokens, int bin, 
             if ((k & mask) != key) return;
             const int d = (k >> down) & (size - 1);
             atomicAdd(&sh.count[d], 1u);
-            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[d]), (unsigned long long)key_weight(k));
+            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[d]), (unsigned long long)key_mass(k));
         });
         __syncthreads();
         find_bin<BY_MASS>(sh, size, above, most, limit);
@@ -287,13 +335,133 @@ __device__ uint32_t find_index(RowShared& sh, const Tokens<F32>& tokens, uint32_
     }
 }
 
+// The rules that cut a row's tokens, and where each may cut.
+struct Cuts {
+    bool by_count, by_mass, only_first;
+    uint64_t k;
+    float p;
+    double low;
+    int bin_k, bin_p_lo, bin_p_hi, bin_m;   // -1: none
+
+    __device__ __forceinline__ bool wanted(int bin) const {
+        return bin == bin_k || bin == bin_m || (bin >= bin_p_lo && bin <= bin_p_hi);
+    }
+};
+
+// Tokens stay whose key is above `key`, or equal to it with an index below `index`.
+struct Cut {
+    uint32_t key, index;
+};
+
+// A list that gives each thread one token at most: every token is ranked
+// against the others of its bin, which settles all rules at once.
 template <bool F32>
+__device__ Cut cut_short(RowShared& sh, const Cuts& c) {
+    const int tid = threadIdx.x, n = sh.listed;
+    const bool mine = tid < n && sh.list_key[tid] != kNoKey;
+    const uint32_t key = mine ? sh.list_key[tid] : 0, index = mine ? sh.list_index[tid] : 0;
+    const int bin = key_bin(key);
+    uint32_t rank = 0;
+    uint64_t before = 0;   // the mass before it in its bin
+    for (int i = 0; i < n; ++i) {
+        const uint32_t k = sh.list_key[i], j = sh.list_index[i];
+        const bool first = key_bin(k) == bin && (k > key || (k == key && j < index));
+        rank += first;
+        before += first ? uint32_t(key_weight(k)) : 0;
+    }
+    uint64_t mass = sh.found[3];   // of the whole row
+    if (c.by_count) {
+        uint64_t in_bin;
+        const bool top_k = mine && bin == c.bin_k && sh.above_n[bin] + rank < c.k;
+        block_scan(top_k ? key_mass(key) : 0, sh.tmp, &in_bin);
+        mass = sh.above_m[c.bin_k] + in_bin;
+    }
+    const double limit = double(c.p) * double(mass);
+    int at = max(c.bin_k, c.bin_m);   // the bin of the highest cut
+    if (c.by_mass && !c.only_first) at = max(at, row_bin<true>(sh, 0, limit));
+    bool stays = mine && bin == at;
+    if (c.only_first)
+        stays = stays && rank == 0 && sh.above_n[bin] == 0;
+    else {
+        if (c.by_count) stays = stays && sh.above_n[bin] + rank < c.k;
+        if (c.by_mass) stays = stays && double(sh.above_m[bin] + before) < limit;
+        stays = stays && double(key_weight(key)) >= c.low;
+    }
+    // the last that stays: the smallest of (key, then the larger index)
+    uint64_t last = stays ? (uint64_t(key) << 32) | (0xffffffffu - index) : ~0ull;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) last = min(last, uint64_t(__shfl_xor(last, d)));
+    __syncthreads();
+    if ((tid & 63) == 0) sh.tmp[tid >> 6] = last;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) last = min(last, sh.tmp[w]);
+    if (last == ~0ull) return Cut{((uint32_t(at) + 1) << kBinShift) - 1, 0};   // none of that bin
+    return Cut{uint32_t(last >> 32), 0xffffffffu - uint32_t(last) + 1};
+}
+
+// Any number of tokens: radix selections within the bins.
+template <bool F32>
+__device__ Cut cut_long(RowShared& sh, const Cuts& c, const Tokens<F32>& tokens) {
+    uint32_t key = 0;
+    uint64_t stay = ~0ull, same = 0;   // of the `same` tokens at the key the first `stay` stay
+    uint64_t mass = sh.found[3];
+    __syncthreads();
+    if (c.only_first) {
+        key = kTopKey, stay = 1, same = ~0ull;
+    } else {
+        if (c.by_count) {
+            key = find_key<false>(sh, tokens, c.bin_k, sh.above_n[c.bin_k], c.k, 0.0);
+            stay = c.k - sh.found[1];
+            same = sh.found[2];
+            uint64_t part = 0, in_bin;   // the mass of the top k
+            tokens.each(sh, [&](uint32_t t, uint32_t) { part += key_bin(t) == c.bin_k && t > key ? key_mass(t) : 0; });
+            block_scan(part, sh.tmp, &in_bin);
+            mass = sh.above_m[c.bin_k] + in_bin + stay * key_mass(key);
+        }
+        if (c.by_mass) {
+            const double limit = double(c.p) * double(mass);
+            const int bin = row_bin<true>(sh, 0, limit);
+            const uint32_t key_p = find_key<true>(sh, tokens, bin, sh.above_m[bin], 0, limit);
+            const uint64_t above = sh.found[1], n = sh.found[2], w = key_mass(key_p);
+            // of these the e-th stays if above + e w < limit
+            uint64_t e = uint64_t(fmin((limit - double(above)) / double(w), double(n)));
+            while (e > 0 && !(double(above + (e - 1) * w) < limit)) --e;
+            while (e < n && double(above + e * w) < limit) ++e;
+            if (!c.by_count || key_p > key)
+                key = key_p, stay = e, same = n;
+            else if (key_p == key)
+                stay = min(stay, e);
+        }
+        if (c.bin_m >= 0) {
+            // low has the 24 bits of min_p, so the least weight that stays is exact in fp32
+            const uint32_t key_m = weight_key(float(ceil(c.low)));
+            if (key < key_m) key = key_m, stay = same = ~0ull;
+        }
+    }
+    __syncthreads();
+    return Cut{key, stay < same ? find_index(sh, tokens, key, stay) : 0xffffffffu};
+}
+
+template <bool F32, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
 sample_draw_kernel(SampleArgs a) {
     extern __shared__ char raw[];
     RowShared& sh = *reinterpret_cast<RowShared*>(raw);
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const void* row = row_of(a, r, F32 ? 4 : 2);
+    const uint64_t* bins = reinterpret_cast<const uint64_t*>(a.bins) + int64_t(r) * a.chunks * kBins;
+
+    // the row's bins, the highest at thread 0, and what lies above each
+    const int my_bin = kBins - 1 - tid;
+    uint64_t n = 0, m = 0;
+    if (my_bin >= 0) {
+#pragma unroll 8
+        for (int c = 0; c < a.chunks; ++c) {
+            const uint64_t x = bins[c * kBins + my_bin];
+            n += x >> kMassBits, m += x & (kOneToken - 1);
+        }
+    }
     const float top = row_max(a, r), inverse = row_inverse(a, r);
     if (top == -INFINITY) {
         if (tid == 0) {
@@ -302,154 +470,117 @@ sample_draw_kernel(SampleArgs a) {
         }
         return;
     }
+    Cuts cuts;
     const int k = inverse > 0.0f ? (a.top_k ? a.top_k[r] : 0) : 1;
-    const float p = a.top_p ? a.top_p[r] : 1.0f;
-    double low = a.min_p ? double(a.min_p[r]) * double(kSteps) : 0.0;
-    const uint64_t* bins = reinterpret_cast<const uint64_t*>(a.bins) + int64_t(r) * a.chunks * kBins;
-
-    // the row's bins
-    uint64_t mine_n = 0, mine_m = 0;
-    if (tid < kBins)
-        for (int c = 0; c < a.chunks; ++c) {
-            const uint64_t x = bins[c * kBins + tid];
-            mine_n += x >> kMassBits, mine_m += x & (kOneToken - 1);
-        }
+    cuts.k = uint64_t(max(k, 0));
+    cuts.p = a.top_p ? a.top_p[r] : 1.0f;
+    cuts.low = a.min_p ? double(a.min_p[r]) * double(kSteps) : 0.0;
     uint64_t some, mass;
-    block_scan(mine_n, sh.tmp, &some);
-    block_scan(mine_m, sh.tmp, &mass);
-    auto put_bins = [&] {
-        __syncthreads();
-        sh.count[tid] = uint32_t(mine_n), sh.mass[tid] = mine_m;
-        __syncthreads();
-    };
-    put_bins();
+    const uint64_t above_n = block_scan(n, sh.tmp, &some), above_m = block_scan(m, sh.tmp, &mass);
+    if (my_bin >= 0) sh.above_n[my_bin] = uint32_t(above_n), sh.above_m[my_bin] = above_m;
+    if (tid == 0) sh.found[3] = mass, sh.listed = 0;
+    __syncthreads();
 
-    // Which bins hold a threshold: that of the top k, those that may hold the
-    // top p's (the mass of the top k is known to within its last bin), and
-    // that of min_p.
-    const bool by_count = k > 0 && uint64_t(k) < some;
-    bool only_first = !(low <= double(kSteps));
-    int bin_k = -1, bin_p_lo = -1, bin_p_hi = -1, bin_m = -1;
-    uint64_t above_k = 0;
-    uint64_t mass_lo = mass, mass_hi = mass;
-    if (by_count) {
-        find_bin<false>(sh, kBins, 0, uint64_t(k), 0.0);
-        bin_k = int(sh.found[0]);
-        above_k = sh.found[1];
-        const uint64_t in_bin = uint64_t(k) - above_k;
-        uint64_t all;
-        const uint64_t above_mass = (block_scan(tid < kBins && tid > bin_k ? mine_m : 0, sh.tmp, &all), all);
-        mass_lo = above_mass + in_bin * uint64_t(key_weight(uint32_t(bin_k) << kBinShift));
-        mass_hi = above_mass + in_bin * uint64_t(key_weight(uint32_t(bin_k + 1) << kBinShift));
-    }
-    const bool by_mass = !(p >= 1.0f);
-    if (by_mass) {
-        if (!(double(p) * double(mass) > 0.0)) only_first = true;
-        if (!only_first) {
-            find_bin<true>(sh, kBins, 0, 0, double(p) * double(mass_hi));
-            bin_p_lo = int(sh.found[0]);
-            find_bin<true>(sh, kBins, 0, 0, double(p) * double(mass_lo));
-            bin_p_hi = int(sh.found[0]);
+    // Which bins hold a cut: that of the top k, those that may hold the top
+    // p's (the mass of the top k is known to within its last bin), and min_p's.
+    cuts.by_count = k > 0 && uint64_t(k) < some;
+    cuts.by_mass = !(cuts.p >= 1.0f);
+    cuts.only_first = !(cuts.low <= double(kSteps)) || (cuts.by_mass && !(double(cuts.p) * double(mass) > 0.0));
+    cuts.bin_k = cuts.bin_p_lo = cuts.bin_p_hi = cuts.bin_m = -1;
+    if (cuts.only_first) {
+        cuts.bin_m = kBins - 1;
+    } else {
+        uint64_t mass_lo = mass, mass_hi = mass;
+        if (cuts.by_count) {
+            cuts.bin_k = row_bin<false>(sh, cuts.k, 0.0);
+            const uint64_t in_bin = cuts.k - sh.above_n[cuts.bin_k];
+            mass_lo = sh.above_m[cuts.bin_k] + in_bin * key_mass(uint32_t(cuts.bin_k) << kBinShift);
+            mass_hi = sh.above_m[cuts.bin_k] + in_bin * key_mass(uint32_t(cuts.bin_k + 1) << kBinShift);
         }
+        if (cuts.by_mass) {
+            cuts.bin_p_lo = row_bin<true>(sh, 0, double(cuts.p) * double(mass_hi));
+            cuts.bin_p_hi = row_bin<true>(sh, 0, double(cuts.p) * double(mass_lo));
+        }
+        if (cuts.low > 1.0) cuts.bin_m = key_bin(weight_key(float(fmin(ceil(cuts.low), double(kSteps)))));
     }
-    if (low > 1.0 && !only_first) bin_m = key_bin(weight_key(float(fmin(ceil(low), double(kSteps)))));
-    if (only_first) bin_k = bin_p_lo = bin_p_hi = -1, bin_m = kBins - 1;
-    const int lowest = min(min(bin_k < 0 ? kBins : bin_k, bin_p_lo < 0 ? kBins : bin_p_lo), bin_m < 0 ? kBins : bin_m);
-    auto wanted = [&](int bin) { return bin == bin_k || bin == bin_m || (bin >= bin_p_lo && bin <= bin_p_hi); };
+    if (cuts.only_first) cuts.by_count = cuts.by_mass = false;
+    const bool any = cuts.bin_k >= 0 || cuts.bin_p_hi >= 0 || cuts.bin_m >= 0;
 
-    // Their tokens into the list.
+    Cut cut{0, 0xffffffffu};
     Tokens<F32> tokens{row, a.vocab, top, inverse, true};
-    if (lowest < kBins) {
+    if (any) {
+        // Their tokens into the list, from the chunks that have any.
         uint64_t many;
-        block_scan(tid < kBins && wanted(tid) ? mine_n : 0, sh.tmp, &many);
+        block_scan(my_bin >= 0 && cuts.wanted(my_bin) ? n : 0, sh.tmp, &many);
         tokens.in_list = many <= uint64_t(kListMax);
-        if (tid == 0) sh.listed = 0;
-        __syncthreads();
         if (tokens.in_list) {
-            // nothing below this can lie in the lowest of the bins (log and exp are off by far less than 1e-3)
-            const float cut = logf(key_weight(uint32_t(lowest) << kBinShift) / kSteps) - 1e-3f;
-            for (int begin = 0; begin < a.vocab; begin += kChunk) {
-                float x[kPer];
-                load_chunk<F32>(row, begin, a.vocab, x);
+            for (int c = tid >> 6; c < a.chunks; c += kRowWaves) {
+                uint64_t some_here = 0;
+#pragma unroll 8
+                for (int b = lane; b < kBins; b += 64) some_here |= cuts.wanted(b) ? bins[c * kBins + b] >> kMassBits : 0;
+                const bool has = __any(some_here != 0);
+                if (lane == 0) sh.chunk_has[c] = has;
+            }
+            __syncthreads();
+            // First by the exponent d alone, a little wider than the bins (log and
+            // exp are off by far less than 1e-4): a comparison or two a token.
+            // What passes is few, and gets its exact weight afterwards.
+            struct Range {
+                float lo, hi;
+            };
+            auto range = [](int lo, int hi) {
+                if (hi < 0) return Range{1.0f, -1.0f};
+                return Range{logf(key_weight(uint32_t(lo) << kBinShift) / kSteps) - 1e-4f,
+                             logf((key_weight(uint32_t(hi + 1) << kBinShift) + 1.0f) / kSteps) + 1e-4f};
+            };
+            const Range rk = range(cuts.bin_k, cuts.bin_k), rp = range(cuts.bin_p_lo, cuts.bin_p_hi),
+                        rm = range(cuts.bin_m, cuts.bin_m);
+            const float least = fminf(fminf(rk.lo, rp.lo), rm.lo);
+            const float scale = inverse == 0.0f ? INFINITY : inverse;   // T = 0: below the maximum is far below
+            Piece<F32, WIDE, kThreads> piece;
+            for (int c = 0; c < a.chunks; ++c) {
+                if (!sh.chunk_has[c]) continue;
+                piece.load(row, c * kChunk, a.vocab);
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
-                    if (!(x[j] == top) && !((x[j] - top) * inverse >= cut)) continue;
-                    const float w = weight(x[j], top, inverse);
-                    if (w < 1.0f || !wanted(key_bin(weight_key(w)))) continue;
+                    const float x = piece.x[j], d = x == top ? 0.0f : (x - top) * scale;
+                    if (!(d >= least)) continue;
+                    if (!((d >= rk.lo && d <= rk.hi) || (d >= rp.lo && d <= rp.hi) || (d >= rm.lo && d <= rm.hi))) continue;
                     const int at = atomicAdd(&sh.listed, 1);   // the order of the list matters to nothing below
-                    sh.list_key[at] = weight_key(w);
-                    sh.list_index[at] = uint32_t(begin + j * kThreads + tid);
+                    if (at < kListMax) {
+                        sh.list_key[at] = f32_bits(x);
+                        sh.list_index[at] = uint32_t(piece.token_at(c * kChunk, j));
+                    }
                 }
             }
             __syncthreads();
+            tokens.in_list = sh.listed <= kListMax;
+            if (tokens.in_list)
+                for (int i = tid; i < sh.listed; i += kThreads) {
+                    const float w = weight(bits_f32(sh.list_key[i]), top, inverse);
+                    const uint32_t t = w >= 1.0f ? weight_key(w) : kNoKey;
+                    sh.list_key[i] = t != kNoKey && cuts.wanted(key_bin(t)) ? t : kNoKey;
+                }
+            __syncthreads();
         }
+        cut = tokens.in_list && sh.listed <= kShort ? cut_short<F32>(sh, cuts) : cut_long<F32>(sh, cuts, tokens);
     }
 
-    // The threshold: tokens stay above `key`, and at it below index `index`.
-    uint32_t key = 0, index = 0xffffffffu;
-    uint64_t stay = ~0ull, same = 0;   // of the `same` tokens at the key the first `stay` stay
-    if (only_first) {
-        key = kTopKey;
-        stay = 1;
-        uint64_t n;
-        block_scan(tid == kBins - 1 ? mine_n : 0, sh.tmp, &n);
-        same = n;
-    } else {
-        if (by_count) {
-            key = find_key<false>(sh, tokens, bin_k, above_k, uint64_t(k), 0.0);
-            stay = uint64_t(k) - sh.found[1];
-            same = sh.found[2];
-            uint64_t part = 0;   // the mass of the top k
-            tokens.each(sh, [&](uint32_t t, uint32_t) { part += key_bin(t) == bin_k && t > key ? uint64_t(key_weight(t)) : 0; });
-            uint64_t in_bin, above;
-            block_scan(part, sh.tmp, &in_bin);
-            block_scan(tid < kBins && tid > bin_k ? mine_m : 0, sh.tmp, &above);
-            mass = above + in_bin + stay * uint64_t(key_weight(key));
-        }
-        if (by_mass) {
-            const double limit = double(p) * double(mass);
-            put_bins();
-            find_bin<true>(sh, kBins, 0, 0, limit);
-            const int bin = int(sh.found[0]);
-            const uint64_t above_bin = sh.found[1];
-            const uint32_t key_p = find_key<true>(sh, tokens, bin, above_bin, 0, limit);
-            const uint64_t above = sh.found[1], n = sh.found[2], w = uint64_t(key_weight(key_p));
-            // of these the e-th stays if above + e w < limit
-            uint64_t e = uint64_t(fmin((limit - double(above)) / double(w), double(n)));
-            while (e > 0 && !(double(above + (e - 1) * w) < limit)) --e;
-            while (e < n && double(above + e * w) < limit) ++e;
-            if (!by_count || key_p > key)
-                key = key_p, stay = e, same = n;
-            else if (key_p == key)
-                stay = min(stay, e);
-        }
-        if (bin_m >= 0) {
-            // low has the 24 bits of min_p, so the least weight that stays is exact in fp32
-            const uint32_t key_m = weight_key(float(ceil(low)));
-            if (key < key_m) key = key_m - 1, stay = 0, same = 0;
-        }
-    }
-    if (stay < same) index = stay ? find_index(sh, tokens, key, stay) : 0;
-    const bool none_at_key = stay == 0;
-    if (none_at_key) index = 0;
-
-    // The mass that stays, by chunks: whole bins above the threshold's, and that bin's tokens.
-    const int bin = key_bin(key);
-    const bool all_of_bin = key == 0 && !none_at_key && index == 0xffffffffu;   // no threshold at all
-    for (int c = tid; c < a.chunks; c += kThreads) sh.chunk_mass[c] = 0;
+    // The mass that stays, by chunks: whole bins above the cut's, and that bin's tokens.
+    const int bin = any ? key_bin(cut.key) : -1;
     __syncthreads();
     for (int c = tid >> 6; c < a.chunks; c += kRowWaves) {
-        uint64_t m = 0;
-        for (int b = lane; b < kBins; b += 64)
-            if (b > bin || (all_of_bin && b == bin)) m += bins[c * kBins + b] & (kOneToken - 1);
-        m = wave_sum(m);
-        if (lane == 0) sh.chunk_mass[c] = m;
+        uint64_t sum = 0;
+#pragma unroll 8
+        for (int b = lane; b < kBins; b += 64) sum += b > bin ? bins[c * kBins + b] & (kOneToken - 1) : 0;
+        sum = wave_sum(sum);
+        if (lane == 0) sh.chunk_mass[c] = sum;
     }
     __syncthreads();
-    if (!all_of_bin)
+    if (any)
         tokens.each(sh, [&](uint32_t t, uint32_t i) {
-            if (key_bin(t) == bin && (t > key || (t == key && i < index)))
-                atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk_mass[i / kChunk]), (unsigned long long)key_weight(t));
+            if (key_bin(t) == bin && (t > cut.key || (t == cut.key && i < cut.index)))
+                atomicAdd(reinterpret_cast<unsigned long long*>(&sh.chunk_mass[i / kChunk]), (unsigned long long)key_mass(t));
         });
     __syncthreads();
     uint64_t total;
@@ -462,26 +593,41 @@ sample_draw_kernel(SampleArgs a) {
     __syncthreads();
     const int begin = int(sh.found[0]) * kChunk + tid * kPer;
     const uint64_t base = sh.found[1];
-    float w[kPer];
+    float x[kPer];
+    if (WIDE && begin + kPer <= a.vocab) {
+        constexpr int kVec = F32 ? 4 : 8;
+#pragma unroll
+        for (int v = 0; v < kPer / kVec; ++v) {
+            const u32x4 raw16 = load16(static_cast<const char*>(row) + int64_t(begin + v * kVec) * (F32 ? 4 : 2));
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const float y = F32 ? bits_f32(raw16[j % 4]) : bits_f32(j % 2 ? raw16[j / 2 % 4] & 0xffff0000u : raw16[j / 2 % 4] << 16);
+                x[v * kVec + j] = y != y ? -INFINITY : y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) x[j] = begin + j < a.vocab ? logit<F32>(row, begin + j) : -INFINITY;
+    }
+    uint32_t w[kPer];
     uint64_t sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const int i = begin + j;
-        w[j] = i < a.vocab ? weight(logit<F32>(row, i), top, inverse) : 0.0f;
-        const uint32_t t = w[j] >= 1.0f ? weight_key(w[j]) : 0;
-        if (w[j] < 1.0f || t < key || (t == key && uint32_t(i) >= index)) w[j] = 0.0f;
-        sum += uint64_t(w[j]);
+        const float y = weight(x[j], top, inverse);
+        const uint32_t t = y >= 1.0f ? weight_key(y) : 0;
+        w[j] = y >= 1.0f && (t > cut.key || (t == cut.key && uint32_t(begin + j) < cut.index)) ? uint32_t(y) : 0;
+        sum += w[j];
     }
     uint64_t all;
     uint64_t run = base + block_scan(sum, sh.tmp, &all);
     if (target < run || target >= run + sum) return;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        if (target >= run && target < run + uint64_t(w[j])) {
+        if (target >= run && target < run + w[j]) {
             a.token[r] = begin + j;
             if (a.logprob) a.logprob[r] = logf(float(double(w[j]) / double(total)));
         }
-        run += uint64_t(w[j]);
+        run += w[j];
     }
 }
 
@@ -491,17 +637,19 @@ int check_sample_shape(int64_t rows, int64_t vocab) {
     return rows >= 0 && rows <= 65535 && vocab >= 1 && vocab <= (int64_t(1) << 22) ? NVFP4_OK : NVFP4_ERR_SHAPE;
 }
 
-// The bins of every row's chunks, then their maxima.
+int64_t pieces_of(int64_t vocab) { return (vocab + kMaxThreads * kPer - 1) / (kMaxThreads * kPer); }
+
+// The bins of every row's chunks, then the pieces' maxima.
 int64_t bins_bytes(int64_t rows, int64_t chunks) { return (rows * chunks * kBins * 8 + 15) / 16 * 16; }
 
-template <bool F32>
+template <bool F32, bool WIDE>
 int launch_sample(const SampleArgs& a, int64_t rows, hipStream_t s) {
-    const dim3 grid(a.chunks, static_cast<unsigned>(rows));
-    hipLaunchKernelGGL(sample_max_kernel<F32>, grid, dim3(kThreads), 0, s, a);
+    const unsigned n = static_cast<unsigned>(rows);
+    hipLaunchKernelGGL((sample_max_kernel<F32, WIDE>), dim3(a.pieces, n), dim3(kMaxThreads), 0, s, a);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-    hipLaunchKernelGGL(sample_bins_kernel<F32>, grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((sample_bins_kernel<F32, WIDE>), dim3(a.chunks, n), dim3(kThreads), 0, s, a);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-    hipLaunchKernelGGL(sample_draw_kernel<F32>, dim3(grid.y), dim3(kThreads), sizeof(RowShared), s, a);
+    hipLaunchKernelGGL((sample_draw_kernel<F32, WIDE>), dim3(n), dim3(kThreads), sizeof(RowShared), s, a);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
@@ -510,7 +658,10 @@ int launch_sample(const SampleArgs& a, int64_t rows, hipStream_t s) {
 namespace nvfp4 {
 
 int sample_setup() {
-    for (const void* fn : {reinterpret_cast<const void*>(sample_draw_kernel<true>), reinterpret_cast<const void*>(sample_draw_kernel<false>)})
+    for (const void* fn : {reinterpret_cast<const void*>(sample_draw_kernel<true, true>),
+                           reinterpret_cast<const void*>(sample_draw_kernel<true, false>),
+                           reinterpret_cast<const void*>(sample_draw_kernel<false, true>),
+                           reinterpret_cast<const void*>(sample_draw_kernel<false, false>)})
         if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLdsBytes) != hipSuccess) return NVFP4_ERR_HIP;
     return NVFP4_OK;
 }
@@ -521,7 +672,7 @@ extern "C" int nvfp4_sample_workspace(int64_t rows, int64_t vocab, int64_t* byte
     if (!bytes) return NVFP4_ERR_NULL;
     const int st = check_sample_shape(rows, vocab);
     const int64_t chunks = (vocab + kChunk - 1) / kChunk;
-    if (st == NVFP4_OK) *bytes = bins_bytes(rows, chunks) + rows * chunks * int64_t(sizeof(float));
+    if (st == NVFP4_OK) *bytes = bins_bytes(rows, chunks) + rows * pieces_of(vocab) * int64_t(sizeof(float));
     return st;
 }
 
@@ -545,8 +696,13 @@ extern "C" int nvfp4_sample(const void* logits, int logits_type, int64_t rows, i
     const int64_t chunks = (vocab + kChunk - 1) / kChunk;
     char* ws = static_cast<char*>(workspace);
     const SampleArgs a{logits, pitch, static_cast<int>(vocab), u, temperature, top_k, top_p, min_p, token, logprob,
-                       static_cast<int>(chunks), reinterpret_cast<float*>(ws + bins_bytes(rows, chunks)),
+                       static_cast<int>(chunks), static_cast<int>(pieces_of(vocab)),
+                       reinterpret_cast<float*>(ws + bins_bytes(rows, chunks)),
                        reinterpret_cast<unsigned long long*>(ws)};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return logits_type == NVFP4_LOGITS_F32 ? launch_sample<true>(a, rows, s) : launch_sample<false>(a, rows, s);
+    // 16-byte loads where every row begins on 16 bytes (the head's fp32 logits of 151552 tokens do)
+    const bool f32 = logits_type == NVFP4_LOGITS_F32;
+    const bool wide = !misaligned(logits, 16) && (rows == 1 || pitch % (f32 ? 4 : 8) == 0);
+    if (f32) return wide ? launch_sample<true, true>(a, rows, s) : launch_sample<true, false>(a, rows, s);
+    return wide ? launch_sample<false, true>(a, rows, s) : launch_sample<false, false>(a, rows, s);
 }
