@@ -86,35 +86,41 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int r, int si
     return static_cast<const char*>(a.logits) + int64_t(r) * a.pitch * size;
 }
 
-// The thread's kPer logits of the `threads * kPer` from `begin` on, -inf beyond
-// the vocabulary: 16 bytes at a time where the rows are aligned for it.
-// Element e of the result is token token_at(e).
+// The thread's kPer logits of the THREADS * kPer from `begin` on, 16 bytes at a
+// time where rows are aligned for it and whole (WIDE).  load() only loads, from
+// places held to the row so that it never branches; at() gives element e, token
+// token_at(e), with NaN and what lies beyond the vocabulary as -inf.
 template <bool F32, bool WIDE, int THREADS>
 struct Piece {
     static constexpr int kVec = WIDE ? (F32 ? 4 : 8) : 1;
-    float x[kPer];
+    u32x4 wide[WIDE ? kPer / kVec : 1];
+    float one[WIDE ? 1 : kPer];
 
-    __device__ __forceinline__ int token_at(int begin, int e) const {
+    static __device__ __forceinline__ int token_at(int begin, int e) {
         return begin + (e / kVec * THREADS + int(threadIdx.x)) * kVec + e % kVec;
     }
     __device__ __forceinline__ void load(const void* row, int begin, int vocab) {
 #pragma unroll
         for (int v = 0; v < kPer / kVec; ++v) {
-            const int i = token_at(begin, v * kVec);
-            if constexpr (WIDE) {
-                if (i + kVec <= vocab) {
-                    const u32x4 raw = load16(static_cast<const char*>(row) + int64_t(i) * (F32 ? 4 : 2));
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j)
-                        x[v * kVec + j] = F32 ? bits_f32(raw[j % 4]) : bits_f32(j % 2 ? raw[j / 2 % 4] & 0xffff0000u : raw[j / 2 % 4] << 16);
-                    continue;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) x[v * kVec + j] = i + j < vocab ? logit<F32>(row, i + j) : -INFINITY;
+            const int i = min(token_at(begin, v * kVec), vocab - kVec);
+            if constexpr (WIDE)
+                wide[v] = load16(static_cast<const char*>(row) + int64_t(i) * (F32 ? 4 : 2));
+            else
+                one[v] = F32 ? static_cast<const float*>(row)[i] : bf16_to_f32(static_cast<const uint16_t*>(row)[i]);
         }
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) x[e] = x[e] != x[e] ? -INFINITY : x[e];
+    }
+    __device__ __forceinline__ float raw(int e) const {
+        if constexpr (WIDE) {
+            const int v = e / kVec, j = e % kVec;
+            const uint32_t w = F32 ? wide[v][j % 4] : wide[v][j / 2 % 4];
+            return F32 ? bits_f32(w) : bits_f32(j % 2 ? w & 0xffff0000u : w << 16);
+        } else {
+            return one[e];
+        }
+    }
+    __device__ __forceinline__ float at(int begin, int vocab, int e) const {
+        const float x = raw(e);
+        return x == x && token_at(begin, e) < vocab ? x : -INFINITY;
     }
 };
 
@@ -124,10 +130,11 @@ sample_max_kernel(SampleArgs a) {
     __shared__ float tmp[kMaxThreads / 64];
     const int r = blockIdx.y, c = blockIdx.x;
     Piece<F32, WIDE, kMaxThreads> p;
-    p.load(row_of(a, r, F32 ? 4 : 2), c * kMaxThreads * kPer, a.vocab);
-    float top = p.x[0];
+    const int begin = c * kMaxThreads * kPer;
+    p.load(row_of(a, r, F32 ? 4 : 2), begin, a.vocab);
+    float top = -INFINITY;
 #pragma unroll
-    for (int j = 1; j < kPer; ++j) top = fmaxf(top, p.x[j]);
+    for (int j = 0; j < kPer; ++j) top = fmaxf(top, p.at(begin, a.vocab, j));
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = top;
@@ -165,7 +172,7 @@ sample_bins_kernel(SampleArgs a) {
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const float w = weight(p.x[j], top, inverse);
+        const float w = weight(p.at(c * kChunk, a.vocab, j), top, inverse);
         if (w >= 1.0f) atomicAdd(&bins[key_bin(weight_key(w))], kOneToken | (unsigned long long)uint32_t(w));
     }
     __syncthreads();
@@ -174,32 +181,46 @@ sample_bins_kernel(SampleArgs a) {
 
 // ---- launch 3: the thresholds and the draw, one workgroup a row
 
-__device__ __forceinline__ uint64_t wave_sum(uint64_t x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+// x of the lane that the row operation CTRL names, 0 where there is none or the
+// row is not in ROWS: a move between lanes inside the vector unit (a scan by
+// shuffles goes through LDS and took 1.3 us a workgroup, this 0.5 us).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t lane_move(uint64_t x) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(x)), CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(x >> 32)), CTRL, ROWS, 0xf, false);
+    return (uint64_t(hi) << 32) | lo;
+}
+
+// Sum over this lane and those before it.
+__device__ __forceinline__ uint64_t wave_scan(uint64_t x) {
+    x += lane_move<0x111, 0xf>(x);   // 1, 2, 4 and 8 lanes within each row of 16
+    x += lane_move<0x112, 0xf>(x);
+    x += lane_move<0x114, 0xf>(x);
+    x += lane_move<0x118, 0xf>(x);
+    x += lane_move<0x142, 0xa>(x);   // row 0's last into row 1, row 2's into row 3
+    x += lane_move<0x143, 0xc>(x);   // the first half's last into rows 2 and 3
     return x;
 }
 
+__device__ __forceinline__ uint64_t last_lane(uint64_t x) {
+    return (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(uint32_t(x >> 32)), 63))) << 32) |
+           uint32_t(__builtin_amdgcn_readlane(int(uint32_t(x)), 63));
+}
+
+__device__ __forceinline__ uint64_t wave_sum(uint64_t x) { return last_lane(wave_scan(x)); }
+
 // Sum over the threads before this one, and over all.
 __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* tmp, uint64_t* all) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t sum = x;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t y = __shfl_up(sum, d);
-        if (lane >= d) sum += y;
-    }
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint64_t sum = wave_scan(x);
     __syncthreads();
     if (lane == 63) tmp[wave] = sum;
     __syncthreads();
-    uint64_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) {
-        const uint64_t y = tmp[w];
-        if (w < wave) before += y;
-        total += y;
-    }
-    *all = total;
+    const uint64_t mine = tmp[lane & (kRowWaves - 1)];
+    const uint64_t waves = wave_scan(lane < kRowWaves ? mine : 0);   // lane i: wavefronts 0 .. i
+    *all = last_lane(waves);
+    const uint64_t before = wave == 0 ? 0 : (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(uint32_t(waves >> 32)), (wave - 1) & 63))) << 32) |
+                                                uint32_t(__builtin_amdgcn_readlane(int(uint32_t(waves)), (wave - 1) & 63));
     return before + sum - x;
 }
 
@@ -363,7 +384,7 @@ __device__ Cut cut_short(RowShared& sh, const Cuts& c) {
     const int bin = key_bin(key);
     uint32_t rank = 0;
     uint64_t before = 0;   // the mass before it in its bin
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < n && __any(mine); ++i) {
         const uint32_t k = sh.list_key[i], j = sh.list_index[i];
         const bool first = key_bin(k) == bin && (k > key || (k == key && j < index));
         rank += first;
@@ -512,7 +533,7 @@ sample_draw_kernel(SampleArgs a) {
         // Their tokens into the list, from the chunks that have any.
         uint64_t many;
         block_scan(my_bin >= 0 && cuts.wanted(my_bin) ? n : 0, sh.tmp, &many);
-        tokens.in_list = many <= uint64_t(kListMax);
+        tokens.in_list = many <= uint64_t(kListMax) && top < INFINITY;   // d of an infinite logit is none
         if (tokens.in_list) {
             for (int c = tid >> 6; c < a.chunks; c += kRowWaves) {
                 uint64_t some_here = 0;
@@ -523,8 +544,10 @@ sample_draw_kernel(SampleArgs a) {
             }
             __syncthreads();
             // First by the exponent d alone, a little wider than the bins (log and
-            // exp are off by far less than 1e-4): a comparison or two a token.
-            // What passes is few, and gets its exact weight afterwards.
+            // exp are off by far less than 1e-4): every token against the hull of
+            // the bins, which is two operations and two comparisons, and what
+            // passes against each range.  What is listed is few, and gets its
+            // exact weight afterwards.
             struct Range {
                 float lo, hi;
             };
@@ -535,23 +558,30 @@ sample_draw_kernel(SampleArgs a) {
             };
             const Range rk = range(cuts.bin_k, cuts.bin_k), rp = range(cuts.bin_p_lo, cuts.bin_p_hi),
                         rm = range(cuts.bin_m, cuts.bin_m);
-            const float least = fminf(fminf(rk.lo, rp.lo), rm.lo);
-            const float scale = inverse == 0.0f ? INFINITY : inverse;   // T = 0: below the maximum is far below
-            Piece<F32, WIDE, kThreads> piece;
-            for (int c = 0; c < a.chunks; ++c) {
-                if (!sh.chunk_has[c]) continue;
-                piece.load(row, c * kChunk, a.vocab);
+            const Range hull{fminf(fminf(rk.lo, rp.lo), rm.lo), fmaxf(fmaxf(rk.hi, rp.hi), rm.hi)};
+            const float scale = inverse == 0.0f ? 1e30f : inverse;   // T = 0: below the maximum is far below
+            auto next_chunk = [&](int c) {
+                while (c < a.chunks && !sh.chunk_has[c]) ++c;
+                return c;
+            };
+            int c = next_chunk(0);
+            Piece<F32, WIDE, kThreads> piece, ahead;
+            piece.load(row, min(c, a.chunks - 1) * kChunk, a.vocab);
+            while (c < a.chunks) {
+                const int next = next_chunk(c + 1);
+                ahead.load(row, min(next, a.chunks - 1) * kChunk, a.vocab);   // also past the end, so that no wait depends on a branch
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
-                    const float x = piece.x[j], d = x == top ? 0.0f : (x - top) * scale;
-                    if (!(d >= least)) continue;
-                    if (!((d >= rk.lo && d <= rk.hi) || (d >= rp.lo && d <= rp.hi) || (d >= rm.lo && d <= rm.hi))) continue;
+                    const float x = piece.raw(j), d = (x - top) * scale;   // NaN passes no comparison
+                    if (!((d >= hull.lo) & (d <= hull.hi))) continue;
+                    const int token = piece.token_at(c * kChunk, j);
+                    if (!((d >= rk.lo && d <= rk.hi) || (d >= rp.lo && d <= rp.hi) || (d >= rm.lo && d <= rm.hi)) || token >= a.vocab)
+                        continue;
                     const int at = atomicAdd(&sh.listed, 1);   // the order of the list matters to nothing below
-                    if (at < kListMax) {
-                        sh.list_key[at] = f32_bits(x);
-                        sh.list_index[at] = uint32_t(piece.token_at(c * kChunk, j));
-                    }
+                    if (at < kListMax) sh.list_key[at] = f32_bits(x), sh.list_index[at] = uint32_t(token);
                 }
+                piece = ahead;
+                c = next;
             }
             __syncthreads();
             tokens.in_list = sh.listed <= kListMax;
@@ -593,27 +623,14 @@ sample_draw_kernel(SampleArgs a) {
     __syncthreads();
     const int begin = int(sh.found[0]) * kChunk + tid * kPer;
     const uint64_t base = sh.found[1];
-    float x[kPer];
-    if (WIDE && begin + kPer <= a.vocab) {
-        constexpr int kVec = F32 ? 4 : 8;
-#pragma unroll
-        for (int v = 0; v < kPer / kVec; ++v) {
-            const u32x4 raw16 = load16(static_cast<const char*>(row) + int64_t(begin + v * kVec) * (F32 ? 4 : 2));
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const float y = F32 ? bits_f32(raw16[j % 4]) : bits_f32(j % 2 ? raw16[j / 2 % 4] & 0xffff0000u : raw16[j / 2 % 4] << 16);
-                x[v * kVec + j] = y != y ? -INFINITY : y;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) x[j] = begin + j < a.vocab ? logit<F32>(row, begin + j) : -INFINITY;
-    }
+    Piece<F32, WIDE, 1> last;   // consecutive tokens
+    const int lane_begin = begin - tid * Piece<F32, WIDE, 1>::kVec;
+    last.load(row, lane_begin, a.vocab);
     uint32_t w[kPer];
     uint64_t sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const float y = weight(x[j], top, inverse);
+        const float y = weight(last.at(lane_begin, a.vocab, j), top, inverse);
         const uint32_t t = y >= 1.0f ? weight_key(y) : 0;
         w[j] = y >= 1.0f && (t > cut.key || (t == cut.key && uint32_t(begin + j) < cut.index)) ? uint32_t(y) : 0;
         sum += w[j];
@@ -700,9 +717,10 @@ extern "C" int nvfp4_sample(const void* logits, int logits_type, int64_t rows, i
                        reinterpret_cast<float*>(ws + bins_bytes(rows, chunks)),
                        reinterpret_cast<unsigned long long*>(ws)};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    // 16-byte loads where every row begins on 16 bytes (the head's fp32 logits of 151552 tokens do)
+    // 16-byte loads where every row begins on 16 bytes and is whole ones (the head's 151552 fp32 logits are)
     const bool f32 = logits_type == NVFP4_LOGITS_F32;
-    const bool wide = !misaligned(logits, 16) && (rows == 1 || pitch % (f32 ? 4 : 8) == 0);
+    const int vec = f32 ? 4 : 8;
+    const bool wide = !misaligned(logits, 16) && vocab % vec == 0 && (rows == 1 || pitch % vec == 0);
     if (f32) return wide ? launch_sample<true, true>(a, rows, s) : launch_sample<true, false>(a, rows, s);
     return wide ? launch_sample<false, true>(a, rows, s) : launch_sample<false, false>(a, rows, s);
 }
