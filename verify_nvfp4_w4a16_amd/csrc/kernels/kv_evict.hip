@@ -155,99 +155,165 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 constexpr int kSelect = 1024;
+constexpr int kSelectWaves = kSelect / 64;
+constexpr int kSelectBins = 2048;
 
-// Exclusive sums over the workgroup of two counts, in thread order, and their totals.
-__device__ __forceinline__ void scan2(int x, int y, int* before_x, int* before_y, int* all_x, int* all_y, int (*tmp)[2]) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int sx = x, sy = y;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int ux = __shfl_up(sx, d), uy = __shfl_up(sy, d);
-        if (lane >= d) sx += ux, sy += uy;
-    }
-    __syncthreads();
-    if (lane == 63) tmp[wave][0] = sx, tmp[wave][1] = sy;
-    __syncthreads();
-    int bx = 0, by = 0, ax = 0, ay = 0;
-    for (int w = 0; w < kSelect / 64; ++w) {
-        if (w < wave) bx += tmp[w][0], by += tmp[w][1];
-        ax += tmp[w][0], ay += tmp[w][1];
-    }
-    *before_x = bx + sx - x, *before_y = by + sy - y, *all_x = ax, *all_y = ay;
+// A lane's value plus those of all lanes before it, by moves between lanes.
+__device__ __forceinline__ uint32_t scan32(uint32_t x) {
+    x += uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x111, 0xf, 0xf, false));   // 1, 2, 4, 8 lanes within a row of 16
+    x += uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x112, 0xf, 0xf, false));
+    x += uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x114, 0xf, 0xf, false));
+    x += uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x118, 0xf, 0xf, false));
+    x += uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x142, 0xa, 0xf, false));   // a row's last into the next
+    x += uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x143, 0xc, 0xf, false));   // the first half's last into the second
+    return x;
 }
 
+// The weights of one (sequence, head): wavefront w has the slots
+// [w, w + 1) * span, 64 neighbours at a time.  HELD > 0: their keys stay in
+// HELD registers a lane; 0: they are read again each time.
+template <int HELD>
+struct Keys {
+    const float* w;
+    int begin, end;   // of this wavefront
+    uint32_t held[HELD > 0 ? HELD : 1];
+
+    __device__ __forceinline__ Keys(const float* weights, int n) : w(weights) {
+        const int span = HELD > 0 ? HELD * 64 : (n + kSelect - 1) / kSelect * 64;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        begin = min(wave * span, n), end = min(begin + span, n);
+        if constexpr (HELD > 0) {
+            const int last = max(n - 1, 0);
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) held[i] = n > 0 ? f32_bits(w[min(begin + i * 64 + int(threadIdx.x & 63), last)]) : 0;
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) held[i] = order_key(bits_f32(held[i]));
+        }
+    }
+    // fn(slot, key, there) for every 64 slots of the wavefront, all lanes together
+    template <class Fn>
+    __device__ __forceinline__ void each(Fn fn) const {
+        const int lane = threadIdx.x & 63;
+        if constexpr (HELD > 0) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                if (begin + i * 64 < end) fn(begin + i * 64 + lane, held[i], begin + i * 64 + lane < end);
+        } else {
+            for (int j = begin; j < end; j += 64) fn(j + lane, j + lane < end ? order_key(w[j + lane]) : 0, j + lane < end);
+        }
+    }
+};
+
 // Which slots stay: one workgroup a (sequence, head).
+template <int HELD>
 __global__ void __launch_bounds__(kSelect)
 kv_select_kernel(EvictArgs a) {
-    __shared__ int bins[256];
-    __shared__ int tmp[kSelect / 64][2];
+    __shared__ uint32_t bins[kSelectBins];
+    __shared__ uint32_t tmp[kSelectWaves][2];
     __shared__ uint32_t found[2];
-    const int s = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+    const int s = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = a.len(s);
     const int64_t seq_head = int64_t(s) * a.v.kv_heads + h;
     const float* w = a.weights + seq_head * a.weights_pitch;
     int32_t* kept = a.kept + seq_head * a.keep;
     float* kept_w = a.kept_weights + seq_head * a.keep;
     if (h == 0 && tid == 0) a.new_lens[s] = min(n, a.keep);
-    const int lo = n > a.keep ? a.sink : n, hi = n > a.keep ? n - a.recent : n;   // the choice is among [lo, hi)
-    int need = n > a.keep ? a.keep - a.sink - a.recent : 0;
-    uint32_t key = 0, mask = 0;   // the threshold's known leading bits
-    if (need > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kSelect) bins[i] = 0;
-            __syncthreads();
-            for (int j = lo + tid; j < hi; j += kSelect) {
-                const uint32_t k = order_key(w[j]);
-                if ((k & mask) == key) atomicAdd(&bins[(k >> shift) & 255], 1);
-            }
-            __syncthreads();
-            if (tid == 0) {
-                int left = need, d = 255;
-                while (d > 0 && bins[d] < left) left -= bins[d--];
-                found[0] = uint32_t(d), found[1] = uint32_t(left);
-            }
-            __syncthreads();
-            key |= found[0] << shift;
-            mask |= 255u << shift;
-            need = int(found[1]);   // still wanted among the keys with these leading bits
-            __syncthreads();
-        }
-    }
-    // `need` of the slots at the threshold stay, the lowest first
-    int at = 0, ties = 0;
-    for (int j0 = 0; j0 < n; j0 += kSelect) {
-        const int j = j0 + tid;
-        bool sure = false, tie = false;
-        if (j < n) {
-            const uint32_t k = order_key(w[j]);
-            const bool open = j >= lo && j < hi;
-            sure = !open || (a.keep - a.sink - a.recent > 0 && k > key);
-            tie = open && a.keep - a.sink - a.recent > 0 && k == key;
-        }
-        int bs, bt, as, al;
-        scan2(sure, tie, &bs, &bt, &as, &al, tmp);
-        const int tie_rank = ties + bt;
-        if (sure || (tie && tie_rank < need)) {
-            const int to = at + bs + (min(tie_rank, need) - min(ties, need));
-            kept[to] = j;
-            kept_w[to] = w[j];
-        }
-        at += as + (min(ties + al, need) - min(ties, need));
-        ties += al;
-    }
     for (int i = min(n, a.keep) + tid; i < a.keep; i += kSelect) {
         kept[i] = -1;
         kept_w[i] = 0.0f;
     }
+    if (n <= a.keep) {
+        for (int i = tid; i < n; i += kSelect) {
+            kept[i] = i;
+            kept_w[i] = w[i];
+        }
+        return;
+    }
+    const Keys<HELD> keys(w, n);
+    const int lo = a.sink, hi = n - a.recent;   // the choice is among [lo, hi)
+    const int wanted = a.keep - a.sink - a.recent;
+    uint32_t need = uint32_t(wanted), key = 0xffffffffu;
+    if (wanted > 0) {
+        // the key of the last slot that is chosen, 11, 11 and 10 bits at a time
+        uint32_t mask = 0;
+        key = 0;
+        for (int level = 0; level < 3; ++level) {
+            const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
+            const uint32_t digits = level < 2 ? 2047 : 1023;
+            bins[tid] = bins[tid + kSelect] = 0;
+            __syncthreads();
+            keys.each([&](int j, uint32_t k, bool there) {
+                const bool in = there && j >= lo && j < hi && (k & mask) == key;
+                const uint64_t all = __ballot(in);
+                if (!all) return;
+                // equal digits of a wavefront (the many zeros of a fresh cache) are added at once
+                const uint32_t d = (k >> shift) & digits;
+                const int first = __ffsll(static_cast<unsigned long long>(all)) - 1;
+                const uint32_t common = uint32_t(__builtin_amdgcn_readlane(int(d), first));
+                const uint64_t same = __ballot(in && d == common);
+                if (lane == first) atomicAdd(&bins[common], uint32_t(__popcll(same)));
+                if (in && d != common) atomicAdd(&bins[d], 1u);
+            });
+            __syncthreads();
+            // thread t has bins 2 (1023 - t) + 1 and 2 (1023 - t): the highest first
+            const int at = 2 * (kSelect - 1 - tid);
+            const uint32_t high = bins[at + 1], low = bins[at];
+            const uint32_t sum = scan32(high + low);
+            if (lane == 63) tmp[wave][0] = sum;
+            __syncthreads();
+            uint32_t before = sum - high - low;
+            for (int i = 0; i < wave; ++i) before += tmp[i][0];
+            if (before < need && before + high >= need)
+                found[0] = uint32_t(at + 1), found[1] = need - before;
+            else if (before + high < need && before + high + low >= need)
+                found[0] = uint32_t(at), found[1] = need - before - high;
+            __syncthreads();
+            key |= found[0] << shift;
+            mask |= digits << shift;
+            need = found[1];   // still wanted among the keys with these leading bits
+        }
+    }
+    // `need` of the slots at the key stay, the lowest first.  Wavefronts count
+    // theirs, then number them from where those before them end.
+    auto sure = [&](int j, uint32_t k, bool there) { return there && (j < lo || j >= hi || (wanted > 0 && k > key)); };
+    auto tie = [&](int j, uint32_t k, bool there) { return there && j >= lo && j < hi && wanted > 0 && k == key; };
+    uint32_t mine = 0, ties = 0;
+    keys.each([&](int j, uint32_t k, bool there) {
+        mine += uint32_t(__popcll(__ballot(sure(j, k, there))));
+        ties += uint32_t(__popcll(__ballot(tie(j, k, there))));
+    });
+    __syncthreads();
+    if (lane == 0) tmp[wave][0] = mine, tmp[wave][1] = ties;
+    __syncthreads();
+    uint32_t at = 0, seen = 0;   // sure slots and ties before
+    for (int i = 0; i < wave; ++i) at += tmp[i][0], seen += tmp[i][1];
+    const uint64_t below = (1ull << lane) - 1;
+    keys.each([&](int j, uint32_t k, bool there) {
+        const bool is_sure = sure(j, k, there), is_tie = tie(j, k, there);
+        const uint64_t sures = __ballot(is_sure), equal = __ballot(is_tie);
+        const uint32_t rank = seen + uint32_t(__popcll(equal & below));
+        if (is_sure || (is_tie && rank < need)) {
+            const uint32_t to = at + uint32_t(__popcll(sures & below)) + min(rank, need);
+            kept[to] = j;
+            kept_w[to] = w[j];
+        }
+        at += uint32_t(__popcll(sures));
+        seen += uint32_t(__popcll(equal));
+    });
 }
 
 // The rows that stay, one destination page a workgroup.
 template <int D>
-__global__ void __launch_bounds__(256)
+constexpr int kMoveThreads = D == 64 ? 128 : 256;
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads<D>)
 kv_move_kernel(EvictArgs a) {
     using R = KvRecord<D>;
     __shared__ const uint8_t* from[kPage];
     __shared__ int slot_in[kPage];
+    __shared__ bool live[kPage];
     const int s = blockIdx.y, tid = threadIdx.x;
     const int h = blockIdx.x % a.v.kv_heads, page = blockIdx.x / a.v.kv_heads;
     const int n = min(a.len(s), a.keep);
@@ -257,38 +323,52 @@ kv_move_kernel(EvictArgs a) {
     uint8_t* to = a.dst + (to_page * a.v.kv_heads + h) * R::kBytes;
     if (tid < kPage) {
         const int at = page * kPage + tid;
-        const uint8_t* rec = nullptr;
-        int slot = 0;
-        if (at < n) {
-            const int j = a.kept[(int64_t(s) * a.v.kv_heads + h) * a.keep + at];
-            rec = a.v.record<D>(s, j / kPage, h);
-            slot = j % kPage;
-        }
-        from[tid] = rec;
-        slot_in[tid] = slot;
+        const int j = at < n ? a.kept[(int64_t(s) * a.v.kv_heads + h) * a.keep + at] : 0;
+        const int id = a.v.page_id(s, j / kPage);
+        live[tid] = at < n && a.v.has(id);
+        from[tid] = a.v.pages > 0 ? a.v.record_or_first<D>(id, h) : to;   // (a cache without pages has no live slot)
+        slot_in[tid] = j % kPage;
     }
     __syncthreads();
-    for (int i = tid; i < kPage * (D / 32); i += 256) {   // K codes, 16 bytes each
-        const int slot = i / (D / 32), part = i % (D / 32);
-        u32x4 x = {0, 0, 0, 0};
-        if (from[slot]) x = load16(from[slot] + R::k_code(slot_in[slot]) + 16 * part);
-        *reinterpret_cast<u32x4*>(to + R::k_code(slot) + 16 * part) = x;
+    // All loads first, from a place that is there in any case: with a branch
+    // around each they would wait for one another.
+    constexpr int kThreads = kMoveThreads<D>, kKParts = kPage * (D / 32) / kThreads, kVDwords = 8 * D / kThreads;
+    u32x4 kc[kKParts];
+#pragma unroll
+    for (int i = 0; i < kKParts; ++i) {   // K codes, 16 bytes each
+        const int slot = (i * kThreads + tid) / (D / 32), part = (i * kThreads + tid) % (D / 32);
+        kc[i] = load16(from[slot] + R::k_code(slot_in[slot]) + 16 * part);
     }
-    for (int i = tid; i < kPage * (D / 16); i += 256) {   // scales
-        const int slot = i / (D / 16), g = i % (D / 16);
-        const uint8_t* rec = from[slot];
-        const int j = slot_in[slot];
-        to[R::k_scale(slot, g)] = rec ? rec[R::k_scale(j, g)] : 0;
-        to[R::v_scale(slot / 8, g) + slot % 8] = rec ? rec[R::v_scale(j / 8, g) + j % 8] : 0;
+    uint32_t vc[kVDwords][8];
+#pragma unroll
+    for (int i = 0; i < kVDwords; ++i) {   // V codes: a dword is 8 slots at a dim
+        const int block = (i * kThreads + tid) / D, dim = (i * kThreads + tid) % D;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int j = slot_in[8 * block + e];
+            vc[i][e] = *reinterpret_cast<const uint32_t*>(from[8 * block + e] + R::v_code(j / 8, dim));
+        }
     }
-    for (int i = tid; i < 8 * D; i += 256) {              // V codes: a dword is 8 slots at a dim
-        const int block = i / D, dim = i % D;
+    for (int i = tid; i < kPage * (D / 16); i += kThreads) {   // scales
+        const int slot = i / (D / 16), g = i % (D / 16), j = slot_in[slot];
+        const uint8_t ks = from[slot][R::k_scale(j, g)], vs = from[slot][R::v_scale(j / 8, g) + j % 8];
+        to[R::k_scale(slot, g)] = live[slot] ? ks : 0;
+        to[R::v_scale(slot / 8, g) + slot % 8] = live[slot] ? vs : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kKParts; ++i) {
+        const int slot = (i * kThreads + tid) / (D / 32), part = (i * kThreads + tid) % (D / 32);
+        const u32x4 none = {0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(to + R::k_code(slot) + 16 * part) = live[slot] ? kc[i] : none;
+    }
+#pragma unroll
+    for (int i = 0; i < kVDwords; ++i) {
+        const int block = (i * kThreads + tid) / D, dim = (i * kThreads + tid) % D;
         uint32_t w = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint8_t* rec = from[8 * block + e];
-            const int j = slot_in[8 * block + e];
-            if (rec) w |= (*reinterpret_cast<const uint32_t*>(rec + R::v_code(j / 8, dim)) >> (4 * (j % 8)) & 15u) << (4 * e);
+            const int slot = 8 * block + e;
+            w |= (live[slot] ? vc[i][e] >> (4 * (slot_in[slot] % 8)) & 15u : 0u) << (4 * e);
         }
         *reinterpret_cast<uint32_t*>(to + R::v_code(block, dim)) = w;
     }
@@ -298,7 +378,7 @@ template <int D>
 int launch_move(const EvictArgs& a, hipStream_t st) {
     const int64_t blocks = int64_t((a.keep + kPage - 1) / kPage) * a.v.kv_heads;
     if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL(kv_move_kernel<D>, dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(kv_move_kernel<D>, dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(kMoveThreads<D>), 0, st, a);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
@@ -347,7 +427,13 @@ extern "C" int nvfp4_kv_evict(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs
     const EvictArgs a{kv_view(cache, seqs), weights, weights_pitch, static_cast<int>(keep), static_cast<int>(sink),
                       static_cast<int>(recent), dst->data, dst->pages, dst_table, dst_pitch, kept, kept_weights, new_lens};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    hipLaunchKernelGGL(kv_select_kernel, dim3(cache->kv_heads, static_cast<unsigned>(seqs->seqs)), dim3(kSelect), 0, s, a);
+    // keys in registers up to 65536 slots a sequence (64 a lane, read once); longer ones are read five times
+    const int64_t longest = std::min(weights_pitch, seqs->table_pitch * kPage);
+    const auto select = longest <= 4 * kSelect    ? kv_select_kernel<4>
+                        : longest <= 16 * kSelect ? kv_select_kernel<16>
+                        : longest <= 64 * kSelect ? kv_select_kernel<64>
+                                                  : kv_select_kernel<0>;
+    hipLaunchKernelGGL(select, dim3(cache->kv_heads, static_cast<unsigned>(seqs->seqs)), dim3(kSelect), 0, s, a);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     switch (cache->head_dim) {
         case 64: return launch_move<64>(a, s);
