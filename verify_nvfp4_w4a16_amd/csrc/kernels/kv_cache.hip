@@ -1,12 +1,10 @@
 // Filling and reading the paged NVFP4 cache (include/nvfp4_kv.h).
 //
-// A unit of work is one block of 8 slots of one sequence and head: V's codes
-// of 8 slots share a dword at each dim, so one workgroup owns the block and
-// merges the new rows' nibbles into it, with no atomics.  A workgroup has D
-// threads: first one thread for each 16-dim group of the block's K and V rows
-// (8 slots x D/16 groups x 2), then one thread for each dim's V dword.
-// Bound by latency at one token a sequence and by the bf16 rows' bytes for
-// prompts; see the measurements at the launches.
+// V's codes of 8 slots share a dword at each dim, so a workgroup owns whole
+// 8-slot blocks (four for append, one for read) of one sequence and head and
+// merges the new rows' nibbles into them, with no atomics.  A thread takes one
+// 16-dim group of a row, then dwords of V at a dim.  Bound by latency at one
+// token a sequence and by the bf16 rows' bytes for prompts.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -17,31 +15,42 @@
 
 namespace {
 
-// Nearest e4m3 code to u >= 0, ties to even, saturating at 448.  The
-// quantum's reciprocal is a power of two, so u / quantum is exact.
-__device__ __forceinline__ uint32_t e4m3_code(double u) {
-    if (!(u < 448.0)) return 0x7E;
-    int e;
-    (void)frexp(u, &e);                       // u in [2^(e-1), 2^e); 0 gives e = 0
-    if (u == 0.0) return 0;
-    const int lo = e - 1 < -6 ? -6 : e - 1;
-    const double r = rint(ldexp(u, 3 - lo));  // 0..16 quanta of 2^(lo - 3)
-    const uint32_t n = static_cast<uint32_t>(r);
-    // codes are consecutive across binades: subnormals 0..7 at lo = -6
-    const uint32_t code = lo == -6 ? n : ((uint32_t(lo + 7) << 3) + (n - 8));
-    return code > 0x7E ? 0x7E : code;
+// The rounding rules in exact arithmetic: a code is settled by comparing the
+// bf16 magnitude with a boundary times a scale, which 64 bits hold exactly (the
+// tensor scale has 24 bits, an e4m3 value 4, a boundary at most 5), so a tie is
+// a real tie.  No quotient is formed, where 64 bits would cost most.
+struct Scale {
+    double t, six_t;
+    float inverse;   // 1 / (6 t), for a first guess
+};
+
+__device__ __forceinline__ Scale scale_of(float t) { return Scale{double(t), 6.0 * double(t), 1.0f / (6.0f * t)}; }
+
+// The e4m3 code nearest to amax / (6 t), ties to even, saturating at 448.
+__device__ __forceinline__ uint32_t e4m3_code(float amax, const Scale& sc) {
+    const float guess = fminf(amax * sc.inverse, 448.0f);
+    const uint32_t c = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(guess, guess, 0, false)) & 0x7f;
+    const double a = double(amax), v = double(e4m3_f32(c));
+    if (c < 0x7E) {
+        const double up = 0.5 * (v + double(e4m3_f32(c + 1))) * sc.six_t;
+        if (a > up || (a == up && (c & 1))) return c + 1;
+    }
+    if (c > 0) {
+        const double down = 0.5 * (v + double(e4m3_f32(c - 1))) * sc.six_t;
+        if (a < down || (a == down && (c & 1))) return c - 1;
+    }
+    return c;
 }
 
-// The e2m1 code of x at the group scale big = e4m3 * t: a magnitude is at
-// least a threshold times big, compared in 64 bits, where the product of the
-// 28-bit big and a 3-bit threshold is exact (as is the comparison with x, a
-// bf16), so ties are real ties and go to the even code.
-__device__ __forceinline__ uint32_t e2m1_code(float x, double big) {
-    const double a = fabs(double(x));
-    const uint32_t m = uint32_t(a > 0.25 * big) + uint32_t(a >= 0.75 * big) + uint32_t(a > 1.25 * big) +
-                       uint32_t(a >= 1.75 * big) + uint32_t(a > 2.5 * big) + uint32_t(a >= 3.5 * big) +
-                       uint32_t(a > 5.0 * big);
-    return m | (x < 0.0f && m ? 8u : 0u);
+// The least bf16 magnitude (as its bits) that is above bound * big, or equal
+// to it where STRICT is false.
+template <bool STRICT>
+__device__ __forceinline__ uint32_t least_above(double bound, double big) {
+    const double at = bound * big;
+    const float f = float(at);
+    const uint32_t u = f32_bits(f);
+    const double back = double(f);
+    return (u >> 16) + uint32_t((u & 0xffff) != 0 || (STRICT ? at >= back : at > back));
 }
 
 struct Rows {
@@ -49,73 +58,145 @@ struct Rows {
     int64_t pitch, head_pitch;
 };
 
-// One group of 16 of a row: its scale byte and its codes (code i in nibble i).
-__device__ __forceinline__ uint64_t quantise16(const uint16_t* row, float t, uint32_t* scale) {
-    float x[16];
-    const u32x4 lo = load16(row), hi = load16(row + 8);
-    uint16_t raw[16];
-    __builtin_memcpy(raw, &lo, 16);
-    __builtin_memcpy(raw + 8, &hi, 16);
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        x[i] = bf16_to_f32(raw[i]);
-        x[i] = x[i] != x[i] ? 0.0f : x[i];    // a NaN is stored as 0
-        amax = fmaxf(amax, fabsf(x[i]));
-    }
-    const uint32_t s = e4m3_code((double(amax) / 6.0) / double(t));
-    *scale = s;
-    const double big = double(e4m3_f32(s)) * double(t);
-    uint64_t codes = 0;
-    if (s != 0) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) codes |= uint64_t(e2m1_code(x[i], big)) << (4 * i);
-    }
-    return codes;
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t yes, uint32_t no) { return (mask & yes) | (~mask & no); }
+
+// -1 in each half where the magnitude there is at least the bound (bound less 1 is given).
+__device__ __forceinline__ uint32_t reaches(uint32_t mags, uint32_t bound_less_1) {
+    i16x2 m, b;
+    __builtin_memcpy(&m, &mags, 4);
+    __builtin_memcpy(&b, &bound_less_1, 4);
+    const i16x2 d = (b - m) >> 15;
+    uint32_t r;
+    __builtin_memcpy(&r, &d, 4);
+    asm("" : "+v"(r));   // a mask to the compiler too: it would go back to a comparison and a select a half
+    return r;
 }
 
+// One group of 16 of a row: its scale byte and its codes (code i in nibble i).
+// Two elements at a time in halves of a register: three halving steps among
+// the seven boundaries give a code's bits as masks, with no carries and no
+// branches (20 operations an element; comparing with all seven took 40, and the
+// kernel 67 us for 32,800 tokens of 8 heads of 128 against 50 us).
+__device__ __forceinline__ uint64_t quantise16(const u32x4 lo, const u32x4 hi, const Scale& sc, uint32_t* scale) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t mag[8];
+    u16x2 most = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        mag[i] = (i < 4 ? lo[i] : hi[i - 4]) & 0x7fff7fffu;
+        u16x2 m;
+        __builtin_memcpy(&m, &mag[i], 4);
+        most = __builtin_elementwise_max(most, m);
+    }
+    uint32_t top = max(uint32_t(most[0]), uint32_t(most[1]));
+    if (top > 0x7f80) {   // a NaN is stored as 0
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if ((mag[i] & 0xffff) > 0x7f80) mag[i] &= 0xffff0000u;
+            if (mag[i] > 0x7f80ffffu) mag[i] &= 0xffffu;
+            top = max(top, max(mag[i] & 0xffff, mag[i] >> 16));
+        }
+    }
+    const uint32_t s = e4m3_code(bits_f32(top << 16), sc);
+    *scale = s;
+    if (s == 0) return 0;
+    const double big = double(e4m3_f32(s)) * sc.t;
+    // boundaries between the magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6: a tie goes to the even code
+    uint32_t b[7] = {least_above<true>(0.25, big), least_above<false>(0.75, big), least_above<true>(1.25, big),
+                     least_above<false>(1.75, big), least_above<true>(2.5, big), least_above<false>(3.5, big),
+                     least_above<true>(5.0, big)};
+#pragma unroll
+    for (int j = 0; j < 7; ++j) b[j] = (b[j] - 1) * 0x10001u;   // at least 1, at most 0x7f80: signed halves hold all differences
+    uint32_t codes[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t m2 = reaches(mag[i], b[3]);
+        const uint32_t m1 = reaches(mag[i], pick(m2, b[5], b[1]));
+        const uint32_t m0 = reaches(mag[i], pick(m2, pick(m1, b[6], b[4]), pick(m1, b[2], b[0])));
+        uint32_t c = pick(0x00040004u, m2, pick(0x00020002u, m1, m0 & 0x00010001u));
+        // the sign, but for a zero
+        const uint32_t some = (m2 | m1 | m0) & 0x00080008u;
+        c |= ((i < 4 ? lo[i] : hi[i - 4]) >> 12) & some;
+        codes[i / 4] |= ((c | c >> 12) & 0xff) << (8 * (i % 4));
+    }
+    return uint64_t(codes[1]) << 32 | codes[0];
+}
+
+// A workgroup takes one page's new slots for one head, so that a whole page of
+// new rows is written in whole lines; the heads of a page lie next to each
+// other in the grid, as their rows do in memory.
 template <int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(256)
 kv_append_kernel(KvView v, Rows kr, Rows vr, float kt, float vt) {
-    constexpr int kGroups = D / 16;
-    __shared__ uint8_t vcode[8][D];
-    const int u = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-    const int s = unit_sequence(v, u);
+    constexpr int kGroups = D / 16, kItems = kPage * kGroups / 256;
+    __shared__ uint64_t vcode[kPage][kGroups];              // 16 codes each
+    __shared__ __attribute__((aligned(16))) uint8_t scales[8 * D];   // K's and V's, in the record's order
+    const int u = blockIdx.x / v.kv_heads, h = blockIdx.x % v.kv_heads, tid = threadIdx.x;
+    const int s = last_sequence(v, [&](int i) { return v.start(i) / kPage + 2 * i <= u; });
     if (s < 0) return;
     const int t0 = v.start(s), nq = v.start(s + 1) - t0;
     if (nq <= 0) return;
     const int n = v.len(s), first = n - nq;            // slot of the first new token, maybe negative
-    const int block = (first < 0 ? 0 : first / 8) + (u - (t0 / 8 + 2 * s));
-    const int slot0 = block * 8;
+    const int page = (first < 0 ? 0 : first / kPage) + (u - (t0 / kPage + 2 * s)), slot0 = page * kPage;
     if (slot0 >= n) return;
-    uint8_t* rec = v.record<D>(s, slot0 / kPage, h);
-    if (!rec) return;
-    const int in_page = slot0 % kPage;
-    const int lo = first > slot0 ? first - slot0 : 0;  // new slots of the block: [lo, hi)
-    const int hi = n - slot0 < 8 ? n - slot0 : 8;
+    const int id = v.page_id(s, page);
+    const int lo = first > slot0 ? first - slot0 : 0;  // new slots of the page: [lo, hi)
+    const int hi = n - slot0 < kPage ? n - slot0 : kPage;
+    const bool whole = lo == 0 && hi == kPage;
+    const Scale ksc = scale_of(kt), vsc = scale_of(vt);
 
-    const bool is_v = tid >= 8 * kGroups;
-    const int item = tid % (8 * kGroups);
-    const int i = item / kGroups, g = item % kGroups;  // slot in the block, group
-    if (i >= lo && i < hi) {
-        const int64_t token = t0 + (slot0 + i - first);
-        const Rows& r = is_v ? vr : kr;
-        uint32_t scale;
-        const uint64_t codes = quantise16(r.p + token * r.pitch + h * r.head_pitch + g * 16, is_v ? vt : kt, &scale);
-        if (is_v) {
+    u32x4 rows[kItems][4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) vcode[i][g * 16 + j] = uint8_t((codes >> (4 * j)) & 15);
-            rec[KvRecord<D>::v_scale(in_page / 8, g) + i] = uint8_t(scale);
+    for (int x = 0; x < kItems; ++x) {
+        const int i = (x * 256 + tid) / kGroups, g = (x * 256 + tid) % kGroups;   // slot, group
+        if (i < lo || i >= hi) continue;
+        const int64_t token = t0 + (slot0 + i - first);
+        const uint16_t* kp = kr.p + token * kr.pitch + h * kr.head_pitch + g * 16;
+        const uint16_t* vp = vr.p + token * vr.pitch + h * vr.head_pitch + g * 16;
+        rows[x][0] = load16_stream(kp), rows[x][1] = load16_stream(kp + 8);
+        rows[x][2] = load16_stream(vp), rows[x][3] = load16_stream(vp + 8);
+    }
+    uint8_t* rec = v.record_of<D>(id, h);   // the page's number came while the rows were on their way
+    if (!rec) return;
+#pragma unroll
+    for (int x = 0; x < kItems; ++x) {
+        const int i = (x * 256 + tid) / kGroups, g = (x * 256 + tid) % kGroups;
+        if (i < lo || i >= hi) continue;
+        uint32_t ks, vs;
+        *reinterpret_cast<uint64_t*>(rec + KvRecord<D>::k_code(i) + g * 8) = quantise16(rows[x][0], rows[x][1], ksc, &ks);
+        vcode[i][g] = quantise16(rows[x][2], rows[x][3], vsc, &vs);
+        const int k_at = KvRecord<D>::k_scale(i, g), v_at = KvRecord<D>::v_scale(i / 8, g) + i % 8;
+        if (whole) {
+            scales[k_at - KvRecord<D>::kKScales] = uint8_t(ks);
+            scales[v_at - KvRecord<D>::kKScales] = uint8_t(vs);
         } else {
-            *reinterpret_cast<uint64_t*>(rec + KvRecord<D>::k_code(in_page + i) + g * 8) = codes;
-            rec[KvRecord<D>::k_scale(in_page + i, g)] = uint8_t(scale);
+            rec[k_at] = uint8_t(ks);
+            rec[v_at] = uint8_t(vs);
         }
     }
     __syncthreads();
-    uint32_t* word = reinterpret_cast<uint32_t*>(rec + KvRecord<D>::v_code(in_page / 8, tid));
-    uint32_t w = lo == 0 && hi == 8 ? 0u : *word;
-    for (int j = lo; j < hi; ++j) w = (w & ~(15u << (4 * j))) | (uint32_t(vcode[j][tid]) << (4 * j));
-    *word = w;
+    if (whole && tid < D / 2)
+        *reinterpret_cast<u32x4*>(rec + KvRecord<D>::kKScales + 16 * tid) = *reinterpret_cast<const u32x4*>(scales + 16 * tid);
+    // V's dwords: 8 slots at a dim, the ones that are not new kept
+    for (int x = tid; x < 8 * D; x += 256) {
+        const int block = x / D, dim = x % D;
+        const int from = max(lo - 8 * block, 0), to = min(hi - 8 * block, 8);
+        if (from >= to) continue;
+        uint32_t* word = reinterpret_cast<uint32_t*>(rec + KvRecord<D>::v_code(block, dim));
+        uint32_t w = from == 0 && to == 8 ? 0u : *word;
+        const uint32_t* codes = reinterpret_cast<const uint32_t*>(&vcode[8 * block][dim / 16]) + (dim / 8 & 1);
+        const int shift = 4 * (dim % 8);
+        if (from == 0 && to == 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w |= (codes[2 * kGroups * j] >> shift & 15u) << (4 * j);
+        } else {
+            for (int j = from; j < to; ++j) w = (w & ~(15u << (4 * j))) | ((codes[2 * kGroups * j] >> shift & 15u) << (4 * j));
+        }
+        *word = w;
+    }
 }
 
 // bf16 of the fp32 product t * (e4m3 * e2m1), two codes of byte `sel`.
@@ -132,7 +213,7 @@ __global__ void __launch_bounds__(D)
 kv_read_kernel(KvView v, uint16_t* k_out, uint16_t* v_out, float kt, float vt) {
     constexpr int kGroups = D / 16;
     __shared__ uint16_t vval[8][D + 8];
-    const int u = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+    const int u = blockIdx.x / v.kv_heads, h = blockIdx.x % v.kv_heads, tid = threadIdx.x;
     const int s = unit_sequence(v, u);
     if (s < 0) return;
     const int t0 = v.start(s), nq = v.start(s + 1) - t0;
@@ -180,14 +261,16 @@ kv_read_kernel(KvView v, uint16_t* k_out, uint16_t* v_out, float kt, float vt) {
 }
 
 template <int D>
-int launch_append(const KvView& v, const Rows& k, const Rows& vr, float kt, float vt, unsigned units, hipStream_t st) {
-    hipLaunchKernelGGL(kv_append_kernel<D>, dim3(units, v.kv_heads), dim3(D), 0, st, v, k, vr, kt, vt);
+int launch_append(const KvView& v, const Rows& k, const Rows& vr, float kt, float vt, int64_t units, hipStream_t st) {
+    if (units * v.kv_heads > 0x7fffffff) return NVFP4_ERR_SHAPE;
+    hipLaunchKernelGGL(kv_append_kernel<D>, dim3(static_cast<unsigned>(units * v.kv_heads)), dim3(256), 0, st, v, k, vr, kt, vt);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
 template <int D>
-int launch_read(const KvView& v, uint16_t* k, uint16_t* vo, float kt, float vt, unsigned units, hipStream_t st) {
-    hipLaunchKernelGGL(kv_read_kernel<D>, dim3(units, v.kv_heads), dim3(D), 0, st, v, k, vo, kt, vt);
+int launch_read(const KvView& v, uint16_t* k, uint16_t* vo, float kt, float vt, int64_t units, hipStream_t st) {
+    if (units * v.kv_heads > 0x7fffffff) return NVFP4_ERR_SHAPE;
+    hipLaunchKernelGGL(kv_read_kernel<D>, dim3(static_cast<unsigned>(units * v.kv_heads)), dim3(D), 0, st, v, k, vo, kt, vt);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
@@ -206,7 +289,7 @@ extern "C" int nvfp4_kv_append(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seq
     const KvView view = kv_view(cache, seqs);
     const Rows kr{static_cast<const uint16_t*>(k), k_pitch, k_head_pitch};
     const Rows vr{static_cast<const uint16_t*>(v), v_pitch, v_head_pitch};
-    const unsigned units = static_cast<unsigned>(unit_count(seqs));
+    const int64_t units = seqs->total / kPage + 2 * seqs->seqs;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (cache->head_dim) {
         case 64: return launch_append<64>(view, kr, vr, cache->k_scale, cache->v_scale, units, s);
@@ -227,7 +310,7 @@ extern "C" int nvfp4_kv_read(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_
     const KvView view = kv_view(cache, seqs);
     uint16_t* ko = static_cast<uint16_t*>(k_out);
     uint16_t* vo = static_cast<uint16_t*>(v_out);
-    const unsigned units = static_cast<unsigned>(unit_count(seqs));
+    const int64_t units = unit_count(seqs);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (cache->head_dim) {
         case 64: return launch_read<64>(view, ko, vo, cache->k_scale, cache->v_scale, units, s);
