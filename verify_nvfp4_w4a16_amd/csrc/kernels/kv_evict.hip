@@ -3,8 +3,8 @@
 //
 // Weights: S[rows x slots] = Q K^T with K as the right operand, so a lane owns
 // one slot (a column) and adds the rows' exp(z - lse) in registers: sums over
-// rows run in row order with no atomics, and each page's K is read and decoded
-// once however many rows see it.
+// rows run in row order with no atomics.  The rows are staged in LDS, 64 or 128
+// at a time, and a page's K is read and decoded once for each such block.
 //
 // Eviction: per (sequence, kv head) the weight of the last slot that stays is
 // found by a radix selection over order-preserving keys (most significant
@@ -31,103 +31,185 @@ struct WeightArgs {
     int64_t max_kv;
 };
 
-// K of one 16-slot tile (h, t) as f16 operands: lane (n, b) holds slot
+// One page's K of a lane (n, b): of each 16-slot tile ht = (h, t) the slot
 // 32 h + 8 (n / 4) + 4 t + n % 4, dims b D/4 ..
-template <int D, int HT, int J>
-__device__ __forceinline__ void decode_tile(const uint32_t (&codes)[D / 32], const uint32_t (&ks)[D / 64], f16x8 (&out)[D / 32]) {
-    if constexpr (J < D / 64) {
-        constexpr int i = HT * (D / 64) + J;
-        const f16x2 s = scale_both<i % 4>(ks[i / 4]);
-        out[2 * J] = decode_row(codes[2 * J], s);
-        out[2 * J + 1] = decode_row(codes[2 * J + 1], s);
-        decode_tile<D, HT, J + 1>(codes, ks, out);
-    }
-}
-
-template <int D, int HT>
-__device__ __forceinline__ void load_tile(const uint8_t* rec, int n, int b, const uint32_t (&ks)[D / 64], f16x8 (&out)[D / 32]) {
-    uint32_t codes[D / 32];
-    const int slot = 32 * (HT >> 1) + (n >> 2) * 8 + (HT & 1) * 4 + (n & 3);
-    __builtin_memcpy(codes, __builtin_assume_aligned(rec + KvRecord<D>::k_code(slot) + b * (D / 8), D / 8), D / 8);
-    decode_tile<D, HT, 0>(codes, ks, out);
-}
-
-// One wavefront a page; all rows that see it pass by.
 template <int D>
-__global__ void __launch_bounds__(256)
+struct KRegs {
+    uint32_t codes[4][D / 32], scales[D / 64];
+
+    static __device__ __forceinline__ int slot(int ht, int n) { return 32 * (ht >> 1) + (n >> 2) * 8 + (ht & 1) * 4 + (n & 3); }
+    __device__ __forceinline__ void load(const uint8_t* rec, int n, int b) {
+#pragma unroll
+        for (int ht = 0; ht < 4; ++ht)
+            __builtin_memcpy(codes[ht], __builtin_assume_aligned(rec + KvRecord<D>::k_code(slot(ht, n)) + b * (D / 8), D / 8), D / 8);
+        __builtin_memcpy(scales, __builtin_assume_aligned(rec + KvRecord<D>::kKScales + (n * 4 + b) * (D / 16), D / 16), D / 16);
+    }
+    template <int HT, int J>
+    __device__ __forceinline__ void decode(f16x8 (&out)[D / 32]) const {
+        if constexpr (J < D / 64) {
+            constexpr int i = HT * (D / 64) + J;
+            const f16x2 s = scale_both<i % 4>(scales[i / 4]);
+            out[2 * J] = decode_row(codes[HT][2 * J], s);
+            out[2 * J + 1] = decode_row(codes[HT][2 * J + 1], s);
+            decode<HT, J + 1>(out);
+        }
+    }
+};
+
+// Query rows of a workgroup in LDS: f16, each row's 16-byte chunks permuted so
+// that the 16 rows of a matrix operand's read fall on different banks, and
+// what a row's scores need.
+template <int D, int ROWS>
+struct QueryBlock {
+    static constexpr int kRows = ROWS;
+
+    f16x8 q[kRows * D / 8];
+    float f[kRows], lse[kRows];   // the factor of its sums; lse * log2(e), +inf for a row that gives nothing
+    int lo[kRows], hi[kRows];
+
+    static __device__ __forceinline__ int chunk_at(int row, int chunk) {
+        return row * (D / 8) + (chunk ^ (D == 64 ? (row >> 1) & 7 : row & 15));
+    }
+    // Rows r0 .. of the sequence, by all 256 threads, D / 8 lanes a row: all
+    // loads first (rows past the last are loaded as the last).
+    __device__ __forceinline__ void fill(const WeightArgs& a, const QueryRows& rows, int hk, int r0) {
+        constexpr int kLanes = D / 8, kStep = 256 / kLanes, kTurns = kRows / kStep;
+        const int chunk = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+        const int many = (min(rows.count - r0, kRows) + 15) / 16 * 16;   // whole tiles
+        u32x4 raw[kTurns][1];
+        float l[kTurns];
+#pragma unroll
+        for (int x = 0; x < kTurns; ++x) {
+            const int r = min(r0 + x * kStep + row, rows.count - 1);
+            raw[x][0] = load16(query_at(a.sc, rows.row(a.sc, r), hk) + 8 * chunk);
+            l[x] = a.lse[rows.place(a.sc, r, hk)];
+        }
+#pragma unroll
+        for (int x = 0; x < kTurns; ++x) {
+            const int i = x * kStep + row;
+            if (i >= many) break;
+            f16x8 y[1];
+            const float factor = convert_query<1, 1, kLanes>(a.sc, raw[x], y);
+            q[chunk_at(i, chunk)] = y[0];
+            if (chunk == 0) {
+                const QueryRow me = rows.row(a.sc, r0 + i);
+                f[i] = factor;
+                lse[i] = l[x] == -INFINITY || r0 + i >= rows.count ? INFINITY : l[x] * kLog2e;
+                lo[i] = me.lo, hi[i] = me.hi;
+            }
+        }
+    }
+};
+
+// PAGES pages a wavefront; all rows that see them pass by, a block at a time.
+template <int D, int PAGES>
+__global__ void __launch_bounds__(256, D == 256 ? 1 : PAGES == 1 ? 3 : 2)
 kv_weights_kernel(WeightArgs a) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    using Block = QueryBlock<D, PAGES == 1 ? 32 : D == 256 ? 64 : 128>;
+    __shared__ Block block;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, b = lane >> 4;
     const int s = blockIdx.y, hk = blockIdx.x % a.v.kv_heads;
-    const int page = blockIdx.x / a.v.kv_heads * 4 + wave;
-    const int base = page * kPage;
-    if (base >= a.max_kv) return;
+    const int group0 = blockIdx.x / a.v.kv_heads * 4 * PAGES;     // the workgroup's first page
+    const int page0 = group0 + wave * PAGES;
+    const int64_t out = (int64_t(s) * a.v.kv_heads + hk) * a.max_kv;
+    if (group0 * kPage >= a.v.len(s)) {   // beyond the sequence: most workgroups where lengths differ much
+        for (int64_t j = int64_t(group0) * kPage + threadIdx.x; j < min(a.max_kv, int64_t(group0 + 4 * PAGES) * kPage); j += 256)
+            a.weights[out + j] = 0.0f;
+        return;
+    }
     const QueryRows rows(a.v, a.sc, s);
-    float sum[4] = {0, 0, 0, 0};
-    const uint8_t* rec = base < rows.len ? a.v.record<D>(s, page, hk) : nullptr;
-    if (rec && rows.count > 0) {
-        uint32_t ks[D / 64];
-        __builtin_memcpy(ks, __builtin_assume_aligned(rec + KvRecord<D>::kKScales + (n * 4 + b) * (D / 16), D / 16), D / 16);
-        f16x8 k[4][D / 32];
-        load_tile<D, 0>(rec, n, b, ks, k[0]);
-        load_tile<D, 1>(rec, n, b, ks, k[1]);
-        load_tile<D, 2>(rec, n, b, ks, k[2]);
-        load_tile<D, 3>(rec, n, b, ks, k[3]);
-        // rows that see any slot of this page
-        int i_lo = 0, i_hi = rows.new_tokens;
-        if (a.sc.causal) i_lo = max(0, base - (rows.len - rows.new_tokens));
-        if (a.sc.window > 0) i_hi = min(i_hi, max(0, base + kPage - 1 + a.sc.window - (rows.len - rows.new_tokens)));
-        const int r_hi = i_hi * rows.group;
-        for (int r0 = i_lo * rows.group; r0 < r_hi; r0 += 16) {
-            f16x8 q[D / 32];
-            const QueryRow me = rows.row(a.sc, r0 + n);
-            const float f_n = load_query<D / 32, 8, 16>(a.sc, query_at(a.sc, me, hk) + b * (D / 4), q);
-            const float lse_n = a.lse[rows.place(a.sc, min(r0 + n, rows.count - 1), hk)];
-            const bool live_n = r0 + n < r_hi && lse_n != -INFINITY;
-            const int lo_n = live_n ? me.lo : 0, hi_n = live_n ? me.hi : 0;
-            f32x4 z[4];
+
+    // rows that see any slot of the workgroup's pages
+    const int first = group0 * kPage, past = first + 4 * PAGES * kPage, shift = rows.len - rows.new_tokens;
+    int i_lo = 0, i_hi = first < rows.len && a.v.pages > 0 ? rows.new_tokens : 0;
+    if (a.sc.causal) i_lo = max(0, first - shift);
+    if (a.sc.window > 0) i_hi = min(i_hi, max(0, past - 1 + a.sc.window - shift));
+    const int r_lo = i_lo * rows.group, r_hi = i_hi * rows.group;
+
+    float sum[PAGES][4] = {};
+    int ids[PAGES];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                z[t] = f32x4{0, 0, 0, 0};
+    for (int x = 0; x < PAGES; ++x) {
+        const int page = page0 + x;
+        ids[x] = r_lo < r_hi && page * kPage < rows.len ? a.v.page_id(s, page) : -1;
+    }
+    KRegs<D> raw;
+    if (r_lo < r_hi) raw.load(a.v.record_or_first<D>(ids[0], hk), n, b);
+    for (int r0 = r_lo; r0 < r_hi; r0 += Block::kRows) {
+        if (r0 != r_lo) __syncthreads();
+        block.fill(a, rows, hk, r0);
+        __syncthreads();
+        const int tiles = (min(r_hi - r0, Block::kRows) + 15) / 16;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[i], k[t][i], z[t], 0, 0, 0);
-            }
+        for (int x = 0; x < PAGES; ++x) {
+            f16x8 k[4][D / 32];
+            raw.template decode<0, 0>(k[0]);
+            raw.template decode<1, 0>(k[1]);
+            raw.template decode<2, 0>(k[2]);
+            raw.template decode<3, 0>(k[3]);
+            raw.load(a.v.record_or_first<D>(ids[(x + 1) % PAGES], hk), n, b);   // also for the next block of rows
+            if (!a.v.has(ids[x])) continue;
+            const int base = (page0 + x) * kPage;
+            for (int t = 0; t < tiles; ++t) {
+                f32x4 z[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {   // row r0 + 4 b + c, held by lane 4 b + c
-                const float f = __shfl(f_n, 4 * b + c);
-                const float lse = __shfl(lse_n, 4 * b + c) * kLog2e;
-                const int lo = __shfl(lo_n, 4 * b + c), hi = __shfl(hi_n, 4 * b + c);
-                float x[4] = {z[0][c], z[1][c], z[2][c], z[3][c]};
-                a.sc.shape(x, f);
+                for (int ht = 0; ht < 4; ++ht) z[ht] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int slot = base + 32 * (t >> 1) + (n >> 2) * 8 + (t & 1) * 4 + (n & 3);
-                    const float p = __builtin_amdgcn_exp2f(x[t] - lse);
-                    sum[t] += slot >= lo && slot < hi ? p : 0.0f;
+                for (int i = 0; i < D / 32; ++i) {
+                    const f16x8 q = block.q[Block::chunk_at(16 * t + n, b * (D / 32) + i)];
+#pragma unroll
+                    for (int ht = 0; ht < 4; ++ht) z[ht] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q, k[ht][i], z[ht], 0, 0, 0);
+                }
+                const f32x4 f = *reinterpret_cast<const f32x4*>(block.f + 16 * t + 4 * b);
+                const f32x4 lse = *reinterpret_cast<const f32x4*>(block.lse + 16 * t + 4 * b);
+                // the tile's rows in order see ever later slots: its first and last say whether all see the page
+                if (base >= block.lo[16 * t + 15] && base + kPage <= block.hi[16 * t] && a.sc.cap == 0.0f) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int ht = 0; ht < 4; ++ht) sum[x][ht] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[ht][c], f[c], -lse[c]));
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int lo = block.lo[16 * t + 4 * b + c], hi = block.hi[16 * t + 4 * b + c];
+                    float y[4] = {z[0][c], z[1][c], z[2][c], z[3][c]};
+                    a.sc.shape(y, f[c]);
+#pragma unroll
+                    for (int ht = 0; ht < 4; ++ht) {
+                        const int slot = base + KRegs<D>::slot(ht, n);
+                        const float p = __builtin_amdgcn_exp2f(y[ht] - lse[c]);
+                        sum[x][ht] += slot >= lo && slot < hi ? p : 0.0f;
+                    }
                 }
             }
         }
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        sum[t] += __shfl_xor(sum[t], 16);
-        sum[t] += __shfl_xor(sum[t], 32);
-    }
-    if (b != 0) return;
+    for (int x = 0; x < PAGES; ++x) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int slot = base + 32 * (t >> 1) + (n >> 2) * 8 + (t & 1) * 4 + (n & 3);
-        if (slot >= a.max_kv) continue;
-        const int64_t at = (int64_t(s) * a.v.kv_heads + hk) * a.max_kv + slot;
-        a.weights[at] = slot < rows.len ? (a.prior ? a.prior[at] : 0.0f) + sum[t] : 0.0f;
+        for (int ht = 0; ht < 4; ++ht) {
+            float w = sum[x][ht];
+            w += __shfl_xor(w, 16);
+            w += __shfl_xor(w, 32);
+            const int slot = (page0 + x) * kPage + KRegs<D>::slot(ht, n);
+            if (b != ht || slot >= a.max_kv) continue;   // lanes of group b write tile b
+            a.weights[out + slot] = slot < rows.len ? (a.prior ? a.prior[out + slot] : 0.0f) + w : 0.0f;
+        }
     }
 }
 
 template <int D>
-int launch_weights(const WeightArgs& a, hipStream_t st) {
-    const int64_t blocks = (a.max_kv + 4 * kPage - 1) / (4 * kPage) * a.v.kv_heads;
+int launch_weights(const WeightArgs& a, int64_t rows, hipStream_t st) {
+    // One page a wavefront where few rows and pages leave nothing else to run
+    // beside, four where a page's rows are worth staging once for all of them.
+    const bool four = rows > 32 || a.max_kv / kPage * a.v.kv_heads * a.v.seqs > 32768;
+    const int64_t slots = 4 * kPage * (four ? 4 : 1);
+    const int64_t blocks = (a.max_kv + slots - 1) / slots * a.v.kv_heads;
     if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL(kv_weights_kernel<D>, dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((four ? kv_weights_kernel<D, 4> : kv_weights_kernel<D, 1>), dim3(static_cast<unsigned>(blocks), a.v.seqs),
+                       dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
@@ -400,9 +482,9 @@ extern "C" int nvfp4_kv_weights(const nvfp4_kv_cache_t* cache, const nvfp4_kv_se
     const WeightArgs a{kv_view(cache, seqs), kv_scores(cache, queries), lse, prior, weights, queries->max_kv};
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (cache->head_dim) {
-        case 64: return launch_weights<64>(a, s);
-        case 128: return launch_weights<128>(a, s);
-        default: return launch_weights<256>(a, s);
+        case 64: return launch_weights<64>(a, queries->max_q * a.sc.group, s);
+        case 128: return launch_weights<128>(a, queries->max_q * a.sc.group, s);
+        default: return launch_weights<256>(a, queries->max_q * a.sc.group, s);
     }
 }
 

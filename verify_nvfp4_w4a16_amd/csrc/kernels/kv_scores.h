@@ -107,23 +107,20 @@ struct QueryRows {
 // bf16 reaches further than f16, so the row is scaled by the power of two that
 // puts its largest magnitude into [2^14, 2^15): every element within 2^-28 of
 // it keeps all its bits.  The lanes that share the row (those whose numbers
-// differ in bits FIRST .. 32) agree on the power.  Returns the factor that turns
+// differ in the bits FIRST .. LAST / 2) agree on the power.  Returns the factor that turns
 // a sum of products into the score (times log2(e) where scores are not capped).
-template <int N, int STEP, int FIRST>
-__device__ __forceinline__ float load_query(const KvScores& sc, const uint16_t* p, f16x8 (&q)[N]) {
-    u32x4 raw[N];
+template <int N, int FIRST, int LAST>
+__device__ __forceinline__ float convert_query(const KvScores& sc, const u32x4 (&raw)[N], f16x8 (&q)[N]) {
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        raw[i] = load16(p + STEP * i);
+    for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             top = fmaxf(top, fabsf(bits_f32(raw[i][j] << 16)));
             top = fmaxf(top, fabsf(bits_f32(raw[i][j] & 0xffff0000u)));
         }
-    }
 #pragma unroll
-    for (int d = FIRST; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    for (int d = FIRST; d < LAST; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     // the power from the exponent field, held to what 2^14 / 2^e needs to stay finite
     const int e = min(max(int(f32_bits(top) >> 23) - 127, -100), 126);
     const float up = ldexpf(1.0f, 14 - e);
@@ -136,6 +133,14 @@ __device__ __forceinline__ float load_query(const KvScores& sc, const uint16_t* 
         }
     const float f = sc.scale * ldexpf(1.0f, e - 14);
     return sc.cap == 0.0f ? f * kLog2e : f;
+}
+
+template <int N, int STEP, int FIRST>
+__device__ __forceinline__ float load_query(const KvScores& sc, const uint16_t* p, f16x8 (&q)[N]) {
+    u32x4 raw[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) raw[i] = load16(p + STEP * i);
+    return convert_query<N, FIRST, 64>(sc, raw, q);
 }
 
 __device__ __forceinline__ const uint16_t* query_at(const KvScores& sc, const QueryRow& r, int hk) {
