@@ -239,20 +239,17 @@ struct RowShared {
 };
 
 // The lowest of the row's bins at which fewer than `most` tokens, or a mass
-// below `limit`, lie above.  Both fall towards higher bins, so a halving search
-// that every thread makes by itself finds it.  The caller knows that the rule
+// below `limit`, lie above.  Both fall towards higher bins, so every wavefront
+// finds it by itself in two looks of 64 lanes.  The caller knows that the rule
 // ends among the row's tokens, and then the bin has one.
 template <bool BY_MASS>
 __device__ __forceinline__ int row_bin(const RowShared& sh, uint64_t most, double limit) {
-    int lo = 0, hi = kBins - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (BY_MASS ? double(sh.above_m[mid]) < limit : sh.above_n[mid] < most)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    return lo;
+    const int lane = threadIdx.x & 63;
+    auto holds = [&](int bin) { return BY_MASS ? double(sh.above_m[bin]) < limit : sh.above_n[bin] < most; };
+    static_assert(kBins <= 8 * 64);
+    // bin 8 i + 7 of lane i: the first lane for which it holds has the bin among its eight
+    const int eight = 8 * (__ffsll(static_cast<unsigned long long>(__ballot(holds(min(8 * lane + 7, kBins - 1))))) - 1);
+    return min(eight + __ffsll(static_cast<unsigned long long>(__ballot(holds(min(eight + (lane & 7), kBins - 1))))) - 1, kBins - 1);
 }
 
 // Of `size` (at most kThreads) bins in sh.count and sh.mass the lowest with
@@ -374,13 +371,14 @@ struct Cut {
     uint32_t key, index;
 };
 
-// A list that gives each thread one token at most: every token is ranked
-// against the others of its bin, which settles all rules at once.
-template <bool F32>
+// A list of few tokens: each is ranked against the others of its bin, which
+// settles all rules at once.  WAVE: at most 64, one a lane, by every wavefront
+// for itself and without a barrier; else one a thread.
+template <bool F32, bool WAVE>
 __device__ Cut cut_short(RowShared& sh, const Cuts& c) {
-    const int tid = threadIdx.x, n = sh.listed;
-    const bool mine = tid < n && sh.list_key[tid] != kNoKey;
-    const uint32_t key = mine ? sh.list_key[tid] : 0, index = mine ? sh.list_index[tid] : 0;
+    const int at_list = threadIdx.x & (WAVE ? 63 : kThreads - 1), n = sh.listed;
+    const bool mine = at_list < n && sh.list_key[at_list] != kNoKey;
+    const uint32_t key = mine ? sh.list_key[at_list] : 0, index = mine ? sh.list_index[at_list] : 0;
     const int bin = key_bin(key);
     uint32_t rank = 0;
     uint64_t before = 0;   // the mass before it in its bin
@@ -392,9 +390,12 @@ __device__ Cut cut_short(RowShared& sh, const Cuts& c) {
     }
     uint64_t mass = sh.found[3];   // of the whole row
     if (c.by_count) {
-        uint64_t in_bin;
         const bool top_k = mine && bin == c.bin_k && sh.above_n[bin] + rank < c.k;
-        block_scan(top_k ? key_mass(key) : 0, sh.tmp, &in_bin);
+        uint64_t in_bin = top_k ? key_mass(key) : 0;
+        if constexpr (WAVE)
+            in_bin = wave_sum(in_bin);
+        else
+            block_scan(in_bin, sh.tmp, &in_bin);
         mass = sh.above_m[c.bin_k] + in_bin;
     }
     const double limit = double(c.p) * double(mass);
@@ -412,11 +413,13 @@ __device__ Cut cut_short(RowShared& sh, const Cuts& c) {
     uint64_t last = stays ? (uint64_t(key) << 32) | (0xffffffffu - index) : ~0ull;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) last = min(last, uint64_t(__shfl_xor(last, d)));
-    __syncthreads();
-    if ((tid & 63) == 0) sh.tmp[tid >> 6] = last;
-    __syncthreads();
+    if constexpr (!WAVE) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) sh.tmp[threadIdx.x >> 6] = last;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) last = min(last, sh.tmp[w]);
+        for (int w = 0; w < kRowWaves; ++w) last = min(last, sh.tmp[w]);
+    }
     if (last == ~0ull) return Cut{((uint32_t(at) + 1) << kBinShift) - 1, 0};   // none of that bin
     return Cut{uint32_t(last >> 32), 0xffffffffu - uint32_t(last) + 1};
 }
@@ -473,16 +476,36 @@ sample_draw_kernel(SampleArgs a) {
     const void* row = row_of(a, r, F32 ? 4 : 2);
     const uint64_t* bins = reinterpret_cast<const uint64_t*>(a.bins) + int64_t(r) * a.chunks * kBins;
 
-    // the row's bins, the highest at thread 0, and what lies above each
-    const int my_bin = kBins - 1 - tid;
-    uint64_t n = 0, m = 0;
-    if (my_bin >= 0) {
-#pragma unroll 8
-        for (int c = 0; c < a.chunks; ++c) {
-            const uint64_t x = bins[c * kBins + my_bin];
-            n += x >> kMassBits, m += x & (kOneToken - 1);
+    // Every wavefront takes one chunk's bins (and every sixteenth after it),
+    // kept in registers: the sums over chunks go through LDS.
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int kLaneBins = (kBins + 63) / 64;
+    uint64_t held[kLaneBins];
+    auto load_bins = [&](int c, uint64_t (&to)[kLaneBins]) {
+#pragma unroll
+        for (int i = 0; i < kLaneBins; ++i) to[i] = bins[c * kBins + min(lane + 64 * i, kBins - 1)];
+    };
+    load_bins(min(wave, a.chunks - 1), held);
+    auto each_chunk = [&](auto fn) {   // fn(chunk, its bins of this lane)
+        if (wave < a.chunks) fn(wave, held);
+        for (int c = wave + kRowWaves; c < a.chunks; c += kRowWaves) {
+            uint64_t more[kLaneBins];
+            load_bins(c, more);
+            fn(c, more);
         }
-    }
+    };
+    if (tid < kBins) sh.count[tid] = 0, sh.mass[tid] = 0;
+    if (tid == 0) sh.listed = 0;
+    __syncthreads();
+    each_chunk([&](int, const uint64_t (&x)[kLaneBins]) {
+#pragma unroll
+        for (int i = 0; i < kLaneBins; ++i) {
+            const int bin = lane + 64 * i;
+            if (bin >= kBins || x[i] == 0) continue;
+            atomicAdd(&sh.count[bin], uint32_t(x[i] >> kMassBits));
+            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[bin]), (unsigned long long)(x[i] & (kOneToken - 1)));
+        }
+    });
     const float top = row_max(a, r), inverse = row_inverse(a, r);
     if (top == -INFINITY) {
         if (tid == 0) {
@@ -496,10 +519,14 @@ sample_draw_kernel(SampleArgs a) {
     cuts.k = uint64_t(max(k, 0));
     cuts.p = a.top_p ? a.top_p[r] : 1.0f;
     cuts.low = a.min_p ? double(a.min_p[r]) * double(kSteps) : 0.0;
+    // the row's bins, the highest at thread 0, and what lies above each
+    __syncthreads();
+    const int my_bin = kBins - 1 - tid;
+    const uint64_t n = my_bin >= 0 ? sh.count[my_bin] : 0, m = my_bin >= 0 ? sh.mass[my_bin] : 0;
     uint64_t some, mass;
     const uint64_t above_n = block_scan(n, sh.tmp, &some), above_m = block_scan(m, sh.tmp, &mass);
     if (my_bin >= 0) sh.above_n[my_bin] = uint32_t(above_n), sh.above_m[my_bin] = above_m;
-    if (tid == 0) sh.found[3] = mass, sh.listed = 0;
+    if (tid == 0) sh.found[3] = mass;
     __syncthreads();
 
     // Which bins hold a cut: that of the top k, those that may hold the top
@@ -531,17 +558,21 @@ sample_draw_kernel(SampleArgs a) {
     Tokens<F32> tokens{row, a.vocab, top, inverse, true};
     if (any) {
         // Their tokens into the list, from the chunks that have any.
-        uint64_t many;
-        block_scan(my_bin >= 0 && cuts.wanted(my_bin) ? n : 0, sh.tmp, &many);
+        auto tokens_of = [&](int lo, int hi) {   // of a range of bins
+            if (hi < 0) return 0u;
+            return (lo > 0 ? sh.above_n[lo - 1] : uint32_t(some)) - sh.above_n[hi];
+        };
+        const uint64_t many = uint64_t(tokens_of(cuts.bin_k, cuts.bin_k)) + tokens_of(cuts.bin_p_lo, cuts.bin_p_hi) +
+                              tokens_of(cuts.bin_m, cuts.bin_m);   // or less, where they overlap
         tokens.in_list = many <= uint64_t(kListMax) && top < INFINITY;   // d of an infinite logit is none
         if (tokens.in_list) {
-            for (int c = tid >> 6; c < a.chunks; c += kRowWaves) {
-                uint64_t some_here = 0;
-#pragma unroll 8
-                for (int b = lane; b < kBins; b += 64) some_here |= cuts.wanted(b) ? bins[c * kBins + b] >> kMassBits : 0;
-                const bool has = __any(some_here != 0);
+            each_chunk([&](int c, const uint64_t (&x)[kLaneBins]) {
+                bool has = false;
+#pragma unroll
+                for (int i = 0; i < kLaneBins; ++i) has |= lane + 64 * i < kBins && x[i] != 0 && cuts.wanted(lane + 64 * i);
+                has = __any(has);
                 if (lane == 0) sh.chunk_has[c] = has;
-            }
+            });
             __syncthreads();
             // First by the exponent d alone, a little wider than the bins (log and
             // exp are off by far less than 1e-4): every token against the hull of
@@ -593,19 +624,24 @@ sample_draw_kernel(SampleArgs a) {
                 }
             __syncthreads();
         }
-        cut = tokens.in_list && sh.listed <= kShort ? cut_short<F32>(sh, cuts) : cut_long<F32>(sh, cuts, tokens);
+        cut = tokens.in_list && sh.listed <= 64       ? cut_short<F32, true>(sh, cuts)
+              : tokens.in_list && sh.listed <= kShort ? cut_short<F32, false>(sh, cuts)
+                                                      : cut_long<F32>(sh, cuts, tokens);
     }
 
     // The mass that stays, by chunks: whole bins above the cut's, and that bin's tokens.
     const int bin = any ? key_bin(cut.key) : -1;
     __syncthreads();
-    for (int c = tid >> 6; c < a.chunks; c += kRowWaves) {
+    each_chunk([&](int c, const uint64_t (&x)[kLaneBins]) {
         uint64_t sum = 0;
-#pragma unroll 8
-        for (int b = lane; b < kBins; b += 64) sum += b > bin ? bins[c * kBins + b] & (kOneToken - 1) : 0;
+#pragma unroll
+        for (int i = 0; i < kLaneBins; ++i) {
+            const int b = lane + 64 * i;
+            sum += b < kBins && b > bin ? x[i] & (kOneToken - 1) : 0;
+        }
         sum = wave_sum(sum);
         if (lane == 0) sh.chunk_mass[c] = sum;
-    }
+    });
     __syncthreads();
     if (any)
         tokens.each(sh, [&](uint32_t t, uint32_t i) {
@@ -642,7 +678,7 @@ sample_draw_kernel(SampleArgs a) {
     for (int j = 0; j < kPer; ++j) {
         if (target >= run && target < run + w[j]) {
             a.token[r] = begin + j;
-            if (a.logprob) a.logprob[r] = logf(float(double(w[j]) / double(total)));
+            if (a.logprob) a.logprob[r] = float(log(double(w[j]) / double(total)));
         }
         run += w[j];
     }
