@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "nvfp4_kv.h"
 #include "nvfp4_common.h"
@@ -382,7 +383,9 @@ __device__ Cut cut_short(RowShared& sh, const Cuts& c) {
     const int bin = key_bin(key);
     uint32_t rank = 0;
     uint64_t before = 0;   // the mass before it in its bin
-    for (int i = 0; i < n && __any(mine); ++i) {
+    const int others = __any(mine) ? n : 0;
+#pragma unroll 8
+    for (int i = 0; i < others; ++i) {
         const uint32_t k = sh.list_key[i], j = sh.list_index[i];
         const bool first = key_bin(k) == bin && (k > key || (k == key && j < index));
         rank += first;
@@ -575,45 +578,58 @@ sample_draw_kernel(SampleArgs a) {
             });
             __syncthreads();
             // First by the exponent d alone, a little wider than the bins (log and
-            // exp are off by far less than 1e-4): every token against the hull of
-            // the bins, which is two operations and two comparisons, and what
-            // passes against each range.  What is listed is few, and gets its
+            // exp are off by far less than 1e-4): its distance from the middle of
+            // each of the one to three ranges.  What passes is few, and gets its
             // exact weight afterwards.
             struct Range {
-                float lo, hi;
+                float middle, half;
             };
-            auto range = [](int lo, int hi) {
-                if (hi < 0) return Range{1.0f, -1.0f};
-                return Range{logf(key_weight(uint32_t(lo) << kBinShift) / kSteps) - 1e-4f,
-                             logf((key_weight(uint32_t(hi + 1) << kBinShift) + 1.0f) / kSteps) + 1e-4f};
+            Range r0{0.0f, -1.0f}, r1 = r0, r2 = r0;
+            int ranges = 0;
+            auto add_range = [&](int lo, int hi) {
+                const float from = logf(key_weight(uint32_t(lo) << kBinShift) / kSteps) - 1e-4f;
+                const float to = logf((key_weight(uint32_t(hi + 1) << kBinShift) + 1.0f) / kSteps) + 1e-4f;
+                r2 = r1, r1 = r0, r0 = Range{0.5f * (from + to), 0.5f * (to - from)};
+                ++ranges;
             };
-            const Range rk = range(cuts.bin_k, cuts.bin_k), rp = range(cuts.bin_p_lo, cuts.bin_p_hi),
-                        rm = range(cuts.bin_m, cuts.bin_m);
-            const Range hull{fminf(fminf(rk.lo, rp.lo), rm.lo), fmaxf(fmaxf(rk.hi, rp.hi), rm.hi)};
+            if (cuts.bin_p_hi >= 0) add_range(cuts.bin_p_lo, cuts.bin_p_hi);
+            if (cuts.bin_k >= 0 && (cuts.bin_k < cuts.bin_p_lo || cuts.bin_k > cuts.bin_p_hi)) add_range(cuts.bin_k, cuts.bin_k);
+            if (cuts.bin_m >= 0 && (cuts.bin_m < cuts.bin_p_lo || cuts.bin_m > cuts.bin_p_hi) && cuts.bin_m != cuts.bin_k)
+                add_range(cuts.bin_m, cuts.bin_m);
             const float scale = inverse == 0.0f ? 1e30f : inverse;   // T = 0: below the maximum is far below
             auto next_chunk = [&](int c) {
                 while (c < a.chunks && !sh.chunk_has[c]) ++c;
                 return c;
             };
-            int c = next_chunk(0);
-            Piece<F32, WIDE, kThreads> piece, ahead;
-            piece.load(row, min(c, a.chunks - 1) * kChunk, a.vocab);
-            while (c < a.chunks) {
-                const int next = next_chunk(c + 1);
-                ahead.load(row, min(next, a.chunks - 1) * kChunk, a.vocab);   // also past the end, so that no wait depends on a branch
+            auto gather = [&](auto count) {
+                constexpr int kRanges = decltype(count)::value;
+                int c = next_chunk(0);
+                Piece<F32, WIDE, kThreads> piece, ahead;
+                piece.load(row, min(c, a.chunks - 1) * kChunk, a.vocab);
+                while (c < a.chunks) {
+                    const int next = next_chunk(c + 1);
+                    ahead.load(row, min(next, a.chunks - 1) * kChunk, a.vocab);   // also past the end, so that no wait depends on a branch
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const float x = piece.raw(j), d = (x - top) * scale;   // NaN passes no comparison
-                    if (!((d >= hull.lo) & (d <= hull.hi))) continue;
-                    const int token = piece.token_at(c * kChunk, j);
-                    if (!((d >= rk.lo && d <= rk.hi) || (d >= rp.lo && d <= rp.hi) || (d >= rm.lo && d <= rm.hi)) || token >= a.vocab)
-                        continue;
-                    const int at = atomicAdd(&sh.listed, 1);   // the order of the list matters to nothing below
-                    if (at < kListMax) sh.list_key[at] = f32_bits(x), sh.list_index[at] = uint32_t(token);
+                    for (int j = 0; j < kPer; ++j) {
+                        const float x = piece.raw(j), d = (x - top) * scale;   // NaN is near nothing
+                        bool in = fabsf(d - r0.middle) <= r0.half;
+                        if constexpr (kRanges > 1) in |= fabsf(d - r1.middle) <= r1.half;
+                        if constexpr (kRanges > 2) in |= fabsf(d - r2.middle) <= r2.half;
+                        const int token = piece.token_at(c * kChunk, j);
+                        if (!in || token >= a.vocab) continue;
+                        const int at = atomicAdd(&sh.listed, 1);   // the order of the list matters to nothing below
+                        if (at < kListMax) sh.list_key[at] = f32_bits(x), sh.list_index[at] = uint32_t(token);
+                    }
+                    piece = ahead;
+                    c = next;
                 }
-                piece = ahead;
-                c = next;
-            }
+            };
+            if (ranges == 1)
+                gather(std::integral_constant<int, 1>{});
+            else if (ranges == 2)
+                gather(std::integral_constant<int, 2>{});
+            else
+                gather(std::integral_constant<int, 3>{});
             __syncthreads();
             tokens.in_list = sh.listed <= kListMax;
             if (tokens.in_list)
