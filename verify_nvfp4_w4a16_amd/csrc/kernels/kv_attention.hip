@@ -415,7 +415,8 @@ struct PageTiles {
         return (slot * (D / 8) + (chunk ^ (D == 64 ? (slot >> 1) & 7 : slot & 15))) * 16;
     }
     static __device__ __forceinline__ int v_at(int dim, int block) {
-        return kPage * D * 2 + (dim * 8 + (block ^ ((dim >> 1) & 7))) * 16;
+        // rows of 8 chunks: reads run along the dims, writes along every fourth (D = 128)
+        return kPage * D * 2 + (dim * 8 + (block ^ ((dim >> 1) & 7) ^ ((dim >> 4) & 1))) * 16;
     }
 };
 
@@ -474,6 +475,23 @@ struct PageShare {
 
 constexpr int kMaxSplits = 1024;
 
+// Order of N matrix instructions and the LDS reads of their operands: kAhead
+// reads ahead of the instruction that takes them.  Left alone the compiler reads
+// one ahead, and each instruction (32 cycles) waits most of a read's latency.
+constexpr int kAhead = 3;
+
+template <int N>
+__device__ __forceinline__ void reads_ahead() {
+    __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+    for (int i = 0; i < N - kAhead; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+}
+
+
 template <int D>
 __global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
 kv_attend_tile_kernel(AttendArgs a) {
@@ -499,7 +517,14 @@ kv_attend_tile_kernel(AttendArgs a) {
     const QueryRow me = rows.row(a.sc, my0 + n);
     const Span span = rows.span(a.sc, min(my0, rows.count - 1), min(my0 + 32, rows.count) - 1);
     f16x8 q[D / 16];   // step i: dims 16 i + 8 b ..
-    const float to_log2 = load_query<D / 16, 16, 32>(a.sc, query_at(a.sc, me, hk) + 8 * b, q);
+    float to_log2 = load_query<D / 16, 16, 32>(a.sc, query_at(a.sc, me, hk) + 8 * b, q);
+    if (to_log2 < 0.0f) {   // a negative scale goes into the query, so that the largest sum is the largest score
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) q[i] = -q[i];
+        to_log2 = -to_log2;
+    }
+    // scores are formed with the exponential's argument; capped ones are whole before
+    const float factor = a.sc.cap == 0.0f ? to_log2 : 1.0f;
 
     f32x16 o[D / 32];
 #pragma unroll
@@ -537,10 +562,11 @@ kv_attend_tile_kernel(AttendArgs a) {
                     z[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[i], z[h], 0, 0, 0);
                 }
             }
+            reads_ahead<kStep * D / 16>();
             float p[16 * kStep];   // [t][8 consecutive slots]: slot 32 half + 16 t + 8 b + j
 #pragma unroll
             for (int i = 0; i < 16 * kStep; ++i) p[i] = z[i >> 4][i & 15];
-            a.sc.shape(p, to_log2);
+            if (a.sc.cap != 0.0f) a.sc.shape(p, to_log2);
             if (base < span.lo_all || base + kPage > span.hi_all) {
 #pragma unroll
                 for (int i = 0; i < 16 * kStep; ++i) {
@@ -551,7 +577,7 @@ kv_attend_tile_kernel(AttendArgs a) {
             float top = p[0];
 #pragma unroll
             for (int i = 1; i < 16 * kStep; ++i) top = fmaxf(top, p[i]);
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = fmaxf(top, __shfl_xor(top, 32)) * factor;
             if (__any(top > m + kSlack)) {
                 const float grown = fmaxf(m, top);
                 const float keep = grown == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
@@ -564,7 +590,7 @@ kv_attend_tile_kernel(AttendArgs a) {
             f16x8 pt[2 * kStep];
 #pragma unroll
             for (int i = 0; i < 16 * kStep; ++i) {
-                const float e = __builtin_amdgcn_exp2f(p[i] - base_m);
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(p[i], factor, -base_m));
                 l += e;
                 pt[i >> 3][i & 7] = static_cast<_Float16>(e);
             }
@@ -575,6 +601,7 @@ kv_attend_tile_kernel(AttendArgs a) {
                     const f16x8 v = *reinterpret_cast<const f16x8*>(lds + PageTiles<D>::v_at(32 * i + n, 2 * (2 * half + t) + b));
                     o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, pt[t], o[i], 0, 0, 0);
                 }
+            reads_ahead<2 * kStep * (D / 32)>();
         }
     }
     l += __shfl_xor(l, 32);
