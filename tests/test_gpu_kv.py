@@ -98,6 +98,46 @@ def test_attention(lens, new, heads, group, d, kw):
     _check(c, qb, new, out, lse, **kw)
 
 
+# 33 to 64 rows a kv head, which one workgroup takes with the page's halves apart
+@pytest.mark.parametrize("lens,new,heads,group,d,kw", [
+    ([333, 64, 65, 1], [9, 2, 16, 1], 2, 4, 128, {}),
+    ([100, 31], [16, 11], 1, 4, 64, dict(window=40)),
+    ([200, 33, 0], [5, 7, 0], 1, 9, 256, dict(softcap=8.0)),
+    ([5000, 40], [16, 3], 1, 4, 128, {}),
+    ([3000, 40], [33, 3], 2, 1, 256, dict(causal=False, window=2000)),
+    ([20, 3], [33, 5], 1, 1, 64, {}),
+])
+def test_attention_of_a_verify_round(lens, new, heads, group, d, kw):
+    c = Paged(lens, heads, d, 300 + sum(lens))
+    qb = _query_bits(sum(new), heads * group, d, 17 + d)
+    out, lse = _attend(c, qb, new, **kw)
+    _check(c, qb, new, out, lse, **kw)
+    again = _attend(c, qb, new, **kw)
+    assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
+
+
+def test_attention_with_a_negative_scale():
+    for new, lens in (([1, 1], [200, 70]), ([40, 3], [200, 70])):
+        c = Paged(lens, 1, 128, 23)
+        qb = _query_bits(sum(new), 4, 128, 24)
+        out, lse = _attend(c, qb, new, scale=-0.2)
+        _check(c, qb, new, out, lse, scale=-0.2)
+
+
+def test_attention_of_many_sequences_of_very_different_lengths():
+    # enough workgroups' worth of bound that the pages are planned from the lengths; empty ones among them
+    g = workload.rng(31)
+    lens = [int(x) for x in np.exp(g.uniform(0, np.log(2500), 70))]
+    lens[3], lens[40], lens[-1] = 0, 12000, 1
+    new = [min(1, n) for n in lens]
+    c = Paged(lens, 4, 64, 32)
+    qb = _query_bits(sum(new), 8, 64, 33)
+    out, lse = _attend(c, qb, new)
+    _check(c, qb, new, out, lse)
+    again = _attend(c, qb, new)
+    assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
+
+
 @pytest.mark.parametrize("d,new,group", [(64, 1, 4), (128, 1, 4), (128, 40, 4), (256, 20, 2)])
 def test_attention_over_many_splits_repeats_its_bits(d, new, group):
     lens = [5000, 1, 2049]
@@ -365,6 +405,30 @@ def test_evict_into_another_cache_then_attend():
     c.lens, c.cache, c.table_t, c.lens_t = [128, 90], small, dst, new_lens
     out, lse = _attend(c, qb, [1, 1])
     _check(c, qb, [1, 1], out, lse)
+
+
+def test_evict_of_more_slots_than_registers_hold():
+    # 65536 slots' keys fit the selection's registers; longer sequences are read again for each step
+    g = workload.rng(72)
+    n, keep = 70000, 100
+    cache = nv.KvCache.empty(-(-n // PAGE) + 2, 1, 64, 1.0, 1.0)
+    table = int32(np.arange(-(-n // PAGE))[None])
+    w = _weights(g, (1, 1, n))
+    kept, kept_w, new_lens = nv.kv_evict(torch.from_numpy(w).to(DEV), cache, table, int32([n]), int32([[1094, 1095]]), keep,
+                                         sink=3, recent=10)
+    want = okv.evict(w[0, 0], n, keep, 3, 10)
+    assert np.array_equal(kept.cpu().numpy()[0, 0], want) and new_lens.tolist() == [keep]
+    assert np.array_equal(kept_w.cpu().numpy()[0, 0], w[0, 0, want])
+
+
+def test_sequences_beyond_the_host_s_bounds_are_held_to_them():
+    # nothing is read or written past what the launch was sized for
+    c = Paged([300, 40], 1, 64, 91)
+    q = bf16(_query_bits(41, 2, 64, 92))
+    out, lse = nv.kv_attention(q, c.cache, c.table_t, c.lens_t, starts([40, 1]), 8, 128)
+    w = nv.kv_weights(q, lse, c.cache, c.table_t, c.lens_t, starts([40, 1]), 8, 128)
+    torch.cuda.synchronize()
+    assert w.shape == (2, 1, 128)
 
 
 def test_no_sequences_and_no_tokens():

@@ -39,7 +39,7 @@ struct AttendArgs {
     float* lse;
     float* part_o;    // [splits][total * heads][D]: sums of exp2(z - m) v, without the V scale
     float* part_ml;   // [splits][total * heads][2]: m and the sum of exp2(z - m)
-    bool tile;        // 128-row workgroups
+    int tile;         // rows of a many-row workgroup, 0: few rows
     int splits;       // workgroups over the pages of a row tile, `chunk` pages each
     int chunk;
     int row_tiles;    // of the longest sequence
@@ -403,7 +403,8 @@ kv_attend_rows_kernel(AttendArgs a) {
 
 // ---- many query rows
 
-// A workgroup takes 128 rows, 32 a wavefront, and decodes each page once for
+// A workgroup takes 128 rows, 32 a wavefront (or 64 and the page's halves
+// apart, joined at the end, where there are no more), and decodes each page once for
 // all of them into LDS as f16: K [64 slots][D], V [D][64 slots], in 16-byte
 // chunks whose place within a row is permuted so that the lanes of a matrix
 // operand's read fall on different banks.
@@ -492,28 +493,31 @@ __device__ __forceinline__ void reads_ahead() {
 }
 
 
-template <int D>
+// HALVES 2: wavefronts 0 and 1 have the first 32 slots of each page, 2 and 3 the last.
+template <int D, int HALVES>
 __global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
 kv_attend_tile_kernel(AttendArgs a) {
     extern __shared__ char tiles[];   // two pages
-    constexpr int kStep = D == 256 ? 1 : 2;   // 32-slot tiles between rescalings: registers decide
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int kStep = D == 256 || HALVES == 2 ? 1 : 2;   // 32-slot tiles between rescalings: registers decide
+    constexpr int kRows = kTileRows / HALVES;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row_wave = wave % (kWaves / HALVES), my_half = wave / (kWaves / HALVES);   // my_half: HALVES 2 only
     const int n = lane & 31, b = lane >> 5;
     const int s = blockIdx.y, split = blockIdx.z;
     const int hk = blockIdx.x % a.v.kv_heads;
     const QueryRows rows(a.v, a.sc, s);
     // the last rows see most: they begin first
     const int tile = int(gridDim.x / a.v.kv_heads) - 1 - int(blockIdx.x / a.v.kv_heads);
-    const int row0 = tile * kTileRows;
+    const int row0 = tile * kRows;
     if (row0 >= rows.count) return;
 
-    const Span all = rows.span(a.sc, row0, min(row0 + kTileRows, rows.count) - 1);
+    const Span all = rows.span(a.sc, row0, min(row0 + kRows, rows.count) - 1);
     const int used = used_splits(a, all);
     if (split >= used) return;
     const int begin = pages_lo(all) + split * a.chunk;
     const int end = split + 1 < used ? begin + a.chunk : pages_hi(all);
 
-    const int my0 = row0 + wave * 32;
+    const int my0 = row0 + row_wave * 32;
     const QueryRow me = rows.row(a.sc, my0 + n);
     const Span span = rows.span(a.sc, min(my0, rows.count - 1), min(my0 + 32, rows.count) - 1);
     f16x8 q[D / 16];   // step i: dims 16 i + 8 b ..
@@ -551,7 +555,8 @@ kv_attend_tile_kernel(AttendArgs a) {
         if (!here || base >= span.hi || base + kPage <= span.lo) continue;
 
 #pragma unroll
-        for (int half = 0; half < 2; half += kStep) {   // kStep 32-slot tiles at a time
+        for (int turn = 0; turn < 2 / HALVES; turn += kStep) {   // kStep 32-slot tiles at a time
+            const int half = HALVES == 2 ? my_half : turn;
             f32x16 z[kStep];
 #pragma unroll
             for (int h = 0; h < kStep; ++h) {
@@ -606,11 +611,37 @@ kv_attend_tile_kernel(AttendArgs a) {
     }
     l += __shfl_xor(l, 32);
     if (l != l && m == -INFINITY) m = 0.0f;   // all scores NaN: the row stays NaN
+    if constexpr (HALVES == 2) {
+        // the second half's results through LDS to the first's wavefronts, lane by lane
+        constexpr int kParts = D / 32 * 16 + 2;
+        float* meet = reinterpret_cast<float*>(tiles) + row_wave * 64 * kParts + lane;
+        __syncthreads();
+        if (my_half == 1) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int c = 0; c < 16; ++c) meet[(16 * i + c) * 64] = o[i][c];
+            meet[(kParts - 2) * 64] = m;
+            meet[(kParts - 1) * 64] = l;
+        }
+        __syncthreads();
+        if (my_half == 0) {
+            const float other_m = meet[(kParts - 2) * 64], grown = fmaxf(m, other_m);
+            const float f0 = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - grown);
+            const float f1 = other_m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(other_m - grown);
+            l = l * f0 + meet[(kParts - 1) * 64] * f1;
+            m = grown;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int c = 0; c < 16; ++c) o[i][c] = o[i][c] * f0 + meet[(16 * i + c) * 64] * f1;
+        }
+    }
 
     const bool live = my0 + n < rows.count;
     const int64_t at = rows.place(a.sc, min(my0 + n, rows.count - 1), hk);
     if (used > 1) {
-        if (!live) return;
+        if (!live || (HALVES == 2 && my_half == 1)) return;
         const int64_t slice = int64_t(a.v.total) * a.sc.heads;
         float* po = a.part_o + (split * slice + at) * D;
         if (m > -INFINITY)
@@ -627,10 +658,10 @@ kv_attend_tile_kernel(AttendArgs a) {
     }
     // bf16 rows through LDS, then 16-byte stores along them
     const float f = l > 0.0f || l != l ? a.v_scale / l : 0.0f;
-    if (a.lse && live && b == 0) a.lse[at] = (m + log2f(l)) * kLn2;
+    if (a.lse && live && b == 0 && (HALVES == 1 || my_half == 0)) a.lse[at] = (m + log2f(l)) * kLn2;
     __syncthreads();
     constexpr int kRow = D * 2 + 16;   // bytes of a staged row
-    char* stage = tiles + wave * 32 * kRow;
+    char* stage = tiles + wave * 32 * kRow;   // the second half's wavefronts stage for nothing
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -643,6 +674,7 @@ kv_attend_tile_kernel(AttendArgs a) {
             *reinterpret_cast<u32x2*>(stage + n * kRow + (32 * i + 2 * c + 4 * b) * 2) = x;
         }
     __syncthreads();
+    if (HALVES == 2 && my_half == 1) return;
     for (int i = lane; i < 32 * (D / 8); i += 64) {
         const int r = i / (D / 8), part = i % (D / 8);
         if (my0 + r >= rows.count) break;
@@ -671,8 +703,8 @@ kv_join_kernel(AttendArgs a) {
     int used;
     int64_t first, step, last;
     if (a.tile) {
-        const int row0 = r / kTileRows * kTileRows;
-        used = used_splits(a, rows.span(a.sc, row0, min(row0 + kTileRows, rows.count) - 1));
+        const int row0 = r / a.tile * a.tile;
+        used = used_splits(a, rows.span(a.sc, row0, min(row0 + a.tile, rows.count) - 1));
         first = at, step = slice, last = at + (used - 1) * slice;
     } else {
         const int pages = segment_pages(a, rows), chunk = a.plan ? a.plan[0] : a.chunk;
@@ -731,7 +763,7 @@ kv_join_kernel(AttendArgs a) {
 // How a call is laid out: 16-row or 128-row workgroups, and over how many
 // workgroups each sequence's pages are split.
 struct Plan {
-    bool tile;
+    int tile;            // rows of a many-row workgroup, 0: few rows
     int64_t row_tiles;
     int splits, chunk;   // tile
     bool planned;        // else
@@ -742,8 +774,8 @@ struct Plan {
 Plan plan_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
     const int64_t rows = q->max_q * (q->heads / c->kv_heads);
     Plan p{};
-    p.tile = rows > 32;
-    const int64_t per_tile = p.tile ? kTileRows : kRowTile;
+    p.tile = rows <= 32 ? 0 : rows <= kTileRows / 2 ? kTileRows / 2 : kTileRows;
+    const int64_t per_tile = p.tile ? p.tile : kRowTile;
     p.row_tiles = (rows + per_tile - 1) / per_tile;
     const int64_t base = std::max<int64_t>(s->seqs * c->kv_heads * p.row_tiles, 1);
     int64_t slots = q->max_kv;
@@ -789,9 +821,11 @@ constexpr size_t tile_lds() {
 
 template <int D>
 bool allow_lds() {
+    static_assert(tile_lds<D>() >= 2 * 64 * (D / 2 + 2) * sizeof(float));
     static_assert(tile_lds<D>() >= kTileRows * (D * 2 + 16) && tile_lds<D>() <= kMaxLdsBytes);
     for (const void* fn : {reinterpret_cast<const void*>(kv_attend_rows_kernel<D>),
-                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D>)})
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 1>),
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 2>)})
         if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLdsBytes) != hipSuccess) return false;
     return true;
 }
@@ -802,8 +836,8 @@ int launch_attend(const AttendArgs& a, const Plan& plan, hipStream_t st) {
         // parts of a tile's pages along the slowest axis: those that short sequences do not need come last
         const int64_t blocks = plan.row_tiles * a.v.kv_heads;
         if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-        hipLaunchKernelGGL(kv_attend_tile_kernel<D>, dim3(static_cast<unsigned>(blocks), a.v.seqs, plan.splits),
-                           dim3(64 * kWaves), tile_lds<D>(), st, a);
+        hipLaunchKernelGGL((plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1> : kv_attend_tile_kernel<D, 2>),
+                           dim3(static_cast<unsigned>(blocks), a.v.seqs, plan.splits), dim3(64 * kWaves), tile_lds<D>(), st, a);
     } else {
         if (plan.planned) {
             hipLaunchKernelGGL(kv_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
