@@ -251,45 +251,65 @@ __device__ __forceinline__ uint32_t scan32(uint32_t x) {
     return x;
 }
 
-// The weights of one (sequence, head): wavefront w has the slots
-// [w, w + 1) * span, 64 neighbours at a time.  HELD > 0: their keys stay in
-// HELD registers a lane; 0: they are read again each time.
-template <int HELD>
+// The keys of one (sequence, head): wavefront w has the slots
+// [w, w + 1) * span, 64 neighbours at a time.  A slot outside the choice
+// [lo, hi) has key 0, below every weight's.  HELD > 0: the keys stay in HELD
+// registers a lane and SHARED places of LDS; 0: the weights are read again each
+// time.
+template <int HELD, int SHARED>
 struct Keys {
     const float* w;
-    int begin, end;   // of this wavefront
+    uint32_t* shared;
+    int lo, hi, begin, end;   // begin, end: of this wavefront
     uint32_t held[HELD > 0 ? HELD : 1];
 
-    __device__ __forceinline__ Keys(const float* weights, int n) : w(weights) {
-        const int span = HELD > 0 ? HELD * 64 : (n + kSelect - 1) / kSelect * 64;
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __device__ __forceinline__ Keys(const float* weights, uint32_t* lds, int n, int first, int past)
+        : w(weights), shared(lds), lo(first), hi(past) {
+        const int span = (n + kSelect - 1) / kSelect * 64;   // at most (HELD + SHARED) * 64, by the choice of HELD
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
         begin = min(wave * span, n), end = min(begin + span, n);
         if constexpr (HELD > 0) {
-            const int last = max(n - 1, 0);
 #pragma unroll
-            for (int i = 0; i < HELD; ++i) held[i] = n > 0 ? f32_bits(w[min(begin + i * 64 + int(threadIdx.x & 63), last)]) : 0;
+            for (int i = 0; i < SHARED; ++i) {
+                const int j = begin + (HELD + i) * 64 + lane;
+                const float x = w[min(j, n - 1)];
+                shared[i * kSelect + threadIdx.x] = j >= lo && j < hi ? order_key(x) : 0;
+            }
 #pragma unroll
-            for (int i = 0; i < HELD; ++i) held[i] = order_key(bits_f32(held[i]));
+            for (int i = 0; i < HELD; ++i) held[i] = f32_bits(w[min(begin + i * 64 + lane, n - 1)]);
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) {
+                const int j = begin + i * 64 + lane;
+                held[i] = j >= lo && j < hi ? order_key(bits_f32(held[i])) : 0;
+            }
         }
     }
-    // fn(slot, key, there) for every 64 slots of the wavefront, all lanes together
+    // fn(slot, key) for every 64 slots of the wavefront, all lanes together
     template <class Fn>
     __device__ __forceinline__ void each(Fn fn) const {
         const int lane = threadIdx.x & 63;
         if constexpr (HELD > 0) {
+            int last = end;
+            asm volatile("" : "+s"(last));   // compared anew: kept from one walk to the next, the results would fill the registers
 #pragma unroll
             for (int i = 0; i < HELD; ++i)
-                if (begin + i * 64 < end) fn(begin + i * 64 + lane, held[i], begin + i * 64 + lane < end);
+                if (begin + i * 64 < last) fn(begin + i * 64 + lane, held[i]);
+            for (int i = 0; i < SHARED && begin + (HELD + i) * 64 < last; ++i)
+                fn(begin + (HELD + i) * 64 + lane, shared[i * kSelect + threadIdx.x]);
         } else {
-            for (int j = begin; j < end; j += 64) fn(j + lane, j + lane < end ? order_key(w[j + lane]) : 0, j + lane < end);
+            for (int j0 = begin; j0 < end; j0 += 64) {
+                const int j = j0 + lane;
+                fn(j, j >= lo && j < hi ? order_key(w[j]) : 0);
+            }
         }
     }
 };
 
 // Which slots stay: one workgroup a (sequence, head).
-template <int HELD>
+template <int HELD, int SHARED>
 __global__ void __launch_bounds__(kSelect)
 kv_select_kernel(EvictArgs a) {
+    __shared__ uint32_t more[SHARED > 0 ? SHARED * kSelect : 1];
     __shared__ uint32_t bins[kSelectBins];
     __shared__ uint32_t tmp[kSelectWaves][2];
     __shared__ uint32_t found[2];
@@ -301,86 +321,80 @@ kv_select_kernel(EvictArgs a) {
     int32_t* kept = a.kept + seq_head * a.keep;
     float* kept_w = a.kept_weights + seq_head * a.keep;
     if (h == 0 && tid == 0) a.new_lens[s] = min(n, a.keep);
-    for (int i = min(n, a.keep) + tid; i < a.keep; i += kSelect) {
-        kept[i] = -1;
-        kept_w[i] = 0.0f;
+    // slots that stay whatever they weigh: all, or the first and the last ones
+    const bool all = n <= a.keep;
+    const int lo = all ? n : a.sink, hi = all ? n : n - a.recent;   // the choice is among [lo, hi)
+    const int wanted = all ? 0 : a.keep - a.sink - a.recent;
+    for (int i = tid; i < a.keep; i += kSelect) {
+        if (i >= lo && i < lo + wanted) continue;
+        const int j = i < lo ? i : i - lo - wanted + hi;
+        kept[i] = j < n ? j : -1;
+        kept_w[i] = j < n ? w[j] : 0.0f;
     }
-    if (n <= a.keep) {
-        for (int i = tid; i < n; i += kSelect) {
-            kept[i] = i;
-            kept_w[i] = w[i];
-        }
-        return;
-    }
-    const Keys<HELD> keys(w, n);
-    const int lo = a.sink, hi = n - a.recent;   // the choice is among [lo, hi)
-    const int wanted = a.keep - a.sink - a.recent;
-    uint32_t need = uint32_t(wanted), key = 0xffffffffu;
-    if (wanted > 0) {
-        // the key of the last slot that is chosen, 11, 11 and 10 bits at a time
-        uint32_t mask = 0;
-        key = 0;
-        for (int level = 0; level < 3; ++level) {
-            const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-            const uint32_t digits = level < 2 ? 2047 : 1023;
-            bins[tid] = bins[tid + kSelect] = 0;
-            __syncthreads();
-            keys.each([&](int j, uint32_t k, bool there) {
-                const bool in = there && j >= lo && j < hi && (k & mask) == key;
-                const uint64_t all = __ballot(in);
-                if (!all) return;
-                // equal digits of a wavefront (the many zeros of a fresh cache) are added at once
-                const uint32_t d = (k >> shift) & digits;
-                const int first = __ffsll(static_cast<unsigned long long>(all)) - 1;
-                const uint32_t common = uint32_t(__builtin_amdgcn_readlane(int(d), first));
-                const uint64_t same = __ballot(in && d == common);
-                if (lane == first) atomicAdd(&bins[common], uint32_t(__popcll(same)));
-                if (in && d != common) atomicAdd(&bins[d], 1u);
-            });
-            __syncthreads();
-            // thread t has bins 2 (1023 - t) + 1 and 2 (1023 - t): the highest first
-            const int at = 2 * (kSelect - 1 - tid);
-            const uint32_t high = bins[at + 1], low = bins[at];
-            const uint32_t sum = scan32(high + low);
-            if (lane == 63) tmp[wave][0] = sum;
-            __syncthreads();
-            uint32_t before = sum - high - low;
-            for (int i = 0; i < wave; ++i) before += tmp[i][0];
-            if (before < need && before + high >= need)
-                found[0] = uint32_t(at + 1), found[1] = need - before;
-            else if (before + high < need && before + high + low >= need)
-                found[0] = uint32_t(at), found[1] = need - before - high;
-            __syncthreads();
-            key |= found[0] << shift;
-            mask |= digits << shift;
-            need = found[1];   // still wanted among the keys with these leading bits
-        }
+    if (wanted == 0) return;
+    const Keys<HELD, SHARED> keys(w, more, n, lo, hi);
+    // the key of the last slot that is chosen, 11, 11 and 10 bits at a time
+    uint32_t need = uint32_t(wanted), mask = 0, key = 0;
+#pragma unroll 1
+    for (int level = 0; level < 3; ++level) {
+        const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
+        const uint32_t digits = level < 2 ? 2047 : 1023;
+        bins[tid] = bins[tid + kSelect] = 0;
+        __syncthreads();
+        keys.each([&](int, uint32_t k) {
+            const bool in = (k & mask) == key;
+            const uint64_t lanes = __ballot(in);
+            if (!lanes) return;
+            // equal digits of a wavefront (the many zeros of a fresh cache) are added at once
+            const uint32_t d = (k >> shift) & digits;
+            const int first = __ffsll(static_cast<unsigned long long>(lanes)) - 1;
+            const uint32_t common = uint32_t(__builtin_amdgcn_readlane(int(d), first));
+            const uint64_t same = __ballot(in && d == common);
+            if (in && (d != common || lane == first)) atomicAdd(&bins[d], d == common ? uint32_t(__popcll(same)) : 1u);
+        });
+        __syncthreads();
+        // thread t has bins 2 (1023 - t) + 1 and 2 (1023 - t): the highest first
+        const int at = 2 * (kSelect - 1 - tid);
+        const uint32_t high = bins[at + 1], low = bins[at];
+        const uint32_t sum = scan32(high + low);
+        if (lane == 63) tmp[wave][0] = sum;
+        __syncthreads();
+        uint32_t before = sum - high - low;
+        for (int i = 0; i < wave; ++i) before += tmp[i][0];
+        if (before < need && before + high >= need)
+            found[0] = uint32_t(at + 1), found[1] = need - before;
+        else if (before + high < need && before + high + low >= need)
+            found[0] = uint32_t(at), found[1] = need - before - high;
+        __syncthreads();
+        key |= found[0] << shift;
+        mask |= digits << shift;
+        need = found[1];   // still wanted among the keys with these leading bits
     }
     // `need` of the slots at the key stay, the lowest first.  Wavefronts count
     // theirs, then number them from where those before them end.
-    auto sure = [&](int j, uint32_t k, bool there) { return there && (j < lo || j >= hi || (wanted > 0 && k > key)); };
-    auto tie = [&](int j, uint32_t k, bool there) { return there && j >= lo && j < hi && wanted > 0 && k == key; };
     uint32_t mine = 0, ties = 0;
-    keys.each([&](int j, uint32_t k, bool there) {
-        mine += uint32_t(__popcll(__ballot(sure(j, k, there))));
-        ties += uint32_t(__popcll(__ballot(tie(j, k, there))));
+    keys.each([&](int, uint32_t k) {
+        mine += uint32_t(k > key);
+        ties += uint32_t(k == key);
     });
+    mine = scan32(mine), ties = scan32(ties);
+    if (lane == 63) tmp[wave][0] = mine, tmp[wave][1] = ties;
     __syncthreads();
-    if (lane == 0) tmp[wave][0] = mine, tmp[wave][1] = ties;
-    __syncthreads();
-    uint32_t at = 0, seen = 0;   // sure slots and ties before
-    for (int i = 0; i < wave; ++i) at += tmp[i][0], seen += tmp[i][1];
+    uint32_t above = 0, seen = 0;   // chosen slots and ties before
+    for (int i = 0; i < wave; ++i) above += tmp[i][0], seen += tmp[i][1];
     const uint64_t below = (1ull << lane) - 1;
-    keys.each([&](int j, uint32_t k, bool there) {
-        const bool is_sure = sure(j, k, there), is_tie = tie(j, k, there);
-        const uint64_t sures = __ballot(is_sure), equal = __ballot(is_tie);
+    key = uint32_t(__builtin_amdgcn_readfirstlane(int(key)));
+    asm("" : "+s"(key));   // compared anew: kept from the count, the comparisons' results would fill the registers
+    keys.each([&](int j, uint32_t k) {
+        const uint64_t high = __ballot(k > key), equal = __ballot(k == key);
+        if (!(high | equal)) return;
         const uint32_t rank = seen + uint32_t(__popcll(equal & below));
-        if (is_sure || (is_tie && rank < need)) {
-            const uint32_t to = at + uint32_t(__popcll(sures & below)) + min(rank, need);
+        if (k > key || (k == key && rank < need)) {
+            const uint32_t to = uint32_t(lo) + above + uint32_t(__popcll(high & below)) + min(rank, need);
             kept[to] = j;
             kept_w[to] = w[j];
         }
-        at += uint32_t(__popcll(sures));
+        above += uint32_t(__popcll(high));
         seen += uint32_t(__popcll(equal));
     });
 }
@@ -509,12 +523,14 @@ extern "C" int nvfp4_kv_evict(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs
     const EvictArgs a{kv_view(cache, seqs), weights, weights_pitch, static_cast<int>(keep), static_cast<int>(sink),
                       static_cast<int>(recent), dst->data, dst->pages, dst_table, dst_pitch, kept, kept_weights, new_lens};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    // keys in registers up to 65536 slots a sequence (64 a lane, read once); longer ones are read five times
+    // Keys held up to 65536 slots a sequence (56 in registers and 8 in LDS a lane, which is what a
+    // 1024-thread workgroup's registers take) and read once; of longer sequences they are read five
+    // times (8 sequences of up to 65000 slots, 8 heads: 102 us instead of 51).
     const int64_t longest = std::min(weights_pitch, seqs->table_pitch * kPage);
-    const auto select = longest <= 4 * kSelect    ? kv_select_kernel<4>
-                        : longest <= 16 * kSelect ? kv_select_kernel<16>
-                        : longest <= 64 * kSelect ? kv_select_kernel<64>
-                                                  : kv_select_kernel<0>;
+    const auto select = longest <= 4 * kSelect    ? kv_select_kernel<4, 0>
+                        : longest <= 16 * kSelect ? kv_select_kernel<16, 0>
+                        : longest <= 64 * kSelect ? kv_select_kernel<56, 8>
+                                                  : kv_select_kernel<0, 0>;
     hipLaunchKernelGGL(select, dim3(cache->kv_heads, static_cast<unsigned>(seqs->seqs)), dim3(kSelect), 0, s, a);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     switch (cache->head_dim) {
