@@ -39,6 +39,7 @@ constexpr unsigned long long kOneToken = 1ull << kMassBits;
 constexpr int kListMax = 8192;
 constexpr int kShort = 256;                  // list length up to which every token is ranked against all
 constexpr uint32_t kNoKey = 0xffffffffu;
+constexpr uint32_t kNegInf = 0xff800000u, kNegInf2 = 0xff80ff80u;   // -inf in fp32, twice in bf16
 constexpr int kMaxThreads = 256;             // launch 1: pieces of 4096
 
 struct SampleArgs {
@@ -68,11 +69,10 @@ __device__ __forceinline__ float logit(const void* row, int i) {
     return x != x ? -INFINITY : x;
 }
 
-// inverse is 1 / T, or 0 for the maximum alone.
+// inverse is 1 / T, or +inf for the maximum alone: what is less is then at -inf.  0 or NaN for x NaN.
 __device__ __forceinline__ float weight(float x, float top, float inverse) {
-    if (x == top) return kSteps;
-    if (inverse == 0.0f) return 0.0f;
-    return floorf(expf((x - top) * inverse) * kSteps);
+    const float w = floorf(expf((x - top) * inverse) * kSteps);
+    return x == top ? kSteps : w;
 }
 
 __device__ __forceinline__ uint32_t weight_key(float w) { return f32_bits(w) - kOneBits; }   // w >= 1
@@ -89,8 +89,8 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int r, int si
 
 // The thread's kPer logits of the THREADS * kPer from `begin` on, 16 bytes at a
 // time where rows are aligned for it and whole (WIDE).  load() only loads, from
-// places held to the row so that it never branches; at() gives element e, token
-// token_at(e), with NaN and what lies beyond the vocabulary as -inf.
+// places held to the row so that it never branches; clip() makes -inf of what lies
+// beyond the vocabulary; raw() gives element e, token token_at(e).
 template <bool F32, bool WIDE, int THREADS>
 struct Piece {
     static constexpr int kVec = WIDE ? (F32 ? 4 : 8) : 1;
@@ -119,9 +119,17 @@ struct Piece {
             return one[e];
         }
     }
-    __device__ __forceinline__ float at(int begin, int vocab, int e) const {
-        const float x = raw(e);
-        return x == x && token_at(begin, e) < vocab ? x : -INFINITY;
+    __device__ __forceinline__ void clip(int begin, int vocab) {
+        if (token_at(begin, kPer - 1) < vocab) return;   // this thread's last
+#pragma unroll
+        for (int e = 0; e < kPer; e += kVec) {
+            if (token_at(begin, e) < vocab) continue;   // 16 bytes are inside or outside whole
+            if constexpr (WIDE)
+                wide[e / kVec] = F32 ? u32x4{kNegInf, kNegInf, kNegInf, kNegInf}
+                                     : u32x4{kNegInf2, kNegInf2, kNegInf2, kNegInf2};
+            else
+                one[e] = -INFINITY;
+        }
     }
 };
 
@@ -132,10 +140,10 @@ sample_max_kernel(SampleArgs a) {
     const int r = blockIdx.y, c = blockIdx.x;
     Piece<F32, WIDE, kMaxThreads> p;
     const int begin = c * kMaxThreads * kPer;
-    p.load(row_of(a, r, F32 ? 4 : 2), begin, a.vocab);
+    p.load(row_of(a, r, F32 ? 4 : 2), begin, a.vocab);   // (the last tokens again where there are none)
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) top = fmaxf(top, p.at(begin, a.vocab, j));
+    for (int j = 0; j < kPer; ++j) top = fmaxf(top, p.raw(j));   // passes NaN over
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = top;
@@ -156,8 +164,25 @@ __device__ __forceinline__ float row_max(const SampleArgs& a, int r) {
 
 __device__ __forceinline__ float row_inverse(const SampleArgs& a, int r) {
     const float t = a.temperature ? a.temperature[r] : 1.0f;
-    return t > 0.0f ? 1.0f / t : 0.0f;
+    return t > 0.0f ? 1.0f / t : INFINITY;
 }
+
+// Bounds of the logits whose weight is at least, or at most, w.  Wide by 1e-4 of
+// the weight, which is far more than log and exp are off, and by 4 roundings of
+// the bound itself.
+__device__ __forceinline__ float logit_below(float w, float top, float inverse) {
+    const float x = top + (logf(w / kSteps) - 1e-4f) / inverse;
+    return x - fabsf(x) * 0x1p-21f;
+}
+__device__ __forceinline__ float logit_above(float w, float top, float inverse) {
+    const float x = top + (logf(w / kSteps) + 1e-4f) / inverse;
+    return x + fabsf(x) * 0x1p-21f;
+}
+
+struct Range {
+    float lo, hi;
+    __device__ __forceinline__ bool has(float x) const { return __builtin_amdgcn_fmed3f(x, lo, hi) == x; }   // not NaN
+};
 
 // ---- launch 2: each chunk's tokens and mass by bins of the weight
 
@@ -171,9 +196,10 @@ sample_bins_kernel(SampleArgs a) {
     const float top = row_max(a, r), inverse = row_inverse(a, r);
     if (tid < kBins) bins[tid] = 0;
     __syncthreads();
+    p.clip(c * kChunk, a.vocab);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const float w = weight(p.at(c * kChunk, a.vocab, j), top, inverse);
+        const float w = weight(p.raw(j), top, inverse);
         if (w >= 1.0f) atomicAdd(&bins[key_bin(weight_key(w))], kOneToken | (unsigned long long)uint32_t(w));
     }
     __syncthreads();
@@ -225,6 +251,10 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* tmp, uint64
     return before + sum - x;
 }
 
+struct Listed {
+    uint32_t key, index;   // kNoKey: not one of the bins' after all
+};
+
 struct RowShared {
     uint32_t count[kThreads];        // a selection step's bins
     uint64_t mass[kThreads];
@@ -233,8 +263,7 @@ struct RowShared {
     uint64_t tmp[kRowWaves];
     uint64_t found[4];
     uint64_t chunk_mass[kMaxChunks];
-    uint32_t list_key[kListMax];     // kNoKey: not one of the bins' after all
-    uint32_t list_index[kListMax];
+    Listed list[kListMax];
     int listed;
     int chunk_has[kMaxChunks];       // tokens of those bins
 };
@@ -289,7 +318,7 @@ struct Tokens {
     template <class Fn>
     __device__ __forceinline__ void each(const RowShared& sh, Fn fn) const {
         if (in_list) {
-            for (int i = threadIdx.x; i < sh.listed; i += kThreads) fn(sh.list_key[i], sh.list_index[i]);
+            for (int i = threadIdx.x; i < sh.listed; i += kThreads) fn(sh.list[i].key, sh.list[i].index);
         } else {
             for (int i = threadIdx.x; i < vocab; i += kThreads) {
                 const float w = weight(logit<F32>(row, i), top, inverse);
@@ -312,10 +341,20 @@ __device__ uint32_t find_key(RowShared& sh, const Tokens<F32>& tokens, int bin, 
         tokens.each(sh, [&](uint32_t k, uint32_t) {
             if ((k & mask) != key) return;
             const int d = (k >> down) & (size - 1);
-            atomicAdd(&sh.count[d], 1u);
-            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[d]), (unsigned long long)key_mass(k));
+            // Small weights are few integers, the same for many tokens: a wavefront's
+            // first one is counted at once for all lanes that share it.
+            const int common = __builtin_amdgcn_readfirstlane(d);
+            const uint64_t same = __ballot(d == common);
+            if (d != common)
+                atomicAdd(&sh.count[d], 1u);
+            else if (int(threadIdx.x & 63) == __ffsll(static_cast<unsigned long long>(same)) - 1)
+                atomicAdd(&sh.count[d], uint32_t(__popcll(same)));
+            if (down > 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[d]), (unsigned long long)key_mass(k));
         });
         __syncthreads();
+        // at the last step a bin is one weight; the thread's bin is the one that find_bin has it read
+        const int own = size - 1 - int(threadIdx.x);
+        if (down == 0 && own >= 0) sh.mass[own] = sh.count[own] * key_mass(key | uint32_t(own));
         find_bin<BY_MASS>(sh, size, above, most, limit);
         // a bin that holds the rule's last token always has one here
         key |= uint32_t(sh.found[0]) << down;
@@ -374,27 +413,35 @@ struct Cut {
 
 // A list of few tokens: each is ranked against the others of its bin, which
 // settles all rules at once.  WAVE: at most 64, one a lane, by every wavefront
-// for itself and without a barrier; else one a thread.
+// for itself and without a barrier; else one for four neighbouring lanes, which
+// share its comparisons (256 tokens by one lane each took 26 us).
 template <bool F32, bool WAVE>
 __device__ Cut cut_short(RowShared& sh, const Cuts& c) {
-    const int at_list = threadIdx.x & (WAVE ? 63 : kThreads - 1), n = sh.listed;
-    const bool mine = at_list < n && sh.list_key[at_list] != kNoKey;
-    const uint32_t key = mine ? sh.list_key[at_list] : 0, index = mine ? sh.list_index[at_list] : 0;
+    constexpr int kShare = WAVE ? 1 : kThreads / kShort;
+    static_assert(kShare == 1 || kShare == 4);
+    const int at_list = (threadIdx.x & (WAVE ? 63 : kThreads - 1)) / kShare, part = threadIdx.x % kShare, n = sh.listed;
+    const bool mine = at_list < n && sh.list[at_list].key != kNoKey;
+    const uint32_t key = mine ? sh.list[at_list].key : 0, index = mine ? sh.list[at_list].index : 0;
     const int bin = key_bin(key);
     uint32_t rank = 0;
     uint64_t before = 0;   // the mass before it in its bin
     const int others = __any(mine) ? n : 0;
+    const uint32_t width = (uint32_t(bin + 1) << kBinShift) - key;   // from its key to its bin's end
 #pragma unroll 8
-    for (int i = 0; i < others; ++i) {
-        const uint32_t k = sh.list_key[i], j = sh.list_index[i];
-        const bool first = key_bin(k) == bin && (k > key || (k == key && j < index));
+    for (int i = part; i < others; i += kShare) {
+        const uint32_t k = sh.list[i].key, higher = k - key;
+        const bool first = higher < width && (higher > 0 || sh.list[i].index < index);
         rank += first;
         before += first ? uint32_t(key_weight(k)) : 0;
+    }
+    if constexpr (kShare == 4) {
+        rank += __shfl_xor(rank, 1), before += __shfl_xor(before, 1);
+        rank += __shfl_xor(rank, 2), before += __shfl_xor(before, 2);
     }
     uint64_t mass = sh.found[3];   // of the whole row
     if (c.by_count) {
         const bool top_k = mine && bin == c.bin_k && sh.above_n[bin] + rank < c.k;
-        uint64_t in_bin = top_k ? key_mass(key) : 0;
+        uint64_t in_bin = top_k && part == 0 ? key_mass(key) : 0;
         if constexpr (WAVE)
             in_bin = wave_sum(in_bin);
         else
@@ -518,7 +565,7 @@ sample_draw_kernel(SampleArgs a) {
         return;
     }
     Cuts cuts;
-    const int k = inverse > 0.0f ? (a.top_k ? a.top_k[r] : 0) : 1;
+    const int k = !a.temperature || a.temperature[r] > 0.0f ? (a.top_k ? a.top_k[r] : 0) : 1;
     cuts.k = uint64_t(max(k, 0));
     cuts.p = a.top_p ? a.top_p[r] : 1.0f;
     cuts.low = a.min_p ? double(a.min_p[r]) * double(kSteps) : 0.0;
@@ -577,26 +624,20 @@ sample_draw_kernel(SampleArgs a) {
                 if (lane == 0) sh.chunk_has[c] = has;
             });
             __syncthreads();
-            // First by the exponent d alone, a little wider than the bins (log and
-            // exp are off by far less than 1e-4): its distance from the middle of
-            // each of the one to three ranges.  What passes is few, and gets its
-            // exact weight afterwards.
-            struct Range {
-                float middle, half;
-            };
-            Range r0{0.0f, -1.0f}, r1 = r0, r2 = r0;
+            // First by the logit alone, a little wider than the bins.  What
+            // passes is few, and gets its exact weight afterwards.
+            Range r0{INFINITY, -INFINITY}, r1 = r0, r2 = r0;
             int ranges = 0;
             auto add_range = [&](int lo, int hi) {
-                const float from = logf(key_weight(uint32_t(lo) << kBinShift) / kSteps) - 1e-4f;
-                const float to = logf((key_weight(uint32_t(hi + 1) << kBinShift) + 1.0f) / kSteps) + 1e-4f;
-                r2 = r1, r1 = r0, r0 = Range{0.5f * (from + to), 0.5f * (to - from)};
+                r2 = r1, r1 = r0;
+                r0 = Range{logit_below(key_weight(uint32_t(lo) << kBinShift), top, inverse),
+                           logit_above(key_weight(uint32_t(hi + 1) << kBinShift) + 1.0f, top, inverse)};
                 ++ranges;
             };
             if (cuts.bin_p_hi >= 0) add_range(cuts.bin_p_lo, cuts.bin_p_hi);
             if (cuts.bin_k >= 0 && (cuts.bin_k < cuts.bin_p_lo || cuts.bin_k > cuts.bin_p_hi)) add_range(cuts.bin_k, cuts.bin_k);
             if (cuts.bin_m >= 0 && (cuts.bin_m < cuts.bin_p_lo || cuts.bin_m > cuts.bin_p_hi) && cuts.bin_m != cuts.bin_k)
                 add_range(cuts.bin_m, cuts.bin_m);
-            const float scale = inverse == 0.0f ? 1e30f : inverse;   // T = 0: below the maximum is far below
             auto next_chunk = [&](int c) {
                 while (c < a.chunks && !sh.chunk_has[c]) ++c;
                 return c;
@@ -609,16 +650,30 @@ sample_draw_kernel(SampleArgs a) {
                 while (c < a.chunks) {
                     const int next = next_chunk(c + 1);
                     ahead.load(row, min(next, a.chunks - 1) * kChunk, a.vocab);   // also past the end, so that no wait depends on a branch
+                    uint64_t hits[kPer];   // of the wavefront: places in the list are taken for all its tokens at once
+                    int many_hits = 0;
 #pragma unroll
                     for (int j = 0; j < kPer; ++j) {
-                        const float x = piece.raw(j), d = (x - top) * scale;   // NaN is near nothing
-                        bool in = fabsf(d - r0.middle) <= r0.half;
-                        if constexpr (kRanges > 1) in |= fabsf(d - r1.middle) <= r1.half;
-                        if constexpr (kRanges > 2) in |= fabsf(d - r2.middle) <= r2.half;
-                        const int token = piece.token_at(c * kChunk, j);
-                        if (!in || token >= a.vocab) continue;
-                        const int at = atomicAdd(&sh.listed, 1);   // the order of the list matters to nothing below
-                        if (at < kListMax) sh.list_key[at] = f32_bits(x), sh.list_index[at] = uint32_t(token);
+                        const float x = piece.raw(j);
+                        hits[j] = __ballot(r0.has(x));
+                        if constexpr (kRanges > 1) hits[j] |= __ballot(r1.has(x));
+                        if constexpr (kRanges > 2) hits[j] |= __ballot(r2.has(x));
+                        many_hits += __popcll(hits[j]);
+                    }
+                    if (many_hits) {
+                        int first = 0;
+                        if (lane == 0) first = atomicAdd(&sh.listed, many_hits);   // the order of the list matters to nothing below
+                        first = __builtin_amdgcn_readfirstlane(first);
+                        if (first + many_hits <= kListMax) {   // else the list is not used
+#pragma unroll
+                            for (int j = 0; j < kPer; ++j) {
+                                if (!hits[j]) continue;
+                                if (hits[j] >> lane & 1)
+                                    sh.list[__builtin_amdgcn_mbcnt_hi(uint32_t(hits[j] >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(hits[j]), first))] =
+                                        Listed{f32_bits(piece.raw(j)), uint32_t(piece.token_at(c * kChunk, j))};
+                                first += __popcll(hits[j]);
+                            }
+                        }
                     }
                     piece = ahead;
                     c = next;
@@ -634,9 +689,9 @@ sample_draw_kernel(SampleArgs a) {
             tokens.in_list = sh.listed <= kListMax;
             if (tokens.in_list)
                 for (int i = tid; i < sh.listed; i += kThreads) {
-                    const float w = weight(bits_f32(sh.list_key[i]), top, inverse);
-                    const uint32_t t = w >= 1.0f ? weight_key(w) : kNoKey;
-                    sh.list_key[i] = t != kNoKey && cuts.wanted(key_bin(t)) ? t : kNoKey;
+                    const float w = weight(bits_f32(sh.list[i].key), top, inverse);
+                    const uint32_t t = w >= 1.0f && int(sh.list[i].index) < a.vocab ? weight_key(w) : kNoKey;
+                    sh.list[i].key = t != kNoKey && cuts.wanted(key_bin(t)) ? t : kNoKey;
                 }
             __syncthreads();
         }
@@ -678,11 +733,17 @@ sample_draw_kernel(SampleArgs a) {
     Piece<F32, WIDE, 1> last;   // consecutive tokens
     const int lane_begin = begin - tid * Piece<F32, WIDE, 1>::kVec;
     last.load(row, lane_begin, a.vocab);
+    last.clip(lane_begin, a.vocab);
     uint32_t w[kPer];
     uint64_t sum = 0;
+    // most rows keep few tokens: what lies below the cut needs no exponential
+    const float low = any ? logit_below(key_weight(cut.key), top, inverse) : -INFINITY;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const float y = weight(last.at(lane_begin, a.vocab, j), top, inverse);
+        w[j] = 0;
+        const float x = last.raw(j);
+        if (!__any(!(x < low))) continue;   // (below an infinite maximum low is NaN)
+        const float y = weight(x, top, inverse);
         const uint32_t t = y >= 1.0f ? weight_key(y) : 0;
         w[j] = y >= 1.0f && (t > cut.key || (t == cut.key && uint32_t(begin + j) < cut.index)) ? uint32_t(y) : 0;
         sum += w[j];
@@ -690,14 +751,17 @@ sample_draw_kernel(SampleArgs a) {
     uint64_t all;
     uint64_t run = base + block_scan(sum, sh.tmp, &all);
     if (target < run || target >= run + sum) return;
+    int token = 0;
+    uint32_t mine = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        if (target >= run && target < run + w[j]) {
-            a.token[r] = begin + j;
-            if (a.logprob) a.logprob[r] = float(log(double(w[j]) / double(total)));
-        }
+        const bool here = target >= run && target < run + w[j];
+        token = here ? begin + j : token;
+        mine = here ? w[j] : mine;
         run += w[j];
     }
+    a.token[r] = token;
+    if (a.logprob) a.logprob[r] = float(log(double(mine) / double(total)));
 }
 
 bool misaligned(const void* p, uintptr_t al) { return (reinterpret_cast<uintptr_t>(p) & (al - 1)) != 0; }
