@@ -74,16 +74,17 @@ struct QueryBlock {
     // loads first (rows past the last are loaded as the last).
     __device__ __forceinline__ void fill(const WeightArgs& a, const QueryRows& rows, int hk, int r0) {
         constexpr int kLanes = D / 8, kStep = 256 / kLanes, kTurns = kRows / kStep;
-        const int chunk = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));   // what follows from it is found anew: kept between blocks it would not fit the registers
+        const int chunk = tid % kLanes, row = tid / kLanes;
         const int many = (min(rows.count - r0, kRows) + 15) / 16 * 16;   // whole tiles
         u32x4 raw[kTurns][1];
-        float l[kTurns];
 #pragma unroll
-        for (int x = 0; x < kTurns; ++x) {
-            const int r = min(r0 + x * kStep + row, rows.count - 1);
-            raw[x][0] = load16(query_at(a.sc, rows.row(a.sc, r), hk) + 8 * chunk);
-            l[x] = a.lse[rows.place(a.sc, r, hk)];
-        }
+        for (int x = 0; x < kTurns; ++x)
+            raw[x][0] = load16(query_at(a.sc, rows.row(a.sc, r0 + x * kStep + row), hk) + 8 * chunk);
+        const int own = min(tid, kRows - 1);   // the row whose statistics this thread brings
+        const QueryRow mine = rows.row(a.sc, r0 + own);
+        const float l = a.lse[rows.place(a.sc, mine, hk)];
 #pragma unroll
         for (int x = 0; x < kTurns; ++x) {
             const int i = x * kStep + row;
@@ -91,22 +92,22 @@ struct QueryBlock {
             f16x8 y[1];
             const float factor = convert_query<1, 1, kLanes>(a.sc, raw[x], y);
             q[chunk_at(i, chunk)] = y[0];
-            if (chunk == 0) {
-                const QueryRow me = rows.row(a.sc, r0 + i);
-                f[i] = factor;
-                lse[i] = l[x] == -INFINITY || r0 + i >= rows.count ? INFINITY : l[x] * kLog2e;
-                lo[i] = me.lo, hi[i] = me.hi;
-            }
+            if (chunk == 0) f[i] = factor;
+        }
+        if (tid < kRows) {
+            lse[own] = l == -INFINITY || r0 + own >= rows.count ? INFINITY : l * kLog2e;
+            lo[own] = mine.lo, hi[own] = mine.hi;
         }
     }
 };
 
 // PAGES pages a wavefront; all rows that see them pass by, a block at a time.
 template <int D, int PAGES>
-__global__ void __launch_bounds__(256, D == 256 ? 1 : PAGES == 1 ? 3 : 2)
+__global__ void __launch_bounds__(256, D == 256 ? 2 : 3)
 kv_weights_kernel(WeightArgs a) {
     using Block = QueryBlock<D, PAGES == 1 ? 32 : D == 256 ? 64 : 128>;
     __shared__ Block block;
+    __shared__ f32x4 sums[4][PAGES][64];   // of a wavefront's pages, a lane's slots: in registers only while their page is
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, b = lane >> 4;
     const int s = blockIdx.y, hk = blockIdx.x % a.v.kv_heads;
@@ -127,32 +128,40 @@ kv_weights_kernel(WeightArgs a) {
     if (a.sc.window > 0) i_hi = min(i_hi, max(0, past - 1 + a.sc.window - shift));
     const int r_lo = i_lo * rows.group, r_hi = i_hi * rows.group;
 
-    float sum[PAGES][4] = {};
-    int ids[PAGES];
-#pragma unroll
-    for (int x = 0; x < PAGES; ++x) {
-        const int page = page0 + x;
-        ids[x] = r_lo < r_hi && page * kPage < rows.len ? a.v.page_id(s, page) : -1;
-    }
+    // lane x has the id of page x
+    int ids = -1;
+    if (r_lo < r_hi && lane < PAGES && (page0 + lane) * kPage < rows.len) ids = a.v.page_id(s, page0 + lane);
     KRegs<D> raw;
-    if (r_lo < r_hi) raw.load(a.v.record_or_first<D>(ids[0], hk), n, b);
+    if (r_lo < r_hi) raw.load(a.v.record_or_first<D>(__builtin_amdgcn_readlane(ids, 0), hk), n, b);
+    auto my_slot = [&](int x) { return (page0 + x) * kPage + KRegs<D>::slot(b, n); };   // that this lane writes
+#pragma unroll
+    for (int x = 0; x < PAGES; ++x) sums[wave][x][lane] = f32x4{0, 0, 0, 0};
     for (int r0 = r_lo; r0 < r_hi; r0 += Block::kRows) {
         if (r0 != r_lo) __syncthreads();
         block.fill(a, rows, hk, r0);
         __syncthreads();
         const int tiles = (min(r_hi - r0, Block::kRows) + 15) / 16;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < PAGES; ++x) {
             f16x8 k[4][D / 32];
             raw.template decode<0, 0>(k[0]);
             raw.template decode<1, 0>(k[1]);
             raw.template decode<2, 0>(k[2]);
             raw.template decode<3, 0>(k[3]);
-            raw.load(a.v.record_or_first<D>(ids[(x + 1) % PAGES], hk), n, b);   // also for the next block of rows
-            if (!a.v.has(ids[x])) continue;
+            raw.load(a.v.record_or_first<D>(__builtin_amdgcn_readlane(ids, (x + 1) % PAGES), hk), n, b);   // also for the next block of rows
+            if (!a.v.has(__builtin_amdgcn_readlane(ids, x))) continue;
+            f32x4 sum = sums[wave][x][lane];
             const int base = (page0 + x) * kPage;
-            for (int t = 0; t < tiles; ++t) {
-                f32x4 z[4];
+            // Tokens in order see ever later slots: those from see_lo on and before see_hi see
+            // all of the page, and so do their rows (and those past the last, which give nothing).
+            const int see_lo = a.sc.causal ? min(max(base + kPage - 1 - shift, 0), rows.new_tokens) : 0;
+            const int see_hi = a.sc.window > 0 ? max(base + a.sc.window - shift, 0) : rows.new_tokens;
+            const bool simple = a.sc.cap == 0.0f && base + kPage <= rows.len;
+            const int full_lo = simple ? (see_lo * rows.group - r0 + 15) / 16 : tiles;   // in tiles
+            const int full_hi = see_hi >= rows.new_tokens ? tiles : (see_hi * rows.group - r0) / 16;
+            const int t_lo = min(max(full_lo, 0), tiles), t_hi = max(min(full_hi, tiles), t_lo);
+
+            auto products = [&](int t, f32x4 (&z)[4]) {
 #pragma unroll
                 for (int ht = 0; ht < 4; ++ht) z[ht] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -161,16 +170,18 @@ kv_weights_kernel(WeightArgs a) {
 #pragma unroll
                     for (int ht = 0; ht < 4; ++ht) z[ht] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q, k[ht][i], z[ht], 0, 0, 0);
                 }
+            };
+            auto add_full = [&](int t, const f32x4 (&z)[4]) {
                 const f32x4 f = *reinterpret_cast<const f32x4*>(block.f + 16 * t + 4 * b);
                 const f32x4 lse = *reinterpret_cast<const f32x4*>(block.lse + 16 * t + 4 * b);
-                // the tile's rows in order see ever later slots: its first and last say whether all see the page
-                if (base >= block.lo[16 * t + 15] && base + kPage <= block.hi[16 * t] && a.sc.cap == 0.0f) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int ht = 0; ht < 4; ++ht) sum[x][ht] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[ht][c], f[c], -lse[c]));
-                    continue;
-                }
+                    for (int ht = 0; ht < 4; ++ht) sum[ht] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[ht][c], f[c], -lse[c]));
+            };
+            auto add_seen = [&](int t, const f32x4 (&z)[4]) {
+                const f32x4 f = *reinterpret_cast<const f32x4*>(block.f + 16 * t + 4 * b);
+                const f32x4 lse = *reinterpret_cast<const f32x4*>(block.lse + 16 * t + 4 * b);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int lo = block.lo[16 * t + 4 * b + c], hi = block.hi[16 * t + 4 * b + c];
@@ -180,23 +191,35 @@ kv_weights_kernel(WeightArgs a) {
                     for (int ht = 0; ht < 4; ++ht) {
                         const int slot = base + KRegs<D>::slot(ht, n);
                         const float p = __builtin_amdgcn_exp2f(y[ht] - lse[c]);
-                        sum[x][ht] += slot >= lo && slot < hi ? p : 0.0f;
+                        sum[ht] += slot >= lo && slot < hi ? p : 0.0f;
                     }
                 }
-            }
+            };
+            f32x4 z[4];
+#pragma unroll 1
+            for (int t = 0; t < t_lo; ++t) products(t, z), add_seen(t, z);
+#pragma unroll 1
+            for (int t = t_lo; t < t_hi; ++t) products(t, z), add_full(t, z);
+#pragma unroll 1
+            for (int t = t_hi; t < tiles; ++t) products(t, z), add_seen(t, z);
+            sums[wave][x][lane] = sum;
         }
     }
+    // a lane of group b has tile b's slot n of each page
+    float before[PAGES];
+#pragma unroll
+    for (int x = 0; x < PAGES; ++x) before[x] = a.prior ? a.prior[out + min(int64_t(my_slot(x)), a.max_kv - 1)] : 0.0f;
 #pragma unroll
     for (int x = 0; x < PAGES; ++x) {
+        f32x4 sum = sums[wave][x][lane];
 #pragma unroll
         for (int ht = 0; ht < 4; ++ht) {
-            float w = sum[x][ht];
-            w += __shfl_xor(w, 16);
-            w += __shfl_xor(w, 32);
-            const int slot = (page0 + x) * kPage + KRegs<D>::slot(ht, n);
-            if (b != ht || slot >= a.max_kv) continue;   // lanes of group b write tile b
-            a.weights[out + slot] = slot < rows.len ? (a.prior ? a.prior[out + slot] : 0.0f) + w : 0.0f;
+            sum[ht] += __shfl_xor(sum[ht], 16);
+            sum[ht] += __shfl_xor(sum[ht], 32);
         }
+        const float w = b < 2 ? (b == 0 ? sum[0] : sum[1]) : (b == 2 ? sum[2] : sum[3]);
+        const int slot = my_slot(x);
+        if (slot < a.max_kv) a.weights[out + slot] = slot < rows.len ? before[x] + w : 0.0f;
     }
 }
 

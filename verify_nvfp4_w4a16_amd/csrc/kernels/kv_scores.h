@@ -13,11 +13,18 @@ struct KvScores {
     const uint16_t* q;
     int64_t q_pitch, q_head_pitch;
     int heads, group;      // query heads, and those of one kv head
+    uint32_t inverse;      // floor((2^32 - 1) / group)
     int window;            // 0: no limit
     int max_q, max_kv;     // what the launch was sized for: sequences are held to it
     int causal;
     float scale;           // of q . (e4m3 * e2m1): the caller's times K's tensor scale
     float cap, cap_inv2;   // softcap and 2 / softcap (0: none)
+
+    // r / group for r in [0, 2^31): the product with the inverse is at most one short (a division takes 30 operations).
+    __device__ __forceinline__ int over_group(int r) const {
+        const int i = int(__umulhi(uint32_t(r), inverse));
+        return r - i * group >= group ? i + 1 : i;
+    }
 
     // z * log2(e) of products' sums x, whose row was scaled by its own power
     // of two (f is scale over that power, times log2(e) where there is no cap).
@@ -45,6 +52,7 @@ inline KvScores kv_scores(const nvfp4_kv_cache_t* c, const nvfp4_kv_queries_t* q
     s.q_head_pitch = q->q_head_pitch;
     s.heads = static_cast<int>(q->heads);
     s.group = static_cast<int>(q->heads / c->kv_heads);
+    s.inverse = 0xffffffffu / uint32_t(s.group);
     s.window = static_cast<int>(q->window < (int64_t(1) << 29) ? q->window : 0);   // no sequence is longer
     s.max_q = static_cast<int>(q->max_q);
     s.max_kv = static_cast<int>(q->max_kv);
@@ -87,19 +95,21 @@ struct QueryRows {
     }
     // For rows first .. last (both below count).
     __device__ __forceinline__ Span span(const KvScores& sc, int first, int last) const {
-        const int i0 = first / group, i1 = last / group;
+        const int i0 = sc.over_group(first), i1 = sc.over_group(last);
         return Span{see_lo(sc, i0), see_hi(sc, i1), see_lo(sc, i1), see_hi(sc, i0)};
     }
     // A row at or beyond count stands in for the last one (its result is dropped).
     __device__ __forceinline__ QueryRow row(const KvScores& sc, int r) const {
         r = min(r, count - 1);
-        const int i = r / group;
+        const int i = sc.over_group(r);
         return QueryRow{first_token + i, r - i * group, see_lo(sc, i), see_hi(sc, i)};
     }
     // Index of a row in [total][heads].
     __device__ __forceinline__ int64_t place(const KvScores& sc, int r, int hk) const {
-        const int i = r / group;
-        return int64_t(first_token + i) * sc.heads + hk * group + (r - i * group);
+        return place(sc, row(sc, r), hk);
+    }
+    static __device__ __forceinline__ int64_t place(const KvScores& sc, const QueryRow& r, int hk) {
+        return int64_t(r.token) * sc.heads + hk * sc.group + r.g;
     }
 };
 
