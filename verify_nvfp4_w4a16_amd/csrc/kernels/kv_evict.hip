@@ -252,12 +252,13 @@ struct EvictArgs {
     __device__ __forceinline__ int len(int s) const { return static_cast<int>(min(int64_t(v.len(s)), weights_pitch)); }
 };
 
-// fp32 to a key that orders as the numbers do; -0 is 0, NaN is -inf.
+// fp32 to a key that orders as the numbers do; -0 is 0, NaN is -inf.  None is below 0x7fffff.
 __device__ __forceinline__ uint32_t order_key(float x) {
-    x = x != x ? -INFINITY : x + 0.0f;
-    const uint32_t u = f32_bits(x);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const uint32_t u = f32_bits(fmaxf(x, -INFINITY) + 0.0f);
+    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
 }
+
+constexpr uint32_t kZeroKey = 0x80000000u;
 
 constexpr int kSelect = 1024;
 constexpr int kSelectWaves = kSelect / 64;
@@ -303,7 +304,8 @@ struct Keys {
 #pragma unroll
             for (int i = 0; i < HELD; ++i) {
                 const int j = begin + i * 64 + lane;
-                held[i] = j >= lo && j < hi ? order_key(bits_f32(held[i])) : 0;
+                held[i] = order_key(bits_f32(held[i]));
+                if (begin + i * 64 < lo || begin + i * 64 + 64 > hi) held[i] = j >= lo && j < hi ? held[i] : 0;
             }
         }
     }
@@ -358,23 +360,12 @@ kv_select_kernel(EvictArgs a) {
     const Keys<HELD, SHARED> keys(w, more, n, lo, hi);
     // the key of the last slot that is chosen, 11, 11 and 10 bits at a time
     uint32_t need = uint32_t(wanted), mask = 0, key = 0;
-#pragma unroll 1
-    for (int level = 0; level < 3; ++level) {
-        const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-        const uint32_t digits = level < 2 ? 2047 : 1023;
+    auto clear = [&] {
         bins[tid] = bins[tid + kSelect] = 0;
         __syncthreads();
-        keys.each([&](int, uint32_t k) {
-            const bool in = (k & mask) == key;
-            const uint64_t lanes = __ballot(in);
-            if (!lanes) return;
-            // equal digits of a wavefront (the many zeros of a fresh cache) are added at once
-            const uint32_t d = (k >> shift) & digits;
-            const int first = __ffsll(static_cast<unsigned long long>(lanes)) - 1;
-            const uint32_t common = uint32_t(__builtin_amdgcn_readlane(int(d), first));
-            const uint64_t same = __ballot(in && d == common);
-            if (in && (d != common || lane == first)) atomicAdd(&bins[d], d == common ? uint32_t(__popcll(same)) : 1u);
-        });
+    };
+    // the bin in which the last of them lies: the next bits of the key
+    auto settle = [&](int shift, uint32_t digits) {
         __syncthreads();
         // thread t has bins 2 (1023 - t) + 1 and 2 (1023 - t): the highest first
         const int at = 2 * (kSelect - 1 - tid);
@@ -392,6 +383,37 @@ kv_select_kernel(EvictArgs a) {
         key |= found[0] << shift;
         mask |= digits << shift;
         need = found[1];   // still wanted among the keys with these leading bits
+    };
+    // A slot outside the choice has a digit below every other's.  The many zeros of
+    // a fresh cache would all meet in one place: a wavefront adds its own at once.
+    clear();
+    uint32_t zeros = 0;
+    keys.each([&](int, uint32_t k) {
+        if (k != kZeroKey)
+            atomicAdd(&bins[k >> 21], 1u);
+        else
+            ++zeros;
+    });
+    zeros = scan32(zeros);
+    if (lane == 63 && zeros > 0) atomicAdd(&bins[kZeroKey >> 21], zeros);
+    settle(21, 2047);
+    // What is left may be the same number: a lane adds a run of equal digits at once.
+#pragma unroll 1
+    for (int shift = 10; shift >= 0; shift -= 10) {
+        const uint32_t digits = shift > 0 ? 2047 : 1023;
+        clear();
+        uint32_t digit = 0, run = 0;
+        keys.each([&](int, uint32_t k) {
+            if ((k & mask) != key) return;
+            const uint32_t d = (k >> shift) & digits;
+            if (d != digit) {
+                if (run > 0) atomicAdd(&bins[digit], run);
+                digit = d, run = 0;
+            }
+            ++run;
+        });
+        if (run > 0) atomicAdd(&bins[digit], run);
+        settle(shift, digits);
     }
     // `need` of the slots at the key stay, the lowest first.  Wavefronts count
     // theirs, then number them from where those before them end.
@@ -405,21 +427,32 @@ kv_select_kernel(EvictArgs a) {
     __syncthreads();
     uint32_t above = 0, seen = 0;   // chosen slots and ties before
     for (int i = 0; i < wave; ++i) above += tmp[i][0], seen += tmp[i][1];
-    const uint64_t below = (1ull << lane) - 1;
     key = uint32_t(__builtin_amdgcn_readfirstlane(int(key)));
     asm("" : "+s"(key));   // compared anew: kept from the count, the comparisons' results would fill the registers
+    auto before = [&](uint64_t lanes) { return __builtin_amdgcn_mbcnt_hi(uint32_t(lanes >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(lanes), 0)); };
+    // Of many slots the weights are fetched afterwards, together: fetched and
+    // stored one after the other they would be waited for at every step.
+    constexpr bool kAtOnce = HELD > 0 && HELD <= 16;
+    auto keep = [&](uint32_t to, int j) {
+        kept[to] = j;
+        if constexpr (kAtOnce) kept_w[to] = w[j];
+    };
     keys.each([&](int j, uint32_t k) {
         const uint64_t high = __ballot(k > key), equal = __ballot(k == key);
         if (!(high | equal)) return;
-        const uint32_t rank = seen + uint32_t(__popcll(equal & below));
-        if (k > key || (k == key && rank < need)) {
-            const uint32_t to = uint32_t(lo) + above + uint32_t(__popcll(high & below)) + min(rank, need);
-            kept[to] = j;
-            kept_w[to] = w[j];
+        if (!equal) {
+            if (k > key) keep(uint32_t(lo) + above + min(seen, need) + before(high), j);
+        } else {
+            const uint32_t rank = seen + before(equal);
+            if (k > key || (k == key && rank < need)) keep(uint32_t(lo) + above + before(high) + min(rank, need), j);
+            seen += uint32_t(__popcll(equal));
         }
         above += uint32_t(__popcll(high));
-        seen += uint32_t(__popcll(equal));
     });
+    if constexpr (!kAtOnce) {
+        __syncthreads();
+        for (int i = lo + tid; i < lo + wanted; i += kSelect) kept_w[i] = w[kept[i]];
+    }
 }
 
 // The rows that stay, one destination page a workgroup.
@@ -546,13 +579,13 @@ extern "C" int nvfp4_kv_evict(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs
     const EvictArgs a{kv_view(cache, seqs), weights, weights_pitch, static_cast<int>(keep), static_cast<int>(sink),
                       static_cast<int>(recent), dst->data, dst->pages, dst_table, dst_pitch, kept, kept_weights, new_lens};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    // Keys held up to 65536 slots a sequence (56 in registers and 8 in LDS a lane, which is what a
+    // Keys held up to 65536 slots a sequence (51 in registers and 13 in LDS a lane, which is what a
     // 1024-thread workgroup's registers take) and read once; of longer sequences they are read five
-    // times (8 sequences of up to 65000 slots, 8 heads: 102 us instead of 51).
+    // times (8 sequences of up to 65000 slots, 8 heads: 92 us instead of 39).
     const int64_t longest = std::min(weights_pitch, seqs->table_pitch * kPage);
     const auto select = longest <= 4 * kSelect    ? kv_select_kernel<4, 0>
                         : longest <= 16 * kSelect ? kv_select_kernel<16, 0>
-                        : longest <= 64 * kSelect ? kv_select_kernel<56, 8>
+                        : longest <= 64 * kSelect ? kv_select_kernel<51, 13>
                                                   : kv_select_kernel<0, 0>;
     hipLaunchKernelGGL(select, dim3(cache->kv_heads, static_cast<unsigned>(seqs->seqs)), dim3(kSelect), 0, s, a);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
