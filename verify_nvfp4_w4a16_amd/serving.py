@@ -17,6 +17,9 @@ import torch
 
 from . import _check, _lib
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32   # a module's own names are found faster, which a one-token step notices
+_empty, _raw_stream = torch.empty, torch._C._cuda_getCurrentRawStream
+
 PAGE = 64
 HEAD_DIMS = (64, 128, 256)
 LOGITS_BF16, LOGITS_F32 = 0, 1
@@ -96,7 +99,7 @@ class KvCache:
 
 
 def _ints(name, t, dim, device):
-    if t.dtype != torch.int32 or t.dim() != dim or t.device != device or not t.is_contiguous():
+    if t.dtype is not _I32 or t.dim() != dim or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dim}-D int32 tensor on {device}")
     return t.data_ptr()
 
@@ -115,24 +118,26 @@ def _seqs(cache, table, kv_lens, q_starts, total) -> _Seqs:
 
 
 def _rows(name, x, cache, heads=None):
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.device != cache.device:
+    if x.dtype is not _BF16 or x.dim() != 3 or x.device != cache.device:
         raise ValueError(f"{name} must be a bf16 [tokens, heads, head_dim] tensor on {cache.device}")
-    if x.shape[2] != cache.head_dim or (heads is not None and x.shape[1] != heads) or x.stride(2) != 1:
+    _, width, dim = x.shape
+    pitch, head_pitch, step = x.stride()
+    if dim != cache.head_dim or (heads is not None and width != heads) or step != 1:
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {cache.head_dim}] with contiguous rows")
-    return x.data_ptr(), x.stride(0), x.stride(1)
+    return x.data_ptr(), pitch, head_pitch
 
 
 def _out(name, t, shape, dtype, device):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        return _empty(shape, dtype=dtype, device=device)
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 
 def _stream(stream, device) -> int:
     # the raw handle at once: torch.cuda.current_stream() would build a Stream object (2 us) first
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def kv_append(cache: KvCache, k, v, table, kv_lens, q_starts, stream=None) -> None:
@@ -150,8 +155,8 @@ def kv_read(cache: KvCache, table, kv_lens, q_starts, total: int, k=None, v=None
     """The bf16 values of each sequence's last q_starts[s+1] - q_starts[s] slots: (k, v), each
     [total, kv_heads, head_dim]; rows without a slot are zeros."""
     shape = (total, cache.kv_heads, cache.head_dim)
-    k = _out("k", k, shape, torch.bfloat16, cache.device)
-    v = _out("v", v, shape, torch.bfloat16, cache.device)
+    k = _out("k", k, shape, _BF16, cache.device)
+    v = _out("v", v, shape, _BF16, cache.device)
     seqs = _seqs(cache, table, kv_lens, q_starts, total)
     _check(_kv().nvfp4_kv_read(cache._c, seqs, k.data_ptr(), v.data_ptr(), _stream(stream, cache.device)),
            "nvfp4_kv_read")
@@ -185,8 +190,8 @@ def kv_attention(q, cache: KvCache, table, kv_lens, q_starts, max_q: int, max_kv
     dev = cache.device
     seqs = _seqs(cache, table, kv_lens, q_starts, q.shape[0])
     queries = _queries(cache, q, max_q, max_kv, scale, causal, window, softcap)
-    out = _out("out", out, q.shape, torch.bfloat16, dev)
-    lse = _out("lse", lse, q.shape[:2], torch.float32, dev)
+    out = _out("out", out, q.shape, _BF16, dev)
+    lse = _out("lse", lse, q.shape[:2], _F32, dev)
     lib = _kv()
     if workspace is None:
         n = ctypes.c_int64()
@@ -216,10 +221,10 @@ def kv_weights(q, lse, cache: KvCache, table, kv_lens, q_starts, max_q: int, max
     seqs = _seqs(cache, table, kv_lens, q_starts, q.shape[0])
     queries = _queries(cache, q, max_q, max_kv, scale, causal, window, softcap)
     shape = (seqs.seqs, cache.kv_heads, max_kv)
-    out = _out("out", out, shape, torch.float32, dev)
+    out = _out("out", out, shape, _F32, dev)
     if prior is not None:
-        _out("prior", prior, shape, torch.float32, dev)
-    _out("lse", lse, q.shape[:2], torch.float32, dev)
+        _out("prior", prior, shape, _F32, dev)
+    _out("lse", lse, q.shape[:2], _F32, dev)
     _check(_kv().nvfp4_kv_weights(cache._c, seqs, queries, lse.data_ptr(), 0 if prior is None else prior.data_ptr(),
                                   out.data_ptr(), _stream(stream, dev)), "nvfp4_kv_weights")
     return out
@@ -238,13 +243,13 @@ def kv_evict(weights, cache: KvCache, table, kv_lens, dst_table, keep: int, *, s
     shape = (seqs.seqs, cache.kv_heads, keep)
     if weights.dim() != 3 or tuple(weights.shape[:2]) != shape[:2]:
         raise ValueError(f"weights must be [{shape[0]}, {shape[1]}, slots]")
-    _out("weights", weights, weights.shape, torch.float32, dev)
+    _out("weights", weights, weights.shape, _F32, dev)
     if dst_table.shape[0] != shape[0]:
         raise ValueError("dst_table must have one row for each sequence")
     dst_ptr = _ints("dst_table", dst_table, 2, dev)
-    kept = _out("kept", kept, shape, torch.int32, dev)
-    kept_weights = _out("kept_weights", kept_weights, shape, torch.float32, dev)
-    new_lens = _out("new_lens", new_lens, shape[:1], torch.int32, dev)
+    kept = _out("kept", kept, shape, _I32, dev)
+    kept_weights = _out("kept_weights", kept_weights, shape, _F32, dev)
+    new_lens = _out("new_lens", new_lens, shape[:1], _I32, dev)
     _check(_kv().nvfp4_kv_evict(cache._c, seqs, weights.data_ptr(), weights.shape[2], keep, sink, recent, dst._c, dst_ptr,
                                 dst_table.shape[1], kept.data_ptr(), kept_weights.data_ptr(), new_lens.data_ptr(),
                                 _stream(stream, dev)), "nvfp4_kv_evict")
@@ -262,25 +267,26 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, *, t
     """One token a row of logits (bf16 or fp32 [rows, vocab], rows may be strided) from the row's
     random number u in [0, 1): (token int32 [rows], logprob fp32 [rows]).  temperature, top_p, min_p
     fp32 and top_k int32 are tensors [rows]; None stands for 1, 1, 0 and 0 (no limit)."""
-    if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or not logits.is_cuda:
+    if logits.dtype not in (_BF16, _F32) or logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a bf16 or float32 [rows, vocab] GPU tensor")
     if logits.stride(1) != 1 and logits.shape[1] > 1:
         raise ValueError("logits must have contiguous rows")
     rows, vocab = logits.shape
     dev = logits.device
-    token = _out("token", token, (rows,), torch.int32, dev)
-    logprob = _out("logprob", logprob, (rows,), torch.float32, dev)
+    f32 = logits.dtype is _F32
+    token = _out("token", token, (rows,), _I32, dev)
+    logprob = _out("logprob", logprob, (rows,), _F32, dev)
     lib = _kv()
     n = ctypes.c_int64()
     _check(lib.nvfp4_sample_workspace(rows, vocab, n), "nvfp4_sample")
     if workspace is None and n.value:
         workspace = _scratch(n.value, dev, stream)
     wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _check(lib.nvfp4_sample(logits.data_ptr(), LOGITS_F32 if logits.dtype == torch.float32 else LOGITS_BF16, rows, vocab,
-                            logits.stride(0) if rows > 1 else vocab, _param("u", u, rows, torch.float32, dev),
-                            _param("temperature", temperature, rows, torch.float32, dev),
-                            _param("top_k", top_k, rows, torch.int32, dev),
-                            _param("top_p", top_p, rows, torch.float32, dev),
-                            _param("min_p", min_p, rows, torch.float32, dev),
+    _check(lib.nvfp4_sample(logits.data_ptr(), LOGITS_F32 if f32 else LOGITS_BF16, rows, vocab,
+                            logits.stride(0) if rows > 1 else vocab, _param("u", u, rows, _F32, dev),
+                            _param("temperature", temperature, rows, _F32, dev),
+                            _param("top_k", top_k, rows, _I32, dev),
+                            _param("top_p", top_p, rows, _F32, dev),
+                            _param("min_p", min_p, rows, _F32, dev),
                             token.data_ptr(), logprob.data_ptr(), wp, wn, _stream(stream, dev)), "nvfp4_sample")
     return token, logprob
