@@ -101,11 +101,11 @@ struct QueryBlock {
     }
 };
 
-// PAGES pages a wavefront; all rows that see them pass by, a block at a time.
-template <int D, int PAGES>
+// PAGES pages a wavefront; all rows that see them pass by, ROWS at a time.
+template <int D, int PAGES, int ROWS>
 __global__ void __launch_bounds__(256, D == 256 ? 2 : 3)
 kv_weights_kernel(WeightArgs a) {
-    using Block = QueryBlock<D, PAGES == 1 ? 32 : D == 256 ? 64 : 128>;
+    using Block = QueryBlock<D, ROWS>;
     __shared__ Block block;
     __shared__ f32x4 sums[4][PAGES][64];   // of a wavefront's pages, a lane's slots: in registers only while their page is
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -225,14 +225,20 @@ kv_weights_kernel(WeightArgs a) {
 
 template <int D>
 int launch_weights(const WeightArgs& a, int64_t rows, hipStream_t st) {
-    // One page a wavefront where few rows and pages leave nothing else to run
-    // beside, four where a page's rows are worth staging once for all of them.
-    const bool four = rows > 32 || a.max_kv / kPage * a.v.kv_heads * a.v.seqs > 32768;
-    const int64_t slots = 4 * kPage * (four ? 4 : 1);
+    // Up to 32 rows a kv head: one page a wavefront where the cache has few, so
+    // that all are under way at once, two where it has many (16 sequences of
+    // 100 .. 16383 slots, 8 heads: 15.4 us with one, 13.7 with two, 14.3 with
+    // four; 4 sequences: 7.1, 8.3, 10.0).  More rows are worth staging 128 at a time for
+    // the four pages of a wavefront (64 at D = 256, where LDS holds no more
+    // for two workgroups).
+    const bool many = rows > 32;
+    const int64_t all = (a.max_kv + kPage - 1) / kPage * a.v.kv_heads * a.v.seqs;
+    const int pages = many ? 4 : all > 8192 ? 2 : 1;
+    const int64_t slots = 4 * kPage * pages;
     const int64_t blocks = (a.max_kv + slots - 1) / slots * a.v.kv_heads;
     if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL((four ? kv_weights_kernel<D, 4> : kv_weights_kernel<D, 1>), dim3(static_cast<unsigned>(blocks), a.v.seqs),
-                       dim3(256), 0, st, a);
+    hipLaunchKernelGGL((many ? kv_weights_kernel<D, 4, D == 256 ? 64 : 128> : pages == 1 ? kv_weights_kernel<D, 1, 32> : kv_weights_kernel<D, 2, 32>),
+                       dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
