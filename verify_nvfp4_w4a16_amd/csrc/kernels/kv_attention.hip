@@ -225,12 +225,17 @@ __device__ __forceinline__ f16x8 to_f16x8(const float* p) {
     return r;
 }
 
+// A row of sums in LDS: 16 bytes more than its dims, so that the 16 rows that are
+// written at once begin on different banks.
+template <int D>
+constexpr int kSumRow = D + 4;
+
 // 16 query rows and one item's pages: the wavefronts take every fourth page,
 // decoded from registers, and join in LDS in wavefront order.
 template <int D>
 __global__ void __launch_bounds__(64 * kWaves, 2)
 kv_attend_rows_kernel(AttendArgs a) {
-    extern __shared__ float lds[];   // [kWaves][16][D] sums, then [kWaves][16][2] statistics
+    extern __shared__ float lds[];   // [kWaves][16][kSumRow<D>] sums, then [kWaves][16][2] statistics
     // the wavefront's number as a scalar: its pages and their addresses are then scalars too
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, b = lane >> 4;
@@ -344,8 +349,8 @@ kv_attend_rows_kernel(AttendArgs a) {
     if (l != l && m == -INFINITY) m = 0.0f;   // all scores NaN: the row stays NaN
 
     // The wavefronts' results meet in LDS and are joined in wavefront order.
-    float* sums = lds + wave * 16 * D;
-    float* stats = lds + kWaves * 16 * D;
+    float* sums = lds + wave * 16 * kSumRow<D>;
+    float* stats = lds + kWaves * 16 * kSumRow<D>;
     if (b == 0) {
         stats[(wave * 16 + n) * 2] = m;
         stats[(wave * 16 + n) * 2 + 1] = l;
@@ -354,7 +359,7 @@ kv_attend_rows_kernel(AttendArgs a) {
     for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int i = 0; i < D / 16; i += 4)
-            *reinterpret_cast<f32x4*>(sums + n * D + (4 * b + c) * (D / 16) + i) =
+            *reinterpret_cast<f32x4*>(sums + n * kSumRow<D> + (4 * b + c) * (D / 16) + i) =
                 f32x4{o[i][c], o[i + 1][c], o[i + 2][c], o[i + 3][c]};
     __syncthreads();
     constexpr int kPer = D / 16;   // dims of a thread: 256 threads, 16 rows
@@ -370,7 +375,7 @@ kv_attend_rows_kernel(AttendArgs a) {
             const float f = __builtin_amdgcn_exp2f(stats[(w * 16 + r) * 2] - top);
             sum += f * stats[(w * 16 + r) * 2 + 1];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] += f * lds[(w * 16 + r) * D + d0 + i];
+            for (int i = 0; i < kPer; ++i) acc[i] += f * lds[(w * 16 + r) * kSumRow<D> + d0 + i];
         }
     }
     const int64_t at = rows.place(a.sc, row0 + r, hk);
@@ -813,7 +818,7 @@ int64_t workspace_bytes_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, 
 
 template <int D>
 constexpr size_t rows_lds() {
-    return (kWaves * 16 * D + kWaves * 16 * 2) * sizeof(float);
+    return (kWaves * 16 * kSumRow<D> + kWaves * 16 * 2) * sizeof(float);
 }
 
 template <int D>
