@@ -362,20 +362,25 @@ kv_attend_rows_kernel(AttendArgs a) {
             *reinterpret_cast<f32x4*>(sums + n * kSumRow<D> + (4 * b + c) * (D / 16) + i) =
                 f32x4{o[i][c], o[i + 1][c], o[i + 2][c], o[i + 3][c]};
     __syncthreads();
-    constexpr int kPer = D / 16;   // dims of a thread: 256 threads, 16 rows
-    const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * kPer;
+    // 16 threads a row, each with 4 dims of every 64
+    constexpr int kParts = D / 64;
+    const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 4;
     if (row0 + r >= rows.count) return;
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * 16 + r) * 2]);
-    float acc[kPer] = {}, sum = 0.0f;
+    f32x4 acc[kParts];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) acc[i] = f32x4{0, 0, 0, 0};
+    float sum = 0.0f;
     if (top > -INFINITY) {
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             const float f = __builtin_amdgcn_exp2f(stats[(w * 16 + r) * 2] - top);
             sum += f * stats[(w * 16 + r) * 2 + 1];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] += f * lds[(w * 16 + r) * kSumRow<D> + d0 + i];
+            for (int i = 0; i < kParts; ++i)
+                acc[i] += f * *reinterpret_cast<const f32x4*>(lds + (w * 16 + r) * kSumRow<D> + 64 * i + d0);
         }
     }
     const int64_t at = rows.place(a.sc, row0 + r, hk);
@@ -384,8 +389,7 @@ kv_attend_rows_kernel(AttendArgs a) {
         float* po = a.part_o + to * D + d0;
         if (top > -INFINITY)
 #pragma unroll
-            for (int i = 0; i < kPer; i += 4)
-                *reinterpret_cast<f32x4*>(po + i) = f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+            for (int i = 0; i < kParts; ++i) *reinterpret_cast<f32x4*>(po + 64 * i) = acc[i];
         if (d0 == 0) {
             a.part_ml[to * 2] = top;
             a.part_ml[to * 2 + 1] = sum;
@@ -395,13 +399,13 @@ kv_attend_rows_kernel(AttendArgs a) {
     const float f = sum > 0.0f || sum != sum ? a.v_scale / sum : 0.0f;
     uint16_t* out = a.out + at * D + d0;
 #pragma unroll
-    for (int i = 0; i < kPer; i += 4) {
+    for (int i = 0; i < kParts; ++i) {
         uint16_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = f32_to_bf16_rne(acc[i + j] * f);
+        for (int j = 0; j < 4; ++j) w[j] = f32_to_bf16_rne(acc[i][j] * f);
         u32x2 x;
         __builtin_memcpy(&x, w, 8);
-        *reinterpret_cast<u32x2*>(out + i) = x;
+        *reinterpret_cast<u32x2*>(out + 64 * i) = x;
     }
     if (a.lse && d0 == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
 }
