@@ -64,7 +64,8 @@ __device__ __forceinline__ int used_splits(const AttendArgs& a, const Span& s) {
 // at the segments' ends, so that long and short sequences together keep the
 // card evenly busy to the end.  (A workgroup without work still holds its
 // registers and LDS while it reads a length: 32 one-token steps over 3 ..
-// 131071 slots took 183 us with 14000 such, 113 us planned.)
+// 131071 slots took 178 us with 14000 such, 124 us planned, of which the plan
+// takes 5 us.)
 __device__ __forceinline__ int segment_pages(const AttendArgs& a, const QueryRows& rows) {
     const Span span = rows.span(a.sc, 0, rows.count - 1);
     return max(pages_hi(span) - pages_lo(span), 1);
@@ -231,7 +232,12 @@ template <int D>
 constexpr int kSumRow = D + 4;
 
 // 16 query rows and one item's pages: the wavefronts take every fourth page,
-// decoded from registers, and join in LDS in wavefront order.
+// decoded from registers, and join in LDS in wavefront order.  A long cache is
+// bound by its reads (32 one-token steps of 32 heads over 3 .. 131071 slots of 8
+// heads of 128: 104 us for 575 MB, 5.5 TB/s with what the memory-side cache
+// kept), a short one by the chain of dependent reads and one page's work (777
+// slots: 10 us; at D = 256 that work and 16 rows of sums in 244 registers leave
+// two wavefronts a SIMD: 16 verify rounds of 5 tokens in a window of 1500 take 25 us for 40 MB).
 template <int D>
 __global__ void __launch_bounds__(64 * kWaves, 2)
 kv_attend_rows_kernel(AttendArgs a) {
@@ -251,9 +257,9 @@ kv_attend_rows_kernel(AttendArgs a) {
 
     // Page numbers are read 64 at a time, one a lane, so that a page's loads
     // never wait for the table.  The next page's K is on its way once the
-    // scores are formed, its V once the sums are: one set of registers, and
-    // four wavefronts a SIMD to cover the wait, measured better than two sets
-    // and two wavefronts (see the launch).
+    // scores are formed, its V once the sums are: one set of registers, with
+    // which three wavefronts a SIMD cover the wait at D = 128, measured better
+    // than two sets and two wavefronts.
     int page = begin + wave, ids = -1, at_id = 0, id = -1;
     auto read_ids = [&](int p) {
         const int mine = p + kWaves * lane;
@@ -416,7 +422,11 @@ kv_attend_rows_kernel(AttendArgs a) {
 // apart, joined at the end, where there are no more), and decodes each page once for
 // all of them into LDS as f16: K [64 slots][D], V [D][64 slots], in 16-byte
 // chunks whose place within a row is permuted so that the lanes of a matrix
-// operand's read fall on different banks.
+// operand's read fall on different banks.  Bound by the matrix unit and the
+// vector unit taking turns (a page's 32 products a wavefront take 1024 cycles,
+// its decode share and exponentials about 1400) at the 1.9 GHz that the card
+// holds under them: ragged prompt chunks of 700 .. 4099 tokens over 4100 ..
+// 8192 slots, 32 heads of 128, take 755 us, 906 TFLOP/s.
 template <int D>
 struct PageTiles {
     static constexpr int kBytes = 2 * kPage * D * 2;
@@ -693,7 +703,8 @@ kv_attend_tile_kernel(AttendArgs a) {
 }
 
 // Joins the parts of one row, one workgroup a row: the wavefronts take every
-// fourth part and meet in LDS, both in a fixed order.
+// fourth part and meet in LDS, both in a fixed order.  Bound by latency (1024
+// rows of up to 37 parts: 6.8 us).
 template <int D>
 __global__ void __launch_bounds__(64 * kWaves)
 kv_join_kernel(AttendArgs a) {
@@ -782,6 +793,11 @@ struct Plan {
 
 Plan plan_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
     const int64_t rows = q->max_q * (q->heads / c->kv_heads);
+    // Rows of a kv head: up to 32 in 16-row workgroups, each decoding the pages
+    // for itself, up to 64 in one workgroup with a page's halves on different
+    // wavefronts, else 128 to a workgroup.  32 sequences of 4096 slots, 8 heads
+    // of 128: 32 rows take 73 us, decoded once for all 78; 36 rows 94 and 77; 64 rows 119 and 91
+    // (and 64 rows over 8192 slots 192 us in 128-row workgroups, 144 in these).
     Plan p{};
     p.tile = rows <= 32 ? 0 : rows <= kTileRows / 2 ? kTileRows / 2 : kTileRows;
     const int64_t per_tile = p.tile ? p.tile : kRowTile;

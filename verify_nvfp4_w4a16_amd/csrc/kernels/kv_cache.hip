@@ -1,7 +1,7 @@
 // Filling and reading the paged NVFP4 cache (include/nvfp4_kv.h).
 //
 // V's codes of 8 slots share a dword at each dim, so a workgroup owns whole
-// 8-slot blocks (four for append, one for read) of one sequence and head and
+// 8-slot blocks (a page's eight for append, one for read) of one sequence and head and
 // merges the new rows' nibbles into them, with no atomics.  A thread takes one
 // 16-dim group of a row, then dwords of V at a dim.  Bound by latency at one
 // token a sequence and by the bf16 rows' bytes for prompts.
@@ -127,7 +127,9 @@ __device__ __forceinline__ uint64_t quantise16(const u32x4 lo, const u32x4 hi, c
 
 // A workgroup takes one page's new slots for one head, so that a whole page of
 // new rows is written in whole lines; the heads of a page lie next to each
-// other in the grid, as their rows do in memory.
+// other in the grid, as their rows do in memory.  Prompts are bound by the rows'
+// bytes and by the rounding, which take about as long (32,800 tokens of 8 heads
+// of 128: 50 us for 172 MB, 3.4 TB/s), single tokens by latency (48: 7 us).
 template <int D>
 __global__ void __launch_bounds__(256)
 kv_append_kernel(KvView v, Rows kr, Rows vr, float kt, float vt) {
@@ -206,8 +208,9 @@ __device__ __forceinline__ uint32_t values2(uint32_t w, float scale, float t) {
     return uint32_t(f32_to_bf16_rne(c[0] * scale * t)) | (uint32_t(f32_to_bf16_rne(c[1] * scale * t)) << 16);
 }
 
-// The same units, the other way; rows whose slot is negative or whose page is
-// outside the cache become zeros.
+// Blocks of 8 slots, the other way; rows whose slot is negative or whose page is
+// outside the cache become zeros.  Bound by the rows' bytes (32,800 tokens of 8
+// heads of 128: 31 us for 172 MB, 5.5 TB/s).
 template <int D>
 __global__ void __launch_bounds__(D)
 kv_read_kernel(KvView v, uint16_t* k_out, uint16_t* v_out, float kt, float vt) {

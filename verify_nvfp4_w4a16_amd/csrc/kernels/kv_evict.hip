@@ -101,7 +101,13 @@ struct QueryBlock {
     }
 };
 
-// PAGES pages a wavefront; all rows that see them pass by, ROWS at a time.
+// PAGES pages a wavefront; all rows that see them pass by, ROWS at a time.  One
+// token's weights are bound by latency and the slots' bytes (16 sequences of 100
+// .. 16383 slots, 8 heads of 128: 13.7 us for 21 MB, most of it weights and
+// their priors), those of many by the exponentials and the products beside the
+// waits of staging (32 tokens of 32 heads over 4 x 9001 .. 32768 slots: 37 us,
+// 590 TFLOP/s; three workgroups a CU, for which a page's sums wait in LDS while
+// the wavefront is at another page, took 39 us where two took 53).
 template <int D, int PAGES, int ROWS>
 __global__ void __launch_bounds__(256, D == 256 ? 2 : 3)
 kv_weights_kernel(WeightArgs a) {
@@ -336,7 +342,9 @@ struct Keys {
     }
 };
 
-// Which slots stay: one workgroup a (sequence, head).
+// Which slots stay: one workgroup a (sequence, head).  Bound by instructions on
+// the CUs that have one (65000 slots of a head: 39 us, of which the first digits
+// take 8 and the numbering 9).
 template <int HELD, int SHARED>
 __global__ void __launch_bounds__(kSelect)
 kv_select_kernel(EvictArgs a) {
@@ -461,7 +469,10 @@ kv_select_kernel(EvictArgs a) {
     }
 }
 
-// The rows that stay, one destination page a workgroup.
+// The rows that stay, one destination page a workgroup.  Bound by its loads: a
+// row's V lies in dwords of 8 slots at each dim, so 8 times its codes are loaded
+// (8 sequences of up to 65000 slots cut to 4000, 8 heads of 128: 40 us for 37
+// MB of pages, of whose sources 52 MB come from beyond L2).
 template <int D>
 constexpr int kMoveThreads = D == 64 ? 128 : 256;
 
@@ -474,15 +485,16 @@ kv_move_kernel(EvictArgs a) {
     __shared__ bool live[kPage];
     const int s = blockIdx.y, tid = threadIdx.x;
     const int h = blockIdx.x % a.v.kv_heads, page = blockIdx.x / a.v.kv_heads;
+    // the length, the kept slots and the page they go to are asked for together
+    const int at = page * kPage + (tid & 63);
+    const int j = max(a.kept[(int64_t(s) * a.v.kv_heads + h) * a.keep + min(at, a.keep - 1)], 0);
+    const int64_t to_page = a.dst_table[int64_t(s) * a.dst_pitch + page];
+    const int id = a.v.page_id(s, min(j / kPage, static_cast<int>(a.v.table_pitch) - 1));
     const int n = min(a.len(s), a.keep);
     if (page * kPage >= n) return;
-    const int64_t to_page = a.dst_table[int64_t(s) * a.dst_pitch + page];
     if (to_page < 0 || to_page >= a.dst_pages) return;
     uint8_t* to = a.dst + (to_page * a.v.kv_heads + h) * R::kBytes;
     if (tid < kPage) {
-        const int at = page * kPage + tid;
-        const int j = at < n ? a.kept[(int64_t(s) * a.v.kv_heads + h) * a.keep + at] : 0;
-        const int id = a.v.page_id(s, j / kPage);
         live[tid] = at < n && a.v.has(id);
         from[tid] = a.v.pages > 0 ? a.v.record_or_first<D>(id, h) : to;   // (a cache without pages has no live slot)
         slot_in[tid] = j % kPage;
@@ -507,11 +519,30 @@ kv_move_kernel(EvictArgs a) {
             vc[i][e] = *reinterpret_cast<const uint32_t*>(from[8 * block + e] + R::v_code(j / 8, dim));
         }
     }
-    for (int i = tid; i < kPage * (D / 16); i += kThreads) {   // scales
-        const int slot = i / (D / 16), g = i % (D / 16), j = slot_in[slot];
-        const uint8_t ks = from[slot][R::k_scale(j, g)], vs = from[slot][R::v_scale(j / 8, g) + j % 8];
-        to[R::k_scale(slot, g)] = live[slot] ? ks : 0;
-        to[R::v_scale(slot / 8, g) + slot % 8] = live[slot] ? vs : 0;
+    // scales, as whole words of the page (a byte at a time: 4 us more of the kernel's 40)
+    constexpr int kPerDims = D / 64;   // bytes of a slot in a word of K's
+    if (tid < 8 * R::kGroups) {        // V: the 8 slots of a block and group
+        const int block = tid / R::kGroups, g = tid % R::kGroups;
+        uint64_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int slot = 8 * block + e, j = slot_in[slot];
+            const uint64_t x = from[slot][R::v_scale(j / 8, g) + j % 8];
+            w |= (live[slot] ? x : 0) << (8 * e);
+        }
+        *reinterpret_cast<uint64_t*>(to + R::v_scale(block, g)) = w;
+    } else if (tid >= kThreads - 64) {   // K: the slots 8 a + r + 4 t + 32 h at a quarter of the dims
+        const int row = (tid & 63) / 4, quarter = tid & 3, slot0 = 8 * (row / 4) + row % 4;
+        uint8_t w[4 * kPerDims];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int slot = slot0 + 32 * (e >> 1) + 4 * (e & 1);
+            uint32_t x = 0;
+            __builtin_memcpy(&x, __builtin_assume_aligned(from[slot] + R::k_scale(slot_in[slot], quarter * kPerDims), kPerDims), kPerDims);
+            x = live[slot] ? x : 0;
+            __builtin_memcpy(w + e * kPerDims, &x, kPerDims);
+        }
+        __builtin_memcpy(__builtin_assume_aligned(to + R::k_scale(slot0, quarter * kPerDims), 4 * kPerDims), w, 4 * kPerDims);
     }
 #pragma unroll
     for (int i = 0; i < kKParts; ++i) {
