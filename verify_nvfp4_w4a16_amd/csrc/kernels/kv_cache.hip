@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../host/kv_shapes.h"
 #include "kv_common.h"
@@ -22,9 +23,13 @@ namespace {
 struct Scale {
     double t, six_t;
     float inverse;   // 1 / (6 t), for a first guess
+    bool near_one;   // quotients can be formed in fp32: neither they nor the scales leave its range
+    bool short_t;    // t has 8 bits, so ties are possible
 };
 
-__device__ __forceinline__ Scale scale_of(float t) { return Scale{double(t), 6.0 * double(t), 1.0f / (6.0f * t)}; }
+__device__ __forceinline__ Scale scale_of(float t) {
+    return Scale{double(t), 6.0 * double(t), 1.0f / (6.0f * t), t > 0x1p-60f && t < 0x1p60f, (f32_bits(t) & 0xffff) == 0};
+}
 
 // The e4m3 code nearest to amax / (6 t), ties to even, saturating at 448.
 __device__ __forceinline__ uint32_t e4m3_code(float amax, const Scale& sc) {
@@ -74,36 +79,11 @@ __device__ __forceinline__ uint32_t reaches(uint32_t mags, uint32_t bound_less_1
     return r;
 }
 
-// One group of 16 of a row: its scale byte and its codes (code i in nibble i).
+// The codes of 16 elements (code i in nibble i) by the boundaries alone.
 // Two elements at a time in halves of a register: three halving steps among
 // the seven boundaries give a code's bits as masks, with no carries and no
-// branches (20 operations an element; comparing with all seven took 40, and the
-// kernel 67 us for 32,800 tokens of 8 heads of 128 against 50 us).
-__device__ __forceinline__ uint64_t quantise16(const u32x4 lo, const u32x4 hi, const Scale& sc, uint32_t* scale) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    uint32_t mag[8];
-    u16x2 most = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        mag[i] = (i < 4 ? lo[i] : hi[i - 4]) & 0x7fff7fffu;
-        u16x2 m;
-        __builtin_memcpy(&m, &mag[i], 4);
-        most = __builtin_elementwise_max(most, m);
-    }
-    uint32_t top = max(uint32_t(most[0]), uint32_t(most[1]));
-    if (top > 0x7f80) {   // a NaN is stored as 0
-        top = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if ((mag[i] & 0xffff) > 0x7f80) mag[i] &= 0xffff0000u;
-            if (mag[i] > 0x7f80ffffu) mag[i] &= 0xffffu;
-            top = max(top, max(mag[i] & 0xffff, mag[i] >> 16));
-        }
-    }
-    const uint32_t s = e4m3_code(bits_f32(top << 16), sc);
-    *scale = s;
-    if (s == 0) return 0;
-    const double big = double(e4m3_f32(s)) * sc.t;
+// branches (20 operations an element).
+__device__ __forceinline__ uint64_t codes_exact(const u32x4 lo, const u32x4 hi, const uint32_t (&mag)[8], double big) {
     // boundaries between the magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6: a tie goes to the even code
     uint32_t b[7] = {least_above<true>(0.25, big), least_above<false>(0.75, big), least_above<true>(1.25, big),
                      least_above<false>(1.75, big), least_above<true>(2.5, big), least_above<false>(3.5, big),
@@ -125,11 +105,89 @@ __device__ __forceinline__ uint64_t quantise16(const u32x4 lo, const u32x4 hi, c
     return uint64_t(codes[1]) << 32 | codes[0];
 }
 
+// Codes -0 made 0.
+__device__ __forceinline__ uint32_t no_minus_zero(uint32_t w) {
+    const uint32_t some = (w | w >> 1 | w >> 2) & 0x11111111u;
+    return w & (some << 3 | 0x77777777u);
+}
+
+// The same codes by quotients in fp32, whose error is below 2^-22, and the
+// conversion to e2m1.
+//  * A tensor scale of 8 bits (a bf16 number, as powers of two are): a boundary
+//    times the scales has at most 15 bits, so an element either is at it or
+//    2^-15 of it away; quotients rounded to 18 bits are then on a boundary or
+//    on its side exactly where the true ones are, and ties are the conversion's.
+//  * Any other: no bf16 number is a tie.  Quotients 2^-20 lower and higher
+//    enclose the true one; where their codes differ the boundaries decide.
+template <bool SHORT>
+__device__ __forceinline__ uint64_t codes_fast(const u32x4 lo, const u32x4 hi, const uint32_t (&mag)[8], double big) {
+    const float inverse = __builtin_amdgcn_rcpf(float(big));
+    const float low = inverse * (1.0f - 0x1p-20f), high = inverse * (1.0f + 0x1p-20f);
+    auto element = [&](int i) { return bits_f32(i % 2 ? (i < 8 ? lo : hi)[i / 2 % 4] & 0xffff0000u : (i < 8 ? lo : hi)[i / 2 % 4] << 16); };
+    auto rounded = [](float x) { return bits_f32((f32_bits(x) + 0x10) & ~0x1fu); };
+    uint32_t w[2] = {0, 0}, v[2] = {0, 0};
+    auto put = [&](auto byte) {
+        constexpr int j = decltype(byte)::value;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float a = element(8 * x + 2 * j), b = element(8 * x + 2 * j + 1);
+            if constexpr (SHORT) {
+                w[x] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[x], rounded(a * inverse), rounded(b * inverse), 1.0f, j);
+            } else {
+                w[x] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[x], a * low, b * low, 1.0f, j);
+                v[x] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v[x], a * high, b * high, 1.0f, j);
+            }
+        }
+    };
+    put(std::integral_constant<int, 0>{});
+    put(std::integral_constant<int, 1>{});
+    put(std::integral_constant<int, 2>{});
+    put(std::integral_constant<int, 3>{});
+    if (!SHORT && (w[0] != v[0] || w[1] != v[1])) return codes_exact(lo, hi, mag, big);
+    return uint64_t(no_minus_zero(w[1])) << 32 | no_minus_zero(w[0]);
+}
+
+// One group of 16 of a row: its scale byte and its codes (code i in nibble i).
+__device__ __forceinline__ uint64_t quantise16(u32x4 lo, u32x4 hi, const Scale& sc, uint32_t* scale) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t mag[8];
+    u16x2 most = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        mag[i] = (i < 4 ? lo[i] : hi[i - 4]) & 0x7fff7fffu;
+        u16x2 m;
+        __builtin_memcpy(&m, &mag[i], 4);
+        most = __builtin_elementwise_max(most, m);
+    }
+    uint32_t top = max(uint32_t(most[0]), uint32_t(most[1]));
+    if (top > 0x7f80) {   // a NaN is stored as 0
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t here = ~0u;
+            if ((mag[i] & 0xffff) > 0x7f80) here &= 0xffff0000u;
+            if (mag[i] > 0x7f80ffffu) here &= 0xffffu;
+            mag[i] &= here;
+            if (i < 4)
+                lo[i] &= here;
+            else
+                hi[i - 4] &= here;
+            top = max(top, max(mag[i] & 0xffff, mag[i] >> 16));
+        }
+    }
+    const uint32_t s = e4m3_code(bits_f32(top << 16), sc);
+    *scale = s;
+    if (s == 0) return 0;
+    const double big = double(e4m3_f32(s)) * sc.t;
+    if (!sc.near_one) return codes_exact(lo, hi, mag, big);
+    return sc.short_t ? codes_fast<true>(lo, hi, mag, big) : codes_fast<false>(lo, hi, mag, big);
+}
+
 // A workgroup takes one page's new slots for one head, so that a whole page of
 // new rows is written in whole lines; the heads of a page lie next to each
 // other in the grid, as their rows do in memory.  Prompts are bound by the rows'
-// bytes and by the rounding, which take about as long (32,800 tokens of 8 heads
-// of 128: 50 us for 172 MB, 3.4 TB/s), single tokens by latency (48: 7 us).
+// bytes (32,800 tokens of 8 heads of 128: 46 us for 172 MB, 3.7 TB/s; 50 us with
+// the codes by the boundaries alone), single tokens by latency (48: 6 us).
 template <int D>
 __global__ void __launch_bounds__(256)
 kv_append_kernel(KvView v, Rows kr, Rows vr, float kt, float vt) {

@@ -472,7 +472,7 @@ kv_select_kernel(EvictArgs a) {
 // The rows that stay, one destination page a workgroup.  Bound by its loads: a
 // row's V lies in dwords of 8 slots at each dim, so 8 times its codes are loaded
 // (8 sequences of up to 65000 slots cut to 4000, 8 heads of 128: 40 us for 37
-// MB of pages, of whose sources 52 MB come from beyond L2).
+// MB of pages, of whose sources 104 MB come from beyond L2).
 template <int D>
 constexpr int kMoveThreads = D == 64 ? 128 : 256;
 
