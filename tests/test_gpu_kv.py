@@ -278,6 +278,34 @@ def test_append_and_read(lens, new, heads, d):
                 assert np.array_equal(a[n:], b[n:])
 
 
+@pytest.mark.parametrize("t", [2.0 ** -7, 1.2421875 * 2.0 ** -5, 1.001953125 * 2.0 ** -4, 2.7e-3, 1.0 / 3.0, 2.0 ** -59, 2.0 ** 59,
+                               2.0 ** -61, 3.3e-21, 7.7e20, 2.0 ** -110])
+def test_append_codes_at_and_beside_the_boundaries(t):
+    """Every boundary between two codes, its bf16 neighbours on both sides, at tensor scales of
+    few and of many bits, within and beyond the range in which quotients are formed in fp32."""
+    d, heads, n = 128, 1, 192
+    t = float(np.float32(t))
+    g = workload.rng(90)
+    bounds = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    s = np.array([0x08, 0x1F, 0x2D, 0x38, 0x3B, 0x47, 0x7E, 0x03])[g.integers(0, 8, (n, d // 16))]
+    big = okv.E4M3[s] * t
+    x = bounds[g.integers(0, 7, (n, d // 16, 16))] * big[..., None]
+    x[..., 0] = 6.0 * big                                     # the scale comes out as s, nearly always
+    bits = workload.f32_to_bf16_bits(np.clip(x, 0, 3e38).astype(np.float32)).astype(np.int64)
+    bits[..., 1:] = np.clip(bits[..., 1:] + g.integers(-1, 2, bits[..., 1:].shape), 0, 0x7F7F)
+    bits |= g.integers(0, 2, bits.shape) << 15
+    bits = bits.reshape(n, heads, d).astype(np.uint16)
+    cache = nv.KvCache.empty(3, heads, d, t, t)
+    rows = bf16(bits)
+    nv.kv_append(cache, rows, rows, int32([[2, 0, 1]]), int32([n]), int32([0, n]))
+    torch.cuda.synchronize()
+    codes, scales = okv.quantise_rows(bits[:, 0], t)
+    got = stored(cache.data.cpu().numpy(), [2, 0, 1], n, 0, d)
+    for which in (0, 2):
+        assert np.array_equal(got[which + 1], scales)
+        assert np.array_equal(got[which], codes)
+
+
 def test_append_one_by_one_equals_append_at_once():
     d, heads, n = 128, 2, 75
     bits = workload.activations_bf16(n, 2 * heads * d, 50).reshape(n, 2 * heads, d)
