@@ -76,6 +76,26 @@ def test_sample_equal_logits_take_the_lowest_index():
     assert np.allclose(lp, [-np.log(300), -np.log(10), -np.log(75), 0, 0, -np.log(5)], rtol=2.0 ** -20, atol=0)
 
 
+@pytest.mark.parametrize("vocab,step", [(3000, 0.5), (20000, 0.125), (20001, 2.0), (60000, 1.0)])
+def test_sample_many_equal_logits(vocab, step):
+    """Cuts among hundreds to tens of thousands of tokens of one weight: only the index decides."""
+    g = workload.rng(96)
+    ks = [1, 5, 64, 65, 200, 257, 1000, 2999, 9000, 15000]
+    x = np.round(g.standard_normal((2 * len(ks), vocab)) / step).astype(np.float32) * np.float32(step)
+    params = [(1.0, k, 1.0, 0.0) for k in ks] + [(0.7, k, 0.9, 0.0) for k in ks]
+    u = g.random(2 * len(ks)).astype(np.float32).tolist()
+    _compare(x, u, params, torch.float32, 6)
+
+
+def test_sample_a_temperature_whose_inverse_is_infinite():
+    x = np.full((4, 1000), -3.0, np.float32)
+    x[:, [10, 500, 999]] = 2.0                                # below the maximum nothing has a weight, and all of it stays
+    x[3, 500] = np.nan
+    _, tok, lp = _run(x, [0.0, 0.5, 0.9, 0.6], [(1e-40, 0, 1.0, 0.0), (1e-40, 0, 1.0, 0.0), (1e-40, 3, 1.0, 0.0), (1e-40, 0, 1.0, 0.0)], torch.float32)
+    assert tok.tolist() == [10, 500, 999, 999]
+    assert np.allclose(lp, np.log([1 / 3, 1 / 3, 1 / 3, 1 / 2]), atol=1e-6)
+
+
 def test_sample_ends_of_the_random_number():
     x = np.zeros((4, 5), np.float32)
     x[:, 0] = x[:, 4] = -np.inf
