@@ -449,6 +449,48 @@ def test_evict_of_more_slots_than_registers_hold():
     assert np.array_equal(kept_w.cpu().numpy()[0, 0], w[0, 0, want])
 
 
+@pytest.mark.parametrize("n", [4097, 9001, 16384, 16385, 40000, 65535, 65537])
+@pytest.mark.parametrize("kind", ["ties", "zeros", "one value", "signs"])
+def test_evict_selection_at_every_length(n, kind):
+    """Which slots stay of long sequences, whose keys are held or read again, with many equal weights."""
+    g = workload.rng(73)
+    need = -(-n // PAGE)
+    lens = [n, n - 4000, 700]
+    w = {"ties": lambda: _weights(g, (3, 1, n)), "zeros": lambda: np.zeros((3, 1, n), np.float32),
+         "one value": lambda: np.full((3, 1, n), 0.125, np.float32),
+         "signs": lambda: g.standard_normal((3, 1, n)).astype(np.float32)}[kind]()
+    w[:, :, 5::97] = np.nan
+    w[:, :, 6::89] = -np.inf
+    keep = 1300
+    pages = -(-keep // PAGE)
+    cache = nv.KvCache.empty(need + 3 * pages, 1, 64, 1.0, 1.0)
+    table = int32(np.tile(np.arange(need), (3, 1)))           # the sequences read the same pages
+    dst = int32(need + np.arange(3 * pages).reshape(3, pages))
+    kept, kept_w, new_lens = nv.kv_evict(torch.from_numpy(w).to(DEV), cache, table, int32(lens), dst, keep, sink=7, recent=64)
+    kept, kept_w = kept.cpu().numpy(), kept_w.cpu().numpy()
+    assert new_lens.tolist() == [min(x, keep) for x in lens]
+    for i, x in enumerate(lens):
+        want = okv.evict(w[i, 0], x, keep, 7, 64)
+        assert np.array_equal(kept[i, 0, :len(want)], want), i
+        assert np.array_equal(kept_w[i, 0, :len(want)], w[i, 0, want], equal_nan=True)
+
+
+def test_slot_weights_do_not_depend_on_the_launch():
+    # a large bound on the lengths gives a wavefront two pages, a small one one; rows of more blocks are added in order
+    lens = [300, 0, 64, 65, 129, 257] * 6
+    c = Paged(lens, 8, 64, 64)
+    wide = int32(np.pad(c.table_t.cpu().numpy(), ((0, 0), (0, 40))))
+    for new in (1, 7):
+        news = [min(new, n) for n in lens]
+        q = bf16(_query_bits(sum(news), 16, 64, 65))
+        args = (c.cache, wide, c.lens_t, starts(news), new)
+        _, lse = nv.kv_attention(q, *args, 320)
+        small = nv.kv_weights(q, lse, *args, 320)
+        large = nv.kv_weights(q, lse, *args, 2500)
+        torch.cuda.synchronize()
+        assert torch.equal(small, large[:, :, :320]) and not large[:, :, 320:].any()
+
+
 def test_sequences_beyond_the_host_s_bounds_are_held_to_them():
     # nothing is read or written past what the launch was sized for
     c = Paged([300, 40], 1, 64, 91)
