@@ -491,6 +491,26 @@ def test_slot_weights_do_not_depend_on_the_launch():
         assert torch.equal(small, large[:, :, :320]) and not large[:, :, 320:].any()
 
 
+@pytest.mark.parametrize("d,new,kw", [(64, 40, {}), (128, 70, dict(window=90)), (256, 40, dict(softcap=9.0)), (128, 64, dict(causal=False))])
+def test_slot_weights_of_many_rows_in_every_launch(d, new, kw):
+    # few pages: a workgroup's wavefronts share one; more: a page each; many and one block of rows: four each
+    lens = [300, 64, 129, 257, 65, 0] * 6
+    c = Paged(lens, 8, d, 66)
+    wide = int32(np.pad(c.table_t.cpu().numpy(), ((0, 0), (0, 20))))
+    news = [min(new, n) for n in lens]
+    q = bf16(_query_bits(sum(news), 16, d, 67))
+    args = (c.cache, wide, c.lens_t, starts(news), new)
+    _, lse = nv.kv_attention(q, *args, 320, **kw)
+    one = nv.kv_weights(q, lse, *args, 320, **kw)
+    four = nv.kv_weights(q, lse, *args, 1600, **kw)
+    part = sum(news[:3])
+    shared = nv.kv_weights(q[:part], lse[:part], c.cache, wide[:3].contiguous(), c.lens_t[:3], starts(news[:3]), new, 320, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(one, four[:, :, :320]) and not four[:, :, 320:].any()
+    # sums of at most 140 numbers that are not negative, in two orders: 2 * 140 * 2^-24 of the sum
+    assert torch.allclose(shared, one[:3], rtol=2e-5, atol=0)
+
+
 def test_sequences_beyond_the_host_s_bounds_are_held_to_them():
     # nothing is read or written past what the launch was sized for
     c = Paged([300, 40], 1, 64, 91)

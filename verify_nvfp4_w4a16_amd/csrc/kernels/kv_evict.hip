@@ -101,34 +101,37 @@ struct QueryBlock {
     }
 };
 
-// PAGES pages a wavefront; all rows that see them pass by, ROWS at a time.  One
+// PAGES pages a wavefront, or SHARE wavefronts' together, which then take the
+// tiles of rows in turn; all rows that see them pass by, ROWS at a time (with
+// more than one page a wavefront there are no more than ROWS).  One
 // token's weights are bound by latency and the slots' bytes (16 sequences of 100
 // .. 16383 slots, 8 heads of 128: 13.7 us for 21 MB, most of it weights and
 // their priors), those of many by the exponentials and the products beside the
 // waits of staging (32 tokens of 32 heads over 4 x 9001 .. 32768 slots: 37 us,
 // 590 TFLOP/s; three workgroups a CU, for which a page's sums wait in LDS while
 // the wavefront is at another page, took 39 us where two took 53).
-template <int D, int PAGES, int ROWS>
+template <int D, int PAGES, int ROWS, int SHARE>
 __global__ void __launch_bounds__(256, D == 256 ? 2 : 3)
 kv_weights_kernel(WeightArgs a) {
     using Block = QueryBlock<D, ROWS>;
+    constexpr int kGroup = 4 / SHARE * PAGES;   // pages of the workgroup
     __shared__ Block block;
     __shared__ f32x4 sums[4][PAGES][64];   // of a wavefront's pages, a lane's slots: in registers only while their page is
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, b = lane >> 4;
     const int s = blockIdx.y, hk = blockIdx.x % a.v.kv_heads;
-    const int group0 = blockIdx.x / a.v.kv_heads * 4 * PAGES;     // the workgroup's first page
-    const int page0 = group0 + wave * PAGES;
+    const int group0 = blockIdx.x / a.v.kv_heads * kGroup;     // the workgroup's first page
+    const int page0 = group0 + wave / SHARE * PAGES;
     const int64_t out = (int64_t(s) * a.v.kv_heads + hk) * a.max_kv;
     if (group0 * kPage >= a.v.len(s)) {   // beyond the sequence: most workgroups where lengths differ much
-        for (int64_t j = int64_t(group0) * kPage + threadIdx.x; j < min(a.max_kv, int64_t(group0 + 4 * PAGES) * kPage); j += 256)
+        for (int64_t j = int64_t(group0) * kPage + threadIdx.x; j < min(a.max_kv, int64_t(group0 + kGroup) * kPage); j += 256)
             a.weights[out + j] = 0.0f;
         return;
     }
     const QueryRows rows(a.v, a.sc, s);
 
     // rows that see any slot of the workgroup's pages
-    const int first = group0 * kPage, past = first + 4 * PAGES * kPage, shift = rows.len - rows.new_tokens;
+    const int first = group0 * kPage, past = first + kGroup * kPage, shift = rows.len - rows.new_tokens;
     int i_lo = 0, i_hi = first < rows.len && a.v.pages > 0 ? rows.new_tokens : 0;
     if (a.sc.causal) i_lo = max(0, first - shift);
     if (a.sc.window > 0) i_hi = min(i_hi, max(0, past - 1 + a.sc.window - shift));
@@ -142,74 +145,98 @@ kv_weights_kernel(WeightArgs a) {
     auto my_slot = [&](int x) { return (page0 + x) * kPage + KRegs<D>::slot(b, n); };   // that this lane writes
 #pragma unroll
     for (int x = 0; x < PAGES; ++x) sums[wave][x][lane] = f32x4{0, 0, 0, 0};
-    for (int r0 = r_lo; r0 < r_hi; r0 += Block::kRows) {
+    auto decode = [&](f16x8 (&k)[4][D / 32]) {
+        raw.template decode<0, 0>(k[0]);
+        raw.template decode<1, 0>(k[1]);
+        raw.template decode<2, 0>(k[2]);
+        raw.template decode<3, 0>(k[3]);
+    };
+    // the rows r0 .. of the block over page x, whose K is k
+    auto look = [&](const f16x8 (&k)[4][D / 32], int x, int r0) {
+        const int tiles = (min(r_hi - r0, Block::kRows) + 15) / 16;
+        if (!a.v.has(__builtin_amdgcn_readlane(ids, x))) return;
+        f32x4 sum = sums[wave][x][lane];
+        const int base = (page0 + x) * kPage;
+        // Tokens in order see ever later slots: those from see_lo on and before see_hi see
+        // all of the page, and so do their rows (and those past the last, which give nothing).
+        const int see_lo = a.sc.causal ? min(max(base + kPage - 1 - shift, 0), rows.new_tokens) : 0;
+        const int see_hi = a.sc.window > 0 ? max(base + a.sc.window - shift, 0) : rows.new_tokens;
+        const bool simple = a.sc.cap == 0.0f && base + kPage <= rows.len;
+        const int full_lo = simple ? (see_lo * rows.group - r0 + 15) / 16 : tiles;   // in tiles
+        const int full_hi = see_hi >= rows.new_tokens ? tiles : (see_hi * rows.group - r0) / 16;
+        const int t_lo = min(max(full_lo, 0), tiles), t_hi = max(min(full_hi, tiles), t_lo);
+
+        auto products = [&](int t, f32x4 (&z)[4]) {
+#pragma unroll
+            for (int ht = 0; ht < 4; ++ht) z[ht] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const f16x8 q = block.q[Block::chunk_at(16 * t + n, b * (D / 32) + i)];
+#pragma unroll
+                for (int ht = 0; ht < 4; ++ht) z[ht] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q, k[ht][i], z[ht], 0, 0, 0);
+            }
+        };
+        auto add_full = [&](int t, const f32x4 (&z)[4]) {
+            const f32x4 f = *reinterpret_cast<const f32x4*>(block.f + 16 * t + 4 * b);
+            const f32x4 lse = *reinterpret_cast<const f32x4*>(block.lse + 16 * t + 4 * b);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int ht = 0; ht < 4; ++ht) sum[ht] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[ht][c], f[c], -lse[c]));
+        };
+        auto add_seen = [&](int t, const f32x4 (&z)[4]) {
+            int n = lane & 15, b = lane >> 4;
+            asm volatile("" : "+v"(n), "+v"(b));   // what follows from them is found anew: kept beside the tiles it would not fit the registers
+            const f32x4 f = *reinterpret_cast<const f32x4*>(block.f + 16 * t + 4 * b);
+            const f32x4 lse = *reinterpret_cast<const f32x4*>(block.lse + 16 * t + 4 * b);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int lo = block.lo[16 * t + 4 * b + c], hi = block.hi[16 * t + 4 * b + c];
+                float y[4] = {z[0][c], z[1][c], z[2][c], z[3][c]};
+                a.sc.shape(y, f[c]);
+#pragma unroll
+                for (int ht = 0; ht < 4; ++ht) {
+                    const int slot = base + KRegs<D>::slot(ht, n);
+                    const float p = __builtin_amdgcn_exp2f(y[ht] - lse[c]);
+                    sum[ht] += slot >= lo && slot < hi ? p : 0.0f;
+                }
+            }
+        };
+        f32x4 z[4];
+        int t = wave % SHARE;
+#pragma unroll 1
+        for (; t < t_lo; t += SHARE) products(t, z), add_seen(t, z);
+#pragma unroll 1
+        for (; t < t_hi; t += SHARE) products(t, z), add_full(t, z);
+#pragma unroll 1
+        for (; t < tiles; t += SHARE) products(t, z), add_seen(t, z);
+        sums[wave][x][lane] = sum;
+    };
+    auto stage = [&](int r0) {
         if (r0 != r_lo) __syncthreads();
         block.fill(a, rows, hk, r0);
         __syncthreads();
-        const int tiles = (min(r_hi - r0, Block::kRows) + 15) / 16;
+    };
+    if constexpr (PAGES == 1) {   // decoded once for all rows
+        f16x8 k[4][D / 32];
+        if (r_lo < r_hi) decode(k);
+        for (int r0 = r_lo; r0 < r_hi; r0 += Block::kRows) {
+            stage(r0);
+            look(k, 0, r0);
+        }
+    } else if (r_lo < r_hi) {     // one block has all rows
+        stage(r_lo);
 #pragma unroll 1
         for (int x = 0; x < PAGES; ++x) {
             f16x8 k[4][D / 32];
-            raw.template decode<0, 0>(k[0]);
-            raw.template decode<1, 0>(k[1]);
-            raw.template decode<2, 0>(k[2]);
-            raw.template decode<3, 0>(k[3]);
-            raw.load(a.v.record_or_first<D>(__builtin_amdgcn_readlane(ids, (x + 1) % PAGES), hk), n, b);   // also for the next block of rows
-            if (!a.v.has(__builtin_amdgcn_readlane(ids, x))) continue;
-            f32x4 sum = sums[wave][x][lane];
-            const int base = (page0 + x) * kPage;
-            // Tokens in order see ever later slots: those from see_lo on and before see_hi see
-            // all of the page, and so do their rows (and those past the last, which give nothing).
-            const int see_lo = a.sc.causal ? min(max(base + kPage - 1 - shift, 0), rows.new_tokens) : 0;
-            const int see_hi = a.sc.window > 0 ? max(base + a.sc.window - shift, 0) : rows.new_tokens;
-            const bool simple = a.sc.cap == 0.0f && base + kPage <= rows.len;
-            const int full_lo = simple ? (see_lo * rows.group - r0 + 15) / 16 : tiles;   // in tiles
-            const int full_hi = see_hi >= rows.new_tokens ? tiles : (see_hi * rows.group - r0) / 16;
-            const int t_lo = min(max(full_lo, 0), tiles), t_hi = max(min(full_hi, tiles), t_lo);
-
-            auto products = [&](int t, f32x4 (&z)[4]) {
-#pragma unroll
-                for (int ht = 0; ht < 4; ++ht) z[ht] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const f16x8 q = block.q[Block::chunk_at(16 * t + n, b * (D / 32) + i)];
-#pragma unroll
-                    for (int ht = 0; ht < 4; ++ht) z[ht] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q, k[ht][i], z[ht], 0, 0, 0);
-                }
-            };
-            auto add_full = [&](int t, const f32x4 (&z)[4]) {
-                const f32x4 f = *reinterpret_cast<const f32x4*>(block.f + 16 * t + 4 * b);
-                const f32x4 lse = *reinterpret_cast<const f32x4*>(block.lse + 16 * t + 4 * b);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int ht = 0; ht < 4; ++ht) sum[ht] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[ht][c], f[c], -lse[c]));
-            };
-            auto add_seen = [&](int t, const f32x4 (&z)[4]) {
-                const f32x4 f = *reinterpret_cast<const f32x4*>(block.f + 16 * t + 4 * b);
-                const f32x4 lse = *reinterpret_cast<const f32x4*>(block.lse + 16 * t + 4 * b);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int lo = block.lo[16 * t + 4 * b + c], hi = block.hi[16 * t + 4 * b + c];
-                    float y[4] = {z[0][c], z[1][c], z[2][c], z[3][c]};
-                    a.sc.shape(y, f[c]);
-#pragma unroll
-                    for (int ht = 0; ht < 4; ++ht) {
-                        const int slot = base + KRegs<D>::slot(ht, n);
-                        const float p = __builtin_amdgcn_exp2f(y[ht] - lse[c]);
-                        sum[ht] += slot >= lo && slot < hi ? p : 0.0f;
-                    }
-                }
-            };
-            f32x4 z[4];
-#pragma unroll 1
-            for (int t = 0; t < t_lo; ++t) products(t, z), add_seen(t, z);
-#pragma unroll 1
-            for (int t = t_lo; t < t_hi; ++t) products(t, z), add_full(t, z);
-#pragma unroll 1
-            for (int t = t_hi; t < tiles; ++t) products(t, z), add_seen(t, z);
-            sums[wave][x][lane] = sum;
+            decode(k);
+            raw.load(a.v.record_or_first<D>(__builtin_amdgcn_readlane(ids, min(x + 1, PAGES - 1)), hk), n, b);
+            look(k, x, r_lo);
         }
+    }
+    if constexpr (SHARE > 1) {
+        __syncthreads();
+        if (wave % SHARE > 0) return;
     }
     // a lane of group b has tile b's slot n of each page
     float before[PAGES];
@@ -218,6 +245,8 @@ kv_weights_kernel(WeightArgs a) {
 #pragma unroll
     for (int x = 0; x < PAGES; ++x) {
         f32x4 sum = sums[wave][x][lane];
+#pragma unroll
+        for (int w = 1; w < SHARE; ++w) sum += sums[wave + w][x][lane];
 #pragma unroll
         for (int ht = 0; ht < 4; ++ht) {
             sum[ht] += __shfl_xor(sum[ht], 16);
@@ -234,17 +263,24 @@ int launch_weights(const WeightArgs& a, int64_t rows, hipStream_t st) {
     // Up to 32 rows a kv head: one page a wavefront where the cache has few, so
     // that all are under way at once, two where it has many (16 sequences of
     // 100 .. 16383 slots, 8 heads: 15.4 us with one, 13.7 with two, 14.3 with
-    // four; 4 sequences: 7.1, 8.3, 10.0).  More rows are worth staging 128 at a time for
-    // the four pages of a wavefront (64 at D = 256, where LDS holds no more
-    // for two workgroups).
-    const bool many = rows > 32;
-    const int64_t all = (a.max_kv + kPage - 1) / kPage * a.v.kv_heads * a.v.seqs;
-    const int pages = many ? 4 : all > 8192 ? 2 : 1;
-    const int64_t slots = 4 * kPage * pages;
-    const int64_t blocks = (a.max_kv + slots - 1) / slots * a.v.kv_heads;
+    // four; 4 sequences: 7.1, 8.3, 10.0).
+    // More rows: one page a wavefront, decoded once for all blocks of rows
+    // (4 sequences of 4096 slots, 2048 rows of 8 heads: 139 us; a page a workgroup
+    // 227, four a wavefront 396).  One a workgroup, whose wavefronts take every fourth
+    // tile of the rows, where there are fewer workgroups than CUs (1 sequence:
+    // 110, 74, 394).  Four a wavefront where one block holds the rows, which is then
+    // staged once for all of them, and the card is full with such (16384 slots,
+    // 128 rows: 39, 75, 31).
+    constexpr int kRows = D == 256 ? 64 : 128;   // LDS holds no more for two workgroups at D = 256
+    const int64_t each = (a.max_kv + kPage - 1) / kPage, all = each * a.v.kv_heads * a.v.seqs;
+    const int pages = rows <= 32 ? (all > 8192 ? 8 : 4) : all < 4 * 256 ? 1 : rows <= kRows && all >= 16 * 256 ? 16 : 4;   // of a workgroup
+    const int64_t blocks = (each + pages - 1) / pages * a.v.kv_heads;
     if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL((many ? kv_weights_kernel<D, 4, D == 256 ? 64 : 128> : pages == 1 ? kv_weights_kernel<D, 1, 32> : kv_weights_kernel<D, 2, 32>),
-                       dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(256), 0, st, a);
+    const auto kernel = rows <= 32   ? (pages == 4 ? kv_weights_kernel<D, 1, 32, 1> : kv_weights_kernel<D, 2, 32, 1>)
+                        : pages == 1 ? kv_weights_kernel<D, 1, kRows, 4>
+                        : pages == 4 ? kv_weights_kernel<D, 1, kRows, 1>
+                                     : kv_weights_kernel<D, 4, kRows, 1>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
