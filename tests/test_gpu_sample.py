@@ -87,6 +87,26 @@ def test_sample_many_equal_logits(vocab, step):
     _compare(x, u, params, torch.float32, 6)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [3, 8, 9, 1003, 16384, 16391, 33001])
+def test_sample_rows_at_any_address(vocab, dtype):
+    # rows read 16 bytes at a time from wherever they begin give what whole ones give
+    g = workload.rng(97)
+    n = len(PARAMS)
+    wide = torch.from_numpy((g.standard_normal((n, vocab + 11)) * 3).astype(np.float32)).to(DEV).to(dtype)
+    wide[:, 5 + vocab:] = 100.0                               # beyond a row lies what would win
+    wide[:, :5] = 100.0
+    u = torch.from_numpy(g.random(n).astype(np.float32)).to(DEV)
+    t = [torch.tensor(c, dtype=torch.int32 if i == 1 else torch.float32, device=DEV) for i, c in enumerate(zip(*PARAMS))]
+    rows = wide[:, 5:5 + vocab]
+    padded = torch.full((n, (vocab + 15) // 8 * 8), float("-inf"), device=DEV, dtype=dtype)
+    padded[:, :vocab] = rows
+    got, lp = nv.sample(rows, u, *t)
+    want, want_lp = nv.sample(padded, u, *t)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(lp, want_lp)
+
+
 def test_sample_a_temperature_whose_inverse_is_infinite():
     x = np.full((4, 1000), -3.0, np.float32)
     x[:, [10, 500, 999]] = 2.0                                # below the maximum nothing has a weight, and all of it stays

@@ -43,7 +43,6 @@ constexpr unsigned long long kOneToken = 1ull << kMassBits;
 constexpr int kListMax = 8192;
 constexpr int kShort = 256;                  // list length up to which every token is ranked against all
 constexpr uint32_t kNoKey = 0xffffffffu;
-constexpr uint32_t kNegInf = 0xff800000u, kNegInf2 = 0xff80ff80u;   // -inf in fp32, twice in bf16
 constexpr int kMaxThreads = 256;             // launch 1: pieces of 4096
 
 struct SampleArgs {
@@ -92,9 +91,11 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int r, int si
 }
 
 // The thread's kPer logits of the THREADS * kPer from `begin` on, 16 bytes at a
-// time where rows are aligned for it and whole (WIDE).  load() only loads, from
-// places held to the row so that it never branches; clip() makes -inf of what lies
-// beyond the vocabulary; raw() gives element e, token token_at(e).
+// time where a row has as many (WIDE), at whatever address it begins.  load()
+// only loads, from places held to the row so that it never branches; clip()
+// then puts what the row's last 16 bytes hold in their places, and -inf beyond
+// the vocabulary; raw() gives element e, token token_at(e).  (A value at a time
+// where rows are not whole 16 bytes: 51475 bf16 logits took 32 us instead of 24.)
 template <bool F32, bool WIDE, int THREADS>
 struct Piece {
     static constexpr int kVec = WIDE ? (F32 ? 4 : 8) : 1;
@@ -109,7 +110,7 @@ struct Piece {
         for (int v = 0; v < kPer / kVec; ++v) {
             const int i = min(token_at(begin, v * kVec), vocab - kVec);
             if constexpr (WIDE)
-                wide[v] = load16(static_cast<const char*>(row) + int64_t(i) * (F32 ? 4 : 2));
+                __builtin_memcpy(&wide[v], static_cast<const char*>(row) + int64_t(i) * (F32 ? 4 : 2), 16);
             else
                 one[v] = F32 ? static_cast<const float*>(row)[i] : bf16_to_f32(static_cast<const uint16_t*>(row)[i]);
         }
@@ -126,13 +127,25 @@ struct Piece {
     __device__ __forceinline__ void clip(int begin, int vocab) {
         if (token_at(begin, kPer - 1) < vocab) return;   // this thread's last
 #pragma unroll
-        for (int e = 0; e < kPer; e += kVec) {
-            if (token_at(begin, e) < vocab) continue;   // 16 bytes are inside or outside whole
-            if constexpr (WIDE)
-                wide[e / kVec] = F32 ? u32x4{kNegInf, kNegInf, kNegInf, kNegInf}
-                                     : u32x4{kNegInf2, kNegInf2, kNegInf2, kNegInf2};
-            else
-                one[e] = -INFINITY;
+        for (int v = 0; v < kPer / kVec; ++v) {
+            const int past = token_at(begin, v * kVec) + kVec - vocab;   // elements beyond the row
+            if (past <= 0) continue;
+            if constexpr (WIDE) {
+                // what was loaded is the row's last kVec: the element wanted first lies `past` later
+                constexpr int kBits = F32 ? 32 : 16;
+                const uint64_t fill = F32 ? 0xff800000ff800000u : 0xff80ff80ff80ff80u;   // -inf
+                uint64_t lo = uint64_t(wide[v][1]) << 32 | wide[v][0], hi = uint64_t(wide[v][3]) << 32 | wide[v][2];
+                int shift = min(past, kVec) * kBits;
+                if (shift >= 64) lo = hi, hi = fill, shift -= 64;
+                if (shift >= 64) lo = fill, shift -= 64;
+                if (shift > 0) {
+                    lo = lo >> shift | hi << (64 - shift);
+                    hi = hi >> shift | fill << (64 - shift);
+                }
+                wide[v] = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+            } else {
+                one[v] = -INFINITY;
+            }
         }
     }
 };
@@ -654,6 +667,7 @@ sample_draw_kernel(SampleArgs a) {
                 while (c < a.chunks) {
                     const int next = next_chunk(c + 1);
                     ahead.load(row, min(next, a.chunks - 1) * kChunk, a.vocab);   // also past the end, so that no wait depends on a branch
+                    piece.clip(c * kChunk, a.vocab);
                     uint64_t hits[kPer];   // of the wavefront: places in the list are taken for all its tokens at once
                     int many_hits = 0;
 #pragma unroll
@@ -837,10 +851,7 @@ extern "C" int nvfp4_sample(const void* logits, int logits_type, int64_t rows, i
                        reinterpret_cast<float*>(ws + bins_bytes(rows, chunks)),
                        reinterpret_cast<unsigned long long*>(ws)};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    // 16-byte loads where every row begins on 16 bytes and is whole ones (the head's 151552 fp32 logits are)
-    const bool f32 = logits_type == NVFP4_LOGITS_F32;
-    const int vec = f32 ? 4 : 8;
-    const bool wide = !misaligned(logits, 16) && vocab % vec == 0 && (rows == 1 || pitch % vec == 0);
+    const bool f32 = logits_type == NVFP4_LOGITS_F32, wide = vocab >= (f32 ? 4 : 8);
     if (f32) return wide ? launch_sample<true, true>(a, rows, s) : launch_sample<true, false>(a, rows, s);
     return wide ? launch_sample<false, true>(a, rows, s) : launch_sample<false, false>(a, rows, s);
 }
