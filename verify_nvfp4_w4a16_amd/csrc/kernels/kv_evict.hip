@@ -509,8 +509,10 @@ kv_select_kernel(EvictArgs a) {
 // row's V lies in dwords of 8 slots at each dim, so 8 times its codes are loaded
 // (8 sequences of up to 65000 slots cut to 4000, 8 heads of 128: 40 us for 37
 // MB of pages, of whose sources 104 MB come from beyond L2).
+// Threads of it: 16 bytes of K and 4 dwords of V each (at D = 256 half as many
+// threads took 19.9 us instead of 16.0 for one sequence cut to 256 slots).
 template <int D>
-constexpr int kMoveThreads = D == 64 ? 128 : 256;
+constexpr int kMoveThreads = 2 * D;
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads<D>)
