@@ -24,9 +24,9 @@
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kRowTile = 16;          // few rows: of one workgroup
-constexpr int kTileRows = 32 * kWaves;  // many rows
-constexpr int kItems = 2048;
+constexpr int kRowTile = 16;             // few rows: of one workgroup
+constexpr int kTileRows = 32 * kWaves;   // many rows
+constexpr int kItems = 2048;             // whole chunks of a plan (1280 to 3584 took the same within 3 %)
 
 // Scores may outgrow the running maximum by this much (in powers of two)
 // before the sums are rescaled: the weights then stay below 2^8, within f16.
