@@ -20,7 +20,7 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libnvfp4_w4a16.so")
 ARCH = "gfx950"
 
-HOST_SOURCES = ["host/pack.cpp", "host/tiles.cpp", "host/kv_shapes.cpp"]
+HOST_SOURCES = ["host/pack.cpp", "host/tiles.cpp", "host/kv_shapes.cpp", "host/kv_plan.cpp"]
 HIP_SOURCES = ["kernels/nvfp4_linear.hip", "kernels/nvfp4_gemm.hip", "kernels/nvfp4_fused.hip",
                "kernels/w8a16.hip", "kernels/read_probe.hip", "kernels/library_gemm.hip",
                "kernels/kv_cache.hip", "kernels/kv_attention.hip", "kernels/kv_evict.hip", "kernels/sample.hip"]

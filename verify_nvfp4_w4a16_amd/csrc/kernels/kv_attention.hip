@@ -13,9 +13,9 @@
 // workgroup and over workgroups, joined in a fixed order.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
 #include <cstdint>
 
+#include "../host/kv_plan.h"
 #include "../host/kv_shapes.h"
 #include "kv_common.h"
 #include "kv_scores.h"
@@ -23,10 +23,8 @@
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kRowTile = 16;             // few rows: of one workgroup
-constexpr int kTileRows = 32 * kWaves;   // many rows
-constexpr int kItems = 2048;             // whole chunks of a plan (1280 to 3584 took the same within 3 %)
+constexpr int kWaves = nvfp4::kKvWaves, kRowTile = nvfp4::kKvRowTile, kTileRows = nvfp4::kKvTileRows;
+constexpr int kItems = nvfp4::kKvItems;
 
 // Scores may outgrow the running maximum by this much (in powers of two)
 // before the sums are rescaled: the weights then stay below 2^8, within f16.
@@ -493,8 +491,6 @@ struct PageShare {
     }
 };
 
-constexpr int kMaxSplits = 1024;
-
 // Order of N matrix instructions and the LDS reads of their operands: kAhead
 // reads ahead of the instruction that takes them.  Left alone the compiler reads
 // one ahead, and each instruction (32 cycles) waits most of a read's latency.
@@ -780,62 +776,6 @@ kv_join_kernel(AttendArgs a) {
     if (a.lse && tid == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
 }
 
-// How a call is laid out: 16-row or 128-row workgroups, and over how many
-// workgroups each sequence's pages are split.
-struct Plan {
-    int tile;            // rows of a many-row workgroup, 0: few rows
-    int64_t row_tiles;
-    int splits, chunk;   // tile
-    bool planned;        // else
-    int items;
-    int64_t part_rows;   // rows of partial results
-};
-
-Plan plan_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
-    const int64_t rows = q->max_q * (q->heads / c->kv_heads);
-    // Rows of a kv head: up to 32 in 16-row workgroups, each decoding the pages
-    // for itself, up to 64 in one workgroup with a page's halves on different
-    // wavefronts, else 128 to a workgroup.  32 sequences of 4096 slots, 8 heads
-    // of 128: 32 rows take 73 us, decoded once for all 78; 36 rows 94 and 77; 64 rows 119 and 91
-    // (and 64 rows over 8192 slots 192 us in 128-row workgroups, 144 in these).
-    Plan p{};
-    p.tile = rows <= 32 ? 0 : rows <= kTileRows / 2 ? kTileRows / 2 : kTileRows;
-    const int64_t per_tile = p.tile ? p.tile : kRowTile;
-    p.row_tiles = (rows + per_tile - 1) / per_tile;
-    const int64_t base = std::max<int64_t>(s->seqs * c->kv_heads * p.row_tiles, 1);
-    int64_t slots = q->max_kv;
-    if (q->window > 0) slots = std::min(slots, q->window + q->max_q);
-    const int64_t pages = std::max<int64_t>((slots + kPage - 1) / kPage + (q->window > 0), 1);
-    // Pages of a workgroup: as many as leave 512, which fills the card twice, and
-    // a page a wavefront at least.  Few rows take 32 at most, so that the last to
-    // end is not late by much, and all of 16, which spares the second launch that
-    // joins parts: one sequence of 777 slots takes 9.4 us either way on the card,
-    // and the host one launch less.  (With 8 pages at least, one sequence of 2048
-    // slots took 11.5 us instead of 10.5, at D = 256 16.9 instead of 15.1.)
-    const int64_t low = !p.tile && pages <= 16 ? pages : kWaves, high = p.tile ? pages : std::max<int64_t>(low, 32);
-    const int64_t chunk = std::min(std::max((pages * base + 511) / 512, low), std::max<int64_t>(high, 1));
-    p.splits = static_cast<int>((pages + chunk - 1) / chunk);
-    if (p.tile) {
-        p.splits = std::min(p.splits, kMaxSplits);
-        p.chunk = static_cast<int>((pages + p.splits - 1) / p.splits);
-        p.part_rows = p.splits > 1 ? p.splits * s->total * q->heads : 0;
-    } else {
-        p.chunk = static_cast<int>(chunk);
-        p.planned = p.splits > 2 && base * p.splits > 2048;
-        // planned: at most kItems whole chunks, and a rest a segment
-        p.items = static_cast<int>(p.planned ? std::min(base * p.splits, base + kItems) : base * p.splits);
-        p.part_rows = p.splits > 1 ? int64_t(p.items) * kRowTile : 0;
-    }
-    return p;
-}
-
-int64_t plan_bytes(const nvfp4_kv_seqs_t* s) { return (2 + 2 * s->seqs + 3) / 4 * 16; }
-
-int64_t workspace_bytes_of(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
-    const Plan p = plan_of(c, s, q);
-    return p.part_rows * (c->head_dim + 2) * int64_t(sizeof(float)) + (p.planned ? plan_bytes(s) : 0);
-}
-
 template <int D>
 constexpr size_t rows_lds() {
     return (kWaves * 16 * kSumRow<D> + kWaves * 16 * 2) * sizeof(float);
@@ -858,7 +798,7 @@ bool allow_lds() {
 }
 
 template <int D>
-int launch_attend(const AttendArgs& a, const Plan& plan, hipStream_t st) {
+int launch_attend(const AttendArgs& a, const nvfp4::KvPlan& plan, hipStream_t st) {
     if (plan.tile) {
         // parts of a tile's pages along the slowest axis: those that short sequences do not need come last
         const int64_t blocks = plan.row_tiles * a.v.kv_heads;
@@ -896,7 +836,7 @@ extern "C" int nvfp4_kv_attention_workspace(const nvfp4_kv_cache_t* cache, const
     if ((st = nvfp4::check_kv_cache(cache)) != NVFP4_OK) return st;
     if ((st = nvfp4::check_kv_seqs(seqs, true)) != NVFP4_OK) return st;
     if ((st = nvfp4::check_kv_queries(cache, seqs, queries)) != NVFP4_OK) return st;
-    *bytes = workspace_bytes_of(cache, seqs, queries);
+    *bytes = nvfp4::kv_workspace_bytes(cache, seqs, queries);
     return NVFP4_OK;
 }
 
@@ -910,7 +850,7 @@ extern "C" int nvfp4_kv_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_
     if ((st = nvfp4::check_kv_rows(out, 0, 0, seqs->total)) != NVFP4_OK) return st;
     if ((reinterpret_cast<uintptr_t>(lse) & 3) || (reinterpret_cast<uintptr_t>(workspace) & 15)) return NVFP4_ERR_ALIGN;
     if (seqs->seqs == 0 || seqs->total == 0 || queries->max_q == 0) return NVFP4_OK;
-    const int64_t need = workspace_bytes_of(cache, seqs, queries);
+    const int64_t need = nvfp4::kv_workspace_bytes(cache, seqs, queries);
     if (need > 0 && !workspace) return NVFP4_ERR_NULL;
     if (need > workspace_bytes) return NVFP4_ERR_SCRATCH;
     if ((st = nvfp4::device_setup()) != NVFP4_OK) return st;
@@ -920,13 +860,13 @@ extern "C" int nvfp4_kv_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_
     a.sc = kv_scores(cache, queries);
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    const Plan plan = plan_of(cache, seqs, queries);
+    const nvfp4::KvPlan plan = nvfp4::kv_plan(cache, seqs, queries);
     a.tile = plan.tile;
     a.splits = plan.splits;
     a.chunk = plan.chunk;
     a.row_tiles = static_cast<int>(plan.row_tiles);
     a.plan = plan.planned ? static_cast<int32_t*>(workspace) : nullptr;
-    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + (plan.planned ? plan_bytes(seqs) : 0));
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + (plan.planned ? nvfp4::kv_plan_bytes(seqs) : 0));
     a.part_ml = plan.part_rows > 0 ? a.part_o + plan.part_rows * cache->head_dim : nullptr;
     a.v_scale = cache->v_scale;
     const hipStream_t s = static_cast<hipStream_t>(stream);

@@ -2,6 +2,7 @@
 // the attention kernels and by the one that sums the weights of slots.
 #pragma once
 
+#include "../host/kv_plan.h"
 #include "kv_common.h"
 
 namespace {
@@ -53,7 +54,7 @@ inline KvScores kv_scores(const nvfp4_kv_cache_t* c, const nvfp4_kv_queries_t* q
     s.heads = static_cast<int>(q->heads);
     s.group = static_cast<int>(q->heads / c->kv_heads);
     s.inverse = 0xffffffffu / uint32_t(s.group);
-    s.window = static_cast<int>(q->window < (int64_t(1) << 29) ? q->window : 0);   // no sequence is longer
+    s.window = nvfp4::kv_window(q);
     s.max_q = static_cast<int>(q->max_q);
     s.max_kv = static_cast<int>(q->max_kv);
     s.causal = q->causal;
