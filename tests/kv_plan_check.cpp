@@ -72,7 +72,7 @@ int main() {
     const int64_t windows[] = {0, 1, 63, 64, 65, 1500, 65535, 65536, (int64_t(1) << 29) - 1, int64_t(1) << 29, int64_t(1) << 31,
                                int64_t(1) << 32, big - 65536, big - 1, big};
     const int64_t lens[] = {0, 1, 64, 777, 1025, 2048, 65536, 131071, int64_t(1) << 29};
-    const int64_t news[] = {0, 1, 5, 8, 9, 16, 33, 4099};
+    const int64_t news[] = {0, 1, 5, 8, 9, 16, 33, 4099, int64_t(1) << 24};
     const int64_t seqs[] = {1, 3, 48, 700, 65535};
     for (int64_t w : windows)
         for (int64_t n : lens)

@@ -30,7 +30,8 @@ KvPlan kv_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_
     // and the host one launch less.  (With 8 pages at least, one sequence of 2048
     // slots took 11.5 us instead of 10.5, at D = 256 16.9 instead of 15.1.)
     const int64_t low = !p.tile && pages <= 16 ? pages : kKvWaves, high = p.tile ? pages : std::max<int64_t>(low, 32);
-    const int64_t chunk = std::min(std::max((pages * base + 511) / 512, low), std::max<int64_t>(high, 1));
+    const int64_t many = std::min(base, int64_t(1) << 24);   // more give the most pages too, and the product stays in 64 bits
+    const int64_t chunk = std::min(std::max((pages * many + 511) / 512, low), std::max<int64_t>(high, 1));
     p.splits = static_cast<int>((pages + chunk - 1) / chunk);
     if (p.tile) {
         p.splits = std::min(p.splits, kKvMaxSplits);
