@@ -28,3 +28,49 @@ def test_attention_with_a_window_that_no_sequence_fills(new, group, window):
     wide = _attend(c, qb, news, window=window)
     _check(c, qb, news, *wide)
     assert np.array_equal(none[0], wide[0]) and np.array_equal(none[1], wide[1])
+
+
+def _pool_of(address):
+    """The stream whose pool of torch's allocator the address lies in."""
+    for segment in torch.cuda.memory_snapshot():
+        if segment["address"] <= address < segment["address"] + segment["total_size"]:
+            return segment["stream"]
+    raise AssertionError("not an address of the allocator")
+
+
+def test_what_a_call_makes_belongs_to_its_stream(monkeypatch):
+    """A block that the current stream's pool hands out may be in use by work queued there, so
+    results and workspaces for another stream come from that stream's pool."""
+    from verify_nvfp4_w4a16_amd import serving
+    lib, scratch = serving._kv(), []
+    for name, place in (("nvfp4_kv_attention", 5), ("nvfp4_sample", 12)):
+        def spy(*args, real=getattr(lib, name), place=place):
+            scratch.append(args[place])
+            return real(*args)
+        monkeypatch.setattr(lib, name, spy)
+    c = Paged([3000, 70], 1, 64, 211, extra=2)
+    q, st = bf16(_query_bits(2, 2, 64, 212)), starts([1, 1])
+    logits, u = torch.zeros(2, 500, device=DEV), torch.full((2,), 0.5, device=DEV)
+    dst = int32([[c.free[0]], [c.free[1]]])
+    args = (c.cache, c.table_t, c.lens_t, st)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def calls(stream):
+        out, lse = nv.kv_attention(q, *args, 1, 3000, stream=stream)
+        w = nv.kv_weights(q, lse, *args, 1, 3000, stream=stream)
+        return [out, lse, w, *nv.kv_read(*args, 2, stream=stream), *nv.sample(logits, u, stream=stream),
+                *nv.kv_evict(w, c.cache, c.table_t, c.lens_t, dst, 64, stream=stream)]
+
+    here, first = calls(None), scratch[:]
+    there, second = calls(side), scratch[2:]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert len(first) == len(second) == 2 and all(first) and all(second)
+    assert set(first).isdisjoint(second)
+    for x in [t.data_ptr() for t in there] + second:
+        assert _pool_of(x) == side.cuda_stream
+    for x in [t.data_ptr() for t in here] + first:
+        assert _pool_of(x) == torch.cuda.current_stream().cuda_stream
+    for a, b in zip(here, there):
+        assert torch.equal(a, b)

@@ -7,7 +7,10 @@ runs in the library's HIP kernels.  The C functions, the cache's layout and the
 exact rules are in include/nvfp4_kv.h.  Calls run on `stream` (default: torch's
 current stream of the tensors' device), never wait for the device, and write to
 the tensors they return or were given; those must stay alive until the stream
-has passed, as with any torch call on another stream.
+has passed, as with any torch call on another stream.  Tensors and workspaces
+that a call makes belong to `stream`, like what torch makes under
+torch.cuda.stream(stream): to use a result elsewhere, wait for that stream, and
+record_stream() the result if it is dropped while such work is under way.
 """
 from __future__ import annotations
 
@@ -127,9 +130,18 @@ def _rows(name, x, cache, heads=None):
     return x.data_ptr(), pitch, head_pitch
 
 
-def _out(name, t, shape, dtype, device):
-    if t is None:
+def _new(shape, dtype, device, stream):
+    # from the pool of the stream that writes it: what another stream's pool hands out may still be in
+    # use by work queued there
+    if stream is None:
         return _empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return _empty(shape, dtype=dtype, device=device)
+
+
+def _out(name, t, shape, dtype, device, stream=None):
+    if t is None:
+        return _new(shape, dtype, device, stream)
     if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
@@ -155,8 +167,8 @@ def kv_read(cache: KvCache, table, kv_lens, q_starts, total: int, k=None, v=None
     """The bf16 values of each sequence's last q_starts[s+1] - q_starts[s] slots: (k, v), each
     [total, kv_heads, head_dim]; rows without a slot are zeros."""
     shape = (total, cache.kv_heads, cache.head_dim)
-    k = _out("k", k, shape, _BF16, cache.device)
-    v = _out("v", v, shape, _BF16, cache.device)
+    k = _out("k", k, shape, _BF16, cache.device, stream)
+    v = _out("v", v, shape, _BF16, cache.device, stream)
     seqs = _seqs(cache, table, kv_lens, q_starts, total)
     _check(_kv().nvfp4_kv_read(cache._c, seqs, k.data_ptr(), v.data_ptr(), _stream(stream, cache.device)),
            "nvfp4_kv_read")
@@ -190,26 +202,18 @@ def kv_attention(q, cache: KvCache, table, kv_lens, q_starts, max_q: int, max_kv
     dev = cache.device
     seqs = _seqs(cache, table, kv_lens, q_starts, q.shape[0])
     queries = _queries(cache, q, max_q, max_kv, scale, causal, window, softcap)
-    out = _out("out", out, q.shape, _BF16, dev)
-    lse = _out("lse", lse, q.shape[:2], _F32, dev)
+    out = _out("out", out, q.shape, _BF16, dev, stream)
+    lse = _out("lse", lse, q.shape[:2], _F32, dev, stream)
     lib = _kv()
     if workspace is None:
         n = ctypes.c_int64()
         _check(lib.nvfp4_kv_attention_workspace(cache._c, seqs, queries, n), "nvfp4_kv_attention")
         if n.value:
-            workspace = _scratch(n.value, dev, stream)
+            workspace = _new(n.value, torch.uint8, dev, stream)
     wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(lib.nvfp4_kv_attention(cache._c, seqs, queries, out.data_ptr(), lse.data_ptr(), wp, wn, _stream(stream, dev)),
            "nvfp4_kv_attention")
     return out, lse
-
-
-def _scratch(n, device, stream):
-    """A workspace from torch's allocator, kept from reuse until `stream` has passed."""
-    t = torch.empty(n, dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def kv_weights(q, lse, cache: KvCache, table, kv_lens, q_starts, max_q: int, max_kv: int, *, scale=None, causal=True,
@@ -221,7 +225,7 @@ def kv_weights(q, lse, cache: KvCache, table, kv_lens, q_starts, max_q: int, max
     seqs = _seqs(cache, table, kv_lens, q_starts, q.shape[0])
     queries = _queries(cache, q, max_q, max_kv, scale, causal, window, softcap)
     shape = (seqs.seqs, cache.kv_heads, max_kv)
-    out = _out("out", out, shape, _F32, dev)
+    out = _out("out", out, shape, _F32, dev, stream)
     if prior is not None:
         _out("prior", prior, shape, _F32, dev)
     _out("lse", lse, q.shape[:2], _F32, dev)
@@ -247,9 +251,9 @@ def kv_evict(weights, cache: KvCache, table, kv_lens, dst_table, keep: int, *, s
     if dst_table.shape[0] != shape[0]:
         raise ValueError("dst_table must have one row for each sequence")
     dst_ptr = _ints("dst_table", dst_table, 2, dev)
-    kept = _out("kept", kept, shape, _I32, dev)
-    kept_weights = _out("kept_weights", kept_weights, shape, _F32, dev)
-    new_lens = _out("new_lens", new_lens, shape[:1], _I32, dev)
+    kept = _out("kept", kept, shape, _I32, dev, stream)
+    kept_weights = _out("kept_weights", kept_weights, shape, _F32, dev, stream)
+    new_lens = _out("new_lens", new_lens, shape[:1], _I32, dev, stream)
     _check(_kv().nvfp4_kv_evict(cache._c, seqs, weights.data_ptr(), weights.shape[2], keep, sink, recent, dst._c, dst_ptr,
                                 dst_table.shape[1], kept.data_ptr(), kept_weights.data_ptr(), new_lens.data_ptr(),
                                 _stream(stream, dev)), "nvfp4_kv_evict")
@@ -274,13 +278,13 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, *, t
     rows, vocab = logits.shape
     dev = logits.device
     f32 = logits.dtype is _F32
-    token = _out("token", token, (rows,), _I32, dev)
-    logprob = _out("logprob", logprob, (rows,), _F32, dev)
+    token = _out("token", token, (rows,), _I32, dev, stream)
+    logprob = _out("logprob", logprob, (rows,), _F32, dev, stream)
     lib = _kv()
     n = ctypes.c_int64()
     _check(lib.nvfp4_sample_workspace(rows, vocab, n), "nvfp4_sample")
     if workspace is None and n.value:
-        workspace = _scratch(n.value, dev, stream)
+        workspace = _new(n.value, torch.uint8, dev, stream)
     wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(lib.nvfp4_sample(logits.data_ptr(), LOGITS_F32 if f32 else LOGITS_BF16, rows, vocab,
                             logits.stride(0) if rows > 1 else vocab, _param("u", u, rows, _F32, dev),
