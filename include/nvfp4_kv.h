@@ -26,6 +26,8 @@
  * device and are not read by the host; a length is held to
  * [0, 64 * table_pitch], a start to [0, total], and a page number outside
  * [0, pages) stands for slots that nothing is written to and nothing sees.
+ * Starts ascend; where they do not, nothing beyond the arrays is read or
+ * written, but which of the rows are computed is not defined.
  *
  * Conventions are nvfp4_w4a16.h's: int status codes (nvfp4_strerror),
  * arguments checked before any launch, nothing launched and nothing written

@@ -74,3 +74,51 @@ def test_what_a_call_makes_belongs_to_its_stream(monkeypatch):
         assert _pool_of(x) == torch.cuda.current_stream().cuda_stream
     for a, b in zip(here, there):
         assert torch.equal(a, b)
+
+
+class Guarded:
+    """A tensor inside a larger one whose other elements hold a pattern of their own."""
+
+    def __init__(self, shape, dtype, fill=None):
+        self.n, self.pad = int(np.prod(shape)), 4096
+        size = torch.empty((), dtype=dtype).element_size()
+        self.all = torch.full(((self.n + 2 * self.pad) * size,), 0xA5, dtype=torch.uint8, device=DEV)
+        self.t = self.all.view(dtype)[self.pad:self.pad + self.n].view(shape)
+        self.untouched = self.t.clone()
+        if fill is not None:
+            self.t.copy_(fill)
+        self.edge = self.pad * size
+
+    def check(self):
+        assert bool((self.all[:self.edge] == 0xA5).all()) and bool((self.all[-self.edge:] == 0xA5).all())
+        return self.t
+
+
+@pytest.mark.parametrize("new", [[5, 9], [40, 30]])
+def test_descending_starts_touch_nothing_beyond_the_arrays(new):
+    """Which rows are computed is not defined, but guards around every array stay as they were."""
+    d, heads = 64, 4
+    c = Paged([3000, 90, 500], 2, d, 221)
+    total = sum(new) + 20
+    for order in ([total, 0, new[0], new[0] + new[1]], [7, 3, total, 0], [new[0] + 1, new[0] + 2, 0, new[0]]):
+        data = Guarded(c.data.shape, torch.uint8, c.data)
+        cache = nv.KvCache(data.t, 2, d, c.k_scale, c.v_scale)
+        before = data.t.clone()
+        rows = bf16(workload.activations_bf16(total, 4 * d, 222).reshape(total, 4, d))
+        st = int32(order)
+        q = bf16(_query_bits(total, heads, d, 223))
+        args = (cache, c.table_t, c.lens_t, st)
+        out, lse = Guarded((total, heads, d), torch.bfloat16), Guarded((total, heads), torch.float32)
+        k, v = (Guarded((total, 2, d), torch.bfloat16) for _ in range(2))
+        w = Guarded((3, 2, 3000), torch.float32)
+        ws = nv.kv_attention_workspace(cache, q, c.table_t, c.lens_t, st, max(new), 3000)
+        ws = Guarded((ws,), torch.uint8) if ws else None
+        nv.kv_attention(q, *args, max(new), 3000, out=out.t, lse=lse.t, workspace=ws and ws.t)
+        nv.kv_read(*args, total, k=k.t, v=v.t)
+        nv.kv_weights(q, torch.zeros_like(lse.t), *args, max(new), 3000, out=w.t)
+        assert torch.equal(data.t, before)
+        nv.kv_append(cache, rows[:, :2], rows[:, 2:], c.table_t, c.lens_t, st)
+        torch.cuda.synchronize()
+        for x in (data, out, lse, k, v, w, ws):
+            if x is not None:
+                x.check()

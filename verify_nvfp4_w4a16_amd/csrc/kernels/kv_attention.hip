@@ -15,6 +15,7 @@
 
 #include <cstdint>
 
+#include "../host/kv_index.h"
 #include "../host/kv_plan.h"
 #include "../host/kv_shapes.h"
 #include "kv_common.h"
@@ -713,8 +714,8 @@ kv_join_kernel(AttendArgs a) {
     const int s = last_sequence(a.v, [&](int i) { return a.v.start(i) <= token; });
     if (s < 0) return;
     const QueryRows rows(a.v, a.sc, s);
-    const int r = (token - rows.first_token) * rows.group + head % rows.group;
-    if (r >= rows.count) return;   // no sequence's row
+    const int r = nvfp4::kv_row_of(token, rows.first_token, rows.group, head % rows.group, rows.count);
+    if (r < 0) return;   // no sequence's row
     // where part p of the row lies: the parts of a tile a slice apart, an item's by its number
     int used;
     int64_t first, step, last;

@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "../host/kv_index.h"
 #include "../host/kv_shapes.h"
 #include "kv_common.h"
 #include "setup.h"
@@ -195,13 +196,13 @@ kv_append_kernel(KvView v, Rows kr, Rows vr, float kt, float vt) {
     __shared__ uint64_t vcode[kPage][kGroups];              // 16 codes each
     __shared__ __attribute__((aligned(16))) uint8_t scales[8 * D];   // K's and V's, in the record's order
     const int u = blockIdx.x / v.kv_heads, h = blockIdx.x % v.kv_heads, tid = threadIdx.x;
-    const int s = last_sequence(v, [&](int i) { return v.start(i) / kPage + 2 * i <= u; });
+    const int s = last_sequence(v, [&](int i) { return nvfp4::kv_append_unit(v.start(i), i) <= u; });
     if (s < 0) return;
     const int t0 = v.start(s), nq = v.start(s + 1) - t0;
     if (nq <= 0) return;
     const int n = v.len(s), first = n - nq;            // slot of the first new token, maybe negative
-    const int page = (first < 0 ? 0 : first / kPage) + (u - (t0 / kPage + 2 * s)), slot0 = page * kPage;
-    if (slot0 >= n) return;
+    const int page = nvfp4::kv_append_page(u, t0, s, first), slot0 = page * kPage;
+    if (page < 0 || slot0 >= n) return;
     const int id = v.page_id(s, page);
     const int lo = first > slot0 ? first - slot0 : 0;  // new slots of the page: [lo, hi)
     const int hi = n - slot0 < kPage ? n - slot0 : kPage;
