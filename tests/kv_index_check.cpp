@@ -74,7 +74,7 @@ void check(const std::vector<int>& starts, const std::vector<int>& lens, int tot
 int main() {
     std::mt19937_64 g(3);
     for (int turn = 0; turn < 60000; ++turn) {
-        const int seqs = turn % 50 ? 1 + int(g() % 6) : 60 + int(g() % 80), total = 1 + int(g() % (turn % 3 ? 400 : 20)), pitch = 1 + int(g() % 9);
+        const int seqs = turn % 50 ? 1 + int(g() % 6) : 60 + int(g() % 80), total = 1 + int(g() % (turn % 7 == 1 ? 3000 : turn % 3 ? 400 : 20)), pitch = 1 + int(g() % 9);
         std::vector<int> starts(seqs + 1), lens(seqs);
         for (int& x : starts) x = int(g() % (total + 1));
         for (int& x : lens) x = int(g() % (64 * pitch + 1));
