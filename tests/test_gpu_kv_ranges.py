@@ -122,3 +122,27 @@ def test_descending_starts_touch_nothing_beyond_the_arrays(new):
         for x in (data, out, lse, k, v, w, ws):
             if x is not None:
                 x.check()
+
+
+# few, 33 to 64 and more rows a kv head
+ROWS = [(1, 4), (12, 4), (40, 4)]
+
+
+@pytest.mark.parametrize("new,group", ROWS)
+@pytest.mark.parametrize("kw", [{}, dict(window=100), dict(causal=False), dict(softcap=3.0)])
+def test_attention_at_scale_zero(new, group, kw):
+    # all slots that a query sees weigh alike
+    lens = [3000, 90, 5]
+    news = [new, new, 1]
+    c = Paged(lens, 1, 64, 231)
+    qb = _query_bits(sum(news), group, 64, 232)
+    _check(c, qb, news, *_attend(c, qb, news, scale=0.0, **kw), scale=0.0, **kw)
+
+
+@pytest.mark.parametrize("new,group", ROWS)
+def test_attention_of_zero_queries_over_small_keys(new, group):
+    lens, news = [700, 90], [new, new]
+    c = Paged(lens, 1, 128, 233, k_scale=2.0 ** -100)
+    qb = _query_bits(sum(news), group, 128, 234)
+    qb[::2, 1:] = 0
+    _check(c, qb, news, *_attend(c, qb, news))

@@ -543,6 +543,9 @@ kv_attend_tile_kernel(AttendArgs a) {
         for (int i = 0; i < D / 16; ++i) q[i] = -q[i];
         to_log2 = -to_log2;
     }
+    // Hidden scores are -inf before they meet the factor, so that is never 0 (a scale of 0, a row of zeros over small
+    // keys): sums stay below 2^35, and times 2^-126 they weigh alike as they would times 0.
+    to_log2 = fmaxf(to_log2, 0x1p-126f);
     // scores are formed with the exponential's argument; capped ones are whole before
     const float factor = a.sc.cap == 0.0f ? to_log2 : 1.0f;
 
