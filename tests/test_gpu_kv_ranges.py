@@ -146,3 +146,33 @@ def test_attention_of_zero_queries_over_small_keys(new, group):
     qb = _query_bits(sum(news), group, 128, 234)
     qb[::2, 1:] = 0
     _check(c, qb, news, *_attend(c, qb, news))
+
+
+@pytest.mark.parametrize("t", [2.0 ** -149, 1e-40, 4.8e-40, 5e-40, 2.0 ** -126, 2.0 ** -115, 5.6e37, 5.8e37, 1e38, 3.4e38])
+def test_append_at_the_ends_of_the_tensor_scale(t):
+    """Codes, scales and read values at tensor scales whose sixfold, or its inverse, fp32 does not hold."""
+    d, n = 64, 192
+    t = float(np.float32(t))
+    g = workload.rng(241)
+    # magnitudes from far below the scale's smallest step to beyond its largest
+    size = np.exp(g.uniform(-9, 10, (n, 2, d // 16, 1))) * t
+    x = np.clip(g.standard_normal((n, 2, d // 16, 16)) * size, -3.3e38, 3.3e38).astype(np.float32)
+    x[0] = 0.0
+    x[1, :, 0] = 0.0
+    x[2, :, 1, 3] = np.inf
+    bits = workload.f32_to_bf16_bits(x.reshape(n, 2, d))
+    rows = bf16(bits)
+    cache = nv.KvCache.empty(3, 1, d, t, t)
+    where = (int32([[2, 0, 1]]), int32([n]), int32([0, n]))
+    nv.kv_append(cache, rows[:, :1], rows[:, 1:], *where)
+    read = nv.kv_read(cache, *where, n)
+    torch.cuda.synchronize()
+    got = stored(cache.data.cpu().numpy(), [2, 0, 1], n, 0, d)
+    for which in (0, 1):
+        codes, scales = okv.quantise_rows(bits[:, which], t)
+        assert np.array_equal(got[2 * which + 1], scales)
+        assert np.array_equal(got[2 * which], codes)
+        with np.errstate(over="ignore"):
+            val = okv.values(codes, scales, 1.0).astype(np.float32) * np.float32(t)
+        back = read[which][:, 0].view(torch.int16).cpu().numpy().view(np.uint16)
+        assert np.array_equal(workload.bf16_bits_to_f32(back), workload.bf16_bits_to_f32(workload.f32_to_bf16_bits(val)))

@@ -7,7 +7,9 @@
 // token a sequence and by the bf16 rows' bytes for prompts.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <type_traits>
 
 #include "../host/kv_index.h"
@@ -23,18 +25,25 @@ namespace {
 // a real tie.  No quotient is formed, where 64 bits would cost most.
 struct Scale {
     double t, six_t;
-    float inverse;   // 1 / (6 t), for a first guess
+    float inverse;   // 2^exponent / (6 t), for a first guess: 1 / (6 t) itself leaves fp32 at the largest and the smallest t
+    int exponent;
     bool near_one;   // quotients can be formed in fp32: neither they nor the scales leave its range
     bool short_t;    // t has 8 bits, so ties are possible
 };
 
-__device__ __forceinline__ Scale scale_of(float t) {
-    return Scale{double(t), 6.0 * double(t), 1.0f / (6.0f * t), t > 0x1p-60f && t < 0x1p60f, (f32_bits(t) & 0xffff) == 0};
+// On the host, so that the kernel has them as scalars.
+Scale scale_of(float t) {
+    int e;
+    const float m = static_cast<float>(std::frexp(double(t), &e));
+    uint32_t bits;
+    std::memcpy(&bits, &t, sizeof bits);
+    return Scale{double(t), 6.0 * double(t), 1.0f / (6.0f * m), e, t > 0x1p-60f && t < 0x1p60f, (bits & 0xffff) == 0};
 }
 
 // The e4m3 code nearest to amax / (6 t), ties to even, saturating at 448.
 __device__ __forceinline__ uint32_t e4m3_code(float amax, const Scale& sc) {
-    const float guess = fminf(amax * sc.inverse, 448.0f);
+    // (the power of two saturates only where the quotient does)
+    const float guess = fminf(__builtin_amdgcn_ldexpf(amax, -sc.exponent) * sc.inverse, 448.0f);
     const uint32_t c = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(guess, guess, 0, false)) & 0x7f;
     const double a = double(amax), v = double(e4m3_f32(c));
     if (c < 0x7E) {
@@ -191,7 +200,7 @@ __device__ __forceinline__ uint64_t quantise16(u32x4 lo, u32x4 hi, const Scale& 
 // the codes by the boundaries alone), single tokens by latency (48: 6 us).
 template <int D>
 __global__ void __launch_bounds__(256)
-kv_append_kernel(KvView v, Rows kr, Rows vr, float kt, float vt) {
+kv_append_kernel(KvView v, Rows kr, Rows vr, Scale ksc, Scale vsc) {
     constexpr int kGroups = D / 16, kItems = kPage * kGroups / 256;
     __shared__ uint64_t vcode[kPage][kGroups];              // 16 codes each
     __shared__ __attribute__((aligned(16))) uint8_t scales[8 * D];   // K's and V's, in the record's order
@@ -207,7 +216,6 @@ kv_append_kernel(KvView v, Rows kr, Rows vr, float kt, float vt) {
     const int lo = first > slot0 ? first - slot0 : 0;  // new slots of the page: [lo, hi)
     const int hi = n - slot0 < kPage ? n - slot0 : kPage;
     const bool whole = lo == 0 && hi == kPage;
-    const Scale ksc = scale_of(kt), vsc = scale_of(vt);
 
     u32x4 rows[kItems][4];
 #pragma unroll
@@ -325,7 +333,8 @@ kv_read_kernel(KvView v, uint16_t* k_out, uint16_t* v_out, float kt, float vt) {
 template <int D>
 int launch_append(const KvView& v, const Rows& k, const Rows& vr, float kt, float vt, int64_t units, hipStream_t st) {
     if (units * v.kv_heads > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL(kv_append_kernel<D>, dim3(static_cast<unsigned>(units * v.kv_heads)), dim3(256), 0, st, v, k, vr, kt, vt);
+    hipLaunchKernelGGL(kv_append_kernel<D>, dim3(static_cast<unsigned>(units * v.kv_heads)), dim3(256), 0, st, v, k, vr, scale_of(kt),
+                       scale_of(vt));
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
