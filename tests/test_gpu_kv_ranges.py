@@ -176,3 +176,43 @@ def test_append_at_the_ends_of_the_tensor_scale(t):
             val = okv.values(codes, scales, 1.0).astype(np.float32) * np.float32(t)
         back = read[which][:, 0].view(torch.int16).cpu().numpy().view(np.uint16)
         assert np.array_equal(workload.bf16_bits_to_f32(back), workload.bf16_bits_to_f32(workload.f32_to_bf16_bits(val)))
+
+
+@pytest.mark.parametrize("new,group", ROWS)
+@pytest.mark.parametrize("cap", [1e-40, 0.02, 50.0, 1e3, 1e4, 1e6, 1e8, 1e30, 3.4e38])
+def test_attention_with_a_cap_of_any_size(new, group, cap):
+    """A capped score is off by a relative 2^-20 beside its sum's own error, whatever the cap."""
+    lens, news, d = [300, 70], [new, new], 64
+    c = Paged(lens, 1, d, 251)
+    qb = _query_bits(sum(news), group, d, 252)
+    out, lse = _attend(c, qb, news, softcap=cap)
+    q, at = bf16_bits_to_f64(qb), 0
+    for s, n in enumerate(lens):
+        for h in range(group):
+            k, v = c.k[s][0], c.v[s][0]
+            o, l, spread, size = okv.attention(q[at:at + new, h], k, v, d ** -0.5, softcap=cap)
+            # both scores of a difference, and the exponential's own 2^-20
+            eps = (2 * (d + 8) * 2.0 ** -24 + 2 * 2.0 ** -20) * size[:, None] + 2.0 ** -20
+            tol = 2.0 ** -8 * np.abs(o) + (eps + 2.0 ** -10) * spread + (n + 1) * 2.0 ** -24 * np.abs(v).max()
+            assert np.all(np.abs(out[at:at + new, h] - o) <= tol), (s, h)
+            lim = eps[:, 0] + n * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(l))
+            assert np.all(np.abs(lse[at:at + new, h] - l) <= lim), (s, h, float((np.abs(lse[at:at + new, h] - l) / lim).max()))
+        at += new
+
+
+@pytest.mark.parametrize("cap", [0.02, 50.0, 1e4, 1e8])
+def test_slot_weights_with_a_cap_of_any_size(cap):
+    n, new, group, d = 200, 9, 4, 64
+    c = Paged([n], 1, d, 253)
+    qb = _query_bits(new, group, d, 254)
+    q64 = bf16_bits_to_f64(qb)
+    lses = np.stack([okv.attention(q64[:, h], c.k[0][0], c.v[0][0], d ** -0.5, softcap=cap)[1] for h in range(group)], 1).astype(np.float32)
+    got = nv.kv_weights(bf16(qb), torch.from_numpy(lses).to(DEV), c.cache, c.table_t, c.lens_t, starts([new]), new, n, softcap=cap)
+    got = got.cpu().numpy()[0, 0].astype(np.float64)
+    want, size = np.zeros(n), np.zeros(n)
+    for h in range(group):
+        w, z = okv.slot_weights(q64[:, h], c.k[0][0], lses[:, h].astype(np.float64), d ** -0.5, softcap=cap)
+        want, size = want + w, size + z
+    # as test_slot_weights has it, with the cap's relative 2^-20 of a score in place of a part of the cap
+    tol = (2 * (d + 8) * 2.0 ** -24 + 2.0 ** -20) * size + (2.0 ** -20 + (new * group + 2) * 2.0 ** -24 + np.abs(lses).max() * 2.0 ** -22) * want
+    assert np.all(np.abs(got - want) <= tol + 1e-30), float((np.abs(got - want) / tol).max())

@@ -2,6 +2,9 @@
 // the attention kernels and by the one that sums the weights of slots.
 #pragma once
 
+#include <algorithm>
+#include <limits>
+
 #include "../host/kv_plan.h"
 #include "kv_common.h"
 
@@ -19,7 +22,7 @@ struct KvScores {
     int max_q, max_kv;     // what the launch was sized for: sequences are held to it
     int causal;
     float scale;           // of q . (e4m3 * e2m1): the caller's times K's tensor scale
-    float cap, cap_inv2;   // softcap and 2 / softcap (0: none)
+    float cap, cap_inv;    // softcap (0: none) and its inverse
 
     // r / group for r in [0, 2^31): the product with the inverse is at most one short (a division takes 30 operations).
     __device__ __forceinline__ int over_group(int r) const {
@@ -36,12 +39,17 @@ struct KvScores {
             for (int i = 0; i < N; ++i) x[i] *= f;
             return;
         }
-        // cap * tanh(z / cap) with tanh y = 1 - 2 / (1 + exp(2 y)): exact limits at both ends
-        const float g = f * (cap_inv2 * kLog2e), c = cap * kLog2e;
+        // cap * tanh(z / cap).  From y = z / cap = 1/4 on as 1 - 2 / (1 + exp(2 y)), with exact limits at
+        // both ends; below that the difference would lose what is small beside the cap, and y's power
+        // series to the seventh has it to 2^-21 of itself (the next term is y^8 * 62 / 2835).
+        const float c = cap * kLog2e;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float e = __builtin_amdgcn_exp2f(x[i] * g);
-            x[i] = c - 2.0f * c * __builtin_amdgcn_rcpf(1.0f + e);
+            const float y = x[i] * f * cap_inv, y2 = y * y;
+            const float e = __builtin_amdgcn_exp2f(y * (2.0f * kLog2e));
+            const float far = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e);
+            const float near = y + y * (y2 * (-1.0f / 3.0f + y2 * (2.0f / 15.0f - y2 * (17.0f / 315.0f))));
+            x[i] = c * (fabsf(y) < 0.25f ? near : far);
         }
     }
 };
@@ -59,8 +67,8 @@ inline KvScores kv_scores(const nvfp4_kv_cache_t* c, const nvfp4_kv_queries_t* q
     s.max_kv = static_cast<int>(q->max_kv);
     s.causal = q->causal;
     s.scale = q->scale * c->k_scale;
-    s.cap = q->softcap;
-    s.cap_inv2 = q->softcap > 0.0f ? 2.0f / q->softcap : 0.0f;
+    s.cap = std::min(q->softcap, 0x1p126f);   // more changes no score below 2^100, and its product with log2(e) is in range
+    s.cap_inv = s.cap > 0.0f ? std::min(1.0f / s.cap, std::numeric_limits<float>::max()) : 0.0f;
     return s;
 }
 
