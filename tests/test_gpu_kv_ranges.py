@@ -216,3 +216,26 @@ def test_slot_weights_with_a_cap_of_any_size(cap):
     # as test_slot_weights has it, with the cap's relative 2^-20 of a score in place of a part of the cap
     tol = (2 * (d + 8) * 2.0 ** -24 + 2.0 ** -20) * size + (2.0 ** -20 + (new * group + 2) * 2.0 ** -24 + np.abs(lses).max() * 2.0 ** -22) * want
     assert np.all(np.abs(got - want) <= tol + 1e-30), float((np.abs(got - want) / tol).max())
+
+
+@pytest.mark.parametrize("new,group", ROWS)
+def test_attention_where_the_scales_product_is_too_small_for_fp32(new, group):
+    """A product that has five bits in fp32, between the largest keys and the largest queries, whose scores are ordinary."""
+    n, d = 90, 256
+    k_scale, scale = float(np.float32(2.0 ** -70)), float(np.float32(16.5 * 2.0 ** -79))
+    g = workload.rng(261)
+    kv = np.where(g.random((n, 2, d)) < 0.5, -1.0, 1.0).astype(np.float32) * np.float32(2688 * 2.0 ** -70)
+    kv[::9, 0] = abs(kv[::9, 0])                                # scores near the largest, the others' near 0
+    bits = workload.f32_to_bf16_bits(kv)
+    rows = bf16(bits)
+    c = Paged([n], 1, d, 262, k_scale=k_scale, v_scale=k_scale)
+    nv.kv_append(c.cache, rows[:, :1], rows[:, 1:], c.table_t, c.lens_t, int32([0, n]))
+    for x, col in ((c.k, 0), (c.v, 1)):
+        codes, scales = okv.quantise_rows(bits[:, col], k_scale)
+        x[0] = okv.values(codes, scales, k_scale)[None]
+    qb = workload.f32_to_bf16_bits(np.full((new, group, d), 1.5 * 2.0 ** 126, np.float32))
+    out, lse = _attend(c, qb, [new], scale=scale)
+    _check(c, qb, [new], out, lse, scale=scale)
+    w = nv.kv_weights(bf16(qb), torch.from_numpy(lse).float().to(DEV), c.cache, c.table_t, c.lens_t, starts([new]), new, n, scale=scale)
+    # each query's weights over what it sees sum to 1, but for lse's rounding and the scores' errors
+    assert abs(float(w.double().sum()) - new * group) <= 1e-4 * new * group

@@ -3,7 +3,8 @@
 #pragma once
 
 #include <algorithm>
-#include <limits>
+#include <cfloat>
+#include <cmath>
 
 #include "../host/kv_plan.h"
 #include "kv_common.h"
@@ -21,7 +22,8 @@ struct KvScores {
     int window;            // 0: no limit
     int max_q, max_kv;     // what the launch was sized for: sequences are held to it
     int causal;
-    float scale;           // of q . (e4m3 * e2m1): the caller's times K's tensor scale
+    float scale;           // of q . (e4m3 * e2m1): the caller's times K's tensor scale is scale * 2^(exponent + 14),
+    int exponent;          // apart because the product may be too small for fp32 where scores are not
     float cap, cap_inv;    // softcap (0: none) and its inverse
 
     // r / group for r in [0, 2^31): the product with the inverse is at most one short (a division takes 30 operations).
@@ -66,9 +68,10 @@ inline KvScores kv_scores(const nvfp4_kv_cache_t* c, const nvfp4_kv_queries_t* q
     s.max_q = static_cast<int>(q->max_q);
     s.max_kv = static_cast<int>(q->max_kv);
     s.causal = q->causal;
-    s.scale = q->scale * c->k_scale;
+    s.scale = static_cast<float>(std::frexp(double(q->scale) * double(c->k_scale), &s.exponent));
+    s.exponent -= 14;   // of the row's own power of two (convert_query)
     s.cap = std::min(q->softcap, 0x1p126f);   // more changes no score below 2^100, and its product with log2(e) is in range
-    s.cap_inv = s.cap > 0.0f ? std::min(1.0f / s.cap, std::numeric_limits<float>::max()) : 0.0f;
+    s.cap_inv = s.cap > 0.0f ? std::min(1.0f / s.cap, FLT_MAX) : 0.0f;
     return s;
 }
 
@@ -150,7 +153,7 @@ __device__ __forceinline__ float convert_query(const KvScores& sc, const u32x4 (
             q[i][2 * j] = static_cast<_Float16>(bits_f32(raw[i][j] << 16) * up);
             q[i][2 * j + 1] = static_cast<_Float16>(bits_f32(raw[i][j] & 0xffff0000u) * up);
         }
-    const float f = sc.scale * ldexpf(1.0f, e - 14);
+    const float f = __builtin_amdgcn_ldexpf(sc.scale, sc.exponent + e);
     return sc.cap == 0.0f ? f * kLog2e : f;
 }
 
