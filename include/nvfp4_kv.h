@@ -122,7 +122,7 @@ typedef struct {
                                launch is sized by both: one that is more is
                                taken for one of that size) */
     int64_t window;         /* slots a query sees at most, 0: no limit */
-    float scale;            /* finite */
+    float scale;            /* finite, and its product with k_scale too */
     float softcap;          /* scores become softcap * tanh(score / softcap); 0: not */
     int32_t causal;         /* 1: a query sees its own slot and those before it */
 } nvfp4_kv_queries_t;
@@ -144,7 +144,8 @@ int nvfp4_kv_attention_workspace(const nvfp4_kv_cache_t* cache, const nvfp4_kv_s
  *   out = sum_j softmax(z)_j v_j, bf16 [total][heads][head_dim] contiguous;
  *   lse = log sum_j exp z_j, fp32 [total][heads], may be NULL.
  * A query that sees nothing has out 0 and lse -inf.  Rows that no sequence
- * owns are not written.  Scores, softmax statistics and sums are fp32; the
+ * owns are not written.  Scores, softmax statistics and sums are fp32 (rows
+ * with scores beyond its range are not defined); the
  * weights exp(z - max) are rounded to f16 for the second product.
  * out: 16-byte aligned.  workspace: device, 16-byte aligned, not shared by
  * calls that overlap in time.  Errors: NULL, SHAPE, ALIGN, SCRATCH (the

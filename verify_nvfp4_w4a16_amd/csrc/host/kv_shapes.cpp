@@ -55,6 +55,7 @@ int check_kv_queries(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const 
     if (q->max_q * (q->heads / c->kv_heads) > most || s->total * q->heads > most) return NVFP4_ERR_SHAPE;
     if (q->window < 0 || !std::isfinite(q->scale) || !(q->softcap >= 0.0f) || !std::isfinite(q->softcap))
         return NVFP4_ERR_SHAPE;
+    if (!std::isfinite(q->scale * c->k_scale)) return NVFP4_ERR_SHAPE;   // every score but 0 would leave fp32
     if (q->causal != 0 && q->causal != 1) return NVFP4_ERR_SHAPE;
     return check_kv_rows(q->q, q->q_pitch, q->q_head_pitch, s->total);
 }
