@@ -239,3 +239,24 @@ def test_attention_where_the_scales_product_is_too_small_for_fp32(new, group):
     w = nv.kv_weights(bf16(qb), torch.from_numpy(lse).float().to(DEV), c.cache, c.table_t, c.lens_t, starts([new]), new, n, scale=scale)
     # each query's weights over what it sees sum to 1, but for lse's rounding and the scores' errors
     assert abs(float(w.double().sum()) - new * group) <= 1e-4 * new * group
+
+
+@pytest.mark.parametrize("new,group", ROWS)
+@pytest.mark.parametrize("v_scale", [2.0 ** -126, 2.0 ** -100, 2.0 ** 100])
+def test_attention_of_one_value_at_the_ends_of_v_s_tensor_scale(new, group, v_scale):
+    # weights that sum to one give the value itself, whatever the sum was before
+    n, d = 207126, 64
+    cache = nv.KvCache.empty(-(-n // PAGE), 1, d, 2.0 ** -6, v_scale)
+    where = (int32(np.arange(-(-n // PAGE))[None]), int32([n]))
+    rows = torch.randn(n, 2, d, generator=torch.Generator(device=DEV).manual_seed(271), device=DEV).bfloat16()
+    rows[:, 1] = 6.0 * v_scale
+    nv.kv_append(cache, rows[:, :1], rows[:, 1:], *where, int32([0, n]))
+    q = bf16(_query_bits(new, group, d, 272))
+    for scale in (None, 0.0):
+        out, lse = nv.kv_attention(q, cache, *where, int32([0, new]), new, n, scale=scale)
+        got = out.float().cpu().numpy().astype(np.float64) / (6.0 * v_scale)
+        # f16 weights against the fp32 sum of the same weights, and the output's rounding
+        assert np.all(np.abs(got - 1) <= 2.0 ** -8 + 2.0 ** -10), float(np.abs(got - 1).max())
+        if scale == 0.0:
+            seen = n - new + 1 + np.arange(new)[:, None]
+            assert np.all(np.abs(lse.cpu().numpy() - np.log(seen)) <= n * 2.0 ** -24 + 1e-5)

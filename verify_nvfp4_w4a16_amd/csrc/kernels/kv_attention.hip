@@ -401,13 +401,13 @@ kv_attend_rows_kernel(AttendArgs a) {
         }
         return;
     }
-    const float f = sum > 0.0f || sum != sum ? a.v_scale / sum : 0.0f;
+    const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;   // V's scale apart: their quotient may be too small for fp32
     uint16_t* out = a.out + at * D + d0;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
         uint16_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = f32_to_bf16_rne(acc[i][j] * f);
+        for (int j = 0; j < 4; ++j) w[j] = f32_to_bf16_rne(acc[i][j] * f * a.v_scale);
         u32x2 x;
         __builtin_memcpy(&x, w, 8);
         *reinterpret_cast<u32x2*>(out + 64 * i) = x;
@@ -676,7 +676,7 @@ kv_attend_tile_kernel(AttendArgs a) {
         return;
     }
     // bf16 rows through LDS, then 16-byte stores along them
-    const float f = l > 0.0f || l != l ? a.v_scale / l : 0.0f;
+    const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     if (a.lse && live && b == 0 && (HALVES == 1 || my_half == 0)) a.lse[at] = (m + log2f(l)) * kLn2;
     __syncthreads();
     constexpr int kRow = D * 2 + 16;   // bytes of a staged row
@@ -687,7 +687,7 @@ kv_attend_tile_kernel(AttendArgs a) {
         for (int c = 0; c < 16; c += 4) {
             uint16_t w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = f32_to_bf16_rne(o[i][c + j] * f);
+            for (int j = 0; j < 4; ++j) w[j] = f32_to_bf16_rne(o[i][c + j] * f * a.v_scale);
             u32x2 x;
             __builtin_memcpy(&x, w, 8);
             *reinterpret_cast<u32x2*>(stage + n * kRow + (32 * i + 2 * c + 4 * b) * 2) = x;
@@ -768,13 +768,13 @@ kv_join_kernel(AttendArgs a) {
     __syncthreads();
     if (tid >= D / 2) return;
     sum = weight[0] + weight[1] + weight[2] + weight[3];
-    const float f = sum > 0.0f || sum != sum ? a.v_scale / sum : 0.0f;
+    const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;   // V's scale apart: their quotient may be too small for fp32
     uint32_t w = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int d = 2 * tid + j;
         const float x = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
-        w |= uint32_t(f32_to_bf16_rne(x * f)) << (16 * j);
+        w |= uint32_t(f32_to_bf16_rne(x * f * a.v_scale)) << (16 * j);
     }
     *reinterpret_cast<uint32_t*>(a.out + at * D + 2 * tid) = w;
     if (a.lse && tid == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
