@@ -260,3 +260,33 @@ def test_attention_of_one_value_at_the_ends_of_v_s_tensor_scale(new, group, v_sc
         if scale == 0.0:
             seen = n - new + 1 + np.arange(new)[:, None]
             assert np.all(np.abs(lse.cpu().numpy() - np.log(seen)) <= n * 2.0 ** -24 + 1e-5)
+
+
+@pytest.mark.parametrize("new,group", ROWS)
+def test_attention_keeps_the_mass_of_many_small_weights(new, group):
+    """Every 32nd slot, whose value is zero, has 2^26 times the weight of each other.
+
+    A weight enters the second product as f16 times 2^7, so it is off by half of f16's
+    smallest step, 2^-32 of the largest weight, at most; twice that is allowed."""
+    n, d = 4000, 64
+    large = np.arange(n) % 32 == 0
+    kv = np.zeros((n, 2, d), np.float32)
+    kv[large, 0, 0] = 6.0
+    kv[~large, 1] = 6.0
+    kv[1::2, 1, ::2] = 3.0
+    rows = bf16(workload.f32_to_bf16_bits(kv))
+    c = Paged([n], 1, d, 281, k_scale=2.0 ** -3, v_scale=2.0 ** -3)
+    nv.kv_append(c.cache, rows[:, :1], rows[:, 1:], c.table_t, c.lens_t, int32([0, n]))
+    q = np.zeros((new, group, d), np.float32)
+    q[..., 0] = 3.0
+    scale = 26 * np.log(2.0) / 18                              # those slots' score is 26 log 2, all others' 0
+    out, lse = _attend(c, workload.f32_to_bf16_bits(q), [new], scale=scale)
+    v, top = kv[:, 1].astype(np.float64), np.exp(18 * float(np.float32(scale)))
+    for i in range(new):
+        seen = n - new + i + 1
+        many, few = int((~large[:seen]).sum()), int(large[:seen].sum())
+        mass = few * top + many
+        ref = v[:seen].sum(0) / mass
+        tol = (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -13) * ref + 2 * many * 2.0 ** -32 * 6.0 / few
+        assert np.all(np.abs(out[i] - ref) <= tol), (i, float((np.abs(out[i] - ref) / tol).max()))
+        assert np.all(np.abs(lse[i] - np.log(mass)) <= 1e-5)

@@ -28,8 +28,11 @@ constexpr int kWaves = nvfp4::kKvWaves, kRowTile = nvfp4::kKvRowTile, kTileRows 
 constexpr int kItems = nvfp4::kKvItems;
 
 // Scores may outgrow the running maximum by this much (in powers of two)
-// before the sums are rescaled: the weights then stay below 2^8, within f16.
+// before the sums are rescaled.
 constexpr float kSlack = 8.0f;
+// Weights are held times this power of two, in f16 and in the sums: they reach
+// 2^15, and those below 2^-32 of the largest are lost in f16, not below 2^-25.
+constexpr float kLift = 7.0f;
 
 struct AttendArgs {
     KvView v;
@@ -320,7 +323,7 @@ kv_attend_rows_kernel(AttendArgs a) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[i] *= keep;
         }
-        const float base_m = m == -INFINITY ? 0.0f : m;
+        const float base_m = m == -INFINITY ? 0.0f : m - kLift;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             p[i] = __builtin_amdgcn_exp2f(p[i] - base_m);
@@ -352,6 +355,7 @@ kv_attend_rows_kernel(AttendArgs a) {
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     if (l != l && m == -INFINITY) m = 0.0f;   // all scores NaN: the row stays NaN
+    m -= kLift;                               // what the sums are held against
 
     // The wavefronts' results meet in LDS and are joined in wavefront order.
     float* sums = lds + wave * 16 * kSumRow<D>;
@@ -610,7 +614,7 @@ kv_attend_tile_kernel(AttendArgs a) {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) o[i] *= keep;
             }
-            const float base_m = m == -INFINITY ? 0.0f : m;
+            const float base_m = m == -INFINITY ? 0.0f : m - kLift;
             f16x8 pt[2 * kStep];
 #pragma unroll
             for (int i = 0; i < 16 * kStep; ++i) {
@@ -630,6 +634,7 @@ kv_attend_tile_kernel(AttendArgs a) {
     }
     l += __shfl_xor(l, 32);
     if (l != l && m == -INFINITY) m = 0.0f;   // all scores NaN: the row stays NaN
+    m -= kLift;                               // what the sums are held against
     if constexpr (HALVES == 2) {
         // the second half's results through LDS to the first's wavefronts, lane by lane
         constexpr int kParts = D / 32 * 16 + 2;
