@@ -173,9 +173,10 @@ int nvfp4_kv_weights(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,
  * keep - sink - recent of the rest with the largest weights stay (ties: the
  * lower slot; a NaN counts as -inf), in slot order.
  *   weights      fp32 [seqs][kv_heads][weights_pitch]
- *   dst          a cache of the same geometry (may be the same data), whose
- *                pages in dst_table [seqs][dst_pitch] are none that `seqs`
- *                still reads; dst_pitch * 64 >= keep
+ *   dst          a cache of the same geometry and tensor scales (codes are
+ *                copied as they are; may be the same data), whose pages in
+ *                dst_table [seqs][dst_pitch] are none that `seqs` still reads;
+ *                dst_pitch * 64 >= keep
  *   kept         int32 [seqs][kv_heads][keep], slots ascending, then -1
  *   kept_weights fp32 [seqs][kv_heads][keep], their weights, then 0
  *   new_lens     int32 [seqs], min(n, keep)

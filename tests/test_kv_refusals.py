@@ -20,3 +20,13 @@ def test_refusal_of_scales_whose_product_is_infinite(scale, k_scale, ok):
     if not ok:
         assert lib.nvfp4_kv_attention(c, s, q, A, A, A, 1 << 40, None) == nv.ERR_SHAPE
         assert lib.nvfp4_kv_weights(c, s, q, A, A, A, None) == nv.ERR_SHAPE
+
+
+@pytest.mark.parametrize("scales", [dict(k_scale=0.5), dict(v_scale=2.0), dict(k_scale=3.0, v_scale=0.25)])
+def test_refusal_of_eviction_into_a_cache_of_other_scales(scales):
+    # codes are copied as they are: read at another scale they would stand for other values
+    lib = serving._kv()
+    for c, dst in ((_cache(), _cache(**scales)), (_cache(**scales), _cache())):
+        assert lib.nvfp4_kv_evict(c, _seqs(), A, 100, 64, 1, 2, dst, A, 1, A, A, A, None) == nv.ERR_SHAPE
+    # equal ones pass on to the checks that follow
+    assert lib.nvfp4_kv_evict(_cache(**scales), _seqs(), A, 100, 64, 1, 2, _cache(**scales), A, 1, A, A, None, None) == nv.ERR_NULL

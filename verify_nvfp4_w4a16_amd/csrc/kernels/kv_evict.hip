@@ -642,6 +642,7 @@ extern "C" int nvfp4_kv_evict(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs
     if ((st = nvfp4::check_kv_cache(dst)) != NVFP4_OK) return st;
     if ((st = nvfp4::check_kv_seqs(seqs, false)) != NVFP4_OK) return st;
     if (dst->kv_heads != cache->kv_heads || dst->head_dim != cache->head_dim) return NVFP4_ERR_SHAPE;
+    if (dst->k_scale != cache->k_scale || dst->v_scale != cache->v_scale) return NVFP4_ERR_SHAPE;   // codes are copied as they are
     if (keep < 1 || keep > (int64_t(1) << 30) || sink < 0 || recent < 0 || sink > keep || recent > keep || sink + recent > keep)
         return NVFP4_ERR_SHAPE;
     if (weights_pitch < 0 || weights_pitch > (int64_t(1) << 30)) return NVFP4_ERR_SHAPE;

@@ -238,8 +238,8 @@ def kv_evict(weights, cache: KvCache, table, kv_lens, dst_table, keep: int, *, s
              kept=None, kept_weights=None, new_lens=None, stream=None):
     """Cuts every sequence to at most `keep` slots a kv head: the first `sink`, the last `recent` and
     those between with the largest weights [seqs, kv_heads, n], copied in slot order into the pages
-    of dst_table [seqs, at least keep / 64] of `dst` (default: the same cache; its pages must be ones that
-    no sequence of the call reads).  Returns (kept int32 [seqs, kv_heads, keep], their weights, the new
+    of dst_table [seqs, at least keep / 64] of `dst` (default: the same cache; one with the same geometry
+    and tensor scales, whose pages in dst_table no sequence of the call reads).  Returns (kept int32 [seqs, kv_heads, keep], their weights, the new
     lengths int32 [seqs])."""
     dev = cache.device
     dst = cache if dst is None else dst
