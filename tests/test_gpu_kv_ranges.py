@@ -290,3 +290,13 @@ def test_attention_keeps_the_mass_of_many_small_weights(new, group):
         tol = (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -13) * ref + 2 * many * 2.0 ** -32 * 6.0 / few
         assert np.all(np.abs(out[i] - ref) <= tol), (i, float((np.abs(out[i] - ref) / tol).max()))
         assert np.all(np.abs(lse[i] - np.log(mass)) <= 1e-5)
+
+
+def test_workspaces_elsewhere_or_in_pieces_are_refused():
+    c = Paged([200], 1, 64, 301)
+    q, logits, u = bf16(_query_bits(1, 2, 64, 302)), torch.zeros(1, 500, device=DEV), torch.zeros(1, device=DEV)
+    for bad in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            nv.kv_attention(q, c.cache, c.table_t, c.lens_t, starts([1]), 1, 200, workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            nv.sample(logits, u, workspace=bad)

@@ -30,3 +30,28 @@ def test_refusal_of_eviction_into_a_cache_of_other_scales(scales):
         assert lib.nvfp4_kv_evict(c, _seqs(), A, 100, 64, 1, 2, dst, A, 1, A, A, A, None) == nv.ERR_SHAPE
     # equal ones pass on to the checks that follow
     assert lib.nvfp4_kv_evict(_cache(**scales), _seqs(), A, 100, 64, 1, 2, _cache(**scales), A, 1, A, A, None, None) == nv.ERR_NULL
+
+
+def _host_cache(device="cpu"):
+    """A cache object over host memory, for checks that come before any call of the library."""
+    cache = object.__new__(serving.KvCache)
+    cache.data = torch.zeros(4, 1, 72 * 64, dtype=torch.uint8)
+    cache.kv_heads, cache.head_dim, cache.pages, cache.device = 1, 64, 4, torch.device(device)
+    cache._c = serving._Cache(cache.data.data_ptr(), 4, 1, 64, 1.0, 1.0)
+    return cache
+
+
+def test_python_refuses_a_workspace_elsewhere_or_in_pieces():
+    cache = _host_cache()
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    table, lens, starts = (torch.tensor(x, dtype=torch.int32) for x in ([[0]], [1], [0, 1]))
+    for bad in (torch.zeros(1 << 20, dtype=torch.uint8, device="meta"), torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            serving.kv_attention(q, cache, table, lens, starts, 1, 1, workspace=bad)
+
+
+def test_python_refuses_eviction_into_a_cache_on_another_device():
+    cache, other = _host_cache(), _host_cache("meta")
+    table, lens = torch.tensor([[0]], dtype=torch.int32), torch.tensor([1], dtype=torch.int32)
+    with pytest.raises(ValueError, match="dst"):
+        serving.kv_evict(torch.zeros(1, 1, 1), cache, table, lens, torch.tensor([[1]], dtype=torch.int32), 1, dst=other)

@@ -147,6 +147,15 @@ def _out(name, t, shape, dtype, device, stream=None):
     return t
 
 
+def _room(workspace, device):
+    """Address and bytes of a workspace, or of none."""
+    if workspace is None:
+        return 0, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _stream(stream, device) -> int:
     # the raw handle at once: torch.cuda.current_stream() would build a Stream object (2 us) first
     return _raw_stream(device.index) if stream is None else stream.cuda_stream
@@ -210,7 +219,7 @@ def kv_attention(q, cache: KvCache, table, kv_lens, q_starts, max_q: int, max_kv
         _check(lib.nvfp4_kv_attention_workspace(cache._c, seqs, queries, n), "nvfp4_kv_attention")
         if n.value:
             workspace = _new(n.value, torch.uint8, dev, stream)
-    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    wp, wn = _room(workspace, dev)
     _check(lib.nvfp4_kv_attention(cache._c, seqs, queries, out.data_ptr(), lse.data_ptr(), wp, wn, _stream(stream, dev)),
            "nvfp4_kv_attention")
     return out, lse
@@ -243,6 +252,8 @@ def kv_evict(weights, cache: KvCache, table, kv_lens, dst_table, keep: int, *, s
     lengths int32 [seqs])."""
     dev = cache.device
     dst = cache if dst is None else dst
+    if dst.device != dev:
+        raise ValueError(f"dst must be a cache on {dev}")
     seqs = _seqs(cache, table, kv_lens, None, 0)
     shape = (seqs.seqs, cache.kv_heads, keep)
     if weights.dim() != 3 or tuple(weights.shape[:2]) != shape[:2]:
@@ -285,7 +296,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, *, t
     _check(lib.nvfp4_sample_workspace(rows, vocab, n), "nvfp4_sample")
     if workspace is None and n.value:
         workspace = _new(n.value, torch.uint8, dev, stream)
-    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    wp, wn = _room(workspace, dev)
     _check(lib.nvfp4_sample(logits.data_ptr(), LOGITS_F32 if f32 else LOGITS_BF16, rows, vocab,
                             logits.stride(0) if rows > 1 else vocab, _param("u", u, rows, _F32, dev),
                             _param("temperature", temperature, rows, _F32, dev),
