@@ -300,3 +300,40 @@ def test_workspaces_elsewhere_or_in_pieces_are_refused():
             nv.kv_attention(q, c.cache, c.table_t, c.lens_t, starts([1]), 1, 200, workspace=bad)
         with pytest.raises(ValueError, match="workspace"):
             nv.sample(logits, u, workspace=bad)
+
+
+@pytest.mark.parametrize("max_q,max_kv", [(8, 128), (8, 1100), (20, 128), (70, 1100)])
+def test_sequences_beyond_the_bounds_count_as_ones_of_that_size(max_q, max_kv):
+    """A sequence with more slots or new tokens than the call's bounds is taken for one that ends
+    there: its first max_q rows are those of max_kv slots, and nothing else is written."""
+    lens, new, d, heads = [1500, 40], [90, 1], 64, 4
+    c = Paged(lens, 1, d, 291)
+    total = sum(new)
+    qb = _query_bits(total, heads, d, 292)
+    q, st = bf16(qb), starts(new)
+    args = (c.cache, c.table_t, c.lens_t, st, max_q, max_kv)
+    out, lse, w = Guarded((total, heads, d), torch.bfloat16), Guarded((total, heads), torch.float32), Guarded((2, 1, max_kv), torch.float32)
+    n = nv.kv_attention_workspace(c.cache, q, c.table_t, c.lens_t, st, max_q, max_kv)
+    ws = Guarded((n,), torch.uint8) if n else None
+    nv.kv_attention(q, *args, out=out.t, lse=lse.t, workspace=ws and ws.t)
+    nv.kv_weights(q, lse.t, *args, out=w.t)
+    torch.cuda.synchronize()
+    if ws:
+        ws.check()
+    got, got_lse = out.check().float().cpu().numpy().astype(np.float64), lse.check().cpu().numpy().astype(np.float64)
+    # rows past max_q are as they were
+    assert torch.equal(out.t[max_q:90].view(torch.int16), out.untouched[max_q:90].view(torch.int16))
+    assert torch.equal(lse.t[max_q:90].view(torch.int32), lse.untouched[max_q:90].view(torch.int32))
+    kept = np.r_[0:max_q, 90]
+    c.k, c.v = [x[:, :max_kv] for x in c.k], [x[:, :max_kv] for x in c.v]
+    c.lens = [min(x, max_kv) for x in lens]
+    _check(c, qb[kept], [max_q, 1], got[kept], got_lse[kept])
+    got_w, q64 = w.check().cpu().numpy().astype(np.float64), bf16_bits_to_f64(qb)
+    for s, rows in enumerate((range(0, max_q), [90])):
+        want, size = np.zeros(c.lens[s]), np.zeros(c.lens[s])
+        for h in range(heads):
+            x, z = okv.slot_weights(q64[rows, h], c.k[s][0], got_lse[rows, h], d ** -0.5)
+            want, size = want + x, size + z
+        tol = 2 * (d + 8) * 2.0 ** -24 * size + (2.0 ** -20 + (len(rows) * heads + 2) * 2.0 ** -24 + np.abs(got_lse[rows]).max() * 2.0 ** -22) * want
+        assert np.all(np.abs(got_w[s, 0, :c.lens[s]] - want) <= tol + 1e-30), s
+        assert not got_w[s, 0, c.lens[s]:].any()
