@@ -236,10 +236,10 @@ constexpr int kSumRow = D + 4;
 // 16 query rows and one item's pages: the wavefronts take every fourth page,
 // decoded from registers, and join in LDS in wavefront order.  A long cache is
 // bound by its reads (32 one-token steps of 32 heads over 3 .. 131071 slots of 8
-// heads of 128: 104 us for 575 MB, 5.5 TB/s with what the memory-side cache
+// heads of 128: 103 us for 575 MB, 5.6 TB/s with what the memory-side cache
 // kept), a short one by the chain of dependent reads and one page's work (777
-// slots: 10 us; at D = 256 that work and 16 rows of sums in 244 registers leave
-// two wavefronts a SIMD: 16 verify rounds of 5 tokens in a window of 1500 take 25 us for 40 MB).
+// slots: 10 us; at D = 256 that work and 16 rows of sums in 246 registers leave
+// two wavefronts a SIMD: 16 verify rounds of 5 tokens in a window of 1500 take 24 us for 40 MB).
 template <int D>
 __global__ void __launch_bounds__(64 * kWaves, 2)
 kv_attend_rows_kernel(AttendArgs a) {
@@ -429,7 +429,7 @@ kv_attend_rows_kernel(AttendArgs a) {
 // vector unit taking turns (a page's 32 products a wavefront take 1024 cycles,
 // its decode share and exponentials about 1400) at the 1.9 GHz that the card
 // holds under them: ragged prompt chunks of 700 .. 4099 tokens over 4100 ..
-// 8192 slots, 32 heads of 128, take 755 us, 906 TFLOP/s.
+// 8192 slots, 32 heads of 128, take 767 us, 891 TFLOP/s.
 template <int D>
 struct PageTiles {
     static constexpr int kBytes = 2 * kPage * D * 2;

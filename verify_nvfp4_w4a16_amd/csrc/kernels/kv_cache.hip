@@ -197,7 +197,7 @@ __device__ __forceinline__ uint64_t quantise16(u32x4 lo, u32x4 hi, const Scale& 
 // new rows is written in whole lines; the heads of a page lie next to each
 // other in the grid, as their rows do in memory.  Prompts are bound by the rows'
 // bytes (32,800 tokens of 8 heads of 128: 46 us for 172 MB, 3.7 TB/s; 50 us with
-// the codes by the boundaries alone), single tokens by latency (48: 6 us).
+// the codes by the boundaries alone; at a tensor scale of 24 bits 58 us), single tokens by latency (48: 6 us).
 template <int D>
 __global__ void __launch_bounds__(256)
 kv_append_kernel(KvView v, Rows kr, Rows vr, Scale ksc, Scale vsc) {
