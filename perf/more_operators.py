@@ -1,0 +1,718 @@
+"""Cases for the operators of a verify round over drafted trees: the page tables
+and slot maps of a step, attention of a tree's nodes over the paged 4-bit cache,
+penalties, biases and grammar masks on the nodes' logits, and the accepted
+branch's move to the front of its sequence.
+
+A sequence s of length n = kv_lens[s] has nq = q_starts[s + 1] - q_starts[s]
+new tokens, the last nq of its slots.  Of a drafted tree these are the nodes:
+node 0 is the root (the last token that is settled), parents[i] < i is the node
+that node i continues (-1: none), and a node sees the slots before the tree, its
+ancestors and itself.  A cache page holds 64 slots; the record of one (page, kv
+head) is 72 D bytes:
+
+  0     K codes   [64 slots][D / 2]            low nibble = even dim
+  32 D  V codes   [8 blocks][D][4 bytes]       nibble i = slot 8 block + i
+  64 D  K scales  [4 a][4 r][4 b][2 h][2 t][D / 64 j]
+                  slot = 32 h + 8 a + 4 t + r, 16-dim group = b D / 64 + j
+  68 D  V scales  [8 blocks][D / 16 groups][8 slots]
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+PAGE = 64
+K_SCALE, V_SCALE = 2.0 ** -6, 2.0 ** -7      # static tensor scales of the cache
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+VOCAB = 151552
+
+
+# ---------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # a decode step of 48 conversations: one token each, a few of which begin a page
+        dict(name="plan_step", op="plan", seqs=48, new=1, new_to=1, kept=10, kept_to=8000, tree=0, ends=0.0, mix=1),
+        # a round of drafted trees for 64 conversations: tables, slots, and what each node sees
+        dict(name="plan_trees", op="plan", seqs=64, new=7, new_to=64, kept=100, kept_to=16000, tree=64, ends=0.05, mix=2),
+        # whole prompts beside running conversations, of which a fifth have ended
+        dict(name="plan_prompts", op="plan", seqs=500, new=1, new_to=8191, kept=1, kept_to=9000, tree=0, ends=0.2, mix=3),
+        # one conversation, a tree of 16 nodes: the latency of a short cache
+        dict(name="tree_one", op="attend", seqs=1, new=16, new_to=16, kv=901, kv_to=901, mix=4,
+             heads=32, kv_heads=8, dim=128, window=0, cap=0.0),
+        # a serving batch with small trees over caches of a thousand to sixteen thousand slots
+        dict(name="tree_batch", op="attend", seqs=32, new=9, new_to=16, kv=1000, kv_to=16000, mix=5,
+             heads=32, kv_heads=8, dim=128, window=0, cap=0.0),
+        # trees of up to 64 nodes in a layer with a window and capped scores, wide heads
+        dict(name="tree_window", op="attend", seqs=16, new=40, new_to=64, kv=200, kv_to=9001, mix=6,
+             heads=16, kv_heads=8, dim=256, window=1500, cap=50.0),
+        # few long conversations with the largest trees
+        dict(name="tree_long", op="attend", seqs=4, new=200, new_to=255, kv=20000, kv_to=65000, mix=7,
+             heads=32, kv_heads=8, dim=128, window=0, cap=0.0),
+        # one conversation's next token, with penalties over its history
+        dict(name="adjust_one", op="adjust", seqs=1, new=1, new_to=1, said=2001, said_to=2001, vocab=VOCAB, type="float32",
+             bias=20, grammar=0.0, mix=8),
+        # a large batch's next tokens; some rows follow a grammar
+        dict(name="adjust_batch", op="adjust", seqs=192, new=1, new_to=1, said=10, said_to=32768, vocab=VOCAB, type="bfloat16",
+             bias=64, grammar=0.3, mix=9),
+        # the nodes of 8 trees, each with its own past, all of them under a grammar
+        dict(name="adjust_trees", op="adjust", seqs=8, new=33, new_to=64, said=500, said_to=6000, vocab=VOCAB, type="float32",
+             bias=300, grammar=1.0, mix=10),
+        # one conversation's tree in one layer: its rows go in, the accepted branch moves up
+        dict(name="commit_one", op="commit", seqs=1, new=16, new_to=16, kv=901, kv_to=901, layers=1, kv_heads=8, dim=128, mix=11),
+        # a batch's trees in eight layers
+        dict(name="commit_batch", op="commit", seqs=32, new=24, new_to=64, kv=100, kv_to=4000, layers=8, kv_heads=8, dim=128, mix=12),
+    ]
+
+
+def _log(rng, low, high):
+    return max(low, min(high, int(round(math.exp(rng.uniform(math.log(low), math.log(high)))))))
+
+
+def draw(rng):
+    op = rng.choice(("plan", "attend", "attend", "attend", "adjust", "adjust", "commit"))
+    mix = rng.randrange(1 << 30)
+    if op == "plan":
+        seqs = _log(rng, 1, 500)
+        tree = rng.choice((0, 0, rng.randint(1, 255)))
+        new_to = tree or _log(rng, 1, min(8191, 400000 // seqs))
+        kept_to = _log(rng, 1, 16000)
+        return dict(op=op, seqs=seqs, new=rng.randint(1, new_to), new_to=new_to, kept=rng.randint(1, kept_to), kept_to=kept_to,
+                    tree=tree, ends=rng.choice((0.0, 0.1, 0.3)), mix=mix)
+    if op == "adjust":
+        new_to = rng.choice((1, 1, _log(rng, 2, 255)))
+        seqs = _log(rng, 1, max(1, min(192, 500 // new_to)))
+        said_to = _log(rng, 1, 32768 if seqs * new_to < 200 else 6000)
+        return dict(op=op, seqs=seqs, new=rng.randint(1, new_to), new_to=new_to, said=rng.randint(0, said_to), said_to=said_to,
+                    vocab=_log(rng, 1000, VOCAB), type=rng.choice(("float32", "bfloat16")), bias=rng.choice((0, _log(rng, 1, 1000))),
+                    grammar=rng.choice((0.0, 0.5, 1.0)), mix=mix)
+    dim, kv_heads = rng.choice((64, 128, 128, 256)), rng.choice((1, 2, 4, 8))
+    heads = kv_heads * rng.choice((1, 2, 3, 4, 5, 8))
+    seqs = _log(rng, 1, 32)
+    new_to = _log(rng, 1, 255 if seqs <= 8 else 64)
+    most = min(65000, 260000 // seqs, 100_000_000_000 // (seqs * new_to * heads * dim))
+    kv_to = _log(rng, new_to + 1, max(2 * new_to + 2, most))
+    case = dict(op=op, seqs=seqs, new=rng.randint(1, new_to), new_to=new_to, kv=rng.randint(new_to, kv_to), kv_to=kv_to, mix=mix,
+                kv_heads=kv_heads, dim=dim)
+    if op == "commit":
+        return dict(case, layers=rng.randint(1, 4))
+    return dict(case, heads=heads, window=rng.choice((0, 0, rng.randint(1, 4096))), cap=rng.choice((0.0, 0.0, 30.0)))
+
+
+def _spread(rng, case, low, high):
+    """A number for each sequence between case[low] and case[high]; the first and the last are the range's ends."""
+    a = [_log(rng, max(case[low], 1), max(case[high], 1)) for _ in range(case["seqs"])]
+    a[0], a[-1] = case[low], case[high]
+    return a
+
+
+def _lens(case):
+    """What the sequences hold, and their numbers of new tokens."""
+    rng = random.Random(case["mix"])
+    op = case["op"]
+    if op == "plan":
+        held = _spread(rng, case, "kept", "kept_to")
+        new = _spread(rng, case, "new", "new_to")
+        for i in range(1, case["seqs"]):
+            if rng.random() < case["ends"]:      # a conversation that has ended: its pages are free again
+                held[i], new[i] = -held[i], 0
+        return held, new
+    if op == "adjust":
+        return _spread(rng, case, "said", "said_to"), _spread(rng, case, "new", "new_to")
+    kv = _spread(rng, case, "kv", "kv_to")
+    new = [min(n, m) for n, m in zip(kv, _spread(rng, case, "new", "new_to"))]
+    return kv, new
+
+
+def _pairs(case):
+    """At most this many (node, slot) pairs see each other, and this many slots are seen, over all sequences (chains)."""
+    pairs = slots = 0
+    w = case["window"] or (1 << 40)
+    for n, nq in zip(*_lens(case)):
+        pairs += nq * min(n, w) - (nq * (nq - 1) // 2 if n <= w else 0)
+        slots += min(n, w + nq - 1)
+    return pairs, slots
+
+
+def work(case):
+    op = case["op"]
+    was, new = _lens(case)
+    if op == "plan":
+        tokens, s = sum(new), case["seqs"]
+        grown = sum(max(0, -(-(h + n) // PAGE) - -(-h // PAGE)) for h, n in zip(was, new) if h > 0)
+        ended = sum(-(h // PAGE) for h in was if h < 0)
+        tree = tokens * (4 + 4 + 8 * -(-case["tree"] // 64)) if case["tree"] else 0
+        return {"bytes": s * 28 + grown * 8 + ended * 8 + tokens * 8 + tree, "flops": tokens * 4}
+    if op == "adjust":
+        rows, v = sum(new), case["vocab"]
+        each = 8 if case["type"] == "float32" else 4
+        return {"bytes": rows * v * each + sum(was) * 4 + int(rows * case["grammar"]) * v // 8 + case["seqs"] * case["bias"] * 8,
+                "flops": 4 * rows * v}
+    d, hk = case["dim"], case["kv_heads"]
+    row = d * 9 // 16                        # bytes of one K or V row of one head
+    if op == "commit":                       # rows in (bf16), rows stored, read back as values
+        t = sum(new) * hk * 2 * case["layers"]
+        return {"bytes": t * (2 * d + row + row + 2 * d), "flops": t * d * 4}
+    pairs, slots = _pairs(case)
+    q = sum(new) * case["heads"]
+    return {"bytes": slots * hk * 2 * row + q * (4 * d + 4) + sum(new) * (4 + 8 * -(-max(new) // 64)),
+            "flops": 4 * d * pairs * case["heads"]}
+
+
+# ---------------------------------------------------------------- inputs
+
+def _device():
+    return "cuda" if torch.cuda.is_available() else "cpu"
+
+
+def _codes(x, t):
+    """e2m1 codes and e4m3 scales (as bytes) of x [..., D] at the tensor scale t."""
+    g = x.float().unflatten(-1, (-1, 16))
+    s = (g.abs().amax(-1) / 6.0 / t).clamp(max=448.0).to(torch.float8_e4m3fn)
+    big = (s.float() * t).unsqueeze(-1)
+    v = torch.where(big > 0, g / torch.where(big > 0, big, torch.ones_like(big)), torch.zeros_like(g))
+    a = v.abs()
+    m = (a > 0.25).to(torch.uint8)
+    for at, on in ((0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
+        m += (a >= at) if on else (a > at)
+    return (m | ((v < 0) & (m > 0)).to(torch.uint8) << 3).flatten(-2), s.view(torch.uint8)
+
+
+def _packed(kc, ks, vc, vs):
+    """Records [..., 72 D] of codes [..., 64, D] and scale bytes [..., 64, D / 16]."""
+    d = kc.shape[-1]
+    kb = kc[..., 0::2] | kc[..., 1::2] << 4
+    vt = vc.unflatten(-2, (8, 8)).transpose(-1, -2)                       # [..., block, D, slot]
+    vb = vt[..., 0::2] | vt[..., 1::2] << 4
+    ks = ks.unflatten(-2, (2, 4, 2, 4)).unflatten(-1, (4, d // 64))       # h a t r b j
+    ks = ks.movedim((-5, -3, -2, -6, -4, -1), (-6, -5, -4, -3, -2, -1))   # a r b h t j
+    vs = vs.unflatten(-2, (8, 8)).transpose(-1, -2)
+    return torch.cat([kb.flatten(-2), vb.flatten(-3), ks.flatten(-6), vs.flatten(-3)], -1)
+
+
+def _cache(gen, pages, kv_heads, dim):
+    """Filled pages: normal rows, K with a factor of its own for each channel, as trained keys have."""
+    dev = gen.device
+    data = torch.empty(pages, kv_heads, 72 * dim, dtype=torch.uint8, device=dev)
+    spread = torch.exp(0.5 * torch.randn(kv_heads, 1, dim, generator=gen, device=dev))
+    step = max(1, (1 << 27) // (kv_heads * PAGE * dim))
+    for p in range(0, pages, step):
+        n = min(step, pages - p)
+        k = torch.randn(n, kv_heads, PAGE, dim, generator=gen, device=dev) * spread
+        v = torch.randn(n, kv_heads, PAGE, dim, generator=gen, device=dev)
+        data[p:p + n] = _packed(*_codes(k.bfloat16(), K_SCALE), *_codes(v.bfloat16(), V_SCALE))
+    return data
+
+
+def _trees(seed, new):
+    """Parents of drafted trees, as a drafter grows them: most nodes continue one of the last few."""
+    rng = random.Random(seed)
+    out = []
+    for n in new:
+        out += [-1 if i == 0 else rng.randint(max(0, i - 1 - rng.choice((0, 0, 1, 3, 9))), i - 1) for i in range(n)]
+    return out
+
+
+def _starts(new):
+    at = [0]
+    for n in new:
+        at.append(at[-1] + n)
+    return at
+
+
+def prepare(case, seed):
+    dev = _device()
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    rng = random.Random(seed)
+    st = dict(case)
+    op = case["op"]
+
+    def ints(x, dtype=torch.int32):
+        return torch.tensor(x, dtype=dtype, device=dev)
+
+    was, new = _lens(case)
+    s = case["seqs"]
+    if op == "plan":
+        held = [-(-abs(h) // PAGE) for h in was]
+        total, pages = sum(new), sum(held)
+        grown = sum(-(-(abs(h) + n) // PAGE) for h, n in zip(was, new))
+        order = torch.randperm(max(grown, pages) + 7, generator=gen, device=dev).int()
+        width = max(-(-(abs(h) + n) // PAGE) for h, n in zip(was, new)) + 3
+        table = torch.full((s, width), -1, dtype=torch.int32)
+        numbers = order.cpu()
+        at = 0
+        for i, n in enumerate(held):
+            table[i, :n] = numbers[at:at + n]
+            at += n
+        free = numbers[at:]
+        head = rng.randrange(len(numbers))
+        pool = torch.full((len(numbers),), -1, dtype=torch.int32)
+        pool[(head + torch.arange(len(free))) % len(numbers)] = free
+        st.update(pool=pool.to(dev), state=ints([head, len(free)]), table=table.to(dev), held=ints(held),
+                  kept=ints([max(h, 0) for h in was]), new=ints(new), total=total)
+        if case["tree"]:
+            st["parents"], st["max_q"] = ints(_trees(seed, new)), max(new)
+        return st
+    starts = _starts(new)
+    total = starts[-1]
+    st["total"], st["max_q"] = total, max(new)
+    st["q_starts"] = ints(starts)
+    st["parents"] = ints(_trees(seed, new))
+    if op == "adjust":
+        v = case["vocab"]
+        # a few likely tokens over a broad tail, as a head's logits are
+        x = torch.randn(total, v, generator=gen, device=dev) * 2.0
+        at = (torch.randint(0, v, (total, 1), generator=gen, device=dev) + torch.arange(40, device=dev) * (v // 40)) % v
+        x.scatter_add_(1, at, 8.0 + 3.0 * torch.randn(total, 40, generator=gen, device=dev))
+        st["logits"] = x.to(getattr(torch, case["type"]))
+        # texts repeat: few tokens often, many once
+        u = torch.rand(s, max(max(was), 1), generator=gen, device=dev)
+        st["history"] = (v * u ** 4).int().clamp(max=v - 1)
+        st["history_lens"] = ints(was)
+        st["prompt_lens"] = ints([rng.randint(0, n) for n in was])
+        rows = [rng.choice(((1.1, 0.0, 0.0), (1.0, 0.5, 0.2), (1.3, -0.3, 0.1), (1.0, 0.0, 0.0), (0.9, 0.4, 0.0))) for _ in range(s)]
+        rows[0] = (1.1, 0.5, 0.2)
+        for i, name in enumerate(("repetition", "presence", "frequency")):
+            st[name] = ints([r[i] for r in rows], torch.float32)
+        st["bias_tokens"] = st["bias_values"] = None
+        if case["bias"]:
+            count = min(case["bias"], v)
+            st["bias_tokens"] = torch.stack([torch.randperm(v, generator=gen, device=dev)[:count] for _ in range(s)]).int()
+            st["bias_values"] = 5.0 * torch.randn(s, count, generator=gen, device=dev)
+            st["bias_tokens"][:, count - count // 4:] = -1           # lists of less than the width end early
+        st["allowed"] = st["allowed_rows"] = None
+        if case["grammar"]:
+            states = 37                                              # of a grammar, each with its own tokens
+            few = torch.randint(-2 ** 31, 2 ** 31, (states, -(-v // 32)), generator=gen, device=dev).int()
+            few &= torch.randint(-2 ** 31, 2 ** 31, few.shape, generator=gen, device=dev).int()
+            st["allowed"] = few
+            st["allowed_rows"] = ints([rng.randrange(states) if rng.random() < case["grammar"] else -1 for _ in range(total)])
+        st["drafted"] = st["masks"] = None
+        if max(new) > 1:
+            st["drafted"] = (v * torch.rand(total, generator=gen, device=dev) ** 4).int().clamp(max=v - 1)
+            st["masks"] = _plain_masks(st["parents"], st["q_starts"], st["max_q"])[0]
+        return st
+    hk, d = case["kv_heads"], case["dim"]
+    need = [-(-n // PAGE) for n in was]
+    order = torch.randperm(sum(need), generator=gen, device=dev).int().tolist()
+    table = torch.zeros(s, max(need), dtype=torch.int32)
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = torch.tensor(order[at:at + n])
+        at += n
+    st["table"] = table.to(dev)
+    st["kv_lens"] = ints(was)
+    st["max_kv"] = max(was)
+    layers = case.get("layers", 1)
+    st["data"] = [_cache(gen, sum(need), hk, d) for _ in range(layers)]
+    if op == "attend":
+        h = case["heads"]
+        qkv = torch.randn(total, (h + 2 * hk) * d, generator=gen, device=dev).bfloat16()
+        st["q"] = qkv[:, :h * d].view(total, h, d)                   # a view of one projection's output
+        st["masks"], depth = _plain_masks(st["parents"], st["q_starts"], st["max_q"])
+        owner, before = _owners(st)
+        st["positions"] = (before + depth).int()
+    else:
+        st["rows"] = [torch.randn(total, 2 * hk, d, generator=gen, device=dev).bfloat16() for _ in range(layers)]
+        # the model agrees with one of a node's continuations three times of four
+        tokens = [rng.randrange(VOCAB) for _ in range(total)]
+        chosen = [rng.randrange(VOCAB) for _ in range(total)]
+        parents = st["parents"].tolist()
+        for a, b in zip(starts, starts[1:]):
+            for i in range(a + 1, b):
+                if rng.random() < 0.25:
+                    tokens[i] = tokens[rng.randrange(a, i)]          # drafts repeat a token now and then
+            for i in range(b - a):
+                after = [a + j for j in range(i + 1, b - a) if parents[a + j] == i]
+                if after and rng.random() < 0.75:
+                    chosen[a + i] = tokens[rng.choice(after)]
+        st["drafted"], st["chosen"] = ints(tokens), ints(chosen)
+    if own:
+        import verify_nvfp4_w4a16_amd as nv
+        st["caches"] = [nv.KvCache(x, hk, d, K_SCALE, V_SCALE) for x in st["data"]]
+    return st
+
+
+# ---------------------------------------------------------------- plain forms
+
+def _owners(st):
+    """The sequence of each packed token, and the number of slots before that sequence's new ones."""
+    starts = st["q_starts"].long()
+    t = torch.arange(st["total"], device=starts.device)
+    owner = torch.searchsorted(starts[1:], t, right=True)
+    return owner, (st["kv_lens"].long() - (starts[1:] - starts[:-1]))[owner]
+
+
+def _plain_masks(parents, q_starts, max_q):
+    """Which nodes of its own tree each node sees, as 64-bit words, and its depth."""
+    starts, total = q_starts.long(), parents.shape[0]
+    t = torch.arange(total, device=parents.device)
+    first = starts[torch.searchsorted(starts[1:], t, right=True)]
+    own_place = t - first
+    up = parents.long()
+    up = torch.where((up >= 0) & (up < own_place), up + first, t)      # a root stays where it is
+    words = -(-max_q // 64)
+    sees = torch.zeros(total, words * 64, dtype=torch.bool, device=t.device)
+    sees[t, own_place] = True
+    reach = 1
+    while reach < max_q:
+        sees = sees | sees[up]
+        up = up[up]
+        reach *= 2
+    bits = sees.view(total, words, 64).long() << torch.arange(64, device=t.device)
+    return bits.sum(-1), sees.sum(-1) - 1
+
+
+def _plain_plan(st):
+    table, pool, new = st["table"].clone(), st["pool"].clone(), st["new"].long().clamp(min=0)
+    s, width = table.shape
+    n = pool.shape[0]
+    dev = table.device
+    head, count = int(st["state"][0]), int(st["state"][1])
+    held = st["held"].long().clamp(0, width)
+    kept = torch.minimum(st["kept"].long().clamp(min=0), held * PAGE)
+    want = kept + new
+    need = (want + PAGE - 1) // PAGE
+    fits = need <= width
+    extra = torch.where(fits, (need - held).clamp(min=0), torch.zeros_like(need))
+    asked = torch.cumsum(torch.where(fits, new, torch.zeros_like(new)), 0)
+    pages = torch.cumsum(extra, 0)
+    granted = fits & ((extra == 0) | (pages <= count)) & ((new == 0) | (asked <= st["total"]))
+    lens = torch.where(granted, want, kept)
+    got = torch.where(granted, new, torch.zeros_like(new))
+    after = torch.where(granted, need, held)
+    # pages taken from the pool's front, in the order of the sequences
+    j = torch.arange(width, device=dev)
+    takes = (j >= held[:, None]) & (j < after[:, None])
+    taken = int(takes.sum())
+    frees = (j < held[:, None]) & (j >= after[:, None])
+    freed = table[frees]
+    table[takes] = pool[(head + torch.arange(taken, device=dev)) % n]
+    freed = freed[:n - count]
+    pool[(head + count + torch.arange(freed.shape[0], device=dev)) % n] = freed
+    state = torch.tensor([(head + taken) % n, count - taken + freed.shape[0]], dtype=torch.int32, device=dev)
+    q_starts = torch.cat([torch.zeros(1, dtype=torch.int64, device=dev), torch.cumsum(got, 0)])
+    t = torch.arange(st["total"], device=dev)
+    owner = torch.searchsorted(q_starts[1:], t, right=True).clamp(max=s - 1)
+    live = t < q_starts[-1]
+    slot = lens[owner] - q_starts[owner + 1] + t
+    slot = torch.where(live, slot, torch.zeros_like(slot))
+    page = table[owner, slot // PAGE].long()
+    none = torch.full_like(slot, -1)
+    slots = torch.where(live & (page >= 0) & (page < 1 << 25), page * PAGE + slot % PAGE, none)
+    out = (pool, state, table, after.int(), lens.int(), q_starts.int(), slots.int(), torch.where(live, slot, none).int())
+    if not st["tree"]:
+        return out
+    masks, depth = _plain_masks(st["parents"], q_starts, st["max_q"])
+    before = (lens - got)[owner]
+    return out + (masks, (before + depth).int())
+
+
+def _nibbles(b):
+    return torch.stack((b & 15, b >> 4), -1).flatten(-2)
+
+
+def _unpacked(rec, d):
+    """The inverse of _packed."""
+    kc, vc, ks, vs = rec.split([32 * d, 32 * d, 4 * d, 4 * d], -1)
+    kc = _nibbles(kc.unflatten(-1, (PAGE, d // 2)))
+    ks = ks.unflatten(-1, (4, 4, 4, 2, 2, d // 64))
+    ks = ks.movedim((-6, -5, -4, -3, -2, -1), (-5, -3, -2, -6, -4, -1)).flatten(-2).flatten(-5, -2)
+    vc = _nibbles(vc.unflatten(-1, (8, d, 4))).transpose(-1, -2).flatten(-3, -2)
+    vs = vs.unflatten(-1, (8, d // 16, 8)).transpose(-1, -2).flatten(-3, -2)
+    return kc, ks, vc, vs
+
+
+def _values(c, s, t):
+    sign_and_size = torch.tensor(E2M1 + tuple(-x for x in E2M1), device=c.device)
+    x = sign_and_size[c.int()].unflatten(-1, (-1, 16))
+    return (x * (s.contiguous().view(torch.float8_e4m3fn).float() * t).unsqueeze(-1)).flatten(-2)
+
+
+def _decoded(rec, d):
+    """K and V of records [..., 72 D] in 32 bits: [..., 64, D] each."""
+    kc, ks, vc, vs = _unpacked(rec, d)
+    return _values(kc, ks, K_SCALE), _values(vc, vs, V_SCALE)
+
+
+def _seen_bits(masks, words):
+    return (masks[..., None] >> torch.arange(64, device=masks.device) & 1).bool().flatten(-2)[..., :words * 64]
+
+
+def _plain_attend(st):
+    s, hk, d, mq = st["seqs"], st["kv_heads"], st["dim"], st["max_q"]
+    g = st["heads"] // hk
+    k, v = (x.flatten(2, 3) for x in _decoded(st["data"][0][st["table"].long()].transpose(1, 2), d))
+    lens, starts = st["kv_lens"].long(), st["q_starts"].long()
+    new = starts[1:] - starts[:-1]
+    i = torch.arange(mq, device=k.device)
+    there = i < new[:, None]                                              # [S, mq]
+    at = (starts[:-1, None] + i).clamp(max=max(0, st["total"] - 1))
+    q = st["q"].float()[at].view(s, mq, hk, g, d).permute(0, 2, 3, 1, 4).reshape(s, hk, g * mq, d)
+    z = torch.matmul(q, k.transpose(-1, -2)) * d ** -0.5
+    if st["cap"]:
+        z = st["cap"] * torch.tanh(z / st["cap"])
+    j = torch.arange(k.shape[2], device=k.device)
+    before = lens - new
+    node = j - before[:, None]                                            # [S, slots]: a new slot's place in the tree
+    bits = _seen_bits(st["masks"][at], st["masks"].shape[1])              # [S, mq, words 64]
+    inside = (node >= 0) & (j < lens[:, None])
+    in_tree = bits.gather(2, node.clamp(0, bits.shape[2] - 1)[:, None].expand(-1, mq, -1)) & inside[:, None]
+    cached = (j < before[:, None])[:, None].expand(-1, mq, -1)
+    if st["window"]:
+        cached = cached & (j > st["positions"].long()[at][..., None] - st["window"])
+    seen = (cached | in_tree) & there[..., None]
+    z = z.view(s, hk, g, mq, -1).masked_fill_(~seen[:, None, None], float("-inf"))
+    top = z.amax(-1, keepdim=True)
+    top = torch.where(torch.isinf(top), torch.zeros_like(top), top)
+    e = torch.exp(z - top)
+    total = e.sum(-1, keepdim=True)
+    out = torch.matmul(e.view(s, hk, g * mq, -1), v).view(s, hk, g, mq, -1) / torch.where(total > 0, total, torch.ones_like(total))
+    lse = (torch.log(total) + top).squeeze(-1)
+    pick = torch.nonzero(there.reshape(-1)).squeeze(-1)
+    out = out.permute(0, 3, 1, 2, 4).reshape(s * mq, hk * g, -1)[pick]
+    lse = lse.permute(0, 3, 1, 2).reshape(s * mq, hk * g)[pick]
+    return out.bfloat16(), lse
+
+
+def _plain_adjust(st):
+    x = st["logits"].float()
+    rows, v = x.shape
+    dev = x.device
+    starts = st["q_starts"].long()
+    owner = torch.searchsorted(starts[1:], torch.arange(rows, device=dev), right=True)
+    j = torch.arange(st["history"].shape[1], device=dev)
+    in_text = j < st["history_lens"][:, None]
+    in_prompt = j < st["prompt_lens"][:, None]
+    said = st["history"].long()
+    prompt = torch.zeros(st["seqs"], v, device=dev).scatter_add_(1, said, (in_text & in_prompt).float())
+    times = torch.zeros(st["seqs"], v, device=dev).scatter_add_(1, said, (in_text & ~in_prompt).float())
+    n = times[owner]
+    if st["drafted"] is not None:
+        bits = _seen_bits(st["masks"], st["masks"].shape[1])
+        node = torch.arange(bits.shape[1], device=dev)
+        token = st["drafted"].long()[(starts[owner][:, None] + node).clamp(max=rows - 1)]
+        n.scatter_add_(1, token, bits.float())
+    seen = (n > 0) | (prompt[owner] > 0)
+    r = st["repetition"][owner][:, None]
+    x = torch.where(seen, torch.where(x > 0, x / r, x * r), x)
+    x = x - st["presence"][owner][:, None] * (n > 0) - st["frequency"][owner][:, None] * n
+    if st["bias_tokens"] is not None:
+        token, value = st["bias_tokens"].long(), st["bias_values"]
+        value = torch.where(token >= 0, value, torch.zeros_like(value))
+        x = x + torch.zeros(st["seqs"], v, device=dev).scatter_add_(1, token.clamp(min=0), value)[owner]
+    if st["allowed"] is not None:
+        state = st["allowed_rows"].long()
+        words = st["allowed"][state.clamp(min=0)]
+        free = (words[..., None] >> torch.arange(32, device=dev) & 1).bool().flatten(-2)[:, :v]
+        x = x.masked_fill(~free & (state >= 0)[:, None], float("-inf"))
+    return x.to(st["logits"].dtype)
+
+
+def _plain_commit(st):
+    starts, lens = st["q_starts"].long(), st["kv_lens"].long()
+    new = starts[1:] - starts[:-1]
+    s, mq, d, dev = st["seqs"], st["max_q"], st["dim"], starts.device
+    owner, before = _owners(st)
+    place = torch.arange(st["total"], device=dev) - starts[owner]
+    up = st["parents"].long()
+    # the continuation of each node that carries the model's token, the lowest where several do
+    nodes = torch.full((s, mq + 1), mq, dtype=torch.int64, device=dev)
+    inner = (up >= 0) & (up < place)
+    agrees = inner & (st["drafted"] == st["chosen"][starts[owner] + torch.where(inner, up, place)]) & (st["drafted"] >= 0)
+    nodes.view(-1).scatter_reduce_(0, owner * (mq + 1) + torch.where(agrees, up, torch.full_like(up, mq)),
+                                   torch.where(agrees, place, torch.full_like(place, mq)), "amin")
+    nodes[:, mq] = mq
+    at = torch.where(new > 0, torch.zeros_like(new), torch.full_like(new, mq))
+    path, last = [], at
+    for _ in range(mq):
+        path.append(at)
+        last = torch.where(at < mq, at, last)
+        at = nodes.gather(1, at[:, None]).squeeze(1)
+    path = torch.stack(path, 1)
+    count = (path < mq).sum(1)
+    token = torch.where(new > 0, st["chosen"].long()[(starts[:-1] + last).clamp(max=st["total"] - 1)], torch.full_like(new, -1))
+    new_lens = lens - new + count
+    out = [torch.where(path < mq, path, torch.full_like(path, -1)).int(), count.int(), token.int(), new_lens.int()]
+    slot = before + place
+    page, in_page = st["table"].long()[owner, slot // PAGE], slot % PAGE
+    step = torch.arange(mq, device=dev).expand(s, -1)
+    move = path < mq
+    src = (lens - new)[:, None] + path
+    dst = (lens - new)[:, None] + step
+    src, dst, whose = src[move], dst[move], torch.arange(s, device=dev)[:, None].expand(-1, mq)[move]
+    for data, rows in zip(st["data"], st["rows"]):
+        pages, inverse = torch.unique(page, return_inverse=True)
+        rank = torch.zeros(data.shape[0], dtype=torch.int64, device=dev)
+        rank[pages] = torch.arange(pages.shape[0], device=dev)
+        parts = [x.clone() for x in _unpacked(data[pages], d)]              # [pages, H, 64, ...] each
+        hk = st["kv_heads"]
+        fresh = _codes(rows[:, :hk], K_SCALE) + _codes(rows[:, hk:], V_SCALE)
+        a = rank[st["table"].long()[whose, src // PAGE]]
+        b = rank[st["table"].long()[whose, dst // PAGE]]
+        for part, x in zip(parts, fresh):
+            part[inverse, :, in_page] = x
+            part[b, :, dst % PAGE] = part[a, :, src % PAGE]
+        data[pages] = _packed(*parts)
+        k, v = _values(parts[0], parts[1], K_SCALE), _values(parts[2], parts[3], V_SCALE)
+        out += [k[inverse, :, in_page].bfloat16(), v[inverse, :, in_page].bfloat16()]
+    return tuple(out)
+
+
+def run(state):
+    st, op = state, state["op"]
+    if not own:
+        return {"plan": _plain_plan, "attend": _plain_attend, "adjust": _plain_adjust, "commit": _plain_commit}[op](st)
+    import verify_nvfp4_w4a16_amd as nv
+    if op == "plan":
+        step = nv.kv_pages(st["pool"], st["state"], st["table"], st["held"], st["kept"], st["new"], st["total"])
+        out = (st["pool"], step.state, st["table"], step.held, step.kv_lens, step.q_starts, step.slots, step.positions)
+        if not st["tree"]:
+            return out
+        return out + nv.kv_tree(st["parents"], step.kv_lens, step.q_starts, st["max_q"])
+    if op == "attend":
+        return nv.kv_tree_attention(st["q"], st["caches"][0], st["table"], st["kv_lens"], st["q_starts"], st["masks"], st["positions"],
+                                    st["max_q"], st["max_kv"], window=st["window"], softcap=st["cap"])
+    if op == "adjust":
+        tree = dict(drafted=st["drafted"], masks=st["masks"]) if st["drafted"] is not None else {}
+        return nv.adjust_logits(st["logits"], st["history"], st["history_lens"], prompt_lens=st["prompt_lens"], q_starts=st["q_starts"],
+                                repetition=st["repetition"], presence=st["presence"], frequency=st["frequency"],
+                                bias_tokens=st["bias_tokens"], bias_values=st["bias_values"], allowed=st["allowed"],
+                                allowed_rows=st["allowed_rows"], **tree)
+    where = (st["table"], st["kv_lens"], st["q_starts"])
+    hk = st["kv_heads"]
+    # a tree's rows go in anew, so that a pass finds what the last one moved
+    for cache, rows in zip(st["caches"], st["rows"]):
+        nv.kv_append(cache, rows[:, :hk], rows[:, hk:], *where)
+    out = nv.tree_accept(st["drafted"], st["parents"], st["chosen"], st["kv_lens"], st["q_starts"], st["max_q"])
+    nv.kv_move(st["caches"], *where, out[0])
+    for cache in st["caches"]:
+        out += nv.kv_read(cache, *where, st["total"])
+    return out
+
+
+# ---------------------------------------------------------------- the definition in 64 bits
+
+def _slots64(st, i):
+    """K and V rows of one sequence, one page after the other by the layout's own words: [heads, slots, D] in 64 bits."""
+    d = st["dim"]
+    hk = st["kv_heads"]
+    data = st["data"][0]
+    grid = torch.tensor([(-1.0 if c & 8 else 1.0) * ((c & 1) * 0.5 if c & 6 == 0 else (1 + 0.5 * (c & 1)) * 2.0 ** ((c >> 1 & 3) - 1)) for c in range(16)],
+                        dtype=torch.float64, device=data.device)
+    e4m3 = torch.tensor([(b & 7) * 2.0 ** -9 if b >> 3 == 0 else (8 + (b & 7)) * 2.0 ** ((b >> 3) - 10) for b in range(128)],
+                        dtype=torch.float64, device=data.device)
+    n = int(st["kv_lens"][i])
+    rec = data[st["table"][i, :-(-n // PAGE)].long()]                     # [P, H, 72 D]
+    slot = torch.arange(PAGE, device=rec.device)[:, None]
+    dim = torch.arange(d, device=rec.device)[None]
+    group = dim // 16
+    per = d // 64
+    k_at = slot * (d // 2) + dim // 2
+    v_at = 32 * d + (slot // 8 * d + dim) * 4 + slot % 8 // 2
+    h, a, t, r = slot // 32, slot // 8 % 4, slot // 4 % 2, slot % 4
+    ks_at = 64 * d + ((((a * 4 + r) * 4 + group // per) * 2 + h) * 2 + t) * per + group % per
+    vs_at = 68 * d + (slot // 8 * (d // 16) + group) * 8 + slot % 8
+    k = grid[(rec[..., k_at] >> 4 * (dim % 2).to(torch.uint8) & 15).long()] * e4m3[rec[..., ks_at].long()] * K_SCALE
+    v = grid[(rec[..., v_at] >> 4 * (slot % 2).to(torch.uint8) & 15).long()] * e4m3[rec[..., vs_at].long()] * V_SCALE
+    return (x.transpose(0, 1).reshape(hk, -1, d)[:, :n] for x in (k, v))
+
+
+def _ancestors(parents):
+    """For each node of one tree, the nodes on its way from the root, itself among them."""
+    ways = []
+    for i, p in enumerate(parents):
+        ways.append((ways[p] if 0 <= p < i else []) + [i])
+    return ways
+
+
+def _attended64(st):
+    outs, lses = [], []
+    starts = st["q_starts"].tolist()
+    parents = st["parents"].tolist()
+    for i in range(st["seqs"]):
+        k, v = _slots64(st, i)
+        a, b, n, hk = starts[i], starts[i + 1], k.shape[1], st["kv_heads"]
+        q = st["q"][a:b].double().view(b - a, hk, -1, st["dim"]).permute(1, 2, 0, 3)
+        z = (q.reshape(hk, -1, st["dim"]) @ k.mT.contiguous()).view(hk, -1, b - a, n) / math.sqrt(st["dim"])
+        if st["cap"]:
+            z = torch.tanh(z / st["cap"]) * st["cap"]
+        hidden = torch.ones(b - a, n, dtype=torch.bool)
+        before = n - (b - a)
+        for node, way in enumerate(_ancestors(parents[a:b])):
+            place = before + len(way) - 1
+            hidden[node, max(0, place - st["window"] + 1) if st["window"] else 0:before] = False
+            hidden[node, [before + w for w in way]] = False
+        z = z.masked_fill(hidden.to(z.device), -math.inf)
+        lse = torch.logsumexp(z, -1)
+        o = (torch.exp(z - lse[..., None]).reshape(hk, -1, n) @ v).view(*z.shape[:3], -1)
+        outs.append(o.permute(2, 0, 1, 3).reshape(b - a, st["heads"], -1))
+        lses.append(lse.permute(2, 0, 1).reshape(b - a, st["heads"]))
+    return torch.cat(outs), torch.cat(lses)
+
+
+def _adjusted64(st):
+    x = st["logits"].double()
+    starts = st["q_starts"].tolist()
+    parents = st["parents"].tolist()
+    v = x.shape[1]
+    for i in range(st["seqs"]):
+        text = st["history"][i, :int(st["history_lens"][i])].long()
+        cut = int(st["prompt_lens"][i])
+        asked, said = torch.bincount(text[:cut], minlength=v), torch.bincount(text[cut:], minlength=v)
+        r, p, f = (float(st[name][i]) for name in ("repetition", "presence", "frequency"))
+        ways = _ancestors(parents[starts[i]:starts[i + 1]]) if st["drafted"] is not None else [[]] * (starts[i + 1] - starts[i])
+        for row, way in enumerate(ways, starts[i]):
+            n = said
+            if way:
+                n = n + torch.bincount(st["drafted"][starts[i]:][torch.tensor(way, device=x.device)].long(), minlength=v)
+            y = x[row]
+            y = torch.where((n + asked > 0) & (y > 0), y / r, torch.where(n + asked > 0, y * r, y)) - f * n - p * (n > 0).double()
+            if st["bias_tokens"] is not None:
+                has = st["bias_tokens"][i] >= 0
+                y[st["bias_tokens"][i][has].long()] += st["bias_values"][i][has].double()
+            if st["allowed"] is not None and int(st["allowed_rows"][row]) >= 0:
+                words = st["allowed"][int(st["allowed_rows"][row])]
+                token = torch.arange(v, device=x.device)
+                y[(words[token // 32] >> (token % 32).int() & 1) == 0] = -math.inf
+            x[row] = y
+    return x
+
+
+def _quantised64(x, t):
+    g = x.double().unflatten(-1, (-1, 16))
+    u = (g.abs().amax(-1) / 6 / t).clamp(max=448.0)
+    step = torch.exp2(torch.floor(torch.log2(u.clamp(min=2.0 ** -6))) - 3)
+    s = (torch.round(u / step) * step).clamp(max=448.0) * t
+    v = torch.where(s[..., None] > 0, g / s[..., None].clamp(min=1e-300), torch.zeros_like(g)).clamp(-6, 6)
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=1.0))) - 1)
+    return (torch.round(v / step) * step * s[..., None]).flatten(-2)
+
+
+def _committed64(st):
+    starts, parents = st["q_starts"].tolist(), st["parents"].tolist()
+    drafted, chosen = st["drafted"].tolist(), st["chosen"].tolist()
+    source = list(range(st["total"]))
+    for a, b in zip(starts, starts[1:]):
+        at, step = 0, 0
+        while at is not None and a < b:
+            source[a + step] = a + at
+            step += 1
+            at = next((c for c in range(at + 1, b - a) if parents[a + c] == at and drafted[a + c] == chosen[a + at]), None)
+    out = [None] * 4
+    for rows in st["rows"]:
+        for x, t in ((rows[:, :st["kv_heads"]], K_SCALE), (rows[:, st["kv_heads"]:], V_SCALE)):
+            out.append(_quantised64(x, t)[torch.tensor(source, device=x.device)])
+    return tuple(out)
+
+
+def exact(case, seed):
+    if case["op"] == "plan" or (case["op"] == "attend" and _pairs(case)[0] * case["heads"] * case["dim"] > 2e11):
+        return None
+    global own
+    was, own = own, False
+    st = prepare(case, seed)
+    own = was
+    return {"attend": _attended64, "adjust": _adjusted64, "commit": _committed64}[case["op"]](st)
