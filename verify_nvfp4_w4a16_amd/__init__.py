@@ -362,14 +362,21 @@ def linear(x, w_packed, scales, tensor_scale: float, out=None, out_dtype=None, s
 
 
 # The serving step around the products (paged NVFP4 cache, sampling) lives in
-# serving.py, which needs torch; its names are this package's, loaded on first use.
+# serving.py and the verify round over drafted trees in drafting.py, which need
+# torch; their names are this package's, loaded on first use.
 _SERVING = ("KvCache", "kv_append", "kv_read", "kv_attention", "kv_attention_workspace", "kv_weights", "kv_evict", "sample")
+_DRAFTING = ("KvStep", "kv_pages", "kv_tree", "kv_tree_attention", "kv_tree_attention_workspace", "adjust_logits", "tree_accept", "kv_move")
 
 
 def __getattr__(name):
     if name in _SERVING:
-        from . import serving
-        for n in _SERVING:
-            globals()[n] = getattr(serving, n)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        from . import serving as module
+        names = _SERVING
+    elif name in _DRAFTING:
+        from . import drafting as module
+        names = _DRAFTING
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    for n in names:
+        globals()[n] = getattr(module, n)
+    return globals()[name]

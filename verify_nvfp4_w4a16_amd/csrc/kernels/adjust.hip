@@ -1,0 +1,232 @@
+// Penalties, biases and grammar masks on logits (include/nvfp4_draft.h).
+//
+// A workgroup takes a piece of the vocabulary and up to kRows rows of one
+// sequence.  It counts the sequence's history into LDS, a word a token (counts
+// are whole numbers, so the order of the atomic additions changes nothing),
+// then streams its rows' logits once: read, adjust by the word, write.  A
+// row's own drafted tokens are counted in before the row and out after it.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "../host/draft_shapes.h"
+#include "nvfp4_common.h"
+#include "setup.h"
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kPiece = 8192;   // tokens of a workgroup
+constexpr int kRows = 8;       // rows that share the counted history
+
+// A token's word: how often it was said, its place in the bias list plus 1, and whether the prompt has it.
+constexpr uint32_t kCount = (1u << 20) - 1;
+constexpr int kBiasShift = 20;
+constexpr uint32_t kBias = 0x7ffu << kBiasShift;
+constexpr uint32_t kPrompt = 1u << 31;
+static_assert(nvfp4::kHistoryMax + NVFP4_TREE_MAX < kCount && NVFP4_BIAS_MAX < 0x7ff);
+
+struct AdjustArgs {
+    nvfp4_adjust_t a;
+    void* out;
+    int vocab, pieces, seqs, rows;
+};
+
+// Rows may begin at any element, so whole vectors are read from wherever they begin.
+template <class V>
+__device__ __forceinline__ V load_any(const void* p) {
+    V v;
+    __builtin_memcpy(&v, p, sizeof v);
+    return v;
+}
+
+// The first unit of sequence s, a unit being kRows rows: enough wherever its rows begin.
+__device__ __forceinline__ int first_unit(int start, int s) { return start / kRows + s; }
+
+template <class In, class Out>
+__global__ void __launch_bounds__(kThreads)
+adjust_kernel(AdjustArgs args) {
+    constexpr int kEach = 16 / sizeof(In);   // logits of a load
+    __shared__ __attribute__((aligned(16))) uint32_t words[kPiece];
+    __shared__ float bias[NVFP4_BIAS_MAX];
+    const nvfp4_adjust_t& a = args.a;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int unit = blockIdx.x / args.pieces, piece = blockIdx.x % args.pieces;
+    const int from = piece * kPiece, size = min(kPiece, args.vocab - from);
+
+    // the sequence of this unit and its rows
+    int s = unit, row0 = unit, row_end = unit + 1, first = unit;
+    if (a.q_starts) {
+        auto start = [&](int i) { return min(max(a.q_starts[i], 0), args.rows); };
+        int found = 0;
+        for (int base = 0; base < args.seqs; base += 64) {
+            const int n = __popcll(__ballot(base + lane < args.seqs && first_unit(start(min(base + lane, args.seqs)), base + lane) <= unit));
+            found += n;
+            if (n < 64) break;
+        }
+        s = found - 1;
+        if (s < 0) return;
+        first = start(s);
+        const int end = start(s + 1);
+        row0 = first + (unit - first_unit(first, s)) * kRows;
+        if (row0 < first) return;            // as happens where starts descend
+        row_end = min(row0 + kRows, end);
+        if (row0 >= row_end) return;
+    }
+
+    const float r_in = a.repetition ? a.repetition[s] : 1.0f;
+    const float r = r_in > 0.0f ? r_in : 1.0f;
+    const float p = a.presence ? a.presence[s] : 0.0f, f = a.frequency ? a.frequency[s] : 0.0f;
+    const bool penalised = r != 1.0f || p != 0.0f || f != 0.0f;
+    const bool counted = penalised && a.history, drafts = penalised && a.drafted, biased = a.bias_tokens && a.bias_width > 0;
+    const bool worded = counted || drafts || biased;
+    if (worded) {
+        for (int i = tid * 4; i < kPiece; i += kThreads * 4) *reinterpret_cast<u32x4*>(words + i) = u32x4{0, 0, 0, 0};
+        __syncthreads();
+    }
+    if (counted) {
+        const int32_t* said = a.history + s * a.history_pitch;
+        const int len = static_cast<int>(min(int64_t(max(a.history_lens[s], 0)), a.history_pitch));
+        const int prompt = a.prompt_lens ? min(max(a.prompt_lens[s], 0), len) : 0;
+        auto put = [&](int at, int token) {
+            const uint32_t v = uint32_t(token) - uint32_t(from);
+            if (v >= uint32_t(size)) return;
+            if (at < prompt)
+                atomicOr(&words[v], kPrompt);
+            else
+                atomicAdd(&words[v], 1u);
+        };
+        int i = tid * 4;
+        for (; i + 3 < len; i += kThreads * 4) {
+            const u32x4 t = load_any<u32x4>(said + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) put(i + j, static_cast<int>(t[j]));
+        }
+        for (int j = i; j < min(i + 4, len); ++j) put(j, said[j]);
+    }
+    if (biased) {
+        __syncthreads();
+        // the last entry of a token counts: the largest place wins, above a count that both find
+        for (int i = tid; i < a.bias_width; i += kThreads) {
+            const uint32_t v = uint32_t(a.bias_tokens[s * a.bias_width + i]) - uint32_t(from);
+            if (v >= uint32_t(size)) continue;
+            bias[i] = a.bias_values[s * a.bias_width + i];
+            atomicMax(&words[v], (words[v] & ~kBias) | uint32_t(i + 1) << kBiasShift);
+        }
+    }
+    if (worded) __syncthreads();
+
+    for (int row = row0; row < row_end; ++row) {
+        // the row's drafted tokens, one a thread
+        int drafted = -1;
+        if (drafts) {
+            const int node = tid;
+            if (node < 64 * a.mask_words && first + node < args.rows && (a.masks[row * a.mask_words + node / 64] >> (node & 63) & 1)) {
+                const uint32_t v = uint32_t(a.drafted[first + node]) - uint32_t(from);
+                if (v < uint32_t(size)) drafted = static_cast<int>(v);
+            }
+            if (drafted >= 0) atomicAdd(&words[drafted], 1u);
+            __syncthreads();
+        }
+        const uint32_t* allowed = nullptr;
+        if (a.allowed) {
+            const int64_t state = a.allowed_rows ? a.allowed_rows[row] : row;
+            if (state >= 0 && state < a.states) allowed = a.allowed + state * a.allowed_pitch + from / 32;
+        }
+        const In* in = static_cast<const In*>(a.logits) + row * a.pitch + from;
+        Out* out = static_cast<Out*>(args.out) + row * a.out_pitch + from;
+        auto one = [&](float x, int i) {
+            const uint32_t w = worded ? words[i] : 0;
+            if (w) {
+                const uint32_t n = w & kCount;
+                if (penalised && (w & (kPrompt | kCount))) {
+                    x = x > 0.0f ? x / r : x * r;
+                    if (n) x = x - p - f * float(n);
+                }
+                if (w & kBias) x += bias[((w & kBias) >> kBiasShift) - 1];
+            }
+            return x;
+        };
+        for (int i = tid * kEach; i < size; i += kThreads * kEach) {
+            float x[kEach];
+            const bool whole = i + kEach <= size;
+            uint32_t bits = ~0u;
+            if (allowed) bits = allowed[i / 32] >> (i % 32);
+            if (whole) {
+                const u32x4 v = load_any<u32x4>(in + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (std::is_same_v<In, float>) {
+                        x[j] = bits_f32(v[j]);
+                    } else {
+                        x[2 * j] = bits_f32(v[j] << 16);
+                        x[2 * j + 1] = bits_f32(v[j] & 0xffff0000u);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    if (i + j >= size) continue;
+                    if constexpr (std::is_same_v<In, float>)
+                        x[j] = in[i + j];
+                    else
+                        x[j] = bf16_to_f32(in[i + j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                if (!whole && i + j >= size) continue;
+                x[j] = one(x[j], i + j);
+                if (!(bits >> j & 1)) x[j] = -INFINITY;
+            }
+            if (whole) {
+                if constexpr (std::is_same_v<Out, float>) {
+                    __builtin_memcpy(out + i, x, sizeof x);
+                } else {
+                    uint16_t w[kEach];
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j) w[j] = f32_to_bf16_rne(x[j]);
+                    __builtin_memcpy(out + i, w, sizeof w);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    if (i + j >= size) continue;
+                    if constexpr (std::is_same_v<Out, float>)
+                        out[i + j] = x[j];
+                    else
+                        out[i + j] = f32_to_bf16_rne(x[j]);
+                }
+            }
+        }
+        if (drafts) {
+            __syncthreads();
+            if (drafted >= 0) atomicSub(&words[drafted], 1u);
+        }
+    }
+}
+
+}  // namespace
+
+extern "C" int nvfp4_adjust_logits(const nvfp4_adjust_t* adjust, void* out, void* stream) {
+    int st;
+    if ((st = nvfp4::check_adjust(adjust, out)) != NVFP4_OK) return st;
+    if (adjust->rows == 0 || adjust->seqs == 0) return NVFP4_OK;
+    if ((st = nvfp4::device_setup()) != NVFP4_OK) return st;
+    AdjustArgs a{*adjust, out, static_cast<int>(adjust->vocab), static_cast<int>((adjust->vocab + kPiece - 1) / kPiece),
+                 static_cast<int>(adjust->seqs), static_cast<int>(adjust->rows)};
+    const int64_t units = adjust->q_starts ? adjust->rows / kRows + adjust->seqs : adjust->rows;
+    const dim3 grid(static_cast<unsigned>(units * a.pieces)), block(kThreads);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const bool in32 = adjust->logits_type == NVFP4_LOGITS_F32, out32 = adjust->out_type == NVFP4_LOGITS_F32;
+    if (in32 && out32)
+        hipLaunchKernelGGL((adjust_kernel<float, float>), grid, block, 0, s, a);
+    else if (in32)
+        hipLaunchKernelGGL((adjust_kernel<float, uint16_t>), grid, block, 0, s, a);
+    else if (out32)
+        hipLaunchKernelGGL((adjust_kernel<uint16_t, float>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((adjust_kernel<uint16_t, uint16_t>), grid, block, 0, s, a);
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}

@@ -1,0 +1,340 @@
+// The whole numbers of a verify round (include/nvfp4_draft.h): page tables and
+// slot maps of a step, what the nodes of a drafted tree see, and the branch
+// that the model accepts.  All of it is bound by latency: scans over the
+// sequences, chains of parents, and the launches themselves.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../host/draft_shapes.h"
+#include "../host/kv_shapes.h"
+#include "setup.h"
+
+namespace {
+
+constexpr int kPage = NVFP4_KV_PAGE;
+constexpr int kTreeMax = NVFP4_TREE_MAX;
+constexpr int kScanThreads = 1024;
+constexpr int kFillThreads = 256, kFillEach = 8;   // tokens of a thread
+// Slots and positions of this many tokens at most are filled by the workgroup
+// that makes the tables, which spares a launch.
+constexpr int kFillInline = 4096;
+
+struct PagesArgs {
+    int32_t* pool;
+    const int32_t* state;
+    int32_t* table;
+    const int32_t *held, *keep, *fresh;
+    int32_t *state_out, *held_out, *kv_lens, *q_starts, *slots, *positions;
+    int64_t table_pitch;
+    int capacity, seqs, total;
+};
+
+// The last of the ascending p[first .. last] that is at most t, where p[first] is.
+__device__ __forceinline__ int last_at_most(const int32_t* p, int first, int last, int t) {
+    while (first < last) {
+        const int mid = (first + last + 1) / 2;
+        if (p[mid] <= t)
+            first = mid;
+        else
+            last = mid - 1;
+    }
+    return first;
+}
+
+// Token t's slot and position, where it belongs to one of the sequences first .. last.
+__device__ __forceinline__ void fill_token(const PagesArgs& a, int t, int first, int last, int tokens) {
+    int slot = -1, where = -1;
+    if (t < tokens) {
+        const int s = last_at_most(a.q_starts, first, last, t);
+        where = a.kv_lens[s] - a.q_starts[s + 1] + t;
+        const int page = a.table[s * a.table_pitch + where / kPage];
+        if (page >= 0 && page < (1 << 25)) slot = page * kPage + where % kPage;
+    }
+    if (a.slots) a.slots[t] = slot;
+    if (a.positions) a.positions[t] = where;
+}
+
+// Exclusive sums of x and y over the threads of the workgroup, and the totals.
+template <class T>
+struct Scanned {
+    T x, y, all_x, all_y;
+};
+
+template <class T>
+__device__ __forceinline__ Scanned<T> scan(T x, T y, T (&tmp)[kScanThreads / 64][2], int waves) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    T sx = x, sy = y;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const T ux = __shfl_up(sx, d), uy = __shfl_up(sy, d);
+        if (lane >= d) sx += ux, sy += uy;
+    }
+    __syncthreads();
+    if (lane == 63) tmp[wave][0] = sx, tmp[wave][1] = sy;
+    __syncthreads();
+    Scanned<T> r{sx - x, sy - y, 0, 0};
+#pragma unroll 1
+    for (int w = 0; w < waves; ++w) {   // the ones that have anything
+        if (w < wave) r.x += tmp[w][0], r.y += tmp[w][1];
+        r.all_x += tmp[w][0], r.all_y += tmp[w][1];
+    }
+    return r;
+}
+
+// One workgroup takes the sequences 1024 at a time.  Whether a sequence is
+// granted depends on what those before it ask for, not on what they get, so
+// two sums over the sequences settle a block of them: of what is asked, then
+// of what is given.  Pages are given out from entries of the ring before
+// `count` and come back to entries from there on, so neither waits for the
+// other and their order is fixed.
+__global__ void __launch_bounds__(kScanThreads)
+kv_pages_kernel(PagesArgs a, int fill) {
+    __shared__ int64_t wide[kScanThreads / 64][2];
+    __shared__ int narrow[kScanThreads / 64][2];
+    __shared__ int give_from[kScanThreads];                                    // pages that go back before each sequence's
+    __shared__ int whose[kScanThreads], take_from[kScanThreads];               // those that take pages, and the pages before them
+    __shared__ int first_page[kScanThreads], need_page[kScanThreads];          // a sequence's pages held and needed
+    const int tid = threadIdx.x;
+    const int h0 = a.state[0] % a.capacity, head = h0 < 0 ? h0 + a.capacity : h0;
+    const int count = min(max(a.state[1], 0), a.capacity), room = a.capacity - count;
+    __syncthreads();                // state_out may be state
+    int64_t asked = 0, paged = 0;   // tokens and pages that the sequences before this block ask for
+    int given = 0, taken = 0, freed = 0;
+    for (int base = 0; base < a.seqs; base += kScanThreads) {
+        const int s = base + tid, waves = (min(a.seqs - base, kScanThreads) + 63) / 64;
+        const bool here = s < a.seqs;
+        int held = 0, keep = 0;
+        int64_t fresh = 0, want = 0, need = 0, extra = 0;
+        bool fits = false;
+        if (here) {
+            held = static_cast<int>(min(int64_t(max(a.held[s], 0)), a.table_pitch));
+            keep = min(max(a.keep[s], 0), held * kPage);
+            fresh = max(a.fresh[s], 0);
+            want = keep + fresh;
+            need = (want + kPage - 1) / kPage;
+            fits = need <= a.table_pitch;
+            extra = fits && need > held ? need - held : 0;
+        }
+        const Scanned<int64_t> ask = scan<int64_t>(fits ? fresh : 0, extra, wide, waves);
+        const bool granted = fits && (extra == 0 || paged + ask.y + extra <= count) &&
+                             (fresh == 0 || asked + ask.x + fresh <= a.total);
+        const int got = granted ? static_cast<int>(fresh) : 0;
+        const int after = granted ? static_cast<int>(need) : held;
+        const int take = max(after - held, 0), give = max(held - after, 0);
+        const Scanned<int> got_sum = scan<int>(got, give, narrow, waves);
+        if (here) {
+            a.held_out[s] = after;
+            a.kv_lens[s] = keep + got;
+            a.q_starts[s] = given + got_sum.x;
+        }
+        // pages one a thread, whichever sequence they are of
+        give_from[tid] = got_sum.y;
+        first_page[tid] = held;
+        need_page[tid] = after;
+        const int takes = __syncthreads_count(take > 0);
+        int block_taken = 0;
+        if (takes) {
+            // the ones that take, in order, at the front: their numbers ascend
+            const Scanned<int> at = scan<int>(take > 0, take, narrow, waves);
+            if (take > 0) {
+                whose[at.x] = tid;
+                take_from[at.x] = at.y;
+            }
+            block_taken = at.all_y;
+            __syncthreads();
+            for (int i = tid; i < block_taken; i += kScanThreads) {
+                const int w = last_at_most(take_from, 0, takes - 1, i), q = whose[w];
+                const int64_t from = int64_t(head) + taken + i;
+                a.table[(base + q) * a.table_pitch + first_page[q] + (i - take_from[w])] =
+                    a.pool[from >= a.capacity ? from - a.capacity : from];
+            }
+        }
+        for (int i = tid; i < got_sum.all_y; i += kScanThreads) {
+            if (freed + i >= room) break;
+            const int q = last_at_most(give_from, 0, kScanThreads - 1, i);
+            const int64_t to = int64_t(head) + count + freed + i;
+            a.pool[to >= a.capacity ? to - a.capacity : to] =
+                a.table[(base + q) * a.table_pitch + need_page[q] + (i - give_from[q])];
+        }
+        asked += ask.all_x, paged += ask.all_y;
+        given += got_sum.all_x, taken += block_taken, freed = min(freed + got_sum.all_y, room);
+        __syncthreads();
+    }
+    if (tid == 0) {
+        const int64_t h = int64_t(head) + taken;
+        a.state_out[0] = static_cast<int>(h >= a.capacity ? h - a.capacity : h);
+        a.state_out[1] = count - taken + freed;
+        a.q_starts[a.seqs] = given;
+    }
+    if (!fill) return;
+    __syncthreads();
+    for (int t = tid; t < a.total; t += kScanThreads) fill_token(a, t, 0, max(a.seqs - 1, 0), given);
+}
+
+// Slots and positions of many tokens, once the tables are made.
+__global__ void __launch_bounds__(kFillThreads)
+kv_slots_kernel(PagesArgs a) {
+    const int t0 = blockIdx.x * (kFillThreads * kFillEach), end = min(t0 + kFillThreads * kFillEach, a.total);
+    const int tokens = a.q_starts[a.seqs];
+    int first = 0, last = 0;
+    if (t0 < tokens && a.seqs > 0) {   // the sequences that the workgroup's tokens are of
+        first = last_at_most(a.q_starts, 0, a.seqs - 1, t0);
+        last = last_at_most(a.q_starts, first, a.seqs - 1, end - 1);
+    }
+#pragma unroll
+    for (int i = 0; i < kFillEach; ++i) {
+        const int t = t0 + i * kFillThreads + threadIdx.x;
+        if (t < end) fill_token(a, t, first, last, tokens);
+    }
+}
+
+// ---- trees
+
+struct TreeArgs {
+    const int32_t *kv_lens, *q_starts;
+    int total, max_q;
+};
+
+// A sequence's first row, its nodes and the slots before them.
+struct Tree {
+    int row0, nodes, len;
+
+    __device__ __forceinline__ Tree(const TreeArgs& a, int s) {
+        row0 = min(max(a.q_starts[s], 0), a.total);
+        nodes = min(max(min(max(a.q_starts[s + 1], 0), a.total) - row0, 0), a.max_q);
+        len = max(a.kv_lens[s], 0);
+    }
+};
+
+// A node's mask is its parent's with its own bit, so a node's way to the root
+// doubles with every step: eight steps for 256 nodes.  A workgroup is a tree.
+__global__ void __launch_bounds__(kTreeMax)
+kv_tree_kernel(TreeArgs a, const int32_t* parents, uint64_t* masks, int32_t* positions, int words) {
+    __shared__ uint64_t seen[kTreeMax][NVFP4_TREE_WORDS];
+    __shared__ int up[kTreeMax];
+    const Tree t(a, blockIdx.x);
+    const int i = threadIdx.x;
+    uint64_t m[NVFP4_TREE_WORDS] = {};
+    int next = i;
+    if (i < t.nodes) {
+        const int p = parents[t.row0 + i];
+        if (p >= 0 && p < i) next = p;
+#pragma unroll
+        for (int w = 0; w < NVFP4_TREE_WORDS; ++w) {
+            m[w] = i >> 6 == w ? 1ull << (i & 63) : 0;
+            seen[i][w] = m[w];
+        }
+        up[i] = next;
+    }
+    for (int reach = 1; reach < a.max_q; reach *= 2) {
+        __syncthreads();
+        uint64_t more[NVFP4_TREE_WORDS] = {};
+        int far = next;
+        if (i < t.nodes) {
+#pragma unroll
+            for (int w = 0; w < NVFP4_TREE_WORDS; ++w) more[w] = seen[next][w];
+            far = up[next];
+        }
+        __syncthreads();
+        if (i < t.nodes) {
+            next = far;
+            up[i] = far;
+#pragma unroll
+            for (int w = 0; w < NVFP4_TREE_WORDS; ++w) seen[i][w] = m[w] |= more[w];
+        }
+    }
+    if (i >= t.nodes) return;
+    int depth = -1;
+#pragma unroll
+    for (int w = 0; w < NVFP4_TREE_WORDS; ++w) {
+        depth += __popcll(m[w]);
+        if (w < words) masks[int64_t(t.row0 + i) * words + w] = m[w];
+    }
+    positions[t.row0 + i] = t.len - t.nodes + depth;
+}
+
+// Each node's continuation that the model agrees with, the lowest first (a
+// minimum: no order matters), then one thread walks from the root.
+__global__ void __launch_bounds__(kTreeMax)
+tree_accept_kernel(TreeArgs a, const int32_t* drafted, const int32_t* parents, const int32_t* chosen, int32_t* path,
+                   int32_t* counts, int32_t* token, int32_t* new_lens) {
+    __shared__ int next[kTreeMax], way[kTreeMax];
+    __shared__ int steps;
+    const int s = blockIdx.x, i = threadIdx.x;
+    const Tree t(a, s);
+    if (i < kTreeMax) next[i] = kTreeMax;
+    __syncthreads();
+    if (i < t.nodes) {
+        const int p = parents[t.row0 + i], mine = drafted[t.row0 + i];
+        if (p >= 0 && p < i && mine >= 0 && chosen[t.row0 + p] == mine) atomicMin(&next[p], i);
+    }
+    __syncthreads();
+    if (i == 0) {
+        int n = 0;
+        for (int at = 0; at < t.nodes; at = next[at]) way[n++] = at;
+        steps = n;
+        counts[s] = n;
+        token[s] = n ? chosen[t.row0 + way[n - 1]] : -1;
+        new_lens[s] = max(t.len - t.nodes + n, 0);
+    }
+    __syncthreads();
+    if (i < a.max_q) path[int64_t(s) * a.max_q + i] = i < steps ? way[i] : -1;
+}
+
+int status() { return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP; }
+
+unsigned tree_threads(int64_t max_q) { return static_cast<unsigned>((max_q + 63) / 64 * 64); }
+
+}  // namespace
+
+extern "C" int nvfp4_kv_pages(const nvfp4_kv_pages_t* p, int32_t* state_out, int32_t* held_out, int32_t* kv_lens,
+                              int32_t* q_starts, int32_t* slots, int32_t* positions, void* stream) {
+    int st;
+    if ((st = nvfp4::check_kv_pages(p, state_out, held_out, kv_lens, q_starts, slots, positions)) != NVFP4_OK) return st;
+    if ((st = nvfp4::device_setup()) != NVFP4_OK) return st;
+    const PagesArgs a{p->pool, p->state, p->table, p->held, p->keep, p->fresh, state_out, held_out, kv_lens, q_starts,
+                      slots, positions, p->table_pitch, static_cast<int>(p->capacity), static_cast<int>(p->seqs), static_cast<int>(p->total)};
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const bool wanted = p->total > 0 && (slots || positions), inside = p->total <= kFillInline;
+    hipLaunchKernelGGL(kv_pages_kernel, dim3(1), dim3(kScanThreads), 0, s, a, wanted && inside ? 1 : 0);
+    if ((st = status()) != NVFP4_OK || !wanted || inside) return st;
+    const int64_t each = kFillThreads * kFillEach;
+    hipLaunchKernelGGL(kv_slots_kernel, dim3(static_cast<unsigned>((p->total + each - 1) / each)), dim3(kFillThreads), 0, s, a);
+    return status();
+}
+
+extern "C" int nvfp4_kv_tree(const int32_t* parents, const int32_t* kv_lens, const int32_t* q_starts, int64_t seqs,
+                             int64_t total, int64_t max_q, uint64_t* masks, int32_t* positions, void* stream) {
+    int st;
+    if ((st = nvfp4::check_trees(kv_lens, q_starts, seqs, total, max_q)) != NVFP4_OK) return st;
+    if (seqs == 0 || total == 0) return NVFP4_OK;
+    if ((st = nvfp4::check_words(parents)) != NVFP4_OK || (st = nvfp4::check_words(positions)) != NVFP4_OK) return st;
+    if ((st = nvfp4::check_words(masks)) != NVFP4_OK) return st;
+    if (reinterpret_cast<uintptr_t>(masks) & 7) return NVFP4_ERR_ALIGN;
+    if ((st = nvfp4::device_setup()) != NVFP4_OK) return st;
+    const TreeArgs a{kv_lens, q_starts, static_cast<int>(total), static_cast<int>(max_q)};
+    hipLaunchKernelGGL(kv_tree_kernel, dim3(static_cast<unsigned>(seqs)), dim3(tree_threads(max_q)), 0,
+                       static_cast<hipStream_t>(stream), a, parents, masks, positions, static_cast<int>((max_q + 63) / 64));
+    return status();
+}
+
+extern "C" int nvfp4_tree_accept(const int32_t* drafted, const int32_t* parents, const int32_t* chosen,
+                                 const int32_t* kv_lens, const int32_t* q_starts, int64_t seqs, int64_t total,
+                                 int64_t max_q, int32_t* path, int32_t* counts, int32_t* token, int32_t* new_lens,
+                                 void* stream) {
+    int st;
+    if ((st = nvfp4::check_trees(kv_lens, q_starts, seqs, total, max_q)) != NVFP4_OK) return st;
+    if (seqs == 0) return NVFP4_OK;
+    for (const void* p : {static_cast<const void*>(path), static_cast<const void*>(counts), static_cast<const void*>(token),
+                          static_cast<const void*>(new_lens)})
+        if ((st = nvfp4::check_words(p)) != NVFP4_OK) return st;
+    if (total > 0)
+        for (const int32_t* p : {drafted, parents, chosen})
+            if ((st = nvfp4::check_words(p)) != NVFP4_OK) return st;
+    if ((st = nvfp4::device_setup()) != NVFP4_OK) return st;
+    const TreeArgs a{kv_lens, q_starts, static_cast<int>(total), static_cast<int>(max_q)};
+    hipLaunchKernelGGL(tree_accept_kernel, dim3(static_cast<unsigned>(seqs)), dim3(tree_threads(max_q)), 0,
+                       static_cast<hipStream_t>(stream), a, drafted, parents, chosen, path, counts, token, new_lens);
+    return status();
+}

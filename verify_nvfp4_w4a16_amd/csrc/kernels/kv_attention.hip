@@ -15,6 +15,7 @@
 
 #include <cstdint>
 
+#include "../host/draft_shapes.h"
 #include "../host/kv_index.h"
 #include "../host/kv_plan.h"
 #include "../host/kv_shapes.h"
@@ -68,12 +69,14 @@ __device__ __forceinline__ int used_splits(const AttendArgs& a, const Span& s) {
 // registers and LDS while it reads a length: 32 one-token steps over 3 ..
 // 131071 slots took 178 us with 14000 such, 124 us planned, of which the plan
 // takes 5 us.)
-__device__ __forceinline__ int segment_pages(const AttendArgs& a, const QueryRows& rows) {
+template <class Rows>
+__device__ __forceinline__ int segment_pages(const AttendArgs& a, const Rows& rows) {
     const Span span = rows.span(a.sc, 0, rows.count - 1);
     return max(pages_hi(span) - pages_lo(span), 1);
 }
 
-__device__ __forceinline__ int segment_count(const AttendArgs& a, const QueryRows& rows) {
+template <class Rows>
+__device__ __forceinline__ int segment_count(const AttendArgs& a, const Rows& rows) {
     return (rows.count + kRowTile - 1) / kRowTile * a.v.kv_heads;
 }
 
@@ -240,7 +243,7 @@ constexpr int kSumRow = D + 4;
 // kept), a short one by the chain of dependent reads and one page's work (777
 // slots: 10 us; at D = 256 that work and 16 rows of sums in 246 registers leave
 // two wavefronts a SIMD: 16 verify rounds of 5 tokens in a window of 1500 take 24 us for 40 MB).
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(64 * kWaves, 2)
 kv_attend_rows_kernel(AttendArgs a) {
     extern __shared__ float lds[];   // [kWaves][16][kSumRow<D>] sums, then [kWaves][16][2] statistics
@@ -250,7 +253,7 @@ kv_attend_rows_kernel(AttendArgs a) {
     const Item item = find_item(a, blockIdx.x);
     if (item.s < 0) return;
     const int s = item.s, hk = item.segment % a.v.kv_heads, row0 = item.segment / a.v.kv_heads * kRowTile;
-    const QueryRows rows(a.v, a.sc, s);
+    const QueryRowsOf<TREE> rows(a.v, a.sc, s);
     if (row0 >= rows.count) return;
     const int pages = segment_pages(a, rows);
     if (item.part > 0 && item.part * item.chunk >= pages) return;
@@ -304,10 +307,19 @@ kv_attend_rows_kernel(AttendArgs a) {
         for (int i = 0; i < 16; ++i) p[i] = z[i >> 2][i & 3];
         a.sc.shape(p, to_log2);
         if (!here || base < span.lo_all || base + kPage > span.hi_all) {
+            if constexpr (TREE) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int slot = base + 32 * (i >> 3) + 8 * b + (i & 7);
-                p[i] = here && slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t seen = here ? rows.seen8(a.sc, me, base + 32 * h + 8 * b) : 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) p[8 * h + i] = seen >> i & 1 ? p[8 * h + i] : -INFINITY;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int slot = base + 32 * (i >> 3) + 8 * b + (i & 7);
+                    p[i] = here && slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
+                }
             }
         }
         float top = p[0];
@@ -514,7 +526,7 @@ __device__ __forceinline__ void reads_ahead() {
 
 
 // HALVES 2: wavefronts 0 and 1 have the first 32 slots of each page, 2 and 3 the last.
-template <int D, int HALVES>
+template <int D, int HALVES, bool TREE>
 __global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
 kv_attend_tile_kernel(AttendArgs a) {
     extern __shared__ char tiles[];   // two pages
@@ -525,7 +537,7 @@ kv_attend_tile_kernel(AttendArgs a) {
     const int n = lane & 31, b = lane >> 5;
     const int s = blockIdx.y, split = blockIdx.z;
     const int hk = blockIdx.x % a.v.kv_heads;
-    const QueryRows rows(a.v, a.sc, s);
+    const QueryRowsOf<TREE> rows(a.v, a.sc, s);
     // the last rows see most: they begin first
     const int tile = int(gridDim.x / a.v.kv_heads) - 1 - int(blockIdx.x / a.v.kv_heads);
     const int row0 = tile * kRows;
@@ -596,10 +608,19 @@ kv_attend_tile_kernel(AttendArgs a) {
             for (int i = 0; i < 16 * kStep; ++i) p[i] = z[i >> 4][i & 15];
             if (a.sc.cap != 0.0f) a.sc.shape(p, to_log2);
             if (base < span.lo_all || base + kPage > span.hi_all) {
+                if constexpr (TREE) {
 #pragma unroll
-                for (int i = 0; i < 16 * kStep; ++i) {
-                    const int slot = base + 32 * half + 16 * (i >> 3) + 8 * b + (i & 7);
-                    p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
+                    for (int t = 0; t < 2 * kStep; ++t) {
+                        const uint32_t seen = rows.seen8(a.sc, me, base + 32 * half + 16 * t + 8 * b);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) p[8 * t + i] = seen >> i & 1 ? p[8 * t + i] : -INFINITY;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16 * kStep; ++i) {
+                        const int slot = base + 32 * half + 16 * (i >> 3) + 8 * b + (i & 7);
+                        p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
+                    }
                 }
             }
             float top = p[0];
@@ -710,7 +731,7 @@ kv_attend_tile_kernel(AttendArgs a) {
 // Joins the parts of one row, one workgroup a row: the wavefronts take every
 // fourth part and meet in LDS, both in a fixed order.  Bound by latency (1024
 // rows of up to 37 parts: 6.8 us).
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(64 * kWaves)
 kv_join_kernel(AttendArgs a) {
     __shared__ float sums[kWaves][D];
@@ -721,7 +742,7 @@ kv_join_kernel(AttendArgs a) {
     const int token = static_cast<int>(at / a.sc.heads), head = static_cast<int>(at % a.sc.heads);
     const int s = last_sequence(a.v, [&](int i) { return a.v.start(i) <= token; });
     if (s < 0) return;
-    const QueryRows rows(a.v, a.sc, s);
+    const QueryRowsOf<TREE> rows(a.v, a.sc, s);
     const int r = nvfp4::kv_row_of(token, rows.first_token, rows.group, head % rows.group, rows.count);
     if (r < 0) return;   // no sequence's row
     // where part p of the row lies: the parts of a tile a slice apart, an item's by its number
@@ -799,32 +820,35 @@ template <int D>
 bool allow_lds() {
     static_assert(tile_lds<D>() >= 2 * 64 * (D / 2 + 2) * sizeof(float));
     static_assert(tile_lds<D>() >= kTileRows * (D * 2 + 16) && tile_lds<D>() <= kMaxLdsBytes);
-    for (const void* fn : {reinterpret_cast<const void*>(kv_attend_rows_kernel<D>),
-                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 1>),
-                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 2>)})
+    for (const void* fn : {reinterpret_cast<const void*>(kv_attend_rows_kernel<D, false>),
+                           reinterpret_cast<const void*>(kv_attend_rows_kernel<D, true>),
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 1, false>),
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 1, true>),
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 2, false>),
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 2, true>)})
         if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLdsBytes) != hipSuccess) return false;
     return true;
 }
 
-template <int D>
+template <int D, bool TREE>
 int launch_attend(const AttendArgs& a, const nvfp4::KvPlan& plan, hipStream_t st) {
     if (plan.tile) {
         // parts of a tile's pages along the slowest axis: those that short sequences do not need come last
         const int64_t blocks = plan.row_tiles * a.v.kv_heads;
         if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-        hipLaunchKernelGGL((plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1> : kv_attend_tile_kernel<D, 2>),
+        hipLaunchKernelGGL((plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1, TREE> : kv_attend_tile_kernel<D, 2, TREE>),
                            dim3(static_cast<unsigned>(blocks), a.v.seqs, plan.splits), dim3(64 * kWaves), tile_lds<D>(), st, a);
     } else {
         if (plan.planned) {
             hipLaunchKernelGGL(kv_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
             if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
         }
-        hipLaunchKernelGGL(kv_attend_rows_kernel<D>, dim3(plan.items), dim3(64 * kWaves), rows_lds<D>(), st, a);
+        hipLaunchKernelGGL((kv_attend_rows_kernel<D, TREE>), dim3(plan.items), dim3(64 * kWaves), rows_lds<D>(), st, a);
     }
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     if (plan.part_rows > 0) {
         const int64_t slice = int64_t(a.v.total) * a.sc.heads;
-        hipLaunchKernelGGL(kv_join_kernel<D>, dim3(static_cast<unsigned>(slice)), dim3(64 * kWaves), 0, st, a);
+        hipLaunchKernelGGL((kv_join_kernel<D, TREE>), dim3(static_cast<unsigned>(slice)), dim3(64 * kWaves), 0, st, a);
         if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     }
     return NVFP4_OK;
@@ -838,24 +862,21 @@ int kv_setup() { return allow_lds<64>() && allow_lds<128>() && allow_lds<256>() 
 
 }  // namespace nvfp4
 
-extern "C" int nvfp4_kv_attention_workspace(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,
-                                            const nvfp4_kv_queries_t* queries, int64_t* bytes) {
+namespace {
+
+int check_call(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, const nvfp4_kv_queries_t* queries) {
     int st;
-    if (!bytes) return NVFP4_ERR_NULL;
     if ((st = nvfp4::check_kv_cache(cache)) != NVFP4_OK) return st;
     if ((st = nvfp4::check_kv_seqs(seqs, true)) != NVFP4_OK) return st;
-    if ((st = nvfp4::check_kv_queries(cache, seqs, queries)) != NVFP4_OK) return st;
-    *bytes = nvfp4::kv_workspace_bytes(cache, seqs, queries);
-    return NVFP4_OK;
+    return nvfp4::check_kv_queries(cache, seqs, queries);
 }
 
-extern "C" int nvfp4_kv_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,
-                                  const nvfp4_kv_queries_t* queries, void* out, float* lse, void* workspace,
-                                  int64_t workspace_bytes, void* stream) {
+// tree: NULL where rows see by their order.
+int attend(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, const nvfp4_kv_queries_t* queries,
+           const nvfp4_kv_tree_t* tree, void* out, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
     int st;
-    if ((st = nvfp4::check_kv_cache(cache)) != NVFP4_OK) return st;
-    if ((st = nvfp4::check_kv_seqs(seqs, true)) != NVFP4_OK) return st;
-    if ((st = nvfp4::check_kv_queries(cache, seqs, queries)) != NVFP4_OK) return st;
+    if ((st = check_call(cache, seqs, queries)) != NVFP4_OK) return st;
+    if (tree && (st = nvfp4::check_kv_tree(seqs, queries, tree)) != NVFP4_OK) return st;
     if ((st = nvfp4::check_kv_rows(out, 0, 0, seqs->total)) != NVFP4_OK) return st;
     if ((reinterpret_cast<uintptr_t>(lse) & 3) || (reinterpret_cast<uintptr_t>(workspace) & 15)) return NVFP4_ERR_ALIGN;
     if (seqs->seqs == 0 || seqs->total == 0 || queries->max_q == 0) return NVFP4_OK;
@@ -879,9 +900,46 @@ extern "C" int nvfp4_kv_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_
     a.part_ml = plan.part_rows > 0 ? a.part_o + plan.part_rows * cache->head_dim : nullptr;
     a.v_scale = cache->v_scale;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    switch (cache->head_dim) {
-        case 64: return launch_attend<64>(a, plan, s);
-        case 128: return launch_attend<128>(a, plan, s);
-        default: return launch_attend<256>(a, plan, s);
+    if (tree) {
+        a.sc.causal = 1;   // what a tree's rows see together, and so its pages, are a chain's
+        a.sc.tree = KvTree{reinterpret_cast<const uint32_t*>(tree->masks), tree->positions, static_cast<int>(2 * tree->words)};
+        switch (cache->head_dim) {
+            case 64: return launch_attend<64, true>(a, plan, s);
+            case 128: return launch_attend<128, true>(a, plan, s);
+            default: return launch_attend<256, true>(a, plan, s);
+        }
     }
+    switch (cache->head_dim) {
+        case 64: return launch_attend<64, false>(a, plan, s);
+        case 128: return launch_attend<128, false>(a, plan, s);
+        default: return launch_attend<256, false>(a, plan, s);
+    }
+}
+
+}  // namespace
+
+extern "C" int nvfp4_kv_attention_workspace(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,
+                                            const nvfp4_kv_queries_t* queries, int64_t* bytes) {
+    if (!bytes) return NVFP4_ERR_NULL;
+    const int st = check_call(cache, seqs, queries);
+    if (st != NVFP4_OK) return st;
+    *bytes = nvfp4::kv_workspace_bytes(cache, seqs, queries);
+    return NVFP4_OK;
+}
+
+extern "C" int nvfp4_kv_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, const nvfp4_kv_queries_t* queries,
+                                  void* out, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+    return attend(cache, seqs, queries, nullptr, out, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" int nvfp4_kv_tree_attention_workspace(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,
+                                                 const nvfp4_kv_queries_t* queries, int64_t* bytes) {
+    return nvfp4_kv_attention_workspace(cache, seqs, queries, bytes);
+}
+
+extern "C" int nvfp4_kv_tree_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,
+                                       const nvfp4_kv_queries_t* queries, const nvfp4_kv_tree_t* tree, void* out, float* lse,
+                                       void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!tree) return NVFP4_ERR_NULL;
+    return attend(cache, seqs, queries, tree, out, lse, workspace, workspace_bytes, stream);
 }

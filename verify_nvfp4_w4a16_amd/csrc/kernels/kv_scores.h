@@ -14,6 +14,22 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// What the nodes of drafted trees see of their sequence's new slots.
+struct KvTree {
+    const uint32_t* masks;      // [total][words] (a 64-bit word's low half first), NULL: rows see by their order
+    const int32_t* positions;   // [total], where there is a window
+    int words;
+
+    // Bits `at` .. `at` + 31 of a node's mask, zeros outside it.
+    __device__ __forceinline__ uint32_t bits(int token, int at) const {
+        const uint32_t* m = masks + int64_t(token) * words;
+        const int w = at >> 5;
+        const uint32_t lo = uint32_t(w) < uint32_t(words) ? m[w] : 0;
+        const uint32_t hi = uint32_t(w + 1) < uint32_t(words) ? m[w + 1] : 0;
+        return static_cast<uint32_t>((uint64_t(hi) << 32 | lo) >> (at & 31));
+    }
+};
+
 struct KvScores {
     const uint16_t* q;
     int64_t q_pitch, q_head_pitch;
@@ -25,6 +41,7 @@ struct KvScores {
     float scale;           // of q . (e4m3 * e2m1): the caller's times K's tensor scale is scale * 2^(exponent + 14),
     int exponent;          // apart because the product may be too small for fp32 where scores are not
     float cap, cap_inv;    // softcap (0: none) and its inverse
+    KvTree tree;
 
     // r / group for r in [0, 2^31): the product with the inverse is at most one short (a division takes 30 operations).
     __device__ __forceinline__ int over_group(int r) const {
@@ -72,6 +89,7 @@ inline KvScores kv_scores(const nvfp4_kv_cache_t* c, const nvfp4_kv_queries_t* q
     s.exponent -= 14;   // of the row's own power of two (convert_query)
     s.cap = std::min(q->softcap, 0x1p126f);   // more changes no score below 2^100, and its product with log2(e) is in range
     s.cap_inv = s.cap > 0.0f ? std::min(1.0f / s.cap, FLT_MAX) : 0.0f;
+    s.tree = KvTree{};
     return s;
 }
 
@@ -86,13 +104,16 @@ struct QueryRow {
 };
 
 // The rows of one sequence and kv head: row r is new token r / group, query
-// head r % group of the group.
-struct QueryRows {
+// head r % group of the group.  TREE: the rows are nodes, which see the slots
+// before the tree, from the window's edge at their position on, and the new
+// ones that their masks name.
+template <bool TREE>
+struct QueryRowsOf {
     int first_token, new_tokens, len, count, group;
 
-    __device__ __forceinline__ QueryRows(int first, int count_new, int length, int of_kv_head)
+    __device__ __forceinline__ QueryRowsOf(int first, int count_new, int length, int of_kv_head)
         : first_token(first), new_tokens(count_new), len(length), count(count_new * of_kv_head), group(of_kv_head) {}
-    __device__ __forceinline__ QueryRows(const KvView& v, const KvScores& sc, int s) {
+    __device__ __forceinline__ QueryRowsOf(const KvView& v, const KvScores& sc, int s) {
         first_token = v.start(s);
         new_tokens = min(max(v.start(s + 1) - first_token, 0), sc.max_q);
         len = min(v.len(s), sc.max_kv);
@@ -105,8 +126,12 @@ struct QueryRows {
     __device__ __forceinline__ int see_hi(const KvScores& sc, int i) const {
         return sc.causal ? max(min(len, len - new_tokens + i + 1), 0) : len;
     }
+    // Slots before the tree (a negative number where there are more nodes than slots).
+    __device__ __forceinline__ int before() const { return len - new_tokens; }
     // For rows first .. last (both below count).
     __device__ __forceinline__ Span span(const KvScores& sc, int first, int last) const {
+        // a node's position may be any of the tree's, whatever its place in the order
+        if constexpr (TREE) return Span{see_lo(sc, 0), len, see_lo(sc, new_tokens - 1), max(before(), 0)};
         const int i0 = sc.over_group(first), i1 = sc.over_group(last);
         return Span{see_lo(sc, i0), see_hi(sc, i1), see_lo(sc, i1), see_hi(sc, i0)};
     }
@@ -114,6 +139,12 @@ struct QueryRows {
     __device__ __forceinline__ QueryRow row(const KvScores& sc, int r) const {
         r = min(r, count - 1);
         const int i = sc.over_group(r);
+        if constexpr (TREE) {
+            const int token = first_token + i;
+            // (held to the tree first: a difference of positions of any size would leave 32 bits)
+            const int depth = sc.window > 0 ? min(max(sc.tree.positions[token], before()), len - 1) - before() : 0;
+            return QueryRow{token, r - i * group, min(see_lo(sc, depth), max(before(), 0)), len};
+        }
         return QueryRow{first_token + i, r - i * group, see_lo(sc, i), see_hi(sc, i)};
     }
     // Index of a row in [total][heads].
@@ -123,7 +154,17 @@ struct QueryRows {
     static __device__ __forceinline__ int64_t place(const KvScores& sc, const QueryRow& r, int hk) {
         return int64_t(r.token) * sc.heads + hk * sc.group + r.g;
     }
+    // Whether a row sees slots slot0 .. slot0 + 7 (bit j: slot0 + j).
+    __device__ __forceinline__ uint32_t seen8(const KvScores& sc, const QueryRow& r, int slot0) const {
+        const int first = slot0 - before();   // place of slot0 among the nodes
+        uint32_t m = first > -8 ? sc.tree.bits(r.token, first) : 0;
+        if (first < 0) m |= first > -8 ? (1u << -first) - 1 : 0xffu;                                   // slots before the tree
+        if (slot0 < r.lo && first < 0) m &= r.lo - slot0 < 8 ? ~0u << (r.lo - slot0) : 0u;             // beyond the window
+        return len - slot0 >= 8 ? m : len > slot0 ? m & ((1u << (len - slot0)) - 1) : 0u;
+    }
 };
+
+using QueryRows = QueryRowsOf<false>;
 
 // A query row as f16 operands: N pieces of 8 dims, piece i at p + i * STEP.
 // bf16 reaches further than f16, so the row is scaled by the power of two that
