@@ -35,16 +35,27 @@ def _of_trees(g, lens, new, near=6):
     return masks, positions
 
 
-def _attend(c, qbits, new, masks, positions, words=None, strided=False, max_q=None, max_kv=None, **kw):
+def _wide(c):
+    """The cache's tables with rows so long that, by its bounds, a call is one for the tiles of many rows; what is added is no page."""
+    pitch = 1 << 14
+    table = torch.full((len(c.lens), pitch), -1, dtype=torch.int32, device=DEV)
+    table[:, :c.table_t.shape[1]] = c.table_t
+    return table, pitch * 64
+
+
+def _attend(c, qbits, new, masks, positions, words=None, strided=False, max_q=None, max_kv=None, wide=False, **kw):
     q = bf16(qbits)
     if strided:                                              # a view of a fused projection's output
         total, heads, d = q.shape
-        wide = torch.full((total, heads * d + 2 * c.heads * d), float("nan"), dtype=torch.bfloat16, device=DEV)
-        wide[:, :heads * d] = q.reshape(total, heads * d)
-        q = wide[:, :heads * d].view(total, heads, d)
+        fused = torch.full((total, heads * d + 2 * c.heads * d), float("nan"), dtype=torch.bfloat16, device=DEV)
+        fused[:, :heads * d] = q.reshape(total, heads * d)
+        q = fused[:, :heads * d].view(total, heads, d)
     max_q = max_q or max(max(new), 1)
     words = words or -(-max_q // 64)
-    out, lse = nv.kv_tree_attention(q, c.cache, c.table_t, c.lens_t, starts(new), _masks(masks, words),
+    table = c.table_t
+    if wide:
+        table, max_kv = _wide(c)
+    out, lse = nv.kv_tree_attention(q, c.cache, table, c.lens_t, starts(new), _masks(masks, words),
                                     None if positions is None else int32(positions), max_q,
                                     max_kv if max_kv is not None else max(max(c.lens), 1), **kw)
     torch.cuda.synchronize()
@@ -103,21 +114,23 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lens,new,heads,group,d,kw", CASES)
-def test_tree_attention(lens, new, heads, group, d, kw):
+def test_tree_attention(lens, new, heads, group, d, kw, wide):
     g = workload.rng(sum(lens) + d)
     c = Paged(lens, heads, d, 400 + sum(lens))
     masks, positions = _of_trees(g, lens, new)
     qb = _query_bits(sum(new), heads * group, d, 27 + d)
-    out, lse = _attend(c, qb, new, masks, positions, strided=len(lens) % 2 == 0, **kw)
+    out, lse = _attend(c, qb, new, masks, positions, strided=len(lens) % 2 == 0, wide=wide, **kw)
     _check(c, qb, new, masks, positions, out, lse, **kw)
-    again = _attend(c, qb, new, masks, positions, **kw)
+    again = _attend(c, qb, new, masks, positions, wide=wide, **kw)
     assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
 
 
 @pytest.mark.parametrize("new,group,d", [([12, 40], 2, 128), ([64, 33], 1, 64), ([130, 256], 1, 64), ([20, 9], 2, 256)])
 @pytest.mark.parametrize("window", [0, 50])
-def test_masks_that_are_no_trees(new, group, d, window):
+@pytest.mark.parametrize("wide", [False, True])
+def test_masks_that_are_no_trees(new, group, d, window, wide):
     # any bits: none at all, later nodes, bits beyond the last node, positions outside the tree
     lens = [300, 256]
     g = workload.rng(sum(new) + d)
@@ -129,29 +142,31 @@ def test_masks_that_are_no_trees(new, group, d, window):
     positions = g.integers(-100, 500, rows).tolist()
     positions[1], positions[2] = 2 ** 31 - 1, -(2 ** 31)
     qb = _query_bits(rows, group, d, 5)
-    out, lse = _attend(c, qb, new, masks, positions, words=4, window=window)
+    out, lse = _attend(c, qb, new, masks, positions, words=4, window=window, wide=wide and window == 0)
     _check(c, qb, new, masks, positions, out, lse, window=window)
 
 
-def test_a_row_that_sees_nothing():
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_row_that_sees_nothing(wide):
     # nothing before the tree, and no bits
     for new in ([4], [20], [100]):
         c = Paged(new, 1, 64, 12)
         masks = [0 if i % 3 else 1 << i for i in range(new[0])]
         qb = _query_bits(new[0], 2, 64, 13)
-        out, lse = _attend(c, qb, new, masks, None)
+        out, lse = _attend(c, qb, new, masks, None, wide=wide)
         _check(c, qb, new, masks, None, out, lse)
         assert np.isneginf(lse[1]).all() and not out[1].any()
 
 
-def test_a_chain_sees_what_causal_attention_sees():
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_chain_sees_what_causal_attention_sees(wide):
     for new in ([1, 3], [9, 16], [100, 30]):
         lens = [700, 130]
         c = Paged(lens, 2, 128, 14)
         masks = [(2 << i) - 1 for n in new for i in range(n)]
         positions = [n - nq + i for n, nq in zip(lens, new) for i in range(nq)]
         qb = _query_bits(sum(new), 8, 128, 15)
-        out, lse = _attend(c, qb, new, masks, positions)
+        out, lse = _attend(c, qb, new, masks, positions, wide=wide)
         _check(c, qb, new, masks, positions, out, lse)
         from tests.test_gpu_kv import _check as check_causal
         check_causal(c, qb, new, out, lse)
@@ -168,7 +183,8 @@ def test_bounds_that_exceed_the_trees():
         _check(c, qb, new, masks, positions, out, lse)
 
 
-def test_trees_beyond_the_bound_are_taken_for_their_first_nodes():
+@pytest.mark.parametrize("wide", [False, True])
+def test_trees_beyond_the_bound_are_taken_for_their_first_nodes(wide):
     lens, new, most = [200, 90], [30, 10], 12
     g = workload.rng(7)
     c = Paged(lens, 1, 64, 8)
@@ -177,11 +193,12 @@ def test_trees_beyond_the_bound_are_taken_for_their_first_nodes():
     all_masks, all_positions = [0] * 40, [0] * 40
     for i, m, p in zip(at, masks, positions):
         all_masks[i], all_positions[i] = m, p
-    qb = _query_bits(40, 2, 64, 9)
-    out = Guarded((40, 2, 64), torch.bfloat16)
+    qb = _query_bits(40, 4, 64, 9)
+    out = Guarded((40, 4, 64), torch.bfloat16)
     untouched = out.t.clone()
-    lse = torch.full((40, 2), 7.0, device=DEV)
-    nv.kv_tree_attention(bf16(qb), c.cache, c.table_t, c.lens_t, starts(new), _masks(all_masks, 1), int32(all_positions), most, 200,
+    lse = torch.full((40, 4), 7.0, device=DEV)
+    table, max_kv = _wide(c) if wide else (c.table_t, 200)
+    nv.kv_tree_attention(bf16(qb), c.cache, table, c.lens_t, starts(new), _masks(all_masks, 1), int32(all_positions), most, max_kv,
                          out=out.t, lse=lse)
     torch.cuda.synchronize()
     got = out.check().float().cpu().numpy().astype(np.float64)[at]
@@ -189,24 +206,26 @@ def test_trees_beyond_the_bound_are_taken_for_their_first_nodes():
     assert torch.equal(out.t[most:30].view(torch.int16), untouched[most:30].view(torch.int16)) and bool((lse[most:30] == 7.0).all())
 
 
-def test_nan_and_infinite_queries_stay_in_their_rows():
-    for new in ([5], [40], [120]):
+@pytest.mark.parametrize("wide", [False, True])
+def test_nan_and_infinite_queries_stay_in_their_rows(wide):
+    for new in ([5], [20], [40], [120]):
         c = Paged([250], 1, 64, 8)
         g = workload.rng(9)
         masks, positions = _of_trees(g, [250], new)
         qb = _query_bits(new[0], 3, 64, 9)
-        clean = _attend(c, qb, new, masks, positions)
+        clean = _attend(c, qb, new, masks, positions, wide=wide)
         bad = qb.copy()
         bad[1, 1, 3], bad[3, 2, 0] = 0x7FC0, 0x7F80
-        out, lse = _attend(c, bad, new, masks, positions)
+        out, lse = _attend(c, bad, new, masks, positions, wide=wide)
         hit = np.zeros((new[0], 3), bool)
         hit[1, 1] = hit[3, 2] = True
         assert np.isnan(out[hit]).all() and np.isnan(lse[hit]).all()
         assert np.array_equal(out[~hit], clean[0][~hit]) and np.array_equal(lse[~hit], clean[1][~hit])
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("new", [[9, 8], [30, 16], [90, 64]])
-def test_pages_outside_the_cache(new):
+def test_pages_outside_the_cache(new, wide):
     # a page number that the cache does not have stands for slots that nothing sees, in and before the tree
     lens = [330, 200]
     c = Paged(lens, 1, 64, 12)
@@ -216,7 +235,7 @@ def test_pages_outside_the_cache(new):
     table = c.table.copy()
     table[0, 1], table[1, 2] = 10 ** 6, -7
     c.table_t = int32(table)
-    out, lse = _attend(c, qb, new, masks, positions)
+    out, lse = _attend(c, qb, new, masks, positions, wide=wide)
     q, at = bf16_bits_to_f64(qb), 0
     for s, n in enumerate(lens):
         rows = slice(at, at + new[s])
@@ -231,37 +250,40 @@ def test_pages_outside_the_cache(new):
         at += new[s]
 
 
-def test_negative_and_zero_scales():
+@pytest.mark.parametrize("wide", [False, True])
+def test_negative_and_zero_scales(wide):
     for new in ([5, 4], [40, 30], [128, 20]):
         lens = [300, 170]
         c = Paged(lens, 1, 128, 23)
         masks, positions = _of_trees(workload.rng(3), lens, new)
         qb = _query_bits(sum(new), 2, 128, 24)
         for scale in (-0.2, 0.0):
-            out, lse = _attend(c, qb, new, masks, positions, scale=scale)
+            out, lse = _attend(c, qb, new, masks, positions, scale=scale, wide=wide)
             _check(c, qb, new, masks, positions, out, lse, scale=scale)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("new", [[8, 9], [16, 12], [64, 50]])
-def test_on_another_stream_and_in_a_graph(new):
+def test_on_another_stream_and_in_a_graph(new, wide):
     lens = [3000, 100]
     c = Paged(lens, 2, 128, 21)
     masks, positions = _of_trees(workload.rng(22), lens, new)
     qb = _query_bits(sum(new), 8, 128, 22)
-    want, want_lse = _attend(c, qb, new, masks, positions)
+    want, want_lse = _attend(c, qb, new, masks, positions, wide=wide)
+    table, most = _wide(c) if wide else (c.table_t, 3000)
     q, st, total = bf16(qb), starts(new), sum(new)
     m, p = _masks(masks, 1), int32(positions)
     out = torch.empty((total, 8, 128), dtype=torch.bfloat16, device=DEV)
     lse = torch.empty((total, 8), dtype=torch.float32, device=DEV)
-    ws = torch.empty(nv.kv_tree_attention_workspace(c.cache, q, c.table_t, c.lens_t, st, max(new), 3000), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(nv.kv_tree_attention_workspace(c.cache, q, table, c.lens_t, st, max(new), most), dtype=torch.uint8, device=DEV)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    nv.kv_tree_attention(q, c.cache, c.table_t, c.lens_t, st, m, p, max(new), 3000, out=out, lse=lse, workspace=ws, stream=side)
+    nv.kv_tree_attention(q, c.cache, table, c.lens_t, st, m, p, max(new), most, out=out, lse=lse, workspace=ws, stream=side)
     side.synchronize()
     assert np.array_equal(out.float().cpu().numpy(), want)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        nv.kv_tree_attention(q, c.cache, c.table_t, c.lens_t, st, m, p, max(new), 3000, out=out, lse=lse, workspace=ws)
+        nv.kv_tree_attention(q, c.cache, table, c.lens_t, st, m, p, max(new), most, out=out, lse=lse, workspace=ws)
     for _ in range(4):
         out.zero_()
         lse.zero_()
@@ -270,32 +292,74 @@ def test_on_another_stream_and_in_a_graph(new):
         assert np.array_equal(out.float().cpu().numpy(), want) and np.array_equal(lse.cpu().numpy(), want_lse)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("new", [[5, 9], [40, 30], [16, 14]])
-def test_descending_starts_touch_nothing_beyond_the_arrays(new):
+def test_descending_starts_touch_nothing_beyond_the_arrays(new, wide):
     d, heads, total = 64, 4, sum(new) + 20
     c = Paged([3000, 90, 500], 2, d, 221)
     g = workload.rng(31)
     masks = _masks([int.from_bytes(g.bytes(8), "little") for _ in range(total)], 1)
     q = bf16(_query_bits(total, heads, d, 223))
+    table, most = _wide(c) if wide else (c.table_t, 3000)
     for order in ([total, 0, new[0], new[0] + new[1]], [7, 3, total, 0], [new[0] + 1, new[0] + 2, 0, new[0]]):
         st = int32(order)
         out, lse = Guarded((total, heads, d), torch.bfloat16), Guarded((total, heads), torch.float32)
-        n = nv.kv_tree_attention_workspace(c.cache, q, c.table_t, c.lens_t, st, max(new), 3000)
+        n = nv.kv_tree_attention_workspace(c.cache, q, table, c.lens_t, st, max(new), most)
         ws = Guarded((n,), torch.uint8) if n else None
-        nv.kv_tree_attention(q, c.cache, c.table_t, c.lens_t, st, masks, None, max(new), 3000, out=out.t, lse=lse.t, workspace=ws and ws.t)
+        nv.kv_tree_attention(q, c.cache, table, c.lens_t, st, masks, None, max(new), most, out=out.t, lse=lse.t, workspace=ws and ws.t)
         torch.cuda.synchronize()
         for x in (out, lse, *([ws] if ws else [])):
             x.check()
 
 
-def test_many_sequences_of_very_different_lengths():
-    # enough workgroups' worth of bound that pages are planned from the lengths
+@pytest.mark.parametrize("most,group,wide", [(5, 2, False), (5, 8, True), (12, 8, True)])
+def test_many_sequences_of_very_different_lengths(most, group, wide):
+    # pages planned from the lengths, and more sequences than a wavefront has lanes
     g = workload.rng(31)
     lens = [int(x) for x in np.exp(g.uniform(0, np.log(2500), 70))]
     lens[3], lens[40], lens[-1] = 0, 12000, 1
-    new = [min(int(g.integers(1, 5)), n) for n in lens]
+    new = [min(int(g.integers(1, most)), n) for n in lens]
+    new[-2] = min(most, lens[-2])
     c = Paged(lens, 4, 64, 32)
     masks, positions = _of_trees(g, lens, new)
-    qb = _query_bits(sum(new), 8, 64, 33)
-    out, lse = _attend(c, qb, new, masks, positions)
+    qb = _query_bits(sum(new), 4 * group, 64, 33)
+    out, lse = _attend(c, qb, new, masks, positions, wide=wide)
     _check(c, qb, new, masks, positions, out, lse)
+    again = _attend(c, qb, new, masks, positions, wide=wide)
+    assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
+
+
+def test_many_short_sequences():
+    # none has more pages than a workgroup takes whole, and there are enough of them for the tiles
+    g = workload.rng(41)
+    lens = [int(g.integers(1, 250)) for _ in range(600)]
+    new = [min(n, int(g.integers(1, 12))) for n in lens]
+    c = Paged(lens, 8, 64, 42)
+    masks, positions = _of_trees(g, lens, new)
+    qb = _query_bits(sum(new), 64, 64, 43)
+    out, lse = _attend(c, qb, new, masks, positions, max_q=256)
+    some = [0, 1, 299, 300, 598, 599]
+    at = np.concatenate([[0], np.cumsum(new)])
+    rows = np.concatenate([np.arange(at[s], at[s + 1]) for s in some])
+    few = type("Few", (), dict(lens=[lens[s] for s in some], d=64, heads=8, k=[c.k[s] for s in some], v=[c.v[s] for s in some]))
+    _check(few, qb[rows], [new[s] for s in some], [masks[r] for r in rows], [positions[r] for r in rows], out[rows], lse[rows])
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("d,window,softcap", [(64, 100, 0.0), (64, 1, 0.0), (128, 70, 6.0), (256, 130, 0.0)])
+def test_windows_in_tiles_of_many_rows(d, window, softcap):
+    g = workload.rng(51)
+    lens = [int(g.integers(1, 400)) for _ in range(40)]
+    new = [min(n, int(g.integers(1, 40))) for n in lens]
+    c = Paged(lens, 8, d, 52)
+    masks, positions = _of_trees(g, lens, new)
+    qb = _query_bits(sum(new), 64, d, 53)
+    # a bound of 256 nodes makes it a call for the tiles
+    out, lse = _attend(c, qb, new, masks, positions, max_q=256, window=window, softcap=softcap)
+    some = [0, 7, 20, 39]
+    at = np.concatenate([[0], np.cumsum(new)])
+    rows = np.concatenate([np.arange(at[s], at[s + 1]) for s in some])
+    few = type("Few", (), dict(lens=[lens[s] for s in some], d=d, heads=8, k=[c.k[s] for s in some], v=[c.v[s] for s in some]))
+    _check(few, qb[rows], [new[s] for s in some], [masks[r] for r in rows], [positions[r] for r in rows], out[rows], lse[rows], window=window,
+           softcap=softcap)
+    assert np.isfinite(out).all() and np.isfinite(lse).all()

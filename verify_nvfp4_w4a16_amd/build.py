@@ -21,10 +21,10 @@ LIB = os.path.join(LIB_DIR, "libnvfp4_w4a16.so")
 ARCH = "gfx950"
 
 HOST_SOURCES = ["host/pack.cpp", "host/tiles.cpp", "host/kv_shapes.cpp", "host/kv_plan.cpp",
-                "host/draft_shapes.cpp"]
+                "host/draft_shapes.cpp", "host/tree_plan.cpp"]
 HIP_SOURCES = ["kernels/nvfp4_linear.hip", "kernels/nvfp4_gemm.hip", "kernels/nvfp4_fused.hip",
                "kernels/w8a16.hip", "kernels/read_probe.hip", "kernels/library_gemm.hip",
-               "kernels/kv_cache.hip", "kernels/kv_attention.hip", "kernels/kv_evict.hip", "kernels/sample.hip",
+               "kernels/kv_cache.hip", "kernels/kv_attention.hip", "kernels/kv_tree_attention.hip", "kernels/kv_evict.hip", "kernels/sample.hip",
                "kernels/draft.hip", "kernels/kv_move.hip", "kernels/adjust.hip"]
 
 # -ffp-contract=off keeps the packer's float64 steps unfused (bit-exact rule).

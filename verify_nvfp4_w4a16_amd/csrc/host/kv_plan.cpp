@@ -8,7 +8,7 @@ namespace nvfp4 {
 
 int kv_window(const nvfp4_kv_queries_t* q) { return q->window < q->max_kv ? static_cast<int>(q->window) : 0; }
 
-KvPlan kv_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
+KvPlan kv_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q, bool few) {
     const int64_t rows = q->max_q * (q->heads / c->kv_heads);
     // Rows of a kv head: up to 32 in 16-row workgroups, each decoding the pages
     // for itself, up to 64 in one workgroup with a page's halves on different
@@ -16,7 +16,7 @@ KvPlan kv_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_
     // of 128: 32 rows take 73 us, decoded once for all 78; 36 rows 94 and 77; 64 rows 119 and 91
     // (and 64 rows over 8192 slots 192 us in 128-row workgroups, 144 in these).
     KvPlan p{};
-    p.tile = rows <= 32 ? 0 : rows <= kKvTileRows / 2 ? kKvTileRows / 2 : kKvTileRows;
+    p.tile = few || rows <= 32 ? 0 : rows <= kKvTileRows / 2 ? kKvTileRows / 2 : kKvTileRows;
     const int64_t per_tile = p.tile ? p.tile : kKvRowTile;
     p.row_tiles = (rows + per_tile - 1) / per_tile;
     const int64_t base = std::max<int64_t>(s->seqs * c->kv_heads * p.row_tiles, 1);
@@ -49,8 +49,8 @@ KvPlan kv_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_
 
 int64_t kv_plan_bytes(const nvfp4_kv_seqs_t* s) { return (2 + 2 * s->seqs + 3) / 4 * 16; }
 
-int64_t kv_workspace_bytes(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
-    const KvPlan p = kv_plan(c, s, q);
+int64_t kv_workspace_bytes(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q, bool few) {
+    const KvPlan p = kv_plan(c, s, q, few);
     return p.part_rows * (c->head_dim + 2) * int64_t(sizeof(float)) + (p.planned ? kv_plan_bytes(s) : 0);
 }
 

@@ -29,12 +29,12 @@ struct KvPlan {
 // call is longer, so that a window of any size can be added to a slot.
 int kv_window(const nvfp4_kv_queries_t* q);
 
-// Of checked arguments.
-KvPlan kv_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q);
+// Of checked arguments.  few: 16-row workgroups, however many rows there are.
+KvPlan kv_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q, bool few = false);
 
 // Bytes of the planned items, ahead of the partial results.
 int64_t kv_plan_bytes(const nvfp4_kv_seqs_t* s);
 
-int64_t kv_workspace_bytes(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q);
+int64_t kv_workspace_bytes(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q, bool few = false);
 
 }  // namespace nvfp4

@@ -1,0 +1,47 @@
+// The layout of nvfp4_kv_tree_attention's launches (include/nvfp4_draft.h).
+#include "tree_plan.h"
+
+#include <algorithm>
+#include <cstdint>
+
+#include "kv_plan.h"
+
+namespace nvfp4 {
+
+TreePlan tree_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
+    TreePlan p{};
+    const int64_t rows = q->max_q * (q->heads / c->kv_heads);
+    const int window = kv_window(q);
+    const int64_t slots = window > 0 ? std::min(q->max_kv, window + q->max_q) : q->max_kv;
+    const int64_t pages = std::max<int64_t>((slots + NVFP4_KV_PAGE - 1) / NVFP4_KV_PAGE + (window > 0), 1);
+    // 16-row workgroups decode every page for themselves, but start at once and need no second launch where
+    // a sequence has few pages; 64 or 128 rows that share the decoding pay from many pages x rows on.  One tree of 16 x 4
+    // rows, 8 heads of 128, over 901 slots: 10 us and 30; 16 of 64 x 4 over 1000: 45 and 71; 32 of 9 .. 16 x 4 over
+    // 1000 .. 16000: 155 and 108; 4 of 200 .. 255 x 4 over 20000 .. 65000: 1132 and 700; at D = 256, 16 of 64 x 2 over
+    // 1500: 84 and 86.
+    const int64_t groups = std::min(s->seqs * c->kv_heads, int64_t(1) << 24), work = groups * std::min((rows + 15) / 16 * pages, int64_t(1) << 24);
+    if (rows <= 32 || work < kTreeWork / c->head_dim) return p;
+    p.rows = rows <= 64 ? 64 : 128;
+    const int64_t segments = std::max<int64_t>(s->seqs * c->kv_heads * ((rows + p.rows - 1) / p.rows), 1);
+    p.least = 4;
+    p.added = s->seqs > kTreeLanes;
+    p.whole = pages <= p.least;
+    // as many ranges as workgroups fit the card at once: two on a CU, one at D = 256
+    const int64_t most = c->head_dim == 256 ? 256 : 512;
+    const int64_t many = std::min(segments, int64_t(1) << 24);   // more give the most ranges too, and the product stays in 64 bits
+    p.ranges = static_cast<int>(std::min((many * pages + p.least - 1) / p.least, most));
+    p.workgroups = p.whole ? segments : p.ranges;
+    return p;
+}
+
+int64_t tree_sum_bytes(const nvfp4_kv_seqs_t* s) { return (s->seqs + 1) * 16; }
+
+int64_t tree_workspace_bytes(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q) {
+    const TreePlan p = tree_plan(c, s, q);
+    if (!p.rows) return kv_workspace_bytes(c, s, q, true);
+    if (p.whole && !p.added) return 0;
+    const int64_t parts = p.whole ? 0 : int64_t(2) * p.ranges * p.rows;
+    return parts * (c->head_dim + 2) * int64_t(sizeof(float)) + tree_sum_bytes(s);
+}
+
+}  // namespace nvfp4

@@ -19,7 +19,9 @@
 #include "../host/kv_index.h"
 #include "../host/kv_plan.h"
 #include "../host/kv_shapes.h"
+#include "../host/tree_plan.h"
 #include "kv_common.h"
+#include "kv_pages.h"
 #include "kv_scores.h"
 #include "setup.h"
 
@@ -27,13 +29,6 @@ namespace {
 
 constexpr int kWaves = nvfp4::kKvWaves, kRowTile = nvfp4::kKvRowTile, kTileRows = nvfp4::kKvTileRows;
 constexpr int kItems = nvfp4::kKvItems;
-
-// Scores may outgrow the running maximum by this much (in powers of two)
-// before the sums are rescaled.
-constexpr float kSlack = 8.0f;
-// Weights are held times this power of two, in f16 and in the sums: they reach
-// 2^15, and those below 2^-32 of the largest are lost in f16, not below 2^-25.
-constexpr float kLift = 7.0f;
 
 struct AttendArgs {
     KvView v;
@@ -164,73 +159,6 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int w) {
     return Item{s, in / each, rest ? pages / chunk : in % each, chunk};
 }
 
-// What one wavefront holds of a page: codes and scales as the operands need them.
-template <int D>
-struct PageRegs {
-    uint32_t k[4][D / 32];   // slot tile (h, t); D / 8 bytes of one row
-    uint32_t ks[D / 64];     // 4 tiles x D/64 groups
-    uint32_t v[2][D / 16];   // half page h; one dword a dim
-    uint32_t vs[2][2];
-
-    template <int N>
-    static __device__ __forceinline__ void load(uint32_t* to, const uint8_t* p) {
-        if constexpr (N % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < N / 4; ++i) {
-                const u32x4 x = load16_stream(p + 16 * i);
-                to[4 * i] = x[0], to[4 * i + 1] = x[1], to[4 * i + 2] = x[2], to[4 * i + 3] = x[3];
-            }
-        } else if constexpr (N == 2) {
-            const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
-            to[0] = x[0], to[1] = x[1];
-        } else {
-            to[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
-        }
-    }
-
-    __device__ __forceinline__ void load_k(const uint8_t* rec, int n, int b) {
-        using R = KvRecord<D>;
-#pragma unroll
-        for (int ht = 0; ht < 4; ++ht) {
-            const int slot = 32 * (ht >> 1) + (n >> 2) * 8 + (ht & 1) * 4 + (n & 3);
-            load<D / 32>(k[ht], rec + R::k_code(slot) + b * (D / 8));
-        }
-        load<D / 64>(ks, rec + R::kKScales + (n * 4 + b) * (D / 16));
-    }
-    __device__ __forceinline__ void load_v(const uint8_t* rec, int n, int b) {
-        using R = KvRecord<D>;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            load<D / 16>(v[h], rec + R::v_code(4 * h + b, n * (D / 16)));
-            load<2>(vs[h], rec + R::v_scale(4 * h + b, n * (D / 16) / 16));
-        }
-    }
-
-    // The scale pair of slot tile ht and the lane's 16-dim group j.
-    template <int I>
-    __device__ __forceinline__ f16x2 k_scale() const {
-        return scale_both<I % 4>(ks[I / 4]);
-    }
-};
-
-template <int D, int HT, int J>
-__device__ __forceinline__ f32x4 score_groups(const PageRegs<D>& p, const f16x8 (&q)[D / 32], f32x4 acc) {
-    if constexpr (J < D / 64) {
-        const f16x2 s = p.template k_scale<HT * (D / 64) + J>();
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_row(p.k[HT][2 * J], s), q[2 * J], acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_row(p.k[HT][2 * J + 1], s), q[2 * J + 1], acc, 0, 0, 0);
-        return score_groups<D, HT, J + 1>(p, q, acc);
-    }
-    return acc;
-}
-
-__device__ __forceinline__ f16x8 to_f16x8(const float* p) {
-    f16x8 r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = static_cast<_Float16>(p[i]);
-    return r;
-}
-
 // A row of sums in LDS: 16 bytes more than its dims, so that the 16 rows that are
 // written at once begin on different banks.
 template <int D>
@@ -271,7 +199,7 @@ kv_attend_rows_kernel(AttendArgs a) {
         ids = mine < end ? a.v.page_id(s, mine) : -1;
         at_id = 0;
     };
-    PageRegs<D> cur;
+    PageRegs<D, !TREE> cur;   // a tree's row tiles read the same pages
     const bool any = page < end && a.v.pages > 0;
     if (any) {
         read_ids(page);
@@ -294,10 +222,10 @@ kv_attend_rows_kernel(AttendArgs a) {
         const int base = page * kPage;
         const bool here = a.v.has(id);
         f32x4 z[4];
-        z[0] = score_groups<D, 0, 0>(cur, q, f32x4{0, 0, 0, 0});
-        z[1] = score_groups<D, 1, 0>(cur, q, f32x4{0, 0, 0, 0});
-        z[2] = score_groups<D, 2, 0>(cur, q, f32x4{0, 0, 0, 0});
-        z[3] = score_groups<D, 3, 0>(cur, q, f32x4{0, 0, 0, 0});
+        z[0] = score_groups<D, !TREE, 0, 0>(cur, q, f32x4{0, 0, 0, 0});
+        z[1] = score_groups<D, !TREE, 1, 0>(cur, q, f32x4{0, 0, 0, 0});
+        z[2] = score_groups<D, !TREE, 2, 0>(cur, q, f32x4{0, 0, 0, 0});
+        z[3] = score_groups<D, !TREE, 3, 0>(cur, q, f32x4{0, 0, 0, 0});
         if (at_id == 64) read_ids(page + kWaves);
         id = __builtin_amdgcn_readlane(ids, at_id++);
         const uint8_t* next = a.v.record_or_first<D>(id, hk);
@@ -308,9 +236,12 @@ kv_attend_rows_kernel(AttendArgs a) {
         a.sc.shape(p, to_log2);
         if (!here || base < span.lo_all || base + kPage > span.hi_all) {
             if constexpr (TREE) {
+                int r = row0 + n;   // worked out anew: kept, what follows from it would cost a wavefront a SIMD
+                asm volatile("" : "+v"(r));
+                const QueryRow who = rows.row(a.sc, r);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t seen = here ? rows.seen8(a.sc, me, base + 32 * h + 8 * b) : 0;
+                    const uint32_t seen = here ? rows.seen8(a.sc, who, base + 32 * h + 8 * b) : 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) p[8 * h + i] = seen >> i & 1 ? p[8 * h + i] : -INFINITY;
                 }
@@ -442,91 +373,8 @@ kv_attend_rows_kernel(AttendArgs a) {
 // its decode share and exponentials about 1400) at the 1.9 GHz that the card
 // holds under them: ragged prompt chunks of 700 .. 4099 tokens over 4100 ..
 // 8192 slots, 32 heads of 128, take 767 us, 891 TFLOP/s.
-template <int D>
-struct PageTiles {
-    static constexpr int kBytes = 2 * kPage * D * 2;
-
-    static __device__ __forceinline__ int k_at(int slot, int chunk) {
-        return (slot * (D / 8) + (chunk ^ (D == 64 ? (slot >> 1) & 7 : slot & 15))) * 16;
-    }
-    static __device__ __forceinline__ int v_at(int dim, int block) {
-        // rows of 8 chunks: reads run along the dims, writes along every fourth (D = 128)
-        return kPage * D * 2 + (dim * 8 + (block ^ ((dim >> 1) & 7) ^ ((dim >> 4) & 1))) * 16;
-    }
-};
-
-// A thread's share of a page: D / 4 dims of one slot's K, D / 32 dims of one
-// 8-slot block's V.
-template <int D>
-struct PageShare {
-    uint32_t k[D / 32], v[D / 32];
-    uint32_t ks, vs[2];
-
-    __device__ __forceinline__ void load(const uint8_t* rec, int tid) {
-        using R = KvRecord<D>;
-        const int slot = tid >> 2, part = tid & 3;
-        PageRegs<D>::template load<D / 32>(k, rec + R::k_code(slot) + part * (D / 8));
-        const uint8_t* p = rec + R::k_scale(slot, part * (D / 64));
-        if constexpr (D == 64)
-            ks = *p;
-        else if constexpr (D == 128)
-            ks = *reinterpret_cast<const uint16_t*>(p);
-        else
-            ks = *reinterpret_cast<const uint32_t*>(p);
-        const int block = tid >> 5, dim = (tid & 31) * (D / 32);
-        PageRegs<D>::template load<D / 32>(v, rec + R::v_code(block, dim));
-        PageRegs<D>::template load<2>(vs, rec + R::v_scale(block, dim / 16));
-    }
-
-    template <int J>
-    __device__ __forceinline__ void put_k(char* lds, int slot, int part) const {
-        if constexpr (J < D / 64) {
-            const f16x2 s = scale_both<J>(ks);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<f16x8*>(lds + PageTiles<D>::k_at(slot, part * (D / 32) + 2 * J + e)) =
-                    decode_row(k[2 * J + e], s);
-            put_k<J + 1>(lds, slot, part);
-        }
-    }
-
-    // left: slots of the page before the sequence's end; what lies after may
-    // hold anything, and becomes 0 in V (scores of such slots are masked).
-    __device__ __forceinline__ void put(char* lds, int tid, int left) {
-        put_k<0>(lds, tid >> 2, tid & 3);
-        const int block = tid >> 5, dim = (tid & 31) * (D / 32);
-        if (left < kPage) {
-            const int live = left - 8 * block;
-            const uint64_t mask = live <= 0 ? 0 : live >= 8 ? ~0ull : (1ull << (8 * live)) - 1;
-            vs[0] &= uint32_t(mask);
-            vs[1] &= uint32_t(mask >> 32);
-        }
-        const f16x2 sc[4] = {scale_pair<0>(vs[0]), scale_pair<1>(vs[0]), scale_pair<0>(vs[1]), scale_pair<1>(vs[1])};
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            *reinterpret_cast<f16x8*>(lds + PageTiles<D>::v_at(dim + i, block)) = decode_slots(v[i], sc);
-    }
-};
-
-// Order of N matrix instructions and the LDS reads of their operands: kAhead
-// reads ahead of the instruction that takes them.  Left alone the compiler reads
-// one ahead, and each instruction (32 cycles) waits most of a read's latency.
-constexpr int kAhead = 3;
-
-template <int N>
-__device__ __forceinline__ void reads_ahead() {
-    __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-    for (int i = 0; i < N - kAhead; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
-}
-
-
 // HALVES 2: wavefronts 0 and 1 have the first 32 slots of each page, 2 and 3 the last.
-template <int D, int HALVES, bool TREE>
+template <int D, int HALVES>
 __global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
 kv_attend_tile_kernel(AttendArgs a) {
     extern __shared__ char tiles[];   // two pages
@@ -537,7 +385,7 @@ kv_attend_tile_kernel(AttendArgs a) {
     const int n = lane & 31, b = lane >> 5;
     const int s = blockIdx.y, split = blockIdx.z;
     const int hk = blockIdx.x % a.v.kv_heads;
-    const QueryRowsOf<TREE> rows(a.v, a.sc, s);
+    const QueryRows rows(a.v, a.sc, s);
     // the last rows see most: they begin first
     const int tile = int(gridDim.x / a.v.kv_heads) - 1 - int(blockIdx.x / a.v.kv_heads);
     const int row0 = tile * kRows;
@@ -608,19 +456,10 @@ kv_attend_tile_kernel(AttendArgs a) {
             for (int i = 0; i < 16 * kStep; ++i) p[i] = z[i >> 4][i & 15];
             if (a.sc.cap != 0.0f) a.sc.shape(p, to_log2);
             if (base < span.lo_all || base + kPage > span.hi_all) {
-                if constexpr (TREE) {
 #pragma unroll
-                    for (int t = 0; t < 2 * kStep; ++t) {
-                        const uint32_t seen = rows.seen8(a.sc, me, base + 32 * half + 16 * t + 8 * b);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) p[8 * t + i] = seen >> i & 1 ? p[8 * t + i] : -INFINITY;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16 * kStep; ++i) {
-                        const int slot = base + 32 * half + 16 * (i >> 3) + 8 * b + (i & 7);
-                        p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
-                    }
+                for (int i = 0; i < 16 * kStep; ++i) {
+                    const int slot = base + 32 * half + 16 * (i >> 3) + 8 * b + (i & 7);
+                    p[i] = slot >= me.lo && slot < me.hi ? p[i] : -INFINITY;
                 }
             }
             float top = p[0];
@@ -731,7 +570,7 @@ kv_attend_tile_kernel(AttendArgs a) {
 // Joins the parts of one row, one workgroup a row: the wavefronts take every
 // fourth part and meet in LDS, both in a fixed order.  Bound by latency (1024
 // rows of up to 37 parts: 6.8 us).
-template <int D, bool TREE>
+template <int D>
 __global__ void __launch_bounds__(64 * kWaves)
 kv_join_kernel(AttendArgs a) {
     __shared__ float sums[kWaves][D];
@@ -742,7 +581,7 @@ kv_join_kernel(AttendArgs a) {
     const int token = static_cast<int>(at / a.sc.heads), head = static_cast<int>(at % a.sc.heads);
     const int s = last_sequence(a.v, [&](int i) { return a.v.start(i) <= token; });
     if (s < 0) return;
-    const QueryRowsOf<TREE> rows(a.v, a.sc, s);
+    const QueryRows rows(a.v, a.sc, s);
     const int r = nvfp4::kv_row_of(token, rows.first_token, rows.group, head % rows.group, rows.count);
     if (r < 0) return;   // no sequence's row
     // where part p of the row lies: the parts of a tile a slice apart, an item's by its number
@@ -822,10 +661,8 @@ bool allow_lds() {
     static_assert(tile_lds<D>() >= kTileRows * (D * 2 + 16) && tile_lds<D>() <= kMaxLdsBytes);
     for (const void* fn : {reinterpret_cast<const void*>(kv_attend_rows_kernel<D, false>),
                            reinterpret_cast<const void*>(kv_attend_rows_kernel<D, true>),
-                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 1, false>),
-                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 1, true>),
-                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 2, false>),
-                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 2, true>)})
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 1>),
+                           reinterpret_cast<const void*>(kv_attend_tile_kernel<D, 2>)})
         if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLdsBytes) != hipSuccess) return false;
     return true;
 }
@@ -836,7 +673,7 @@ int launch_attend(const AttendArgs& a, const nvfp4::KvPlan& plan, hipStream_t st
         // parts of a tile's pages along the slowest axis: those that short sequences do not need come last
         const int64_t blocks = plan.row_tiles * a.v.kv_heads;
         if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-        hipLaunchKernelGGL((plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1, TREE> : kv_attend_tile_kernel<D, 2, TREE>),
+        hipLaunchKernelGGL((plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1> : kv_attend_tile_kernel<D, 2>),
                            dim3(static_cast<unsigned>(blocks), a.v.seqs, plan.splits), dim3(64 * kWaves), tile_lds<D>(), st, a);
     } else {
         if (plan.planned) {
@@ -848,7 +685,7 @@ int launch_attend(const AttendArgs& a, const nvfp4::KvPlan& plan, hipStream_t st
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     if (plan.part_rows > 0) {
         const int64_t slice = int64_t(a.v.total) * a.sc.heads;
-        hipLaunchKernelGGL((kv_join_kernel<D, TREE>), dim3(static_cast<unsigned>(slice)), dim3(64 * kWaves), 0, st, a);
+        hipLaunchKernelGGL(kv_join_kernel<D>, dim3(static_cast<unsigned>(slice)), dim3(64 * kWaves), 0, st, a);
         if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     }
     return NVFP4_OK;
@@ -864,6 +701,7 @@ int kv_setup() { return allow_lds<64>() && allow_lds<128>() && allow_lds<256>() 
 
 namespace {
 
+// Argument checks that the calls share.
 int check_call(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, const nvfp4_kv_queries_t* queries) {
     int st;
     if ((st = nvfp4::check_kv_cache(cache)) != NVFP4_OK) return st;
@@ -880,17 +718,19 @@ int attend(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, const nvf
     if ((st = nvfp4::check_kv_rows(out, 0, 0, seqs->total)) != NVFP4_OK) return st;
     if ((reinterpret_cast<uintptr_t>(lse) & 3) || (reinterpret_cast<uintptr_t>(workspace) & 15)) return NVFP4_ERR_ALIGN;
     if (seqs->seqs == 0 || seqs->total == 0 || queries->max_q == 0) return NVFP4_OK;
-    const int64_t need = nvfp4::kv_workspace_bytes(cache, seqs, queries);
+    const int64_t need = tree ? nvfp4::tree_workspace_bytes(cache, seqs, queries) : nvfp4::kv_workspace_bytes(cache, seqs, queries);
     if (need > 0 && !workspace) return NVFP4_ERR_NULL;
     if (need > workspace_bytes) return NVFP4_ERR_SCRATCH;
     if ((st = nvfp4::device_setup()) != NVFP4_OK) return st;
+    if (tree && nvfp4::tree_plan(cache, seqs, queries).rows)
+        return nvfp4::tree_attend(cache, seqs, queries, tree, out, lse, workspace, stream);
 
     AttendArgs a;
     a.v = kv_view(cache, seqs);
     a.sc = kv_scores(cache, queries);
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    const nvfp4::KvPlan plan = nvfp4::kv_plan(cache, seqs, queries);
+    const nvfp4::KvPlan plan = nvfp4::kv_plan(cache, seqs, queries, tree != nullptr);
     a.tile = plan.tile;
     a.splits = plan.splits;
     a.chunk = plan.chunk;
@@ -934,7 +774,12 @@ extern "C" int nvfp4_kv_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_
 
 extern "C" int nvfp4_kv_tree_attention_workspace(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,
                                                  const nvfp4_kv_queries_t* queries, int64_t* bytes) {
-    return nvfp4_kv_attention_workspace(cache, seqs, queries, bytes);
+    if (!bytes) return NVFP4_ERR_NULL;
+    const int st = check_call(cache, seqs, queries);
+    if (st != NVFP4_OK) return st;
+    if (queries->max_q > NVFP4_TREE_MAX) return NVFP4_ERR_SHAPE;
+    *bytes = nvfp4::tree_workspace_bytes(cache, seqs, queries);
+    return NVFP4_OK;
 }
 
 extern "C" int nvfp4_kv_tree_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,

@@ -4,6 +4,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "nvfp4_draft.h"
 #include "nvfp4_w4a16.h"
 
 namespace nvfp4 {
@@ -20,6 +21,13 @@ int w8a16_setup();
 
 // Kernel attributes of the attention over the paged cache (LDS beyond 64 KB).
 int kv_setup();
+
+// Kernel attributes of the attention of trees over the paged cache (LDS beyond 64 KB).
+int tree_setup();
+
+// nvfp4_kv_tree_attention of checked arguments where tree_plan gives tiles.
+int tree_attend(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, const nvfp4_kv_queries_t* queries,
+                const nvfp4_kv_tree_t* tree, void* out, float* lse, void* workspace, void* stream);
 
 // Kernel attributes of nvfp4_sample's kernels (LDS beyond 64 KB).
 int sample_setup();
