@@ -5,6 +5,13 @@
 // are whole numbers, so the order of the atomic additions changes nothing),
 // then streams its rows' logits once: read, adjust by the word, write.  A
 // row's own drafted tokens are counted in before the row and out after it.
+// A row's logits are loaded while the history is counted or the row before is
+// written.
+//
+// Bounds: 192 rows of 151552 bf16 logits take 20 us without penalties (5.8 TB/s;
+// a plain copy 17), 48 us with biases, grammars and histories of 4000 tokens
+// each, of which the counting is 15: the additions in LDS, where a few tokens
+// are most of a text.  8 trees of 48 rows in fp32 take 109 us (4.3 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -16,9 +23,14 @@
 
 namespace {
 
+// 32 KiB of words and eight wavefronts: four workgroups fill a CU.  16384 tokens (two workgroups) took 64 us
+// instead of 48 for 192 rows of 151552 bf16 logits with 4000 tokens of history each, and 4096 tokens of 256
+// threads 51 us, since each piece reads the whole history.
 constexpr int kThreads = 512;
 constexpr int kPiece = 8192;   // tokens of a workgroup
-constexpr int kRows = 8;       // rows that share the counted history
+// Rows that share the counted history.  For trees of 48 rows, fp32, histories of 500..6000 tokens | of 32768:
+// 2 rows 108 | 139 us, 3 rows 109 | 136, 4 rows 115 | 129, 8 rows 132 | 138: many rows leave the card idle at the end.
+constexpr int kRows = 3;
 
 // A token's word: how often it was said, its place in the bias list plus 1, and whether the prompt has it.
 constexpr uint32_t kCount = (1u << 20) - 1;
@@ -30,7 +42,7 @@ static_assert(nvfp4::kHistoryMax + NVFP4_TREE_MAX < kCount && NVFP4_BIAS_MAX < 0
 struct AdjustArgs {
     nvfp4_adjust_t a;
     void* out;
-    int vocab, pieces, seqs, rows;
+    int vocab, pieces, seqs, rows, per;   // per: rows of a unit, kRows or 1
 };
 
 // Rows may begin at any element, so whole vectors are read from wherever they begin.
@@ -41,69 +53,112 @@ __device__ __forceinline__ V load_any(const void* p) {
     return v;
 }
 
-// The first unit of sequence s, a unit being kRows rows: enough wherever its rows begin.
-__device__ __forceinline__ int first_unit(int start, int s) { return start / kRows + s; }
+// The first unit of sequence s.  Units of one row are counted as the rows are; others are kRows rows of a
+// sequence, and a unit more for each sequence is enough wherever its rows begin.
+__device__ __forceinline__ int first_unit(int start, int s, int per) { return per == 1 ? start : start / kRows + s; }
 
 template <class In, class Out>
 __global__ void __launch_bounds__(kThreads)
 adjust_kernel(AdjustArgs args) {
-    constexpr int kEach = 16 / sizeof(In);   // logits of a load
+    constexpr int kEach = 16 / sizeof(In);                      // logits of a load
+    constexpr int kLoads = kPiece / (kThreads * kEach);         // loads of a thread for a row
     __shared__ __attribute__((aligned(16))) uint32_t words[kPiece];
     __shared__ float bias[NVFP4_BIAS_MAX];
     const nvfp4_adjust_t& a = args.a;
     const int tid = threadIdx.x, lane = tid & 63;
-    const int unit = blockIdx.x / args.pieces, piece = blockIdx.x % args.pieces;
+        const int unit = blockIdx.x / args.pieces, piece = blockIdx.x % args.pieces;
     const int from = piece * kPiece, size = min(kPiece, args.vocab - from);
 
     // the sequence of this unit and its rows
     int s = unit, row0 = unit, row_end = unit + 1, first = unit;
     if (a.q_starts) {
-        auto start = [&](int i) { return min(max(a.q_starts[i], 0), args.rows); };
-        int found = 0;
-        for (int base = 0; base < args.seqs; base += 64) {
-            const int n = __popcll(__ballot(base + lane < args.seqs && first_unit(start(min(base + lane, args.seqs)), base + lane) <= unit));
+        auto start = [&](int i) { return min(max(a.q_starts[min(i, args.seqs)], 0), args.rows); };
+        // the last sequence whose first unit is this one or before it, 256 of them in one latency
+        int end = first = 0, found = 0;
+        for (int base = 0; base < args.seqs; base += 256) {
+            int begins[4], ends[4], n = 0;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) begins[y] = start(base + 64 * y + lane), ends[y] = start(base + 64 * y + lane + 1);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int i = base + 64 * y + lane;
+                const int here = __popcll(__ballot(i < args.seqs && first_unit(begins[y], i, args.per) <= unit));
+                if (n == 64 * y && here) first = __builtin_amdgcn_readlane(begins[y], here - 1), end = __builtin_amdgcn_readlane(ends[y], here - 1);
+                if (n == 64 * y) n += here;
+            }
             found += n;
-            if (n < 64) break;
+            if (n < 256) break;
         }
         s = found - 1;
         if (s < 0) return;
-        first = start(s);
-        const int end = start(s + 1);
-        row0 = first + (unit - first_unit(first, s)) * kRows;
+        row0 = first + (unit - first_unit(first, s, args.per)) * args.per;
         if (row0 < first) return;            // as happens where starts descend
-        row_end = min(row0 + kRows, end);
+        row_end = min(row0 + args.per, end);
         if (row0 >= row_end) return;
     }
 
+    // a row's logits are on their way while the history is counted, and the next row's while one is written
+    u32x4 raw[kLoads];
+    auto fetch = [&](int row) {
+        const In* in = static_cast<const In*>(a.logits) + row * a.pitch + from;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            const int i = (x * kThreads + tid) * kEach;
+            if (i + kEach <= size) {
+                raw[x] = load_any<u32x4>(in + i);
+            } else {   // the end of the vocabulary
+                In some[kEach];
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) some[j] = i + j < size ? in[i + j] : In(0);
+                __builtin_memcpy(&raw[x], some, sizeof some);
+            }
+        }
+    };
+    fetch(row0);
+
     const float r_in = a.repetition ? a.repetition[s] : 1.0f;
     const float r = r_in > 0.0f ? r_in : 1.0f;
+    const float inverse = 1.0f / r;
     const float p = a.presence ? a.presence[s] : 0.0f, f = a.frequency ? a.frequency[s] : 0.0f;
     const bool penalised = r != 1.0f || p != 0.0f || f != 0.0f;
     const bool counted = penalised && a.history, drafts = penalised && a.drafted, biased = a.bias_tokens && a.bias_width > 0;
     const bool worded = counted || drafts || biased;
+    const int32_t* said = a.history + s * a.history_pitch;
+    u32x4 t[4] = {};   // four loads of the history at a time; the first goes out before its length is known
+    if (counted && tid * 4 + 4 <= a.history_pitch) t[0] = load_any<u32x4>(said + tid * 4);
     if (worded) {
         for (int i = tid * 4; i < kPiece; i += kThreads * 4) *reinterpret_cast<u32x4*>(words + i) = u32x4{0, 0, 0, 0};
         __syncthreads();
     }
     if (counted) {
-        const int32_t* said = a.history + s * a.history_pitch;
         const int len = static_cast<int>(min(int64_t(max(a.history_lens[s], 0)), a.history_pitch));
         const int prompt = a.prompt_lens ? min(max(a.prompt_lens[s], 0), len) : 0;
-        auto put = [&](int at, int token) {
-            const uint32_t v = uint32_t(token) - uint32_t(from);
+        auto put = [&](int at, uint32_t token) {
+            const uint32_t v = token - uint32_t(from);
             if (v >= uint32_t(size)) return;
             if (at < prompt)
                 atomicOr(&words[v], kPrompt);
             else
                 atomicAdd(&words[v], 1u);
         };
-        int i = tid * 4;
-        for (; i + 3 < len; i += kThreads * 4) {
-            const u32x4 t = load_any<u32x4>(said + i);
+        constexpr int kStep = kThreads * 4;
+        for (int base = 0; base < len; base += 4 * kStep) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) put(i + j, static_cast<int>(t[j]));
+            for (int y = 0; y < 4; ++y) {
+                const int i = base + y * kStep + tid * 4;
+                if (i + 4 <= len && base + y) t[y] = load_any<u32x4>(said + i);
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int i = base + y * kStep + tid * 4;
+                if (i + 4 <= len) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) put(i + j, t[y][j]);
+                } else {
+                    for (int j = i; j < len; ++j) put(j, static_cast<uint32_t>(said[j]));
+                }
+            }
         }
-        for (int j = i; j < min(i + 4, len); ++j) put(j, said[j]);
     }
     if (biased) {
         __syncthreads();
@@ -134,59 +189,53 @@ adjust_kernel(AdjustArgs args) {
             const int64_t state = a.allowed_rows ? a.allowed_rows[row] : row;
             if (state >= 0 && state < a.states) allowed = a.allowed + state * a.allowed_pitch + from / 32;
         }
-        const In* in = static_cast<const In*>(a.logits) + row * a.pitch + from;
         Out* out = static_cast<Out*>(args.out) + row * a.out_pitch + from;
         auto one = [&](float x, int i) {
             const uint32_t w = worded ? words[i] : 0;
             if (w) {
                 const uint32_t n = w & kCount;
                 if (penalised && (w & (kPrompt | kCount))) {
-                    x = x > 0.0f ? x / r : x * r;
+                    float q = x * inverse;   // x / r: the product's error goes back in, in one rounding
+                    const float better = __builtin_fmaf(__builtin_fmaf(-q, r, x), inverse, q);
+                    q = __builtin_isfinite(better) ? better : q;
+                    x = x > 0.0f ? q : x * r;
                     if (n) x = x - p - f * float(n);
                 }
                 if (w & kBias) x += bias[((w & kBias) >> kBiasShift) - 1];
             }
             return x;
         };
-        for (int i = tid * kEach; i < size; i += kThreads * kEach) {
-            float x[kEach];
-            const bool whole = i + kEach <= size;
+        float x[kLoads][kEach];
+#pragma unroll
+        for (int y = 0; y < kLoads; ++y)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (std::is_same_v<In, float>) {
+                    x[y][j] = bits_f32(raw[y][j]);
+                } else {
+                    x[y][2 * j] = bits_f32(raw[y][j] << 16);
+                    x[y][2 * j + 1] = bits_f32(raw[y][j] & 0xffff0000u);
+                }
+            }
+        if (row + 1 < row_end) fetch(row + 1);
+#pragma unroll
+        for (int y = 0; y < kLoads; ++y) {
+            const int i = (y * kThreads + tid) * kEach;
+            if (i >= size) break;
             uint32_t bits = ~0u;
             if (allowed) bits = allowed[i / 32] >> (i % 32);
-            if (whole) {
-                const u32x4 v = load_any<u32x4>(in + i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (std::is_same_v<In, float>) {
-                        x[j] = bits_f32(v[j]);
-                    } else {
-                        x[2 * j] = bits_f32(v[j] << 16);
-                        x[2 * j + 1] = bits_f32(v[j] & 0xffff0000u);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kEach; ++j) {
-                    if (i + j >= size) continue;
-                    if constexpr (std::is_same_v<In, float>)
-                        x[j] = in[i + j];
-                    else
-                        x[j] = bf16_to_f32(in[i + j]);
-                }
-            }
 #pragma unroll
             for (int j = 0; j < kEach; ++j) {
-                if (!whole && i + j >= size) continue;
-                x[j] = one(x[j], i + j);
-                if (!(bits >> j & 1)) x[j] = -INFINITY;
+                x[y][j] = one(x[y][j], i + j);
+                if (!(bits >> j & 1)) x[y][j] = -INFINITY;
             }
-            if (whole) {
+            if (i + kEach <= size) {
                 if constexpr (std::is_same_v<Out, float>) {
-                    __builtin_memcpy(out + i, x, sizeof x);
+                    __builtin_memcpy(out + i, x[y], sizeof x[y]);
                 } else {
                     uint16_t w[kEach];
 #pragma unroll
-                    for (int j = 0; j < kEach; ++j) w[j] = f32_to_bf16_rne(x[j]);
+                    for (int j = 0; j < kEach; ++j) w[j] = f32_to_bf16_rne(x[y][j]);
                     __builtin_memcpy(out + i, w, sizeof w);
                 }
             } else {
@@ -194,9 +243,9 @@ adjust_kernel(AdjustArgs args) {
                 for (int j = 0; j < kEach; ++j) {
                     if (i + j >= size) continue;
                     if constexpr (std::is_same_v<Out, float>)
-                        out[i + j] = x[j];
+                        out[i + j] = x[y][j];
                     else
-                        out[i + j] = f32_to_bf16_rne(x[j]);
+                        out[i + j] = f32_to_bf16_rne(x[y][j]);
                 }
             }
         }
@@ -215,8 +264,11 @@ extern "C" int nvfp4_adjust_logits(const nvfp4_adjust_t* adjust, void* out, void
     if (adjust->rows == 0 || adjust->seqs == 0) return NVFP4_OK;
     if ((st = nvfp4::device_setup()) != NVFP4_OK) return st;
     AdjustArgs a{*adjust, out, static_cast<int>(adjust->vocab), static_cast<int>((adjust->vocab + kPiece - 1) / kPiece),
-                 static_cast<int>(adjust->seqs), static_cast<int>(adjust->rows)};
-    const int64_t units = adjust->q_starts ? adjust->rows / kRows + adjust->seqs : adjust->rows;
+                 static_cast<int>(adjust->seqs), static_cast<int>(adjust->rows), 1};
+    // units of one row where those are fewer
+    const bool single = !adjust->q_starts || adjust->rows <= adjust->rows / kRows + adjust->seqs;
+    a.per = single ? 1 : kRows;
+    const int64_t units = single ? adjust->rows : adjust->rows / kRows + adjust->seqs;
     const dim3 grid(static_cast<unsigned>(units * a.pieces)), block(kThreads);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool in32 = adjust->logits_type == NVFP4_LOGITS_F32, out32 = adjust->out_type == NVFP4_LOGITS_F32;
