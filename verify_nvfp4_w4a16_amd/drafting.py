@@ -275,10 +275,14 @@ def tree_accept(drafted, parents, chosen, kv_lens, q_starts, max_q: int, *, path
     total = parents.shape[0]
     if not 1 <= max_q <= TREE_MAX:
         raise ValueError(f"max_q must be 1..{TREE_MAX}")
-    path = _out("path", path, (seqs, max_q), _I32, dev, stream)
-    counts = _out("counts", counts, (seqs,), _I32, dev, stream)
-    token = _out("token", token, (seqs,), _I32, dev, stream)
-    new_lens = _out("new_lens", new_lens, (seqs,), _I32, dev, stream)
+    if path is counts is token is new_lens is None:   # pieces of one tensor, as kv_pages has them
+        path, counts, token, new_lens = _new(seqs * (max_q + 3), _I32, dev, stream).split_with_sizes((seqs * max_q, seqs, seqs, seqs))
+        path = path.view(seqs, max_q)
+    else:
+        path = _out("path", path, (seqs, max_q), _I32, dev, stream)
+        counts = _out("counts", counts, (seqs,), _I32, dev, stream)
+        token = _out("token", token, (seqs,), _I32, dev, stream)
+        new_lens = _out("new_lens", new_lens, (seqs,), _I32, dev, stream)
     _check(_draft().nvfp4_tree_accept(_array("drafted", drafted, (total,), _I32, dev), _ints("parents", parents, 1, dev),
                                       _array("chosen", chosen, (total,), _I32, dev), lens, starts, seqs, total, max_q,
                                       path.data_ptr(), counts.data_ptr(), token.data_ptr(), new_lens.data_ptr(), _stream(stream, dev)),
