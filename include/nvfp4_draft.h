@@ -50,7 +50,7 @@ typedef struct {
     const int32_t* state;   /* [2]: head, count */
     int64_t capacity;       /* 1..2^30, at least the pages that there are */
     int32_t* table;         /* [seqs][table_pitch] */
-    int64_t table_pitch;    /* 1..2^23 */
+    int64_t table_pitch;    /* 1..2^23, times min(seqs, 1024) at most 2^30 */
     const int32_t* held;    /* [seqs] entries of a table row that the sequence owns */
     const int32_t* keep;    /* [seqs] slots that stay */
     const int32_t* fresh;   /* [seqs] new tokens that are asked for */

@@ -65,6 +65,9 @@ def test_refusals_of_pages():
     for kw in (dict(capacity=0), dict(capacity=(1 << 30) + 1), dict(table_pitch=0), dict(table_pitch=(1 << 23) + 1), dict(seqs=-1),
                dict(seqs=65536), dict(total=-1), dict(total=(1 << 24) + 1)):
         assert call(**kw) == nv.ERR_SHAPE, kw
+    # pages of a block of sequences that would not add up in 32 bits, whatever `held` says
+    for kw in (dict(seqs=129, table_pitch=1 << 23), dict(seqs=1024, table_pitch=(1 << 20) + 1), dict(seqs=65535, table_pitch=(1 << 20) + 1)):
+        assert call(**kw) == nv.ERR_SHAPE, kw
     for name in ("pool", "state", "table", "held", "keep", "fresh", "state_out", "held_out", "kv_lens", "q_starts"):
         assert call(**{name: None}) == nv.ERR_NULL, name
         assert call(**{name: A + 2}) == nv.ERR_ALIGN, name
@@ -261,3 +264,51 @@ def test_oracle_adjust_closed_forms():
     assert x.tolist() == [1.0, -5.0, -3.0, -np.inf]
     x, _ = odraft.adjust([2.0, np.nan], [0, 1], [], r=-1.0)
     assert x[0] == 2.0 and np.isnan(x[1])
+
+
+def test_layout_of_tree_attention_at_the_ends_of_every_field(tmp_path):
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    out = str(tmp_path / "tree_plan_check")
+    host = os.path.join(ROOT, "verify_nvfp4_w4a16_amd", "csrc", "host")
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
+           "-fno-sanitize-recover=all", "-I", os.path.join(ROOT, "include"), os.path.join(ROOT, "tests", "tree_plan_check.cpp"),
+           *(os.path.join(host, n) for n in ("kv_shapes.cpp", "draft_shapes.cpp", "kv_plan.cpp", "tree_plan.cpp")), "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-4000:]
+    r = subprocess.run([out], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "plan ok" in r.stdout, (r.stdout[-2000:], r.stderr[-4000:])
+
+
+def test_calls_run_with_their_tensors_device_current(monkeypatch):
+    from verify_nvfp4_w4a16_amd import serving
+    current, calls = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *error):
+            current[0] = self.before
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda:1"), 77
+
+    monkeypatch.setattr(serving, "_current_device", lambda: current[0])
+    monkeypatch.setattr(serving, "_raw_stream", lambda index: 10 + index)
+    monkeypatch.setattr(serving.torch.cuda, "device", Device)
+
+    def call(*args):
+        calls.append((current[0], args))
+        return nv.OK
+
+    serving._launch("x", call, torch.device("cuda:0"), None, 1)
+    serving._launch("x", call, torch.device("cuda:1"), None, 2)
+    serving._launch("x", call, torch.device("cuda:1"), Stream, 3)
+    assert calls == [(0, (1, 10)), (1, (2, 11)), (1, (3, 77))] and current == [0]
+    with pytest.raises(ValueError, match="stream"):
+        serving._launch("x", call, torch.device("cuda:0"), Stream, 4)
+    assert len(calls) == 3

@@ -225,3 +225,36 @@ def test_refusals_that_need_a_gpu_tensor():
                dict(bias_tokens=torch.zeros(2, 0, dtype=torch.int32, device=DEV), bias_values=torch.zeros(2, 0, device=DEV)),
                dict(allowed=torch.zeros(0, 1, dtype=torch.int32, device=DEV))):
         assert torch.equal(nv.adjust_logits(x, **kw), x)
+
+
+def test_repetition_at_the_ends_of_its_range():
+    # x / r as a product with 1 / r, whose error goes back in: half a step of the result, also where 1 / r is subnormal or
+    # has no number; below 2^-126 steps are 2^-149
+    r = np.array([1e-40, 2e-39, 1.2e-38, 1e-20, 3.0, 1e20, 1e38, 3e38], np.float32)
+    x = np.array([1e-5, 0.3, 7.0, 80.0, -1e-5, -80.0, 3e38, np.inf, 0.0], np.float32)
+    logits = _f32(np.tile(x, (len(r), 1)))
+    said = int32(np.tile(np.arange(len(x)), (len(r), 1)))
+    out = nv.adjust_logits(logits, said, int32([len(x)] * len(r)), repetition=_f32(r)).cpu().numpy().astype(np.float64)
+    with np.errstate(over="ignore"):
+        want = np.where(x > 0, x.astype(np.float64) / r[:, None].astype(np.float64), x.astype(np.float64) * r[:, None].astype(np.float64))
+    most = float(np.finfo(np.float32).max)
+    far = np.abs(want) >= most * (1 + 2.0 ** -25)
+    assert np.array_equal(out[far], np.sign(want[far]) * np.inf)
+    near = ~far
+    assert np.all(np.abs(out[near] - want[near]) <= 2.0 ** -24 * (1 + 2.0 ** -20) * np.abs(want[near]) + 2.0 ** -149)
+
+
+def test_more_logits_than_a_launch_takes():
+    rows, vocab = 8200, 1 << 22
+    if torch.cuda.mem_get_info()[0] < 90e9:
+        pytest.skip("70 GB of logits")
+    logits = torch.zeros((rows, vocab), dtype=torch.bfloat16, device=DEV)
+    tokens = int32(np.stack([np.arange(rows) * 511, np.full(rows, vocab - 1)], 1))
+    values = _f32(np.stack([1.0 + np.arange(rows) % 128, np.full(rows, -3.0)], 1))
+    nv.adjust_logits(logits, bias_tokens=tokens, bias_values=values, out=logits)
+    for row in (0, 1, 4095, 8190, 8191, 8192, 8199):
+        at = logits[row].nonzero().flatten().tolist()
+        assert at == [row * 511, vocab - 1], (row, at)
+        assert logits[row, at].tolist() == [1.0 + row % 128, -3.0]
+    del logits
+    torch.cuda.empty_cache()

@@ -363,3 +363,27 @@ def test_windows_in_tiles_of_many_rows(d, window, softcap):
     _check(few, qb[rows], [new[s] for s in some], [masks[r] for r in rows], [positions[r] for r in rows], out[rows], lse[rows], window=window,
            softcap=softcap)
     assert np.isfinite(out).all() and np.isfinite(lse).all()
+
+
+def test_more_rows_than_a_launch_of_the_join_takes():
+    # 4096 trees over the same short cache, then one over a long one, whose rows are those from 2^25 on
+    lens, nodes, heads, many = [130, 8000], 128, 64, 4096
+    c = Paged(lens, 1, 64, 41, v_scale=0.5)
+    masks, _ = _of_trees(workload.rng(42), lens, [nodes, nodes])
+    total = (many + 1) * nodes
+    qb = _query_bits(2 * nodes, heads, 64, 43)
+    q = torch.empty((total, heads, 64), dtype=torch.bfloat16, device=DEV)
+    ends = bf16(qb)
+    q[:many * nodes].view(many, nodes, heads, 64)[:] = ends[:nodes]
+    q[many * nodes:] = ends[nodes:]
+    m = _masks(masks, 2)
+    m = torch.cat([m[:nodes].repeat(many, 1), m[nodes:]])
+    table = torch.cat([c.table_t[:1].repeat(many, 1), c.table_t[1:]])
+    out, lse = nv.kv_tree_attention(q, c.cache, table, int32([lens[0]] * many + [lens[1]]), starts([nodes] * (many + 1)), m, None, nodes,
+                                    lens[1])
+    pick = torch.cat([torch.arange(nodes), torch.arange(total - nodes, total)]).to(DEV)
+    _check(c, qb, [nodes, nodes], masks, None, out[pick].float().cpu().numpy().astype(np.float64), lse[pick].cpu().numpy().astype(np.float64))
+    # the trees are alike, and the parts that some were joined of change a sum's last bits alone
+    first = out[:nodes].float()
+    for s in (1, 7, 2047, 4095):
+        assert float((out[s * nodes:(s + 1) * nodes].float() - first).abs().max()) <= 2.0 ** -6 * float(first.abs().max())

@@ -25,6 +25,8 @@ int check_kv_pages(const nvfp4_kv_pages_t* p, const int32_t* state_out, const in
     if (p->seqs < 0 || p->seqs > 65535 || p->total < 0 || p->total > kKvMaxTotal) return NVFP4_ERR_SHAPE;
     if (p->capacity < 1 || p->capacity > kPoolMax) return NVFP4_ERR_SHAPE;
     if (p->table_pitch < 1 || p->table_pitch > kKvMaxTablePitch) return NVFP4_ERR_SHAPE;
+    // what a block of sequences may hold, whatever `held` says, is added up in 32 bits
+    if ((p->seqs < kPagesBlock ? p->seqs : int64_t(kPagesBlock)) * p->table_pitch > kPoolMax) return NVFP4_ERR_SHAPE;
     for (const void* a : {static_cast<const void*>(p->pool), static_cast<const void*>(p->state),
                           static_cast<const void*>(state_out), static_cast<const void*>(q_starts)})
         if ((st = check_words(a)) != NVFP4_OK) return st;

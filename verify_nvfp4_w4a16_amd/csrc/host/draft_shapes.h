@@ -8,6 +8,7 @@
 namespace nvfp4 {
 
 constexpr int64_t kPoolMax = int64_t(1) << 30;        // pages of a pool: head + count + new ones stay below 2^31
+constexpr int kPagesBlock = 1024;                      // sequences whose pages are added up at a time
 constexpr int64_t kHistoryMax = int64_t(1) << 19;     // a count and the drafted tokens stay below 2^20
 constexpr int64_t kMoveCaches = 1024;
 

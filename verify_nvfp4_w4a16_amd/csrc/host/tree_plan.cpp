@@ -30,7 +30,9 @@ TreePlan tree_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nv
     const int64_t most = c->head_dim == 256 ? 256 : 512;
     const int64_t many = std::min(segments, int64_t(1) << 24);   // more give the most ranges too, and the product stays in 64 bits
     p.ranges = static_cast<int>(std::min((many * pages + p.least - 1) / p.least, most));
-    p.workgroups = p.whole ? segments : p.ranges;
+    // whole segments: no more than the rows that there are can fill
+    const int64_t filled = (s->seqs + s->total * (q->heads / c->kv_heads) / p.rows) * c->kv_heads;
+    p.workgroups = p.whole ? std::min(segments, std::max<int64_t>(filled, 1)) : p.ranges;
     return p;
 }
 

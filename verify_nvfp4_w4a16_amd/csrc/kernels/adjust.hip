@@ -43,6 +43,7 @@ struct AdjustArgs {
     nvfp4_adjust_t a;
     void* out;
     int vocab, pieces, seqs, rows, per;   // per: rows of a unit, kRows or 1
+    int unit0;                            // first unit of the launch
 };
 
 // Rows may begin at any element, so whole vectors are read from wherever they begin.
@@ -66,7 +67,7 @@ adjust_kernel(AdjustArgs args) {
     __shared__ float bias[NVFP4_BIAS_MAX];
     const nvfp4_adjust_t& a = args.a;
     const int tid = threadIdx.x, lane = tid & 63;
-        const int unit = blockIdx.x / args.pieces, piece = blockIdx.x % args.pieces;
+        const int unit = args.unit0 + blockIdx.x / args.pieces, piece = blockIdx.x % args.pieces;
     const int from = piece * kPiece, size = min(kPiece, args.vocab - from);
 
     // the sequence of this unit and its rows
@@ -118,7 +119,7 @@ adjust_kernel(AdjustArgs args) {
 
     const float r_in = a.repetition ? a.repetition[s] : 1.0f;
     const float r = r_in > 0.0f ? r_in : 1.0f;
-    const float inverse = 1.0f / r;
+    const float up = r < 0x1p-64f ? 0x1p64f : 1.0f, lifted = r * up, inverse = 1.0f / lifted;   // 1 / r itself may be no number
     const float p = a.presence ? a.presence[s] : 0.0f, f = a.frequency ? a.frequency[s] : 0.0f;
     const bool penalised = r != 1.0f || p != 0.0f || f != 0.0f;
     const bool counted = penalised && a.history, drafts = penalised && a.drafted, biased = a.bias_tokens && a.bias_width > 0;
@@ -195,10 +196,9 @@ adjust_kernel(AdjustArgs args) {
             if (w) {
                 const uint32_t n = w & kCount;
                 if (penalised && (w & (kPrompt | kCount))) {
-                    float q = x * inverse;   // x / r: the product's error goes back in, in one rounding
-                    const float better = __builtin_fmaf(__builtin_fmaf(-q, r, x), inverse, q);
-                    q = __builtin_isfinite(better) ? better : q;
-                    x = x > 0.0f ? q : x * r;
+                    const float y = x * up, q = y * inverse;   // x / r: the product's error goes back in, in one rounding
+                    const float better = __builtin_fmaf(__builtin_fmaf(-q, lifted, y), inverse, q);
+                    x = x > 0.0f ? (__builtin_isfinite(better) ? better : q) : x * r;
                     if (n) x = x - p - f * float(n);
                 }
                 if (w & kBias) x += bias[((w & kBias) >> kBiasShift) - 1];
@@ -264,21 +264,22 @@ extern "C" int nvfp4_adjust_logits(const nvfp4_adjust_t* adjust, void* out, void
     if (adjust->rows == 0 || adjust->seqs == 0) return NVFP4_OK;
     if ((st = nvfp4::device_setup()) != NVFP4_OK) return st;
     AdjustArgs a{*adjust, out, static_cast<int>(adjust->vocab), static_cast<int>((adjust->vocab + kPiece - 1) / kPiece),
-                 static_cast<int>(adjust->seqs), static_cast<int>(adjust->rows), 1};
+                 static_cast<int>(adjust->seqs), static_cast<int>(adjust->rows), 1, 0};
     // units of one row where those are fewer
     const bool single = !adjust->q_starts || adjust->rows <= adjust->rows / kRows + adjust->seqs;
     a.per = single ? 1 : kRows;
     const int64_t units = single ? adjust->rows : adjust->rows / kRows + adjust->seqs;
-    const dim3 grid(static_cast<unsigned>(units * a.pieces)), block(kThreads);
+    const dim3 block(kThreads);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool in32 = adjust->logits_type == NVFP4_LOGITS_F32, out32 = adjust->out_type == NVFP4_LOGITS_F32;
-    if (in32 && out32)
-        hipLaunchKernelGGL((adjust_kernel<float, float>), grid, block, 0, s, a);
-    else if (in32)
-        hipLaunchKernelGGL((adjust_kernel<float, uint16_t>), grid, block, 0, s, a);
-    else if (out32)
-        hipLaunchKernelGGL((adjust_kernel<uint16_t, float>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((adjust_kernel<uint16_t, uint16_t>), grid, block, 0, s, a);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+    const auto kernel = in32 ? (out32 ? adjust_kernel<float, float> : adjust_kernel<float, uint16_t>)
+                             : (out32 ? adjust_kernel<uint16_t, float> : adjust_kernel<uint16_t, uint16_t>);
+    const int64_t most = (int64_t(1) << 31) / kThreads / a.pieces;   // a launch holds fewer than 2^32 threads
+    for (int64_t at = 0; at < units; at += most) {
+        a.unit0 = static_cast<int>(at);
+        const int64_t n = units - at < most ? units - at : most;
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(n * a.pieces)), block, 0, s, a);
+        if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+    }
+    return NVFP4_OK;
 }

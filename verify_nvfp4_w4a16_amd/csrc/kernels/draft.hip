@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kPage = NVFP4_KV_PAGE;
 constexpr int kTreeMax = NVFP4_TREE_MAX;
-constexpr int kScanThreads = 1024;
+constexpr int kScanThreads = nvfp4::kPagesBlock;
 constexpr int kFillThreads = 256, kFillEach = 8;   // tokens of a thread
 // Slots and positions of this many tokens at most are filled by the workgroup
 // that makes the tables, which spares a launch.
@@ -158,7 +158,7 @@ kv_pages_kernel(PagesArgs a, int fill) {
                 a.table[(base + q) * a.table_pitch + need_page[q] + (i - give_from[q])];
         }
         asked += ask.all_x, paged += ask.all_y;
-        given += got_sum.all_x, taken += block_taken, freed = min(freed + got_sum.all_y, room);
+        given += got_sum.all_x, taken += block_taken, freed = static_cast<int>(min(int64_t(freed) + got_sum.all_y, int64_t(room)));
         __syncthreads();
     }
     if (tid == 0) {

@@ -42,6 +42,7 @@ struct TreeArgs {
     int whole;         // nothing is cut
     int ranges;        // that the pages are cut into
     int least;         // pages of a range at least
+    int64_t row0;      // first row of a join
     float v_scale;
 };
 
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(256)
 kv_tree_join_kernel(TreeArgs a) {
     constexpr int kPer = D / 64;
     const int lane = threadIdx.x & 63;
-    const int64_t at = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t at = a.row0 + int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (at >= int64_t(a.v.total) * a.sc.heads) return;
     const int token = static_cast<int>(at / a.sc.heads), head = static_cast<int>(at % a.sc.heads);
     const int s = __builtin_amdgcn_readfirstlane(last_sequence(a.v, [&](int i) { return a.v.start(i) <= token; }));
@@ -484,7 +485,7 @@ bool allow_lds() {
 }
 
 template <int D>
-int launch(const TreeArgs& a, const nvfp4::TreePlan& plan, hipStream_t st) {
+int launch(TreeArgs a, const nvfp4::TreePlan& plan, hipStream_t st) {
     if (a.added) {
         hipLaunchKernelGGL(kv_tree_sums_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
         if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
@@ -494,8 +495,12 @@ int launch(const TreeArgs& a, const nvfp4::TreePlan& plan, hipStream_t st) {
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     if (!plan.whole) {
         const int64_t rows = int64_t(a.v.total) * a.sc.heads;
-        hipLaunchKernelGGL(kv_tree_join_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a);
-        if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+        constexpr int64_t kMost = int64_t(1) << 25;   // rows of a launch, which holds fewer than 2^32 threads
+        for (a.row0 = 0; a.row0 < rows; a.row0 += kMost) {
+            const int64_t n = rows - a.row0 < kMost ? rows - a.row0 : kMost;
+            hipLaunchKernelGGL(kv_tree_join_kernel<D>, dim3(static_cast<unsigned>((n + 3) / 4)), dim3(256), 0, st, a);
+            if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+        }
     }
     return NVFP4_OK;
 }
@@ -521,6 +526,7 @@ int tree_attend(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, cons
     a.ranges = plan.ranges;
     a.least = plan.least;
     a.added = plan.added;
+    a.row0 = 0;
     a.sums = static_cast<int64_t*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + tree_sum_bytes(seqs));
     a.part_ml = a.part_o + int64_t(2) * plan.ranges * plan.rows * cache->head_dim;

@@ -16,7 +16,7 @@ from typing import NamedTuple
 import torch
 
 from . import _check, _lib
-from .serving import _BF16, _F32, _I32, LOGITS_BF16, LOGITS_F32, _Cache, _ints, _new, _out, _Queries, _queries, _room, _Seqs, _seqs, _stream
+from .serving import _BF16, _F32, _I32, LOGITS_BF16, LOGITS_F32, _Cache, _ints, _launch, _new, _out, _Queries, _queries, _room, _Seqs, _seqs
 
 _I64 = torch.int64
 
@@ -120,8 +120,8 @@ def kv_pages(pool, state, table, held, keep, fresh, total: int, *, out: KvStep =
     else:
         for name, t, n in zip(KvStep._fields, out, (2, seqs, seqs, seqs + 1, total, total)):
             _array(name, t, (n,), _I32, dev)
-    _check(_draft().nvfp4_kv_pages(p, out.state.data_ptr(), out.held.data_ptr(), out.kv_lens.data_ptr(), out.q_starts.data_ptr(),
-                                   out.slots.data_ptr(), out.positions.data_ptr(), _stream(stream, dev)), "nvfp4_kv_pages")
+    _launch("nvfp4_kv_pages", _draft().nvfp4_kv_pages, dev, stream, p, out.state.data_ptr(), out.held.data_ptr(),
+            out.kv_lens.data_ptr(), out.q_starts.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr())
     return out
 
 
@@ -143,8 +143,8 @@ def kv_tree(parents, kv_lens, q_starts, max_q: int, *, masks=None, positions=Non
         raise ValueError(f"max_q must be 1..{TREE_MAX}")
     masks = _out("masks", masks, (total, (max_q + 63) // 64), _I64, dev, stream)
     positions = _out("positions", positions, (total,), _I32, dev, stream)
-    _check(_draft().nvfp4_kv_tree(up, lens, starts, seqs, total, max_q, masks.data_ptr(), positions.data_ptr(), _stream(stream, dev)),
-           "nvfp4_kv_tree")
+    _launch("nvfp4_kv_tree", _draft().nvfp4_kv_tree, dev, stream, up, lens, starts, seqs, total, max_q, masks.data_ptr(),
+            positions.data_ptr())
     return masks, positions
 
 
@@ -181,8 +181,8 @@ def kv_tree_attention(q, cache, table, kv_lens, q_starts, masks, positions, max_
         if n.value:
             workspace = _new(n.value, torch.uint8, dev, stream)
     wp, wn = _room(workspace, dev)
-    _check(lib.nvfp4_kv_tree_attention(cache._c, seqs, queries, tree, out.data_ptr(), lse.data_ptr(), wp, wn, _stream(stream, dev)),
-           "nvfp4_kv_tree_attention")
+    _launch("nvfp4_kv_tree_attention", lib.nvfp4_kv_tree_attention, dev, stream, cache._c, seqs, queries, tree, out.data_ptr(),
+            lse.data_ptr(), wp, wn)
     return out, lse
 
 
@@ -260,7 +260,7 @@ def adjust_logits(logits, history=None, history_lens=None, *, prompt_lens=None, 
         a.mask_words = masks.shape[1]
         a.drafted = _array("drafted", drafted, (rows,), _I32, dev)
         a.masks = _array("masks", masks, (rows, a.mask_words), _I64, dev)
-    _check(_draft().nvfp4_adjust_logits(a, out.data_ptr(), _stream(stream, dev)), "nvfp4_adjust_logits")
+    _launch("nvfp4_adjust_logits", _draft().nvfp4_adjust_logits, dev, stream, a, out.data_ptr())
     return out
 
 
@@ -283,10 +283,9 @@ def tree_accept(drafted, parents, chosen, kv_lens, q_starts, max_q: int, *, path
         counts = _out("counts", counts, (seqs,), _I32, dev, stream)
         token = _out("token", token, (seqs,), _I32, dev, stream)
         new_lens = _out("new_lens", new_lens, (seqs,), _I32, dev, stream)
-    _check(_draft().nvfp4_tree_accept(_array("drafted", drafted, (total,), _I32, dev), _ints("parents", parents, 1, dev),
-                                      _array("chosen", chosen, (total,), _I32, dev), lens, starts, seqs, total, max_q,
-                                      path.data_ptr(), counts.data_ptr(), token.data_ptr(), new_lens.data_ptr(), _stream(stream, dev)),
-           "nvfp4_tree_accept")
+    _launch("nvfp4_tree_accept", _draft().nvfp4_tree_accept, dev, stream, _array("drafted", drafted, (total,), _I32, dev),
+            _ints("parents", parents, 1, dev), _array("chosen", chosen, (total,), _I32, dev), lens, starts, seqs, total, max_q,
+            path.data_ptr(), counts.data_ptr(), token.data_ptr(), new_lens.data_ptr())
     return path, counts, token, new_lens
 
 
@@ -305,6 +304,5 @@ def kv_move(caches, table, kv_lens, q_starts, path, *, stream=None) -> None:
     max_q = path.shape[1]
     # no packed tensor is touched, so starts are held to nothing but what any call can have
     seqs = _seqs(first, table, kv_lens, q_starts, 1 << 24)
-    _check(_draft().nvfp4_kv_move((_Cache * len(caches))(*(c._c for c in caches)), len(caches), seqs,
-                                  _array("path", path, (seqs.seqs, max_q), _I32, first.device), max_q, _stream(stream, first.device)),
-           "nvfp4_kv_move")
+    _launch("nvfp4_kv_move", _draft().nvfp4_kv_move, first.device, stream, (_Cache * len(caches))(*(c._c for c in caches)),
+            len(caches), seqs, _array("path", path, (seqs.seqs, max_q), _I32, first.device), max_q)

@@ -21,7 +21,7 @@ import torch
 from . import _check, _lib
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32   # a module's own names are found faster, which a one-token step notices
-_empty, _raw_stream = torch.empty, torch._C._cuda_getCurrentRawStream
+_empty, _raw_stream, _current_device = torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 PAGE = 64
 HEAD_DIMS = (64, 128, 256)
@@ -156,9 +156,19 @@ def _room(workspace, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _stream(stream, device) -> int:
-    # the raw handle at once: torch.cuda.current_stream() would build a Stream object (2 us) first
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+def _launch(name, call, device, stream, *args) -> None:
+    """The library call on `stream`, or on torch's current stream of the tensors' device, with that device current."""
+    if stream is None:
+        handle = _raw_stream(device.index)   # at once: torch.cuda.current_stream() would build a Stream object (2 us) first
+    elif stream.device == device:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"stream must be one of {device}")
+    if device.index == _current_device():
+        _check(call(*args, handle), name)
+    else:   # the library launches on the current device, whose default stream has the same handle 0
+        with torch.cuda.device(device):
+            _check(call(*args, handle), name)
 
 
 def kv_append(cache: KvCache, k, v, table, kv_lens, q_starts, stream=None) -> None:
@@ -167,9 +177,8 @@ def kv_append(cache: KvCache, k, v, table, kv_lens, q_starts, stream=None) -> No
     seqs = _seqs(cache, table, kv_lens, q_starts, k.shape[0])
     if v.shape[0] != k.shape[0]:
         raise ValueError("k and v must hold the same tokens")
-    _check(_kv().nvfp4_kv_append(cache._c, seqs, *_rows("k", k, cache, cache.kv_heads),
-                                 *_rows("v", v, cache, cache.kv_heads), _stream(stream, cache.device)),
-           "nvfp4_kv_append")
+    _launch("nvfp4_kv_append", _kv().nvfp4_kv_append, cache.device, stream, cache._c, seqs,
+            *_rows("k", k, cache, cache.kv_heads), *_rows("v", v, cache, cache.kv_heads))
 
 
 def kv_read(cache: KvCache, table, kv_lens, q_starts, total: int, k=None, v=None, stream=None):
@@ -179,8 +188,7 @@ def kv_read(cache: KvCache, table, kv_lens, q_starts, total: int, k=None, v=None
     k = _out("k", k, shape, _BF16, cache.device, stream)
     v = _out("v", v, shape, _BF16, cache.device, stream)
     seqs = _seqs(cache, table, kv_lens, q_starts, total)
-    _check(_kv().nvfp4_kv_read(cache._c, seqs, k.data_ptr(), v.data_ptr(), _stream(stream, cache.device)),
-           "nvfp4_kv_read")
+    _launch("nvfp4_kv_read", _kv().nvfp4_kv_read, cache.device, stream, cache._c, seqs, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -220,8 +228,8 @@ def kv_attention(q, cache: KvCache, table, kv_lens, q_starts, max_q: int, max_kv
         if n.value:
             workspace = _new(n.value, torch.uint8, dev, stream)
     wp, wn = _room(workspace, dev)
-    _check(lib.nvfp4_kv_attention(cache._c, seqs, queries, out.data_ptr(), lse.data_ptr(), wp, wn, _stream(stream, dev)),
-           "nvfp4_kv_attention")
+    _launch("nvfp4_kv_attention", lib.nvfp4_kv_attention, dev, stream, cache._c, seqs, queries, out.data_ptr(), lse.data_ptr(),
+            wp, wn)
     return out, lse
 
 
@@ -238,8 +246,8 @@ def kv_weights(q, lse, cache: KvCache, table, kv_lens, q_starts, max_q: int, max
     if prior is not None:
         _out("prior", prior, shape, _F32, dev)
     _out("lse", lse, q.shape[:2], _F32, dev)
-    _check(_kv().nvfp4_kv_weights(cache._c, seqs, queries, lse.data_ptr(), 0 if prior is None else prior.data_ptr(),
-                                  out.data_ptr(), _stream(stream, dev)), "nvfp4_kv_weights")
+    _launch("nvfp4_kv_weights", _kv().nvfp4_kv_weights, dev, stream, cache._c, seqs, queries, lse.data_ptr(),
+            0 if prior is None else prior.data_ptr(), out.data_ptr())
     return out
 
 
@@ -265,9 +273,8 @@ def kv_evict(weights, cache: KvCache, table, kv_lens, dst_table, keep: int, *, s
     kept = _out("kept", kept, shape, _I32, dev, stream)
     kept_weights = _out("kept_weights", kept_weights, shape, _F32, dev, stream)
     new_lens = _out("new_lens", new_lens, shape[:1], _I32, dev, stream)
-    _check(_kv().nvfp4_kv_evict(cache._c, seqs, weights.data_ptr(), weights.shape[2], keep, sink, recent, dst._c, dst_ptr,
-                                dst_table.shape[1], kept.data_ptr(), kept_weights.data_ptr(), new_lens.data_ptr(),
-                                _stream(stream, dev)), "nvfp4_kv_evict")
+    _launch("nvfp4_kv_evict", _kv().nvfp4_kv_evict, dev, stream, cache._c, seqs, weights.data_ptr(), weights.shape[2], keep,
+            sink, recent, dst._c, dst_ptr, dst_table.shape[1], kept.data_ptr(), kept_weights.data_ptr(), new_lens.data_ptr())
     return kept, kept_weights, new_lens
 
 
@@ -297,11 +304,9 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, *, t
     if workspace is None and n.value:
         workspace = _new(n.value, torch.uint8, dev, stream)
     wp, wn = _room(workspace, dev)
-    _check(lib.nvfp4_sample(logits.data_ptr(), LOGITS_F32 if f32 else LOGITS_BF16, rows, vocab,
-                            logits.stride(0) if rows > 1 else vocab, _param("u", u, rows, _F32, dev),
-                            _param("temperature", temperature, rows, _F32, dev),
-                            _param("top_k", top_k, rows, _I32, dev),
-                            _param("top_p", top_p, rows, _F32, dev),
-                            _param("min_p", min_p, rows, _F32, dev),
-                            token.data_ptr(), logprob.data_ptr(), wp, wn, _stream(stream, dev)), "nvfp4_sample")
+    _launch("nvfp4_sample", lib.nvfp4_sample, dev, stream, logits.data_ptr(), LOGITS_F32 if f32 else LOGITS_BF16, rows, vocab,
+            logits.stride(0) if rows > 1 else vocab, _param("u", u, rows, _F32, dev),
+            _param("temperature", temperature, rows, _F32, dev), _param("top_k", top_k, rows, _I32, dev),
+            _param("top_p", top_p, rows, _F32, dev), _param("min_p", min_p, rows, _F32, dev), token.data_ptr(),
+            logprob.data_ptr(), wp, wn)
     return token, logprob
