@@ -42,7 +42,7 @@ struct TreeArgs {
     int whole;         // nothing is cut
     int ranges;        // that the pages are cut into
     int least;         // pages of a range at least
-    int64_t row0;      // first row of a join
+    int64_t block0;    // first rows of a join, kJoinRows each
     float v_scale;
 };
 
@@ -300,8 +300,8 @@ kv_tree_tile_kernel(TreeArgs a) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) p[i] = z[i];
                 // What is rare comes apart, and works out anew which row it is: kept, that would take 30 registers.
-                if (a.sc.cap != 0.0f || base < span.lo_all || base + kPage > span.hi_all) {
-                    if (a.sc.cap != 0.0f) a.sc.shape(p, to_log2);
+                if (a.sc.cap != 0.0f) a.sc.shape(p, to_log2);
+                if (base < span.lo_all || base + kPage > span.hi_all) {
                     int r = my0 + n;
                     asm volatile("" : "+v"(r));
                     const QueryRow who = rows.row(a.sc, r);
@@ -424,51 +424,66 @@ kv_tree_tile_kernel(TreeArgs a) {
     }
 }
 
-// Joins the parts of a row, a wavefront a row.
+// Joins the parts of a row.  A wavefront takes four query heads of a token, 16
+// lanes each: it waits for the token's sequence, for the parts' maxima and for the parts
+// whatever it joins, so four rows' take little longer than one's (a wavefront a row took 11.9 us
+// behind 32 trees of 9 .. 16 nodes x 32 heads, four of 200 .. 255 x 32 heads 23; this takes 9.1 and 13.5).
+constexpr int kJoinRows = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256)
 kv_tree_join_kernel(TreeArgs a) {
-    constexpr int kPer = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int64_t at = a.row0 + int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (at >= int64_t(a.v.total) * a.sc.heads) return;
-    const int token = static_cast<int>(at / a.sc.heads), head = static_cast<int>(at % a.sc.heads);
+    constexpr int kLanes = 64 / kJoinRows, kPer = D / kLanes;
+    const int lane = threadIdx.x & 63, me = lane % kLanes;
+    const int64_t at = a.block0 + int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int blocks = (a.sc.heads + kJoinRows - 1) / kJoinRows;   // of a token
+    if (at >= int64_t(a.v.total) * blocks) return;
+    const int token = static_cast<int>(at / blocks), head = static_cast<int>(at % blocks) * kJoinRows + lane / kLanes;
     const int s = __builtin_amdgcn_readfirstlane(last_sequence(a.v, [&](int i) { return a.v.start(i) <= token; }));
     if (s < 0) return;
     const int64_t all = a.sums[2 * a.v.seqs + 1], before = a.sums[2 * s + 1];
     const TreeRows rows(a.v, a.sc, s);
-    const int r = nvfp4::kv_row_of(token, rows.first_token, rows.group, head % rows.group, rows.count);
-    if (r < 0) return;   // no sequence's row
+    const int hk = a.sc.over_group(min(head, a.sc.heads - 1));
+    const int r = nvfp4::kv_row_of(token, rows.first_token, rows.group, head - hk * rows.group, rows.count);
+    if (head >= a.sc.heads || r < 0) return;   // no sequence's row
     int page0;
     const int pages = pages_of(a, rows, &page0);
-    const int64_t each = range_of(a, all);
-    const int64_t begin = before + int64_t(r / a.rows * a.v.kv_heads + head / rows.group) * (kStart + pages) + kStart;
-    const int first = static_cast<int>(begin / each), last = static_cast<int>((begin + pages - 1) / each);
+    // which range a page is in: whole ranges before the sequence, and then few enough for a product in fp32 to be at most one off
+    const int64_t each = range_of(a, all), front = before / each, rest = before - front * each;
+    const float inverse = 1.0f / float(each);
+    auto range = [&](int64_t page) {
+        int n = static_cast<int>(float(page) * inverse);
+        const int64_t over = page - n * each;
+        n += over >= each ? 1 : over < 0 ? -1 : 0;
+        return static_cast<int>(front) + n;
+    };
+    const int64_t begin = rest + int64_t(r / a.rows * a.v.kv_heads + hk) * (kStart + pages) + kStart;
+    const int first = range(begin), last = range(begin + pages - 1);
     if (first == last) return;   // written already
     auto part = [&](int w) { return (2 * int64_t(w) + (w == first)) * a.rows + r % a.rows; };
     float top = -INFINITY;
-    for (int w = first + lane; w <= last; w += 64) top = fmaxf(top, a.part_ml[part(w) * 2]);
+    for (int w = first + me; w <= last; w += kLanes) top = fmaxf(top, a.part_ml[part(w) * 2]);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     float acc[kPer] = {}, sum = 0.0f;
-#pragma unroll 4
+#pragma unroll 2
     for (int w = first; w <= last; ++w) {
         const int64_t p = part(w);
         const float m = a.part_ml[p * 2], l = a.part_ml[p * 2 + 1];
         const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
         sum += m == -INFINITY ? 0.0f : f * l;
+        float x[kPer];   // not written where the part saw nothing
+        __builtin_memcpy(x, __builtin_assume_aligned(a.part_o + p * D + me * kPer, 16), sizeof x);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float x = a.part_o[p * D + lane * kPer + i];   // not written where the part saw nothing
-            acc[i] += m == -INFINITY ? 0.0f : f * x;
-        }
+        for (int i = 0; i < kPer; ++i) acc[i] += m == -INFINITY ? 0.0f : f * x[i];
     }
     const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;   // V's scale apart: their quotient may be too small for fp32
     uint16_t w[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) w[i] = f32_to_bf16_rne(acc[i] * f * a.v_scale);
-    __builtin_memcpy(__builtin_assume_aligned(a.out + at * D + lane * kPer, 2 * kPer), w, sizeof w);
-    if (a.lse && lane == 0) a.lse[at] = (top + log2f(sum)) * kLn2;
+    const int64_t row = int64_t(token) * a.sc.heads + head;
+    __builtin_memcpy(__builtin_assume_aligned(a.out + row * D + me * kPer, 2 * kPer > 16 ? 16 : 2 * kPer), w, sizeof w);
+    if (a.lse && me == 0) a.lse[row] = (top + log2f(sum)) * kLn2;
 }
 
 template <int D>
@@ -494,10 +509,10 @@ int launch(TreeArgs a, const nvfp4::TreePlan& plan, hipStream_t st) {
                        tile_lds<D>(), st, a);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     if (!plan.whole) {
-        const int64_t rows = int64_t(a.v.total) * a.sc.heads;
-        constexpr int64_t kMost = int64_t(1) << 25;   // rows of a launch, which holds fewer than 2^32 threads
-        for (a.row0 = 0; a.row0 < rows; a.row0 += kMost) {
-            const int64_t n = rows - a.row0 < kMost ? rows - a.row0 : kMost;
+        const int64_t blocks = int64_t(a.v.total) * ((a.sc.heads + kJoinRows - 1) / kJoinRows);
+        constexpr int64_t kMost = int64_t(1) << 23;   // of a launch, which holds fewer than 2^32 threads
+        for (a.block0 = 0; a.block0 < blocks; a.block0 += kMost) {
+            const int64_t n = blocks - a.block0 < kMost ? blocks - a.block0 : kMost;
             hipLaunchKernelGGL(kv_tree_join_kernel<D>, dim3(static_cast<unsigned>((n + 3) / 4)), dim3(256), 0, st, a);
             if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
         }
@@ -526,7 +541,7 @@ int tree_attend(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, cons
     a.ranges = plan.ranges;
     a.least = plan.least;
     a.added = plan.added;
-    a.row0 = 0;
+    a.block0 = 0;
     a.sums = static_cast<int64_t*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + tree_sum_bytes(seqs));
     a.part_ml = a.part_o + int64_t(2) * plan.ranges * plan.rows * cache->head_dim;
