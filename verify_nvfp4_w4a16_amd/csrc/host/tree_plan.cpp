@@ -15,12 +15,13 @@ TreePlan tree_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nv
     const int64_t slots = window > 0 ? std::min(q->max_kv, window + q->max_q) : q->max_kv;
     const int64_t pages = std::max<int64_t>((slots + NVFP4_KV_PAGE - 1) / NVFP4_KV_PAGE + (window > 0), 1);
     // 16-row workgroups decode every page for themselves, but start at once and need no second launch where
-    // a sequence has few pages; 64 or 128 rows that share the decoding pay from many pages x rows on.  One tree of 16 x 4
-    // rows, 8 heads of 128, over 901 slots: 10 us and 30; 16 of 64 x 4 over 1000: 45 and 71; 32 of 9 .. 16 x 4 over
-    // 1000 .. 16000: 155 and 108; 4 of 200 .. 255 x 4 over 20000 .. 65000: 1132 and 700; at D = 256, 16 of 64 x 2 over
-    // 1500: 84 and 86.
+    // a sequence has few pages; 64 or 128 rows that share the decoding pay from so many (16 rows, page) on, whatever the
+    // dims.  16-row workgroups | tiles, us, 8 heads: D = 64, 16 trees of 64 x 2 rows over 1000 slots (16384 such) 16 | 32, over
+    // 3000 (48128) 66 | 43; D = 128, 32 of 9 x 4 over 3000 (36096) 60 | 59, 16 of 64 x 2 over 1000 24 | 44, over 3000 84 | 61;
+    // D = 256, 4 of 64 x 2 over 10000 (40192) 95 | 93, 16 over 1000 45 | 65, over 3000 134 | 109.  At D = 256 a CU holds one tile, and
+    // three 16-row workgroups are quicker at any length: 32 of 9 x 4 rows over 3000 101 | 115, over 10000 277 | 338.
     const int64_t groups = std::min(s->seqs * c->kv_heads, int64_t(1) << 24), work = groups * std::min((rows + 15) / 16 * pages, int64_t(1) << 24);
-    if (rows <= 32 || work < kTreeWork / c->head_dim) return p;
+    if (rows <= (c->head_dim == 256 ? 48 : 32) || work < kTreeWork) return p;
     p.rows = rows <= 64 ? 64 : 128;
     const int64_t segments = std::max<int64_t>(s->seqs * c->kv_heads * ((rows + p.rows - 1) / p.rows), 1);
     p.least = 4;

@@ -9,7 +9,7 @@
 namespace nvfp4 {
 
 constexpr int kTreeWaves = 4;
-constexpr int64_t kTreeWork = int64_t(1) << 23;   // 16-row tiles x pages x dims from which tiles of 64 and 128 rows pay
+constexpr int64_t kTreeWork = 36 * 1024;   // 16 rows x pages from which tiles of 64 and 128 rows pay
 constexpr int kTreeLanes = 64;   // sequences whose pages a wavefront adds up by itself
 
 struct TreePlan {
