@@ -55,110 +55,164 @@ __device__ __forceinline__ void fill_token(const PagesArgs& a, int t, int first,
     if (a.positions) a.positions[t] = where;
 }
 
-// Exclusive sums of x and y over the threads of the workgroup, and the totals.
-template <class T>
-struct Scanned {
-    T x, y, all_x, all_y;
+// v of the lane that a data-parallel move names, 0 where there is none or its row (16 lanes) is not among ROWS.
+template <int CONTROL, int ROWS = 0xf>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+    return __builtin_amdgcn_update_dpp(0u, v, CONTROL, ROWS, 0xf, false);
+}
+
+// op over the lanes up to this one, of its row and of the wavefront, for which 0 changes nothing.
+template <class Op>
+__device__ __forceinline__ uint32_t row_scan(uint32_t v, Op op) {
+    v = op(v, moved<0x111>(v));   // from 1, 2, 4 and 8 lanes before
+    v = op(v, moved<0x112>(v));
+    v = op(v, moved<0x114>(v));
+    return op(v, moved<0x118>(v));
+}
+template <class Op>
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, Op op) {
+    v = row_scan(v, op);
+    v = op(v, moved<0x142, 0xa>(v));      // the last lane of rows 0 and 2, to the rows after
+    return op(v, moved<0x143, 0xc>(v));   // lane 31, to the second half
+}
+
+// The same over the threads of the workgroup, N values at a time, with the whole and what lies in the wavefronts before.  Through lanes' moves and one
+// barrier: with shuffles, which go through LDS, three such scans were half of the 7 us of a step of 48 sequences.
+constexpr int kScanWaves = kScanThreads / 64;
+
+template <int N, class Op>
+__device__ __forceinline__ void group_scan(uint32_t (&v)[N], uint32_t (&all)[N], uint32_t (&front)[N], uint32_t (&tmp)[kScanWaves][N], Op op) {
+    static_assert(kScanWaves == 16);   // a row
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        v[k] = wave_scan(v[k], op);
+        if (lane == 63) tmp[wave][k] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const uint32_t waves = row_scan(tmp[lane & 15][k], op);
+        all[k] = __builtin_amdgcn_readlane(waves, 15);
+        front[k] = wave > 0 ? __builtin_amdgcn_readlane(waves, wave - 1) : 0;
+        v[k] = op(v[k], front[k]);
+    }
+}
+
+// Pages that are given out or come back are found a chunk at a time: each
+// sequence marks the first of its own in the chunk, and the largest mark up to a
+// page is its sequence (a search for each of 6500 pages kept LDS busy for 8 us).
+constexpr int kEach = 4, kChunk = kEach * kScanThreads;   // pages of a thread, one after the other
+
+struct Marks {
+    uint32_t at[kChunk];
+    uint32_t tmp[kScanWaves][1];
 };
 
-template <class T>
-__device__ __forceinline__ Scanned<T> scan(T x, T y, T (&tmp)[kScanThreads / 64][2], int waves) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    T sx = x, sy = y;
+// The sequences (threads of the block) of pages at + 4 tid .., of which a thread has `own` pages from `from` on.
+__device__ __forceinline__ void owners(Marks& m, int at, int from, int own, int (&whose)[kEach]) {
+    const int tid = threadIdx.x;
+    *reinterpret_cast<uint4*>(m.at + kEach * tid) = uint4{0, 0, 0, 0};
+    __syncthreads();
+    if (own > 0 && from < at + kChunk && from + own > at) m.at[max(from - at, 0)] = tid + 1;
+    __syncthreads();
+    uint32_t mine[kEach], last[1], all[1], front[1];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const T ux = __shfl_up(sx, d), uy = __shfl_up(sy, d);
-        if (lane >= d) sx += ux, sy += uy;
-    }
-    __syncthreads();
-    if (lane == 63) tmp[wave][0] = sx, tmp[wave][1] = sy;
-    __syncthreads();
-    Scanned<T> r{sx - x, sy - y, 0, 0};
-#pragma unroll 1
-    for (int w = 0; w < waves; ++w) {   // the ones that have anything
-        if (w < wave) r.x += tmp[w][0], r.y += tmp[w][1];
-        r.all_x += tmp[w][0], r.all_y += tmp[w][1];
-    }
-    return r;
+    for (int x = 0; x < kEach; ++x) mine[x] = x ? max(m.at[kEach * tid + x], mine[x - 1]) : m.at[kEach * tid];
+    last[0] = mine[kEach - 1];
+    group_scan(last, all, front, m.tmp, [](uint32_t x, uint32_t y) { return max(x, y); });
+    const uint32_t before = max(moved<0x138>(last[0]), front[0]);   // up to the lane before
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) whose[x] = static_cast<int>(max(mine[x], before)) - 1;
 }
 
 // One workgroup takes the sequences 1024 at a time.  Whether a sequence is
 // granted depends on what those before it ask for, not on what they get, so
-// two sums over the sequences settle a block of them: of what is asked, then
+// two scans over the sequences settle a block of them: of what is asked, then
 // of what is given.  Pages are given out from entries of the ring before
 // `count` and come back to entries from there on, so neither waits for the
 // other and their order is fixed.
 __global__ void __launch_bounds__(kScanThreads)
 kv_pages_kernel(PagesArgs a, int fill) {
-    __shared__ int64_t wide[kScanThreads / 64][2];
-    __shared__ int narrow[kScanThreads / 64][2];
-    __shared__ int give_from[kScanThreads];                                    // pages that go back before each sequence's
-    __shared__ int whose[kScanThreads], take_from[kScanThreads];               // those that take pages, and the pages before them
-    __shared__ int first_page[kScanThreads], need_page[kScanThreads];          // a sequence's pages held and needed
+    __shared__ uint32_t tmp_ask[kScanWaves][2], tmp_got[kScanWaves][3];
+    __shared__ Marks marks;
+    __shared__ int take_from[kScanThreads], give_from[kScanThreads];     // pages that are taken and given before each sequence's
+    __shared__ int first_page[kScanThreads], need_page[kScanThreads];    // a sequence's pages held and needed
     const int tid = threadIdx.x;
     const int h0 = a.state[0] % a.capacity, head = h0 < 0 ? h0 + a.capacity : h0;
     const int count = min(max(a.state[1], 0), a.capacity), room = a.capacity - count;
+    // Sums of what is asked are held at one more than there is: what is beyond it is not granted, however far.
+    const uint32_t over = uint32_t(max(a.total, count)) + 1;
+    const auto plus = [](uint32_t x, uint32_t y) { return x + y; };
+    const auto plus_held = [=](uint32_t x, uint32_t y) { return min(x + y, over); };
     __syncthreads();                // state_out may be state
-    int64_t asked = 0, paged = 0;   // tokens and pages that the sequences before this block ask for
+    uint32_t asked = 0, paged = 0;   // tokens and pages that the sequences before this block ask for
     int given = 0, taken = 0, freed = 0;
     for (int base = 0; base < a.seqs; base += kScanThreads) {
-        const int s = base + tid, waves = (min(a.seqs - base, kScanThreads) + 63) / 64;
+        const int s = base + tid;
         const bool here = s < a.seqs;
         int held = 0, keep = 0;
-        int64_t fresh = 0, want = 0, need = 0, extra = 0;
+        int64_t fresh = 0, need = 0, extra = 0;
         bool fits = false;
         if (here) {
             held = static_cast<int>(min(int64_t(max(a.held[s], 0)), a.table_pitch));
             keep = min(max(a.keep[s], 0), held * kPage);
             fresh = max(a.fresh[s], 0);
-            want = keep + fresh;
-            need = (want + kPage - 1) / kPage;
+            need = (keep + fresh + kPage - 1) / kPage;
             fits = need <= a.table_pitch;
             extra = fits && need > held ? need - held : 0;
         }
-        const Scanned<int64_t> ask = scan<int64_t>(fits ? fresh : 0, extra, wide, waves);
-        const bool granted = fits && (extra == 0 || paged + ask.y + extra <= count) &&
-                             (fresh == 0 || asked + ask.x + fresh <= a.total);
+        uint32_t ask[2] = {fits ? static_cast<uint32_t>(min(fresh, int64_t(over))) : 0, static_cast<uint32_t>(min(extra, int64_t(over)))};
+        uint32_t all_ask[2], front_ask[2];
+        group_scan(ask, all_ask, front_ask, tmp_ask, plus_held);
+        const bool granted = fits && (extra == 0 || plus_held(paged, ask[1]) <= uint32_t(count)) &&
+                             (fresh == 0 || plus_held(asked, ask[0]) <= uint32_t(a.total));
         const int got = granted ? static_cast<int>(fresh) : 0;
         const int after = granted ? static_cast<int>(need) : held;
         const int take = max(after - held, 0), give = max(held - after, 0);
-        const Scanned<int> got_sum = scan<int>(got, give, narrow, waves);
+        uint32_t sum[3] = {uint32_t(got), uint32_t(take), uint32_t(give)}, all[3], front[3];
+        group_scan(sum, all, front, tmp_got, plus);
+        const int my_take = static_cast<int>(sum[1]) - take, my_give = static_cast<int>(sum[2]) - give;
         if (here) {
             a.held_out[s] = after;
             a.kv_lens[s] = keep + got;
-            a.q_starts[s] = given + got_sum.x;
+            a.q_starts[s] = given + static_cast<int>(sum[0]) - got;
         }
-        // pages one a thread, whichever sequence they are of
-        give_from[tid] = got_sum.y;
+        take_from[tid] = my_take;
+        give_from[tid] = my_give;
         first_page[tid] = held;
         need_page[tid] = after;
-        const int takes = __syncthreads_count(take > 0);
-        int block_taken = 0;
-        if (takes) {
-            // the ones that take, in order, at the front: their numbers ascend
-            const Scanned<int> at = scan<int>(take > 0, take, narrow, waves);
-            if (take > 0) {
-                whose[at.x] = tid;
-                take_from[at.x] = at.y;
+        const int takes = static_cast<int>(all[1]), gives = min(static_cast<int>(all[2]), room - freed);
+        for (int at = 0; at < takes; at += kChunk) {
+            int q[kEach], page[kEach];
+#pragma unroll
+            for (int x = 0; x < kEach; ++x) {
+                const int64_t from = int64_t(head) + taken + min(at + kEach * tid + x, takes - 1);
+                page[x] = a.pool[from >= a.capacity ? from - a.capacity : from];
             }
-            block_taken = at.all_y;
-            __syncthreads();
-            for (int i = tid; i < block_taken; i += kScanThreads) {
-                const int w = last_at_most(take_from, 0, takes - 1, i), q = whose[w];
-                const int64_t from = int64_t(head) + taken + i;
-                a.table[(base + q) * a.table_pitch + first_page[q] + (i - take_from[w])] =
-                    a.pool[from >= a.capacity ? from - a.capacity : from];
+            owners(marks, at, my_take, take, q);
+#pragma unroll
+            for (int x = 0; x < kEach; ++x) {
+                const int i = at + kEach * tid + x;
+                if (i < takes) a.table[(base + q[x]) * a.table_pitch + first_page[q[x]] + (i - take_from[q[x]])] = page[x];
             }
         }
-        for (int i = tid; i < got_sum.all_y; i += kScanThreads) {
-            if (freed + i >= room) break;
-            const int q = last_at_most(give_from, 0, kScanThreads - 1, i);
-            const int64_t to = int64_t(head) + count + freed + i;
-            a.pool[to >= a.capacity ? to - a.capacity : to] =
-                a.table[(base + q) * a.table_pitch + need_page[q] + (i - give_from[q])];
+        for (int at = 0; at < gives; at += kChunk) {
+            int q[kEach], page[kEach];
+            owners(marks, at, my_give, give, q);
+#pragma unroll
+            for (int x = 0; x < kEach; ++x) {
+                const int i = at + kEach * tid + x;
+                if (i < gives) page[x] = a.table[(base + q[x]) * a.table_pitch + need_page[q[x]] + (i - give_from[q[x]])];
+            }
+#pragma unroll
+            for (int x = 0; x < kEach; ++x) {
+                const int64_t to = int64_t(head) + count + freed + at + kEach * tid + x;
+                if (at + kEach * tid + x < gives) a.pool[to >= a.capacity ? to - a.capacity : to] = page[x];
+            }
         }
-        asked += ask.all_x, paged += ask.all_y;
-        given += got_sum.all_x, taken += block_taken, freed = static_cast<int>(min(int64_t(freed) + got_sum.all_y, int64_t(room)));
+        asked = plus_held(asked, all_ask[0]), paged = plus_held(paged, all_ask[1]);
+        given += static_cast<int>(all[0]), taken += takes, freed += gives;
         __syncthreads();
     }
     if (tid == 0) {
@@ -172,6 +226,18 @@ kv_pages_kernel(PagesArgs a, int fill) {
     for (int t = tid; t < a.total; t += kScanThreads) fill_token(a, t, 0, max(a.seqs - 1, 0), given);
 }
 
+// The last sequence that begins at token t or before it, by a wavefront: two steps for 4096 sequences, where halves take twelve loads
+// one after the other.
+__device__ __forceinline__ int last_start(const PagesArgs& a, int t) {
+    const int lane = threadIdx.x & 63;
+    int s = 0;
+    for (int step = a.seqs > 4096 ? 4096 : 64;; step /= 64) {
+        const int i = s + lane * step;
+        s += (__popcll(__ballot(i < a.seqs && a.q_starts[min(i, a.seqs)] <= t)) - 1) * step;
+        if (step == 1) return s;
+    }
+}
+
 // Slots and positions of many tokens, once the tables are made.
 __global__ void __launch_bounds__(kFillThreads)
 kv_slots_kernel(PagesArgs a) {
@@ -179,8 +245,8 @@ kv_slots_kernel(PagesArgs a) {
     const int tokens = a.q_starts[a.seqs];
     int first = 0, last = 0;
     if (t0 < tokens && a.seqs > 0) {   // the sequences that the workgroup's tokens are of
-        first = last_at_most(a.q_starts, 0, a.seqs - 1, t0);
-        last = last_at_most(a.q_starts, first, a.seqs - 1, end - 1);
+        first = last_start(a, t0);
+        last = last_start(a, end - 1);
     }
 #pragma unroll
     for (int i = 0; i < kFillEach; ++i) {
