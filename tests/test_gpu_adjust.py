@@ -258,3 +258,14 @@ def test_more_logits_than_a_launch_takes():
         assert logits[row, at].tolist() == [1.0 + row % 128, -3.0]
     del logits
     torch.cuda.empty_cache()
+
+
+def test_repetition_is_a_rounded_quotient():
+    g = workload.rng(31)
+    rows, vocab = 64, 20000
+    x = (g.standard_normal((rows, vocab)) * 8).astype(np.float32)
+    r = g.uniform(0.5, 2.0, rows).astype(np.float32)
+    r[:3] = [1.1, 1.0 + 2.0 ** -23, 2.0 - 2.0 ** -23]
+    said = int32(np.tile(np.arange(vocab), (rows, 1)))
+    out = nv.adjust_logits(_f32(x), said, int32([vocab] * rows), repetition=_f32(r)).cpu().numpy()
+    assert np.array_equal(out, np.where(x > 0, x / r[:, None], x * r[:, None]))

@@ -196,9 +196,12 @@ adjust_kernel(AdjustArgs args) {
             if (w) {
                 const uint32_t n = w & kCount;
                 if (penalised && (w & (kPrompt | kCount))) {
-                    const float y = x * up, q = y * inverse;   // x / r: the product's error goes back in, in one rounding
-                    const float better = __builtin_fmaf(__builtin_fmaf(-q, lifted, y), inverse, q);
-                    x = x > 0.0f ? (__builtin_isfinite(better) ? better : q) : x * r;
+                    // x / r, correctly rounded: the product is within two steps, corrected by its remainder within one,
+                    // and from there a remainder settles it (1 / r is rounded correctly itself)
+                    const float y = x * up, q = y * inverse;
+                    float best = __builtin_fmaf(__builtin_fmaf(-q, lifted, y), inverse, q);
+                    best = __builtin_fmaf(__builtin_fmaf(-best, lifted, y), inverse, best);
+                    x = x > 0.0f ? (__builtin_isfinite(best) ? best : q) : x * r;
                     if (n) x = x - p - f * float(n);
                 }
                 if (w & kBias) x += bias[((w & kBias) >> kBiasShift) - 1];
