@@ -365,8 +365,9 @@ def test_windows_in_tiles_of_many_rows(d, window, softcap):
     assert np.isfinite(out).all() and np.isfinite(lse).all()
 
 
-def test_more_rows_than_a_launch_of_the_join_takes():
-    # 4096 trees over the same short cache, then one over a long one, whose rows are those from 2^25 on
+def test_more_rows_than_32_bits_of_threads():
+    # 4096 trees over the same short cache, then one over a long one, whose rows are those from 2^25 on (a wavefront each
+    # would be more threads than a launch has)
     lens, nodes, heads, many = [130, 8000], 128, 64, 4096
     c = Paged(lens, 1, 64, 41, v_scale=0.5)
     masks, _ = _of_trees(workload.rng(42), lens, [nodes, nodes])

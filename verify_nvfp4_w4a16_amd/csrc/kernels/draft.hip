@@ -17,7 +17,8 @@ constexpr int kTreeMax = NVFP4_TREE_MAX;
 constexpr int kScanThreads = nvfp4::kPagesBlock;
 constexpr int kFillThreads = 256, kFillEach = 8;   // tokens of a thread
 // Slots and positions of this many tokens at most are filled by the workgroup
-// that makes the tables, which spares a launch.
+// that makes the tables, which spares a launch: 64 sequences of 16 tokens 5.6 us and 7.8 by a kernel of their own, of
+// 64 tokens 9.5 and 9.0 (and 3 us of the host), of 128 tokens 15 and 8.6.
 constexpr int kFillInline = 4096;
 
 struct PagesArgs {

@@ -42,7 +42,6 @@ struct TreeArgs {
     int whole;         // nothing is cut
     int ranges;        // that the pages are cut into
     int least;         // pages of a range at least
-    int64_t block0;    // first rows of a join, kJoinRows each
     float v_scale;
 };
 
@@ -123,10 +122,15 @@ struct Cut {
     __device__ __forceinline__ int sequence(const TreeArgs& a, int64_t at) const {
         const int lane = threadIdx.x & 63;
         if (!a.added) return __popcll(__ballot(lane < a.v.seqs && (a.whole ? mine.segments : mine.pages) <= at)) - 1;
+        return find(a, at, a.whole ? 0 : 1);
+    }
+    // The same by what a kernel left, of segments (0) or pages (1).
+    static __device__ __forceinline__ int find(const TreeArgs& a, int64_t at, int which) {
+        const int lane = threadIdx.x & 63;
         int s = 0;
-        for (int step = a.v.seqs > 4096 ? 4096 : 64;; step /= 64) {
+        for (int step = a.v.seqs > 4096 ? 4096 : a.v.seqs > 64 ? 64 : 1;; step /= 64) {
             const int i = s + lane * step;
-            s += (__popcll(__ballot(i < a.v.seqs && a.sums[2 * min(i, a.v.seqs) + (a.whole ? 0 : 1)] <= at)) - 1) * step;
+            s += (__popcll(__ballot(i < a.v.seqs && a.sums[2 * min(i, a.v.seqs) + which] <= at)) - 1) * step;
             if (step == 1) return s;
         }
     }
@@ -424,43 +428,35 @@ kv_tree_tile_kernel(TreeArgs a) {
     }
 }
 
-// Joins the parts of a row.  A wavefront takes four query heads of a token, 16
-// lanes each: it waits for the token's sequence, for the parts' maxima and for the parts
-// whatever it joins, so four rows' take little longer than one's (a wavefront a row took 11.9 us
-// behind 32 trees of 9 .. 16 nodes x 32 heads, four of 200 .. 255 x 32 heads 23; this takes 9.1 and 13.5).
-constexpr int kJoinRows = 4;
+// Joins the parts of the segments that ranges cut: a workgroup takes the segment that the beginning of its range cuts, if
+// it is the first to cut it, and 16 of its rows, 16 lanes a row.  So it takes as long as the cuts, not
+// the rows, ask for: 8.9 us behind 32 trees of 9 .. 16 nodes x 32 heads, latency (a wavefront for each four rows
+// of all 9.1; but behind 600 trees of 16 nodes over 300 slots, 214 us in all and now 179).
+constexpr int kJoinRows = 16;
 
 template <int D>
 __global__ void __launch_bounds__(256)
 kv_tree_join_kernel(TreeArgs a) {
-    constexpr int kLanes = 64 / kJoinRows, kPer = D / kLanes;
-    const int lane = threadIdx.x & 63, me = lane % kLanes;
-    const int64_t at = a.block0 + int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int blocks = (a.sc.heads + kJoinRows - 1) / kJoinRows;   // of a token
-    if (at >= int64_t(a.v.total) * blocks) return;
-    const int token = static_cast<int>(at / blocks), head = static_cast<int>(at % blocks) * kJoinRows + lane / kLanes;
-    const int s = __builtin_amdgcn_readfirstlane(last_sequence(a.v, [&](int i) { return a.v.start(i) <= token; }));
-    if (s < 0) return;
-    const int64_t all = a.sums[2 * a.v.seqs + 1], before = a.sums[2 * s + 1];
+    constexpr int kLanes = 16, kPer = D / kLanes;
+    const int me = threadIdx.x % kLanes, range = blockIdx.x + 1;
+    const int64_t all = a.sums[2 * a.v.seqs + 1], each = range_of(a, all), at = range * each;
+    if (at >= all) return;
+    const int s = __builtin_amdgcn_readfirstlane(Cut::find(a, at, 1));
     const TreeRows rows(a.v, a.sc, s);
-    const int hk = a.sc.over_group(min(head, a.sc.heads - 1));
-    const int r = nvfp4::kv_row_of(token, rows.first_token, rows.group, head - hk * rows.group, rows.count);
-    if (head >= a.sc.heads || r < 0) return;   // no sequence's row
+    if (rows.count <= 0) return;
     int page0;
     const int pages = pages_of(a, rows, &page0);
-    // which range a page is in: whole ranges before the sequence, and then few enough for a product in fp32 to be at most one off
-    const int64_t each = range_of(a, all), front = before / each, rest = before - front * each;
-    const float inverse = 1.0f / float(each);
-    auto range = [&](int64_t page) {
-        int n = static_cast<int>(float(page) * inverse);
-        const int64_t over = page - n * each;
-        n += over >= each ? 1 : over < 0 ? -1 : 0;
-        return static_cast<int>(front) + n;
-    };
-    const int64_t begin = rest + int64_t(r / a.rows * a.v.kv_heads + hk) * (kStart + pages) + kStart;
-    const int first = range(begin), last = range(begin + pages - 1);
-    if (first == last) return;   // written already
-    auto part = [&](int w) { return (2 * int64_t(w) + (w == first)) * a.rows + r % a.rows; };
+    const int64_t before = a.sums[2 * s + 1], in = at - before;
+    // (a division of 64 bits takes as long as a read)
+    const int64_t t = in >> 32 ? in / (kStart + pages) : uint32_t(in) / uint32_t(kStart + pages);
+    const int64_t begin = before + t * (kStart + pages) + kStart;   // of its pages
+    if (begin >= at || begin < at - each) return;                   // they begin in this range, or before the last one
+    const int64_t over = begin + pages - 1 - at;                    // fewer than the pages
+    const int first = range - 1, last = range + (over < each ? 0 : static_cast<int>(uint32_t(over) / uint32_t(each)));
+    const int in_tile = blockIdx.y * kJoinRows + threadIdx.x / kLanes;
+    const int hk = static_cast<int>(t % a.v.kv_heads), r = static_cast<int>(t / a.v.kv_heads) * a.rows + in_tile;
+    if (r >= rows.count) return;
+    auto part = [&](int w) { return (2 * int64_t(w) + (w == first)) * a.rows + in_tile; };
     float top = -INFINITY;
     for (int w = first + me; w <= last; w += kLanes) top = fmaxf(top, a.part_ml[part(w) * 2]);
 #pragma unroll
@@ -481,7 +477,7 @@ kv_tree_join_kernel(TreeArgs a) {
     uint16_t w[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) w[i] = f32_to_bf16_rne(acc[i] * f * a.v_scale);
-    const int64_t row = int64_t(token) * a.sc.heads + head;
+    const int64_t row = rows.place(a.sc, r, hk);
     __builtin_memcpy(__builtin_assume_aligned(a.out + row * D + me * kPer, 2 * kPer > 16 ? 16 : 2 * kPer), w, sizeof w);
     if (a.lse && me == 0) a.lse[row] = (top + log2f(sum)) * kLn2;
 }
@@ -500,7 +496,7 @@ bool allow_lds() {
 }
 
 template <int D>
-int launch(TreeArgs a, const nvfp4::TreePlan& plan, hipStream_t st) {
+int launch(const TreeArgs& a, const nvfp4::TreePlan& plan, hipStream_t st) {
     if (a.added) {
         hipLaunchKernelGGL(kv_tree_sums_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
         if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
@@ -508,14 +504,9 @@ int launch(TreeArgs a, const nvfp4::TreePlan& plan, hipStream_t st) {
     hipLaunchKernelGGL((plan.rows == 128 ? kv_tree_tile_kernel<D, 1> : kv_tree_tile_kernel<D, 2>), dim3(plan.workgroups), dim3(64 * kWaves),
                        tile_lds<D>(), st, a);
     if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-    if (!plan.whole) {
-        const int64_t blocks = int64_t(a.v.total) * ((a.sc.heads + kJoinRows - 1) / kJoinRows);
-        constexpr int64_t kMost = int64_t(1) << 23;   // of a launch, which holds fewer than 2^32 threads
-        for (a.block0 = 0; a.block0 < blocks; a.block0 += kMost) {
-            const int64_t n = blocks - a.block0 < kMost ? blocks - a.block0 : kMost;
-            hipLaunchKernelGGL(kv_tree_join_kernel<D>, dim3(static_cast<unsigned>((n + 3) / 4)), dim3(256), 0, st, a);
-            if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-        }
+    if (!plan.whole && plan.ranges > 1) {
+        hipLaunchKernelGGL(kv_tree_join_kernel<D>, dim3(plan.ranges - 1, a.rows / kJoinRows), dim3(256), 0, st, a);
+        if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     }
     return NVFP4_OK;
 }
@@ -541,7 +532,6 @@ int tree_attend(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, cons
     a.ranges = plan.ranges;
     a.least = plan.least;
     a.added = plan.added;
-    a.block0 = 0;
     a.sums = static_cast<int64_t*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + tree_sum_bytes(seqs));
     a.part_ml = a.part_o + int64_t(2) * plan.ranges * plan.rows * cache->head_dim;
