@@ -261,8 +261,14 @@ kv_slots_kernel(PagesArgs a) {
         slots[i] = positions[i] = -1;
         if (t >= tokens) continue;
         if (t >= until) {
-            s = last_at_most(a.q_starts, s, last, t);
-            until = a.q_starts[s + 1];
+            if (i > 0) {   // mostly the next one's first
+                s = min(s + 1, last);
+                until = a.q_starts[s + 1];
+            }
+            if (t >= until) {
+                s = last_at_most(a.q_starts, s, last, t);
+                until = a.q_starts[s + 1];
+            }
             to_slot = a.kv_lens[s] - until;
             held = -1;
         }
