@@ -20,7 +20,7 @@ import numpy as np
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
-from generate import DEV, DIM, FFN, HEADS, HIDDEN, KV_HEADS, LAYERS, VOCAB, Decoder, norm  # noqa: E402,F401
+from generate import DEV, DIM, HEADS, KV_HEADS, LAYERS, VOCAB, Decoder, norm  # noqa: E402
 import verify_nvfp4_w4a16_amd as nv  # noqa: E402
 
 DEPTH = 3

@@ -83,3 +83,79 @@ def test_a_captured_round_repeats_the_eager_one():
         assert torch.equal(getattr(a, name), getattr(b, name)), name
     for x, y in zip(a.caches, b.caches):
         assert torch.equal(x.data, y.data)
+
+
+def _everything(stream=None):
+    """Results of one call of each on fixed inputs: a small round without a model."""
+    import verify_nvfp4_w4a16_amd as nv
+    import workload
+    from tests._kv import Paged, bf16, int32, starts
+    from tests.test_gpu_draft import _parents
+    from tests.test_gpu_kv import _query_bits
+    g = workload.rng(8)
+    lens, new = [300, 70, 129], [20, 33, 7]
+    c = Paged(lens, 2, 128, 77, extra=4)
+    total, most = sum(new), max(new)
+    parents = int32(np.concatenate([_parents(g, n) for n in new]))
+    drafted, chosen = (int32(g.integers(0, 3, total)) for _ in range(2))
+    logits = torch.tensor(g.standard_normal((total, 500)).astype(np.float32), device="cuda:0")
+    history, said = int32(g.integers(0, 500, (3, 40))), int32([40, 7, 0])
+    half = torch.full((3,), 0.5, device="cuda:0")
+    q = bf16(_query_bits(total, 8, 128, 78))
+    pool, state = int32(c.free + [-1] * 8), int32([0, len(c.free)])
+    table, where = c.table_t.clone(), (c.table_t, c.lens_t, starts(new))
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    step = nv.kv_pages(pool, state, table, int32([-(-n // 64) for n in lens]), c.lens_t, int32([3, 60, 0]), 63, stream=stream)
+    masks, positions = nv.kv_tree(parents, *where[1:], most, stream=stream)
+    out, lse = nv.kv_tree_attention(q, c.cache, *where, masks, positions, most, 320, window=200, stream=stream)
+    adjusted = nv.adjust_logits(logits, history, said, q_starts=where[2], repetition=half + 0.7, presence=half, frequency=half,
+                                drafted=drafted, masks=masks, stream=stream)
+    path, counts, token, kept = nv.tree_accept(drafted, parents, chosen, *where[1:], most, stream=stream)
+    nv.kv_move(c.cache, *where, path, stream=stream)
+    if stream is not None:
+        stream.synchronize()
+    torch.cuda.synchronize()
+    return (pool, table, *step, masks, positions, out, lse, adjusted, path, counts, token, kept, c.data)
+
+
+def test_every_call_on_another_stream():
+    want = _everything()
+    side = torch.cuda.Stream()
+    got = _everything(side)
+    assert len(want) == len(got)
+    for i, (a, b) in enumerate(zip(want, got)):
+        assert torch.equal(a, b), i
+
+
+def test_graphs_that_share_a_workspace():
+    import verify_nvfp4_w4a16_amd as nv
+    import workload
+    from tests._kv import DEV, Paged, bf16, starts
+    from tests.test_gpu_kv import _query_bits
+    from tests.test_gpu_tree_attention import _masks, _of_trees, _wide
+    g = workload.rng(9)
+    calls, need = [], 0
+    for lens, new, wide in (([3000, 100], [16, 12], True), ([2500], [5], False), ([700, 900, 64], [64, 40, 33], True)):
+        c = Paged(lens, 1, 128, sum(lens))
+        masks, _ = _of_trees(g, lens, new)
+        q = bf16(_query_bits(sum(new), 4, 128, sum(new)))
+        table, most = _wide(c) if wide else (c.table_t, max(lens))
+        args = (q, c.cache, table, c.lens_t, starts(new), _masks(masks, 1), None, max(new), most)
+        need = max(need, nv.kv_tree_attention_workspace(c.cache, q, *args[2:5], max(new), most))
+        want, want_lse = nv.kv_tree_attention(*args)
+        calls.append((args, want, want_lse, torch.empty_like(want), torch.empty_like(want_lse)))
+    workspace = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for args, _, _, out, lse in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            nv.kv_tree_attention(*args, out=out, lse=lse, workspace=workspace)
+    for turn in range(4):
+        for i in g.permutation(len(graphs)):
+            calls[i][3].zero_()
+            calls[i][4].zero_()
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for _, want, want_lse, out, lse in calls:
+            assert torch.equal(out, want) and torch.equal(lse, want_lse), turn
