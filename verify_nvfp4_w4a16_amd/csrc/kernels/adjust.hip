@@ -10,8 +10,10 @@
 //
 // Bounds: 192 rows of 151552 bf16 logits take 20 us without penalties (5.8 TB/s;
 // a plain copy 17), 48 us with biases, grammars and histories of 4000 tokens
-// each, of which the counting is 15: the additions in LDS, where a few tokens
-// are most of a text.  8 trees of 48 rows in fp32 take 109 us (4.3 TB/s).
+// each: in copies that leave parts out, 44 without the additions in LDS, 38
+// without applying them, 33 without a history.  (A list of the touched tokens, adjusted
+// after the row went by, took 62: its additions give back what was there before.)
+// 8 trees of 48 rows in fp32 take 109 us (4.3 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

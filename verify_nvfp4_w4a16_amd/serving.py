@@ -4,13 +4,14 @@ choice of the next token.
 
 Argument checks and marshalling only, as in the rest of the binding: every step
 runs in the library's HIP kernels.  The C functions, the cache's layout and the
-exact rules are in include/nvfp4_kv.h.  Calls run on `stream` (default: torch's
-current stream of the tensors' device), never wait for the device, and write to
-the tensors they return or were given; those must stay alive until the stream
-has passed, as with any torch call on another stream.  Tensors and workspaces
-that a call makes belong to `stream`, like what torch makes under
-torch.cuda.stream(stream): to use a result elsewhere, wait for that stream, and
-record_stream() the result if it is dropped while such work is under way.
+exact rules are in include/nvfp4_kv.h.  Calls run on `stream` (a stream of the
+tensors' device, default torch's current one of it, whichever device is current),
+never wait for the device, and write to the tensors they return or were given;
+those must stay alive until the stream has passed, as with any torch call on
+another stream.  Tensors and workspaces that a call makes belong to `stream`,
+like what torch makes under torch.cuda.stream(stream): to use a result
+elsewhere, wait for that stream, and record_stream() the result if it is
+dropped while such work is under way.
 """
 from __future__ import annotations
 
