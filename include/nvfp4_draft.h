@@ -104,6 +104,8 @@ typedef struct {
     const uint64_t* masks;      /* [total][words], 8-byte aligned */
     const int32_t* positions;   /* [total]; NULL where there is no window */
     int64_t words;              /* ceil(max_q / 64)..NVFP4_TREE_WORDS */
+    int32_t whole_tree;         /* 1: the window counts before the tree alone, and the masks
+                                   say all that is seen of the tree itself; else 0 */
 } nvfp4_kv_tree_t;
 
 /*
@@ -116,9 +118,11 @@ int nvfp4_kv_tree_attention_workspace(const nvfp4_kv_cache_t* cache, const nvfp4
 /*
  * Device.  nvfp4_kv_attention for the nodes of trees: of n slots and nq new
  * tokens, row i sees
- *   the slots j < n - nq, with j > position - window if window > 0, and
- *   the slots n - nq + a for which bit a of its mask is set (a < nq),
- * so a mask need not be a tree's, and one without bits leaves a row with the
+ *   the slots j < n - nq, with j > its position - window if window > 0, and
+ *   the slots n - nq + a for which bit a of its mask is set (a < nq), with node
+ *   a's position > its own - window if window > 0 and whole_tree is 0,
+ * so a chain of tokens sees what it sees in nvfp4_kv_attention under the same
+ * window.  A mask need not be a tree's, and one without bits leaves a row with the
  * slots before alone (or with nothing: out 0, lse -inf).  A position is taken
  * into [n - nq, n).  queries->causal is not used, queries->max_q is at most
  * NVFP4_TREE_MAX; all else, outputs and workspace are nvfp4_kv_attention's.

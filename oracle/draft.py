@@ -60,18 +60,18 @@ def mask_words(way, words: int) -> list[int]:
     return [(bits >> 64 * w) & (2 ** 64 - 1) for w in range(words)]
 
 
-def visible(n: int, masks, positions, window: int) -> np.ndarray:
+def visible(n: int, masks, positions, window: int, whole_tree: bool = False) -> np.ndarray:
     """[nq, n]: which slots each node sees.  masks: a Python integer of bits a node."""
     nq = len(masks)
     before = n - nq
     seen = np.zeros((nq, n), bool)
+    place = [min(max(int(p), before), n - 1) for p in positions] if positions is not None else [0] * nq
     for i in range(nq):
-        place = min(max(int(positions[i]), before), n - 1) if positions is not None else 0
         for j in range(max(before, 0)):
-            seen[i, j] = not window or j > place - window
+            seen[i, j] = not window or j > place[i] - window
         for a in range(nq):
             if masks[i] >> a & 1 and before + a >= 0:
-                seen[i, before + a] = True
+                seen[i, before + a] = not window or whole_tree or place[a] > place[i] - window
     return seen
 
 

@@ -251,6 +251,52 @@ def test_oracle_trees_closed_forms():
     assert odraft.visible(2, masks, None, 0).tolist() == [[False, False], [False, False], [True, False], [True, True]]
 
 
+def test_oracle_ways_masks_and_branches():
+    assert odraft.ways([-1, 0, 0, 1, 3, 9, 5]) == [[0], [0, 1], [0, 2], [0, 1, 3], [0, 1, 3, 4], [5], [5, 6]]
+    assert odraft.mask_words([0, 63, 64], 2) == [(1 << 63) + 1, 1]
+    assert odraft.accept([5, 6, 6, 7], [-1, 0, 0, 2], [6, 7, 7, 9]) == ([0, 1], 7)      # the lower of equal drafts
+    assert odraft.accept([5, -1], [-1, 0], [-1, 3]) == ([0], -1)                        # no token matches none
+    masks, _ = _chain(9, 4)
+    assert odraft.visible(2, masks, None, 0).tolist() == [[False, False], [False, False], [True, False], [True, True]]
+
+
+def _chain(n, nq):
+    return [(2 << i) - 1 for i in range(nq)], list(range(n - nq, n))
+
+
+@pytest.mark.parametrize("n,nq", [(9, 4), (90, 60), (64, 64), (130, 70), (1, 1), (3, 8)])
+def test_oracle_chain_under_a_window_sees_what_attention_sees(n, nq):
+    masks, positions = _chain(n, nq)
+    for window in (0, 1, 2, 3, 6, 8, nq - 1, nq, nq + 1, n, n + 5):
+        want = okv.visible(n, nq, True, window) if n >= nq else None
+        seen = odraft.visible(n, masks, positions, window)
+        if want is None:                       # nodes without a slot of their own see nothing, the others at most `window`
+            want = np.array([[j <= n - nq + i and (not window or j > n - nq + i - window) for j in range(n)] for i in range(nq)])
+        assert np.array_equal(seen, want), window
+
+
+def test_oracle_windows_in_trees():
+    # node 4's way is 0, 1, 3, at positions 5, 6, 7; 2 is 1's sibling
+    ways = odraft.ways([-1, 0, 0, 1, 3])
+    masks, positions = [sum(1 << a for a in w) for w in ways], [5 + len(w) - 1 for w in ways]
+    for window, first in ((1, [8]), (2, [7, 8]), (3, [6, 7, 8]), (4, [5, 6, 7, 8]), (5, [4, 5, 6, 7, 8])):
+        of = {5: 0, 6: 1, 7: 3, 8: 4}          # the node of 4's way at each position
+        want = [p if p < 5 else 5 + of[p] for p in first]
+        assert np.flatnonzero(odraft.visible(10, masks, positions, window)[4]).tolist() == want, window
+    # masks that say all of the tree: the window counts before it alone
+    seen = odraft.visible(10, masks, positions, 3, whole_tree=True)
+    assert np.flatnonzero(seen[4]).tolist() == [5, 6, 8, 9] and np.flatnonzero(seen[0]).tolist() == [3, 4, 5]
+    # without a window both are the same, and so they are where it has room for the tree
+    for window in (0, 4, 9):
+        assert np.array_equal(odraft.visible(10, masks, positions, window), odraft.visible(10, masks, positions, window, True))
+
+
+def test_refusals_of_a_whole_tree():
+    lib, c, s, q = drafting._draft(), _cache(), _seqs(), _queries()
+    for whole in (-1, 2):
+        assert lib.nvfp4_kv_tree_attention(c, s, q, _tree(whole_tree=whole), A, A, A, 1 << 40, None) == nv.ERR_SHAPE
+
+
 def test_oracle_attention_is_the_cache_s():
     g = np.random.default_rng(4)
     q, k, v = g.standard_normal((3, 64)), g.standard_normal((7, 64)), g.standard_normal((7, 64))

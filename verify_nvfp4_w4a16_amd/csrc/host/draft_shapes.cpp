@@ -49,6 +49,7 @@ int check_trees(const int32_t* kv_lens, const int32_t* q_starts, int64_t seqs, i
 int check_kv_tree(const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q, const nvfp4_kv_tree_t* t) {
     if (!t) return NVFP4_ERR_NULL;
     if (t->words < 1 || t->words > NVFP4_TREE_WORDS || q->max_q > 64 * t->words) return NVFP4_ERR_SHAPE;
+    if (t->whole_tree != 0 && t->whole_tree != 1) return NVFP4_ERR_SHAPE;
     if (s->seqs > 0 && s->total > 0 && (!t->masks || (q->window > 0 && !t->positions))) return NVFP4_ERR_NULL;
     return misaligned(t->masks, 8) || misaligned(t->positions, 4) ? NVFP4_ERR_ALIGN : NVFP4_OK;
 }

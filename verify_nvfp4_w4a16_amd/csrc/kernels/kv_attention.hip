@@ -742,7 +742,7 @@ int attend(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, const nvf
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (tree) {
         a.sc.causal = 1;   // what a tree's rows see together, and so its pages, are a chain's
-        a.sc.tree = KvTree{reinterpret_cast<const uint32_t*>(tree->masks), tree->positions, static_cast<int>(2 * tree->words)};
+        a.sc.tree = kv_tree(tree, queries);
         switch (cache->head_dim) {
             case 64: return launch_attend<64, true>(a, plan, s);
             case 128: return launch_attend<128, true>(a, plan, s);

@@ -8,6 +8,7 @@
 
 #include "../host/kv_plan.h"
 #include "kv_common.h"
+#include "nvfp4_draft.h"
 
 namespace {
 
@@ -19,6 +20,7 @@ struct KvTree {
     const uint32_t* masks;      // [total][words] (a 64-bit word's low half first), NULL: rows see by their order
     const int32_t* positions;   // [total], where there is a window
     int words;
+    int window;                 // of the tree's own slots, 0: no two nodes are so far apart, or the masks alone say what is seen
 
     // Bits `at` .. `at` + 31 of a node's mask, zeros outside it.
     __device__ __forceinline__ uint32_t bits(int token, int at) const {
@@ -73,6 +75,12 @@ struct KvScores {
     }
 };
 
+// What nvfp4_kv_tree_attention's rows see of their trees.  Positions of one tree differ by less than max_q.
+inline KvTree kv_tree(const nvfp4_kv_tree_t* t, const nvfp4_kv_queries_t* q) {
+    return KvTree{reinterpret_cast<const uint32_t*>(t->masks), t->positions, static_cast<int>(2 * t->words),
+                  t->whole_tree || q->window >= q->max_q ? 0 : static_cast<int>(q->window)};
+}
+
 inline KvScores kv_scores(const nvfp4_kv_cache_t* c, const nvfp4_kv_queries_t* q) {
     KvScores s;
     s.q = static_cast<const uint16_t*>(q->q);
@@ -105,8 +113,8 @@ struct QueryRow {
 
 // The rows of one sequence and kv head: row r is new token r / group, query
 // head r % group of the group.  TREE: the rows are nodes, which see the slots
-// before the tree, from the window's edge at their position on, and the new
-// ones that their masks name.
+// before the tree and the new ones that their masks name, both from the
+// window's edge at their position on.
 template <bool TREE>
 struct QueryRowsOf {
     int first_token, new_tokens, len, count, group;
@@ -128,6 +136,10 @@ struct QueryRowsOf {
     }
     // Slots before the tree (a negative number where there are more nodes than slots).
     __device__ __forceinline__ int before() const { return len - new_tokens; }
+    // A node's position.  (Held to the tree: a difference of positions of any size would leave 32 bits.)
+    __device__ __forceinline__ int position(const KvScores& sc, int token) const {
+        return min(max(sc.tree.positions[token], before()), len - 1);
+    }
     // For rows first .. last (both below count).
     __device__ __forceinline__ Span span(const KvScores& sc, int first, int last) const {
         // a node's position may be any of the tree's, whatever its place in the order
@@ -141,8 +153,7 @@ struct QueryRowsOf {
         const int i = sc.over_group(r);
         if constexpr (TREE) {
             const int token = first_token + i;
-            // (held to the tree first: a difference of positions of any size would leave 32 bits)
-            const int depth = sc.window > 0 ? min(max(sc.tree.positions[token], before()), len - 1) - before() : 0;
+            const int depth = sc.window > 0 ? position(sc, token) - before() : 0;
             return QueryRow{token, r - i * group, min(see_lo(sc, depth), max(before(), 0)), len};
         }
         return QueryRow{first_token + i, r - i * group, see_lo(sc, i), see_hi(sc, i)};
@@ -160,7 +171,15 @@ struct QueryRowsOf {
         uint32_t m = first > -8 ? sc.tree.bits(r.token, first) : 0;
         if (first < 0) m |= first > -8 ? (1u << -first) - 1 : 0xffu;                                   // slots before the tree
         if (slot0 < r.lo && first < 0) m &= r.lo - slot0 < 8 ? ~0u << (r.lo - slot0) : 0u;             // beyond the window
-        return len - slot0 >= 8 ? m : len > slot0 ? m & ((1u << (len - slot0)) - 1) : 0u;
+        m &= len - slot0 >= 8 ? 0xffu : len > slot0 ? (1u << (len - slot0)) - 1 : 0u;
+        // ancestors beyond the window: where it has room for the whole tree there are none
+        if (sc.tree.window > 0 && sc.tree.window < new_tokens && first > -8) {
+            const int edge = position(sc, r.token) - sc.tree.window;
+#pragma unroll 1
+            for (int j = max(-first, 0); m >> j; ++j)
+                if (m >> j & 1 && position(sc, first_token + first + j) <= edge) m &= ~(1u << j);
+        }
+        return m;
     }
 };
 

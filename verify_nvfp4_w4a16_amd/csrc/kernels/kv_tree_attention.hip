@@ -524,7 +524,7 @@ int tree_attend(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs, cons
     a.v = kv_view(cache, seqs);
     a.sc = kv_scores(cache, queries);
     a.sc.causal = 1;
-    a.sc.tree = KvTree{reinterpret_cast<const uint32_t*>(tree->masks), tree->positions, static_cast<int>(2 * tree->words)};
+    a.sc.tree = kv_tree(tree, queries);
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
     a.rows = plan.rows;

@@ -36,7 +36,7 @@ class _Pages(ctypes.Structure):
 
 class _Tree(ctypes.Structure):
     """nvfp4_kv_tree_t"""
-    _fields_ = [("masks", _VP), ("positions", _VP), ("words", _I)]
+    _fields_ = [("masks", _VP), ("positions", _VP), ("words", _I), ("whole_tree", ctypes.c_int32)]
 
 
 class _Adjust(ctypes.Structure):
@@ -158,12 +158,13 @@ def kv_tree_attention_workspace(cache, q, table, kv_lens, q_starts, max_q: int, 
 
 
 def kv_tree_attention(q, cache, table, kv_lens, q_starts, masks, positions, max_q: int, max_kv: int, *, scale=None,
-                      window: int = 0, softcap: float = 0.0, out=None, lse=None, workspace=None, stream=None):
+                      window: int = 0, softcap: float = 0.0, whole_tree: bool = False, out=None, lse=None, workspace=None, stream=None):
     """kv_attention for the nodes of trees: each row of q (bf16 [total, heads, head_dim]) sees the
-    slots before its tree (with a window, those after position - window) and, of the tree's own, the
-    ones its mask names.  masks int64 [total, words] and positions int32 [total] as kv_tree gives them;
-    positions may be None where there is no window.  No tree has more than max_q nodes (at most 256).
-    The rest is kv_attention's."""
+    slots before its tree and, of the tree's own, the ones its mask names; with a window, of both those
+    at positions after its own - window.  masks int64 [total, words] and positions int32 [total] as
+    kv_tree gives them; positions may be None where there is no window.  whole_tree: the window counts
+    before the tree alone, for masks that say all about the tree itself.  No tree has more than max_q
+    nodes (at most 256).  The rest is kv_attention's."""
     dev = cache.device
     total = q.shape[0]
     seqs = _seqs(cache, table, kv_lens, q_starts, total)
@@ -171,7 +172,7 @@ def kv_tree_attention(q, cache, table, kv_lens, q_starts, masks, positions, max_
     if masks.dim() != 2:
         raise ValueError("masks must be int64 [total, words]")
     tree = _Tree(_array("masks", masks, (total, masks.shape[1]), _I64, dev), _array("positions", positions, (total,), _I32, dev),
-                 masks.shape[1])
+                 masks.shape[1], bool(whole_tree))
     out = _out("out", out, q.shape, _BF16, dev, stream)
     lse = _out("lse", lse, q.shape[:2], _F32, dev, stream)
     lib = _draft()
