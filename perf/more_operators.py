@@ -573,8 +573,9 @@ def run(state):
             return out
         return out + nv.kv_tree(st["parents"], step.kv_lens, step.q_starts, st["max_q"])
     if op == "attend":
+        # the masks say what is seen of a tree, and the window what is seen before it: the plain form's definition
         return nv.kv_tree_attention(st["q"], st["caches"][0], st["table"], st["kv_lens"], st["q_starts"], st["masks"], st["positions"],
-                                    st["max_q"], st["max_kv"], window=st["window"], softcap=st["cap"])
+                                    st["max_q"], st["max_kv"], window=st["window"], softcap=st["cap"], whole_tree=True)
     if op == "adjust":
         tree = dict(drafted=st["drafted"], masks=st["masks"]) if st["drafted"] is not None else {}
         return nv.adjust_logits(st["logits"], st["history"], st["history_lens"], prompt_lens=st["prompt_lens"], q_starts=st["q_starts"],
