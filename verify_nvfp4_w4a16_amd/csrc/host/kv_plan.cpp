@@ -47,6 +47,8 @@ KvPlan kv_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_
     return p;
 }
 
+int64_t kv_row_tiles(const KvPlan& p, int64_t total, int64_t group) { return std::min(p.row_tiles, (total * group + p.tile - 1) / p.tile); }
+
 int64_t kv_plan_bytes(const nvfp4_kv_seqs_t* s) { return (2 + 2 * s->seqs + 3) / 4 * 16; }
 
 int64_t kv_workspace_bytes(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nvfp4_kv_queries_t* q, bool few) {

@@ -25,6 +25,12 @@ struct KvPlan {
     int64_t part_rows;   // rows of partial results
 };
 
+// Workgroups of a launch: times 256 threads, a launch of 2^32 would be refused.
+constexpr int64_t kKvLaunch = int64_t(1) << 23;
+
+// Row tiles of a sequence in a launch of many-row workgroups: its bound's, but no more than all rows that there are fill.
+int64_t kv_row_tiles(const KvPlan& p, int64_t total, int64_t group);
+
 // The window as the kernels take it: 0 (no limit) where no sequence of the
 // call is longer, so that a window of any size can be added to a slot.
 int kv_window(const nvfp4_kv_queries_t* q);

@@ -40,10 +40,14 @@ struct AttendArgs {
     int tile;         // rows of a many-row workgroup, 0: few rows
     int splits;       // workgroups over the pages of a row tile, `chunk` pages each
     int chunk;
-    int row_tiles;    // of the longest sequence
+    int row_tiles;    // of the longest sequence (tile: that there can be)
     int32_t* plan;    // few rows: the planned items (kv_plan_kernel), or NULL where splits and chunk say all
     float v_scale;
+    int group0;       // first workgroup of the launch (launch_sliced)
 };
+
+// This workgroup's number among all of the grid's first axis.
+__device__ __forceinline__ int group_of(const AttendArgs& a) { return a.group0 + static_cast<int>(blockIdx.x); }
 
 __device__ __forceinline__ int pages_lo(const Span& s) { return s.lo / kPage; }
 __device__ __forceinline__ int pages_hi(const Span& s) { return (s.hi + kPage - 1) / kPage; }
@@ -178,7 +182,7 @@ kv_attend_rows_kernel(AttendArgs a) {
     // the wavefront's number as a scalar: its pages and their addresses are then scalars too
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, b = lane >> 4;
-    const Item item = find_item(a, blockIdx.x);
+    const Item item = find_item(a, group_of(a));
     if (item.s < 0) return;
     const int s = item.s, hk = item.segment % a.v.kv_heads, row0 = item.segment / a.v.kv_heads * kRowTile;
     const QueryRowsOf<TREE> rows(a.v, a.sc, s);
@@ -337,7 +341,7 @@ kv_attend_rows_kernel(AttendArgs a) {
     }
     const int64_t at = rows.place(a.sc, row0 + r, hk);
     if (pages > item.chunk) {
-        const int64_t to = int64_t(blockIdx.x) * kRowTile + r;
+        const int64_t to = int64_t(group_of(a)) * kRowTile + r;
         float* po = a.part_o + to * D + d0;
         if (top > -INFINITY)
 #pragma unroll
@@ -384,10 +388,10 @@ kv_attend_tile_kernel(AttendArgs a) {
     const int row_wave = wave % (kWaves / HALVES), my_half = wave / (kWaves / HALVES);   // my_half: HALVES 2 only
     const int n = lane & 31, b = lane >> 5;
     const int s = blockIdx.y, split = blockIdx.z;
-    const int hk = blockIdx.x % a.v.kv_heads;
+    const int hk = group_of(a) % a.v.kv_heads;
     const QueryRows rows(a.v, a.sc, s);
     // the last rows see most: they begin first
-    const int tile = int(gridDim.x / a.v.kv_heads) - 1 - int(blockIdx.x / a.v.kv_heads);
+    const int tile = a.row_tiles - 1 - group_of(a) / a.v.kv_heads;
     const int row0 = tile * kRows;
     if (row0 >= rows.count) return;
 
@@ -576,7 +580,7 @@ kv_join_kernel(AttendArgs a) {
     __shared__ float sums[kWaves][D];
     __shared__ float weight[kWaves];
     const int64_t slice = int64_t(a.v.total) * a.sc.heads;
-    const int64_t at = blockIdx.x;
+    const int64_t at = group_of(a);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int token = static_cast<int>(at / a.sc.heads), head = static_cast<int>(at % a.sc.heads);
     const int s = last_sequence(a.v, [&](int i) { return a.v.start(i) <= token; });
@@ -667,28 +671,35 @@ bool allow_lds() {
     return true;
 }
 
+// `count` workgroups in as many launches as hold them: each has fewer than 2^32 threads along an axis.
+template <class Kernel>
+int launch_sliced(Kernel kernel, AttendArgs a, int64_t count, unsigned y, unsigned z, size_t lds, hipStream_t st) {
+    for (int64_t at = 0; at < count; at += nvfp4::kKvLaunch) {
+        a.group0 = static_cast<int>(at);
+        const dim3 grid(static_cast<unsigned>(std::min(count - at, nvfp4::kKvLaunch)), y, z);
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, st, a);
+        if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+    }
+    return NVFP4_OK;
+}
+
 template <int D, bool TREE>
-int launch_attend(const AttendArgs& a, const nvfp4::KvPlan& plan, hipStream_t st) {
+int launch_attend(AttendArgs a, const nvfp4::KvPlan& plan, hipStream_t st) {
+    int ok;
     if (plan.tile) {
+        a.row_tiles = static_cast<int>(nvfp4::kv_row_tiles(plan, a.v.total, a.sc.group));
         // parts of a tile's pages along the slowest axis: those that short sequences do not need come last
-        const int64_t blocks = plan.row_tiles * a.v.kv_heads;
-        if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-        hipLaunchKernelGGL((plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1> : kv_attend_tile_kernel<D, 2>),
-                           dim3(static_cast<unsigned>(blocks), a.v.seqs, plan.splits), dim3(64 * kWaves), tile_lds<D>(), st, a);
+        ok = launch_sliced(plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1> : kv_attend_tile_kernel<D, 2>, a,
+                           int64_t(a.row_tiles) * a.v.kv_heads, a.v.seqs, plan.splits, tile_lds<D>(), st);
     } else {
         if (plan.planned) {
             hipLaunchKernelGGL(kv_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
             if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
         }
-        hipLaunchKernelGGL((kv_attend_rows_kernel<D, TREE>), dim3(plan.items), dim3(64 * kWaves), rows_lds<D>(), st, a);
+        ok = launch_sliced(kv_attend_rows_kernel<D, TREE>, a, plan.items, 1, 1, rows_lds<D>(), st);
     }
-    if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-    if (plan.part_rows > 0) {
-        const int64_t slice = int64_t(a.v.total) * a.sc.heads;
-        hipLaunchKernelGGL(kv_join_kernel<D>, dim3(static_cast<unsigned>(slice)), dim3(64 * kWaves), 0, st, a);
-        if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-    }
-    return NVFP4_OK;
+    if (ok != NVFP4_OK || plan.part_rows == 0) return ok;
+    return launch_sliced(kv_join_kernel<D>, a, int64_t(a.v.total) * a.sc.heads, 1, 1, 0, st);
 }
 
 }  // namespace
