@@ -91,3 +91,72 @@ def test_a_bound_on_the_new_tokens_far_above_them():
     out, lse = nv.kv_attention(bf16(qb), c.cache, c.table_t, c.lens_t, starts(new), 1 << 24, 200)
     torch.cuda.synchronize()
     _check(c, qb, new, out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64))
+
+
+@pytest.mark.gpu
+def test_append_and_read_of_more_tokens_than_a_launch_has_threads_for():
+    # of 65535 sequences the first and the last have a page; the others' tokens are dropped, and read as zeros
+    import torch
+
+    import verify_nvfp4_w4a16_amd as nv
+    from tests._kv import DEV, bf16, int32, starts
+    from tests.test_gpu_kv import _query_bits
+    heads, many, d = 129, 65535, 256
+    rows = bf16(_query_bits(2, heads, d, 78))
+    want = nv.KvCache.empty(2, heads, d, 2.0 ** -6, 2.0 ** -7)
+    nv.kv_append(want, rows, rows.flip(0).contiguous(), int32([[0], [1]]), int32([1, 1]), starts([1, 1]))
+    want_k, want_v = nv.kv_read(want, int32([[0], [1]]), int32([1, 1]), starts([1, 1]), 2)
+    got = nv.KvCache.empty(2, heads, d, 2.0 ** -6, 2.0 ** -7)
+    table = torch.full((many, 1), -1, dtype=torch.int32, device=DEV)
+    table[0, 0], table[-1, 0] = 0, 1
+    where = (table, int32([1] * many), starts([1] * many))
+    k, v = (torch.ones((many, heads, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k[0], k[-1], v[0], v[-1] = rows[0], rows[1], rows[1], rows[0]
+    nv.kv_append(got, k, v, *where)
+    assert torch.equal(got.data, want.data)
+    nv.kv_read(got, *where, many, k=k, v=v)
+    for x, y in ((k, want_k), (v, want_v)):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[-1], y[1]) and not bool(x[1:-1].any())
+
+
+@pytest.mark.gpu
+def test_slot_weights_under_the_largest_bound_on_the_slots():
+    import torch
+
+    import verify_nvfp4_w4a16_amd as nv
+    from tests._kv import DEV, Paged, bf16, starts
+    from tests.test_gpu_kv import _query_bits
+    heads, new, pitch = 8, 130, 1 << 23
+    c = Paged([150], heads, 64, 79)
+    q, st = bf16(_query_bits(new, heads, 64, 80)), starts([new])
+    _, lse = nv.kv_attention(q, c.cache, c.table_t, c.lens_t, st, new, 150)
+    want = nv.kv_weights(q, lse, c.cache, c.table_t, c.lens_t, st, new, 150)
+    table = torch.full((1, pitch), -1, dtype=torch.int32, device=DEV)
+    table[:, :c.table_t.shape[1]] = c.table_t
+    got = torch.ones((1, heads, pitch * 64), dtype=torch.float32, device=DEV)
+    nv.kv_weights(q, lse, c.cache, table, c.lens_t, st, new, pitch * 64, out=got)
+    # few pages are shared by a workgroup's wavefronts, many are not: sums of the same 130 numbers, none negative, in two
+    # orders, each with at most 130 roundings of half a step, 2^-24 of a sum that is no larger than the last
+    assert torch.allclose(got[..., :150], want, rtol=2 * new * 2.0 ** -24, atol=0)
+    assert not any(bool(got[0, h, 150:].any()) for h in range(heads))
+
+
+@pytest.mark.gpu
+def test_eviction_to_a_bound_far_above_the_slots():
+    import torch
+
+    import verify_nvfp4_w4a16_amd as nv
+    from tests._kv import DEV, Paged, int32
+    heads, n, d = 64, 150, 256
+    c = Paged([n], heads, d, 81)
+    w = torch.rand((1, heads, n), device=DEV)
+    made = []
+    for keep in (192, (1 << 23) + 64):
+        dst = nv.KvCache.empty(3, heads, d, c.k_scale, c.v_scale)
+        table = torch.full((1, keep // 64), -1, dtype=torch.int32, device=DEV)
+        table[0, :3] = int32([2, 0, 1])
+        kept, weights, lens = nv.kv_evict(w, c.cache, c.table_t, c.lens_t, table, keep, dst=dst)
+        made.append((dst.data, kept[..., :192], weights[..., :192], lens))
+        assert bool((kept[..., n:] == -1).all()) and not bool(weights[..., n:].any())
+    for a, b in zip(*made):
+        assert torch.equal(a, b)

@@ -25,7 +25,7 @@ struct KvPlan {
     int64_t part_rows;   // rows of partial results
 };
 
-// Workgroups of a launch: times 256 threads, a launch of 2^32 would be refused.
+// Workgroups of 256 threads of a launch: one of 2^32 threads along an axis wraps around.
 constexpr int64_t kKvLaunch = int64_t(1) << 23;
 
 // Row tiles of a sequence in a launch of many-row workgroups: its bound's, but no more than all rows that there are fill.

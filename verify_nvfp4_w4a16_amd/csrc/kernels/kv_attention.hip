@@ -671,16 +671,12 @@ bool allow_lds() {
     return true;
 }
 
-// `count` workgroups in as many launches as hold them: each has fewer than 2^32 threads along an axis.
 template <class Kernel>
-int launch_sliced(Kernel kernel, AttendArgs a, int64_t count, unsigned y, unsigned z, size_t lds, hipStream_t st) {
-    for (int64_t at = 0; at < count; at += nvfp4::kKvLaunch) {
-        a.group0 = static_cast<int>(at);
-        const dim3 grid(static_cast<unsigned>(std::min(count - at, nvfp4::kKvLaunch)), y, z);
-        hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, st, a);
-        if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
-    }
-    return NVFP4_OK;
+int launch_groups(Kernel kernel, AttendArgs a, int64_t count, unsigned y, unsigned z, size_t lds, hipStream_t st) {
+    return launch_sliced(count, 64 * kWaves, [&](int first, unsigned n) {
+        a.group0 = first;
+        hipLaunchKernelGGL(kernel, dim3(n, y, z), dim3(64 * kWaves), lds, st, a);
+    });
 }
 
 template <int D, bool TREE>
@@ -689,17 +685,17 @@ int launch_attend(AttendArgs a, const nvfp4::KvPlan& plan, hipStream_t st) {
     if (plan.tile) {
         a.row_tiles = static_cast<int>(nvfp4::kv_row_tiles(plan, a.v.total, a.sc.group));
         // parts of a tile's pages along the slowest axis: those that short sequences do not need come last
-        ok = launch_sliced(plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1> : kv_attend_tile_kernel<D, 2>, a,
+        ok = launch_groups(plan.tile == kTileRows ? kv_attend_tile_kernel<D, 1> : kv_attend_tile_kernel<D, 2>, a,
                            int64_t(a.row_tiles) * a.v.kv_heads, a.v.seqs, plan.splits, tile_lds<D>(), st);
     } else {
         if (plan.planned) {
             hipLaunchKernelGGL(kv_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
             if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
         }
-        ok = launch_sliced(kv_attend_rows_kernel<D, TREE>, a, plan.items, 1, 1, rows_lds<D>(), st);
+        ok = launch_groups(kv_attend_rows_kernel<D, TREE>, a, plan.items, 1, 1, rows_lds<D>(), st);
     }
     if (ok != NVFP4_OK || plan.part_rows == 0) return ok;
-    return launch_sliced(kv_join_kernel<D>, a, int64_t(a.v.total) * a.sc.heads, 1, 1, 0, st);
+    return launch_groups(kv_join_kernel<D>, a, int64_t(a.v.total) * a.sc.heads, 1, 1, 0, st);
 }
 
 }  // namespace

@@ -200,11 +200,11 @@ __device__ __forceinline__ uint64_t quantise16(u32x4 lo, u32x4 hi, const Scale& 
 // the codes by the boundaries alone; at a tensor scale of 24 bits 58 us), single tokens by latency (48: 6 us).
 template <int D>
 __global__ void __launch_bounds__(256)
-kv_append_kernel(KvView v, Rows kr, Rows vr, Scale ksc, Scale vsc) {
+kv_append_kernel(KvView v, Rows kr, Rows vr, Scale ksc, Scale vsc, int group0) {
     constexpr int kGroups = D / 16, kItems = kPage * kGroups / 256;
     __shared__ uint64_t vcode[kPage][kGroups];              // 16 codes each
     __shared__ __attribute__((aligned(16))) uint8_t scales[8 * D];   // K's and V's, in the record's order
-    const int u = blockIdx.x / v.kv_heads, h = blockIdx.x % v.kv_heads, tid = threadIdx.x;
+    const int group = group0 + static_cast<int>(blockIdx.x), u = group / v.kv_heads, h = group % v.kv_heads, tid = threadIdx.x;
     const int s = last_sequence(v, [&](int i) { return nvfp4::kv_append_unit(v.start(i), i) <= u; });
     if (s < 0) return;
     const int t0 = v.start(s), nq = v.start(s + 1) - t0;
@@ -280,10 +280,10 @@ __device__ __forceinline__ uint32_t values2(uint32_t w, float scale, float t) {
 // heads of 128: 31 us for 172 MB, 5.5 TB/s).
 template <int D>
 __global__ void __launch_bounds__(D)
-kv_read_kernel(KvView v, uint16_t* k_out, uint16_t* v_out, float kt, float vt) {
+kv_read_kernel(KvView v, uint16_t* k_out, uint16_t* v_out, float kt, float vt, int group0) {
     constexpr int kGroups = D / 16;
     __shared__ uint16_t vval[8][D + 8];
-    const int u = blockIdx.x / v.kv_heads, h = blockIdx.x % v.kv_heads, tid = threadIdx.x;
+    const int group = group0 + static_cast<int>(blockIdx.x), u = group / v.kv_heads, h = group % v.kv_heads, tid = threadIdx.x;
     const int s = unit_sequence(v, u);
     if (s < 0) return;
     const int t0 = v.start(s), nq = v.start(s + 1) - t0;
@@ -333,16 +333,18 @@ kv_read_kernel(KvView v, uint16_t* k_out, uint16_t* v_out, float kt, float vt) {
 template <int D>
 int launch_append(const KvView& v, const Rows& k, const Rows& vr, float kt, float vt, int64_t units, hipStream_t st) {
     if (units * v.kv_heads > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL(kv_append_kernel<D>, dim3(static_cast<unsigned>(units * v.kv_heads)), dim3(256), 0, st, v, k, vr, scale_of(kt),
-                       scale_of(vt));
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+    const Scale ks = scale_of(kt), vs = scale_of(vt);
+    return launch_sliced(units * v.kv_heads, 256, [&](int first, unsigned n) {
+        hipLaunchKernelGGL(kv_append_kernel<D>, dim3(n), dim3(256), 0, st, v, k, vr, ks, vs, first);
+    });
 }
 
 template <int D>
 int launch_read(const KvView& v, uint16_t* k, uint16_t* vo, float kt, float vt, int64_t units, hipStream_t st) {
     if (units * v.kv_heads > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL(kv_read_kernel<D>, dim3(static_cast<unsigned>(units * v.kv_heads)), dim3(D), 0, st, v, k, vo, kt, vt);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+    return launch_sliced(units * v.kv_heads, D, [&](int first, unsigned n) {
+        hipLaunchKernelGGL(kv_read_kernel<D>, dim3(n), dim3(D), 0, st, v, k, vo, kt, vt, first);
+    });
 }
 
 }  // namespace

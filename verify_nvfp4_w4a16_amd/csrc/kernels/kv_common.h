@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "nvfp4_kv.h"
+#include "../host/kv_plan.h"
 #include "nvfp4_common.h"
 
 namespace {
@@ -81,6 +82,17 @@ struct KvView {
         return record_of<D>(page_id(s, p), h);
     }
 };
+
+// `count` workgroups in as many launches as hold them: launch(first, how many).
+template <class Launch>
+int launch_sliced(int64_t count, int threads, Launch launch) {
+    const int64_t most = nvfp4::kKvLaunch * 256 / threads;
+    for (int64_t at = 0; at < count; at += most) {
+        launch(static_cast<int>(at), static_cast<unsigned>(count - at < most ? count - at : most));
+        if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+    }
+    return NVFP4_OK;
+}
 
 inline KvView kv_view(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s) {
     return KvView{c->data,   c->pages,    c->kv_heads,    s->table, s->kv_lens,

@@ -112,15 +112,16 @@ struct QueryBlock {
 // the wavefront is at another page, took 39 us where two took 53).
 template <int D, int PAGES, int ROWS, int SHARE>
 __global__ void __launch_bounds__(256, D == 256 ? 2 : 3)
-kv_weights_kernel(WeightArgs a) {
+kv_weights_kernel(WeightArgs a, int group_first) {
     using Block = QueryBlock<D, ROWS>;
     constexpr int kGroup = 4 / SHARE * PAGES;   // pages of the workgroup
     __shared__ Block block;
     __shared__ f32x4 sums[4][PAGES][64];   // of a wavefront's pages, a lane's slots: in registers only while their page is
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, b = lane >> 4;
-    const int s = blockIdx.y, hk = blockIdx.x % a.v.kv_heads;
-    const int group0 = blockIdx.x / a.v.kv_heads * kGroup;     // the workgroup's first page
+    const int group = group_first + static_cast<int>(blockIdx.x);
+    const int s = blockIdx.y, hk = group % a.v.kv_heads;
+    const int group0 = group / a.v.kv_heads * kGroup;          // the workgroup's first page
     const int page0 = group0 + wave / SHARE * PAGES;
     const int64_t out = (int64_t(s) * a.v.kv_heads + hk) * a.max_kv;
     if (group0 * kPage >= a.v.len(s)) {   // beyond the sequence: most workgroups where lengths differ much
@@ -280,8 +281,9 @@ int launch_weights(const WeightArgs& a, int64_t rows, hipStream_t st) {
                         : pages == 1 ? kv_weights_kernel<D, 1, kRows, 4>
                         : pages == 4 ? kv_weights_kernel<D, 1, kRows, 1>
                                      : kv_weights_kernel<D, 4, kRows, 1>;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(256), 0, st, a);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+    return launch_sliced(blocks, 256, [&](int first, unsigned n) {
+        hipLaunchKernelGGL(kernel, dim3(n, a.v.seqs), dim3(256), 0, st, a, first);
+    });
 }
 
 struct EvictArgs {
@@ -516,13 +518,13 @@ constexpr int kMoveThreads = 2 * D;
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads<D>)
-kv_move_kernel(EvictArgs a) {
+kv_move_kernel(EvictArgs a, int group0) {
     using R = KvRecord<D>;
     __shared__ const uint8_t* from[kPage];
     __shared__ int slot_in[kPage];
     __shared__ bool live[kPage];
-    const int s = blockIdx.y, tid = threadIdx.x;
-    const int h = blockIdx.x % a.v.kv_heads, page = blockIdx.x / a.v.kv_heads;
+    const int s = blockIdx.y, tid = threadIdx.x, group = group0 + static_cast<int>(blockIdx.x);
+    const int h = group % a.v.kv_heads, page = group / a.v.kv_heads;
     // the length, the kept slots and the page they go to are asked for together
     const int at = page * kPage + (tid & 63);
     const int j = max(a.kept[(int64_t(s) * a.v.kv_heads + h) * a.keep + min(at, a.keep - 1)], 0);
@@ -605,8 +607,9 @@ template <int D>
 int launch_move(const EvictArgs& a, hipStream_t st) {
     const int64_t blocks = int64_t((a.keep + kPage - 1) / kPage) * a.v.kv_heads;
     if (blocks > 0x7fffffff) return NVFP4_ERR_SHAPE;
-    hipLaunchKernelGGL(kv_move_kernel<D>, dim3(static_cast<unsigned>(blocks), a.v.seqs), dim3(kMoveThreads<D>), 0, st, a);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+    return launch_sliced(blocks, kMoveThreads<D>, [&](int first, unsigned n) {
+        hipLaunchKernelGGL(kv_move_kernel<D>, dim3(n, a.v.seqs), dim3(kMoveThreads<D>), 0, st, a, first);
+    });
 }
 
 bool misaligned(const void* p, uintptr_t al) { return (reinterpret_cast<uintptr_t>(p) & (al - 1)) != 0; }
