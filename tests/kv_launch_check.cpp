@@ -32,7 +32,11 @@ void check(const nvfp4_kv_cache_t& c, const nvfp4_kv_seqs_t& s, const nvfp4_kv_q
     expect(nvfp4::kKvLaunch * 256 < int64_t(1) << 32, "threads of a launch", c, s, q);
     expect(s.total * q.heads <= most, "rows to join", c, s, q);
     for (int tree = 0; tree <= (q.max_q <= NVFP4_TREE_MAX ? 1 : 0); ++tree) {
-        if (tree && nvfp4::tree_plan(&c, &s, &q).rows) continue;   // the tiles of trees, which tree_plan_check.cpp drives
+        if (tree && nvfp4::tree_plan(&c, &s, &q).rows) {   // tiles, whose layout tree_plan_check.cpp drives
+            const nvfp4::TreePlan t = nvfp4::tree_plan(&c, &s, &q);
+            expect(t.workgroups >= 1 && t.workgroups <= most && (t.whole || t.workgroups <= nvfp4::kKvLaunch), "workgroups of trees", c, s, q);
+            continue;
+        }
         const nvfp4::KvPlan p = nvfp4::kv_plan(&c, &s, &q, tree);
         if (!p.tile) {
             expect(p.items >= 0 && int64_t(p.items) * nvfp4::kKvRowTile < int64_t(1) << 40, "items", c, s, q);

@@ -160,3 +160,25 @@ def test_eviction_to_a_bound_far_above_the_slots():
         assert bool((kept[..., n:] == -1).all()) and not bool(weights[..., n:].any())
     for a, b in zip(*made):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_more_trees_in_tiles_than_a_launch_has_threads_for():
+    # a bound of 33 nodes makes it a call for the tiles, of whole segments
+    import torch
+
+    import verify_nvfp4_w4a16_amd as nv
+    from tests._kv import Paged, bf16, int32, starts
+    from tests.test_gpu_kv import _query_bits
+    from tests.test_gpu_tree_attention import _check
+    heads, many = 257, 65535
+    c = Paged([3, 60], heads, 64, 82)
+    qb = _query_bits(2, heads, 64, 83)
+    ends = bf16(qb)
+    q = torch.cat([ends[:1].expand(many - 1, heads, 64), ends[1:]])
+    table = torch.cat([c.table_t[:1].repeat(many - 1, 1), c.table_t[1:]])
+    masks = torch.ones((many, 1), dtype=torch.int64, device=q.device)
+    out, lse = nv.kv_tree_attention(q, c.cache, table, int32([3] * (many - 1) + [60]), starts([1] * many), masks, None, 33, 60)
+    _check(c, qb, [1, 1], [1, 1], None, out[[0, many - 1]].float().cpu().numpy().astype(np.float64),
+           lse[[0, many - 1]].cpu().numpy().astype(np.float64))
+    assert _same(out, lse, 1, many - 1)

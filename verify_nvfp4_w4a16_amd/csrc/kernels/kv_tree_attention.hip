@@ -42,6 +42,7 @@ struct TreeArgs {
     int whole;         // nothing is cut
     int ranges;        // that the pages are cut into
     int least;         // pages of a range at least
+    int group0;        // first workgroup of the launch
     float v_scale;
 };
 
@@ -210,7 +211,7 @@ kv_tree_tile_kernel(TreeArgs a) {
         {
             const Cut cut(a);
             if (done == 0 && blockIdx.x == 0 && !a.whole) cut.leave(a);
-            const Piece piece = cut.piece(a, blockIdx.x, done);
+            const Piece piece = cut.piece(a, a.group0 + static_cast<int>(blockIdx.x), done);
             s = scalar(piece.s), take = scalar(piece.take), skip = scalar(piece.skip), pages = scalar(piece.pages);
             if (s < 0) return;
             hk = scalar(piece.index % a.v.kv_heads), row0 = scalar(piece.index / a.v.kv_heads * kRows);
@@ -496,14 +497,18 @@ bool allow_lds() {
 }
 
 template <int D>
-int launch(const TreeArgs& a, const nvfp4::TreePlan& plan, hipStream_t st) {
+int launch(TreeArgs a, const nvfp4::TreePlan& plan, hipStream_t st) {
     if (a.added) {
         hipLaunchKernelGGL(kv_tree_sums_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
         if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
     }
-    hipLaunchKernelGGL((plan.rows == 128 ? kv_tree_tile_kernel<D, 1> : kv_tree_tile_kernel<D, 2>), dim3(plan.workgroups), dim3(64 * kWaves),
-                       tile_lds<D>(), st, a);
-    if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
+    // ranges are one launch's; whole segments may take several
+    const int ok = launch_sliced(plan.workgroups, 64 * kWaves, [&](int first, unsigned n) {
+        a.group0 = first;
+        hipLaunchKernelGGL((plan.rows == 128 ? kv_tree_tile_kernel<D, 1> : kv_tree_tile_kernel<D, 2>), dim3(n), dim3(64 * kWaves), tile_lds<D>(),
+                           st, a);
+    });
+    if (ok != NVFP4_OK) return ok;
     if (!plan.whole && plan.ranges > 1) {
         hipLaunchKernelGGL(kv_tree_join_kernel<D>, dim3(plan.ranges - 1, a.rows / kJoinRows), dim3(256), 0, st, a);
         if (hipGetLastError() != hipSuccess) return NVFP4_ERR_HIP;
