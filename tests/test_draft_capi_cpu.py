@@ -326,6 +326,18 @@ def test_layout_of_tree_attention_at_the_ends_of_every_field(tmp_path):
     assert r.returncode == 0 and "plan ok" in r.stdout, (r.stdout[-2000:], r.stderr[-4000:])
 
 
+def test_a_stream_may_be_a_handle_alone(monkeypatch):
+    from verify_nvfp4_w4a16_amd import serving
+
+    class Handle:
+        cuda_stream = 55
+
+    calls = []
+    monkeypatch.setattr(serving, "_current_device", lambda: 0)
+    serving._launch("x", lambda *args: calls.append(args) or nv.OK, torch.device("cuda:0"), Handle, 1)
+    assert calls == [(1, 55)]
+
+
 def test_calls_run_with_their_tensors_device_current(monkeypatch):
     from verify_nvfp4_w4a16_amd import serving
     current, calls = [0], []

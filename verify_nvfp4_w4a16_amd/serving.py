@@ -161,7 +161,7 @@ def _launch(name, call, device, stream, *args) -> None:
     """The library call on `stream`, or on torch's current stream of the tensors' device, with that device current."""
     if stream is None:
         handle = _raw_stream(device.index)   # at once: torch.cuda.current_stream() would build a Stream object (2 us) first
-    elif stream.device == device:
+    elif getattr(stream, "device", device) == device:   # a handle alone is taken for one of it
         handle = stream.cuda_stream
     else:
         raise ValueError(f"stream must be one of {device}")
