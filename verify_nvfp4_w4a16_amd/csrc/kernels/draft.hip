@@ -106,9 +106,10 @@ __device__ __forceinline__ void group_scan(uint32_t (&v)[N], uint32_t (&all)[N],
 constexpr int kEach = 4, kChunk = kEach * kScanThreads;   // pages of a thread, one after the other
 
 struct Marks {
-    uint32_t at[kChunk];
+    alignas(16) uint32_t at[kChunk];   // cleared 16 bytes at a time
     uint32_t tmp[kScanWaves][1];
 };
+static_assert(alignof(Marks) >= alignof(uint4));
 
 // The sequences (threads of the block) of pages at + 4 tid .., of which a thread has `own` pages from `from` on.
 __device__ __forceinline__ void owners(Marks& m, int at, int from, int own, int (&whose)[kEach]) {
