@@ -78,7 +78,9 @@ typedef struct {
  *   slots      [total]     64 * page + slot in page of each new token; -1 behind
  *                          the last one and for a page outside [0, 2^25)
  *   positions  [total]     its slot's number within the sequence; -1 behind the last
- * slots and positions may be NULL.  state_out may be state, held_out held and
+ * slots are for callers that write a step's rows elsewhere by other means
+ * (nvfp4_kv_append finds them from the table), positions for rotary angles and
+ * the like; either may be NULL.  state_out may be state, held_out held and
  * kv_lens keep: a captured step then carries its own state on.  With other
  * outputs a call repeated on the same inputs gives the same again.  Table
  * entries that no new page takes stay as they were.
@@ -126,6 +128,9 @@ int nvfp4_kv_tree_attention_workspace(const nvfp4_kv_cache_t* cache, const nvfp4
  * slots before alone (or with nothing: out 0, lse -inf).  A position is taken
  * into [n - nq, n).  queries->causal is not used, queries->max_q is at most
  * NVFP4_TREE_MAX; all else, outputs and workspace are nvfp4_kv_attention's.
+ * max_q and max_kv also choose between kernels: bounds far above the trees and
+ * caches (a capacity, in a captured round) change last bits, and cost short
+ * caches up to three times the time.
  * Errors: NULL, SHAPE, ALIGN, SCRATCH, HIP, DEVICE.
  */
 int nvfp4_kv_tree_attention(const nvfp4_kv_cache_t* cache, const nvfp4_kv_seqs_t* seqs,
@@ -168,7 +173,8 @@ typedef struct {
  *   if v is in the bias list:  x = x + its value (the last one's, if several)
  *   if the row's state does not allow v:  x = -inf
  * in fp32, rounded once (ties to even) where out is bf16.  A NaN stays one
- * where it is allowed.  out may be logits (with the same type and pitch).
+ * where it is allowed.  out may be logits (with the same type and pitch), and
+ * must not overlap them otherwise.
  * Rows of no sequence are not written.  Alignment: logits and out to their element
  * size, masks to 8 bytes, the rest to 4.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, HIP, DEVICE.

@@ -20,6 +20,9 @@ TreePlan tree_plan(const nvfp4_kv_cache_t* c, const nvfp4_kv_seqs_t* s, const nv
     // 3000 (48128) 66 | 43; D = 128, 32 of 9 x 4 over 3000 (36096) 60 | 59, 16 of 64 x 2 over 1000 24 | 44, over 3000 84 | 61;
     // D = 256, 4 of 64 x 2 over 10000 (40192) 95 | 93, 16 over 1000 45 | 65, over 3000 134 | 109.  At D = 256 a CU holds one tile, and
     // three 16-row workgroups are quicker at any length: 32 of 9 x 4 rows over 3000 101 | 115, over 10000 277 | 338.
+    // The lengths are the device's, so the host's bounds decide, and one far above them gives short caches tiles.  max_kv the
+    // longest cache | 32768, us, D = 128: 16 of 64 x 2 rows over 1000 slots 25 | 45, 32 of 9 x 4 over 500 14 | 29, 1 of 16 x 4 over
+    // 900 10 | 12, 32 of 16 x 4 over 4000 86 | 78; a max_q of 64 instead of 9: 14 | 21.
     const int64_t groups = std::min(s->seqs * c->kv_heads, int64_t(1) << 24), work = groups * std::min((rows + 15) / 16 * pages, int64_t(1) << 24);
     if (rows <= (c->head_dim == 256 ? 48 : 32) || work < kTreeWork) return p;
     // 64 rows, a page's halves on different wavefronts, or 128: 32 trees of 16 x 4 rows over 3000 slots 63 | 79 us

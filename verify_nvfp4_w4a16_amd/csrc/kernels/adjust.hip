@@ -69,7 +69,7 @@ adjust_kernel(AdjustArgs args) {
     __shared__ float bias[NVFP4_BIAS_MAX];
     const nvfp4_adjust_t& a = args.a;
     const int tid = threadIdx.x, lane = tid & 63;
-        const int unit = args.unit0 + blockIdx.x / args.pieces, piece = blockIdx.x % args.pieces;
+    const int unit = args.unit0 + blockIdx.x / args.pieces, piece = blockIdx.x % args.pieces;
     const int from = piece * kPiece, size = min(kPiece, args.vocab - from);
 
     // the sequence of this unit and its rows

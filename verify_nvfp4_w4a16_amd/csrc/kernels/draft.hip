@@ -17,8 +17,9 @@ constexpr int kTreeMax = NVFP4_TREE_MAX;
 constexpr int kScanThreads = nvfp4::kPagesBlock;
 constexpr int kFillThreads = 256, kFillEach = 8;   // tokens of a thread
 // Slots and positions of this many tokens at most are filled by the workgroup
-// that makes the tables, which spares a launch: 64 sequences of 16 tokens 5.6 us and 7.8 by a kernel of their own, of
-// 64 tokens 9.5 and 9.0 (and 3 us of the host), of 128 tokens 15 and 8.6.
+// that makes the tables, which spares a launch: 64 sequences of 16 tokens 5.6
+// us and 7.8 by a kernel of their own, of 64 tokens 9.5 and 9.0 (and 3 us of
+// the host), of 128 tokens 15 and 8.6.
 constexpr int kFillInline = 4096;
 
 struct PagesArgs {
@@ -56,7 +57,8 @@ __device__ __forceinline__ void fill_token(const PagesArgs& a, int t, int first,
     if (a.positions) a.positions[t] = where;
 }
 
-// v of the lane that a data-parallel move names, 0 where there is none or its row (16 lanes) is not among ROWS.
+// v of the lane that a data-parallel move names, 0 where there is none or its
+// row (16 lanes) is not among ROWS.
 template <int CONTROL, int ROWS = 0xf>
 __device__ __forceinline__ uint32_t moved(uint32_t v) {
     return __builtin_amdgcn_update_dpp(0u, v, CONTROL, ROWS, 0xf, false);
@@ -77,12 +79,15 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v, Op op) {
     return op(v, moved<0x143, 0xc>(v));   // lane 31, to the second half
 }
 
-// The same over the threads of the workgroup, N values at a time, with the whole and what lies in the wavefronts before.  Through lanes' moves and one
-// barrier: with shuffles, which go through LDS, three such scans were half of the 7 us of a step of 48 sequences.
+// The same over the threads of the workgroup, N values at a time, with the
+// whole and what lies in the wavefronts before.  Through lanes' moves and one
+// barrier: with shuffles, which go through LDS, three such scans were half of
+// the 7 us of a step of 48 sequences.
 constexpr int kScanWaves = kScanThreads / 64;
 
 template <int N, class Op>
-__device__ __forceinline__ void group_scan(uint32_t (&v)[N], uint32_t (&all)[N], uint32_t (&front)[N], uint32_t (&tmp)[kScanWaves][N], Op op) {
+__device__ __forceinline__ void group_scan(uint32_t (&v)[N], uint32_t (&all)[N], uint32_t (&front)[N],
+                                           uint32_t (&tmp)[kScanWaves][N], Op op) {
     static_assert(kScanWaves == 16);   // a row
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
@@ -111,7 +116,8 @@ struct Marks {
 };
 static_assert(alignof(Marks) >= alignof(uint4));
 
-// The sequences (threads of the block) of pages at + 4 tid .., of which a thread has `own` pages from `from` on.
+// The sequences (threads of the block) of pages at + 4 tid .., of which a
+// thread has `own` pages from `from` on.
 __device__ __forceinline__ void owners(Marks& m, int at, int from, int own, int (&whose)[kEach]) {
     const int tid = threadIdx.x;
     *reinterpret_cast<uint4*>(m.at + kEach * tid) = uint4{0, 0, 0, 0};
@@ -143,7 +149,8 @@ kv_pages_kernel(PagesArgs a, int fill) {
     const int tid = threadIdx.x;
     const int h0 = a.state[0] % a.capacity, head = h0 < 0 ? h0 + a.capacity : h0;
     const int count = min(max(a.state[1], 0), a.capacity), room = a.capacity - count;
-    // Sums of what is asked are held at one more than there is: what is beyond it is not granted, however far.
+    // Sums of what is asked are held at one more than there is: what is beyond
+    // it is not granted, however far.
     const uint32_t over = uint32_t(max(a.total, count)) + 1;
     const auto plus = [](uint32_t x, uint32_t y) { return x + y; };
     const auto plus_held = [=](uint32_t x, uint32_t y) { return min(x + y, over); };
@@ -228,8 +235,8 @@ kv_pages_kernel(PagesArgs a, int fill) {
     for (int t = tid; t < a.total; t += kScanThreads) fill_token(a, t, 0, max(a.seqs - 1, 0), given);
 }
 
-// The last sequence that begins at token t or before it, by a wavefront: two steps for 4096 sequences, where halves take twelve loads
-// one after the other.
+// The last sequence that begins at token t or before it, by a wavefront: two
+// steps for 4096 sequences, where halves take twelve loads one after the other.
 __device__ __forceinline__ int last_start(const PagesArgs& a, int t) {
     const int lane = threadIdx.x & 63;
     int s = 0;
@@ -240,8 +247,9 @@ __device__ __forceinline__ int last_start(const PagesArgs& a, int t) {
     }
 }
 
-// Slots and positions of many tokens, once the tables are made.  Latency again: 410000 tokens of 500 prompts took 9.8 us with
-// a search and a page number for each, 7.6 with those of a thread one after the other.
+// Slots and positions of many tokens, once the tables are made.  Latency again:
+// 410000 tokens of 500 prompts took 9.8 us with a search and a page number for
+// each, 7.6 with those of a thread one after the other.
 __global__ void __launch_bounds__(kFillThreads)
 kv_slots_kernel(PagesArgs a) {
     const int t0 = blockIdx.x * (kFillThreads * kFillEach), end = min(t0 + kFillThreads * kFillEach, a.total);

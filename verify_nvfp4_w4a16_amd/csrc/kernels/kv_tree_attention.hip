@@ -8,7 +8,7 @@
 // that lie within a range are finished by it; the parts of the others are joined
 // by a second kernel, in the order of their pages.  (Cut by the longest sequence's
 // pages instead, 32 trees of 9 .. 16 nodes x 4 heads over 1000 .. 16000 slots took 175 us
-// and now 104, four of 200 .. 255 over 20000 .. 65000 slots 1010 and now 720.)
+// and now 105, four of 200 .. 255 over 20000 .. 65000 slots 1010 and now 679.)
 // Few pages go to the 16-row workgroups of kv_attention.hip (host/tree_plan.cpp).
 #include <hip/hip_runtime.h>
 
@@ -196,9 +196,15 @@ constexpr int kPageBytes = KTile<D>::kBytes + VTile<D>::kBytes;
 // on wavefronts 0 and 1 and the last on 2 and 3.  A page is decoded once for all of them
 // into LDS, two pages after its loads began (what every wavefront holds of both is 22 registers).  Bound by the
 // matrix unit and the vector unit taking turns, as in kv_attention.hip: at 128 rows of 128
-// dims a page takes a wavefront 1024 cycles of products and about 1300 of vector work, and
-// 570 TFLOP/s of the largest trees is 2.1 us a page with two workgroups a CU.  Products of the
+// dims a page takes a wavefront 1024 cycles of products and about 1200 of vector work, and
+// a workgroup 2.4 us with two of them on a CU (four of 200 .. 255 nodes over 20000 .. 65000 slots:
+// 832 TFLOP/s of what they see, 890 of the tiles' rows).  Products of the
 // next half beside the exponentials of this one left registers for one operand's read ahead, and were no faster.
+//
+// Causal rows of many tokens keep kv_attention.hip's kernel, whose tiles see pages of their own and
+// are cut one by one, and its layout of a page in LDS.  Chains in that | in this, us: D = 128, 32 of 16 x 4 rows
+// over 4000 slots 88 | 75, 4 of 255 x 4 over 32000 606 | 601; D = 256, 16 of 64 x 2 over 8000 244 | 214; D = 64, 64 of
+// 64 x 4 over 4000 183 | 211.  Ranges over segments that see different pages are not tried.
 template <int D, int HALVES>
 __global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
 kv_tree_tile_kernel(TreeArgs a) {

@@ -103,7 +103,8 @@ def kv_pages(pool, state, table, held, keep, fresh, total: int, *, out: KvStep =
     and held (int32 [seqs], entries of a row that the sequence owns) are the sequences' pages.  New
     pages come from the pool's front into table, pages that a sequence no longer needs go to its
     back, both in place; a sequence that ended keeps 0 slots and asks for none.  One whose pages or
-    tokens (`total` rows at most) are not there keeps its slots and gets no new tokens.  out: the
+    tokens (`total` rows at most) are not there keeps its slots and gets no new tokens.  The step's
+    slots serve callers that write rows elsewhere themselves; kv_append takes the table.  out: the
     tensors to write; its state, held and kv_lens may be the call's own state, held and keep, so
     that a captured step carries them on."""
     dev = _gpu("table", table)
@@ -164,7 +165,10 @@ def kv_tree_attention(q, cache, table, kv_lens, q_starts, masks, positions, max_
     at positions after its own - window.  masks int64 [total, words] and positions int32 [total] as
     kv_tree gives them; positions may be None where there is no window.  whole_tree: the window counts
     before the tree alone, for masks that say all about the tree itself.  No tree has more than max_q
-    nodes (at most 256).  The rest is kv_attention's."""
+    nodes (at most 256).  The rest is kv_attention's.
+
+    max_q and max_kv also choose the kernel: a capacity as the bound, as a captured round takes it, costs
+    short caches up to three times the time."""
     dev = cache.device
     total = q.shape[0]
     seqs = _seqs(cache, table, kv_lens, q_starts, total)
