@@ -173,7 +173,7 @@ constexpr int kSumRow = D + 4;
 // bound by its reads (32 one-token steps of 32 heads over 3 .. 131071 slots of 8
 // heads of 128: 103 us for 575 MB, 5.6 TB/s with what the memory-side cache
 // kept), a short one by the chain of dependent reads and one page's work (777
-// slots: 10 us; at D = 256 that work and 16 rows of sums in 246 registers leave
+// slots: 10 us; at D = 256 that work and 16 rows of sums in 241 registers leave
 // two wavefronts a SIMD: 16 verify rounds of 5 tokens in a window of 1500 take 24 us for 40 MB).
 template <int D, bool TREE>
 __global__ void __launch_bounds__(64 * kWaves, 2)
